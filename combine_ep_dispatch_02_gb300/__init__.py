@@ -35,7 +35,9 @@ EXPORTS = ("ep_plan_create", "ep_plan_destroy", "ep_plan_set_variant", "ep_plan_
            "ep_dispatch", "ep_dispatch_route", "ep_dispatch_scatter", "ep_combine", "ep_reset",
            "ep_status", "ep_strerror", "ep_last_error", "ep_route_noalloc",
            "ep_quantize_received", "ep_combine_fp8", "ep_group_by_expert", "ep_ungroup_by_expert",
-           "ep_dispatch_grouped", "ep_quantize_received_fp4", "ep_combine_fp4", "ep_probe_read")
+           "ep_dispatch_grouped", "ep_quantize_received_fp4", "ep_combine_fp4", "ep_probe_read",
+           "ep_rms_norm_fp8", "ep_sort_workspace_bytes", "ep_sort_by_expert", "ep_sorted_rows",
+           "ep_return_rows", "ep_return_rows_backward", "ep_matmul_fp8")
 
 
 class EpError(RuntimeError):
@@ -65,6 +67,7 @@ def load_library(path: Optional[str] = None):
                            "combine_ep_dispatch_02_gb300.build.build()")
     lib = ctypes.CDLL(p)
     V, I, U64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_size_t
+    L, F = ctypes.c_int64, ctypes.c_float
     sig = {
         "ep_plan_create": (I, [ctypes.POINTER(V), I, I, I, I, I, I, I]),
         "ep_plan_destroy": (I, [V]),
@@ -87,6 +90,13 @@ def load_library(path: Optional[str] = None):
         "ep_quantize_received_fp4": (I, [V, V, V, V, U64, V]),
         "ep_combine_fp4": (I, [V, V, V, V, V, V, U64, V]),
         "ep_probe_read": (I, [V, ctypes.POINTER(ctypes.c_uint64), I]),
+        "ep_rms_norm_fp8": (I, [V, L, V, L, V, I, I, L, I, F, V, V, V, V, V]),
+        "ep_sort_workspace_bytes": (SZ, [I, L, I, I]),
+        "ep_sort_by_expert": (I, [V, V, I, L, I, I, L, V, V, V, V, SZ, V, V]),
+        "ep_sorted_rows": (I, [V, V, V, V, I, L, I, L, L, I, V, V, V, V]),
+        "ep_return_rows": (I, [V, V, V, V, I, L, I, L, I, I, V, V, V]),
+        "ep_return_rows_backward": (I, [V, V, V, V, V, I, L, I, L, I, I, V, V, V, V]),
+        "ep_matmul_fp8": (I, [V, V, V, V, V, L, I, I, I, I, I, V, V, V, V]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -426,6 +436,13 @@ class Plan:
                                               _stream(stream)))
         return out
 
+    def sort_received(self, d: Dispatched, max_rows: Optional[int] = None, stream=None) -> "ExpertOrder":
+        """The live dispatch's received rows in compact expert order, every rank's experts in turn (see
+        ``sort_by_expert``).  A routed token's slots are received once each, so max_rows defaults to
+        W * max_tok_per_rank * topk."""
+        return sort_by_expert(d.recv_idx, self.E, max_rows=self.rows * self.k if max_rows is None else max_rows,
+                              counts=d.recv_count, stream=stream)
+
     def reset(self, stream=None):
         _check(self._lib.ep_reset(self._h, _stream(stream)))
 
@@ -442,3 +459,7 @@ class Plan:
         v = ctypes.c_int(0)
         _check(self._lib.ep_status(self._h, ctypes.byref(v)))
         return v.value
+
+
+from .experts import (ExpertOrder, matmul_fp8, matmul_fp8_swiglu, op_status, return_rows,  # noqa: E402
+                      return_rows_backward, rms_norm_fp8, sort_by_expert, sorted_rows, sorted_rows_backward)

@@ -336,6 +336,97 @@ int ep_route_noalloc(int W, int experts_per_rank, int topk, int max_tok_per_rank
  */
 int ep_probe_read(ep_plan* p, uint64_t* ns_host, int n_words);
 
+/*
+ * Expert-layer operators: the steps of a mixture-of-experts layer around dispatch and combine.  They
+ * take caller-owned memory only (outputs, workspace, status word), run on the current device, enqueue
+ * on `stream` and return without waiting.  device_status is one int32 on the device: the first problem
+ * only the GPU can see is recorded there and the work it concerns is skipped; no call clears it.
+ * Arrays are dense and row-major unless a stride is given.  Scales are FP32, one per 128 elements of
+ * a row (the last block may be shorter): ceil(n / 128) per row of n.
+ *
+ * ep_rms_norm_fp8: the residual's addition and the RMS norm, quantised to the rows and scales an
+ * EP_FP8_E4M3 dispatch takes.  Per row, in FP32: h = x + residual; y = h / sqrt(mean(h^2) + eps) *
+ * weight; scale = max|y| / 448 per block (1 for a block of zeros); code = e4m3(y / scale), rounded to
+ * nearest even, saturating at +-448.
+ *   x, residual  [rows][hidden] of dtype (EP_BF16 or EP_FP16), 16-byte aligned, rows x_stride and
+ *                residual_stride elements apart (multiples of 8); residual may be NULL
+ *   weight       [hidden] of dtype, or FP32 if weight_fp32 is not 0; 16-byte aligned
+ *   hidden       a multiple of 16 in 16..32768;  eps >= 0
+ *   q, scales    [rows][hidden] e4m3 codes, [rows][ceil(hidden/128)]
+ *   h, y         [rows][hidden] of dtype: the sum, and the norm before quantising; each may be NULL
+ * h may be x or residual itself, if that is dense.
+ */
+int ep_rms_norm_fp8(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                    const void* weight, int weight_fp32, int dtype, int64_t rows, int hidden, float eps, void* q,
+                    float* scales, void* h, void* y, void* stream);
+
+/*
+ * Received rows in compact expert order, and back.  The order of W ranks' rows [W][rows_per_rank] with
+ * experts_per_rank experts each (W = 1 for one set of rows and experts):
+ *   indices   [W][rows_per_rank][topk] int32 global expert ids.  A pair (row, slot) is sorted if its
+ *             expert lives on the row's rank and the row is below counts[rank]; other ids, -1 among
+ *             them, are left out
+ *   counts    [W] int32 on the device (a dispatch's recv_count), or NULL: every row counts
+ *   max_rows  capacity of the sorted rows.  Pairs that do not fit are left out and recorded as
+ *             EP_ERR_CAPACITY
+ *   offsets   [W*experts_per_rank + 1] int32 out: group g (a global expert) holds sorted rows
+ *             offsets[g] .. offsets[g+1]-1, its pairs in (row, slot) order
+ *   pos       [W][rows_per_rank][topk] int32 out: a pair's sorted row, -1 for none
+ *   src       [max_rows] int32 out: (rank * rows_per_rank + row) * topk + slot of a sorted row, -1 past
+ *             the last
+ * Limits: W*experts_per_rank <= 4096, fewer than 2^31 pairs.  The workspace holds at least
+ * ep_sort_workspace_bytes() (0 for small sorts and for invalid shapes).
+ */
+size_t ep_sort_workspace_bytes(int W, int64_t rows_per_rank, int topk, int experts_per_rank);
+int ep_sort_by_expert(const int32_t* indices, const int32_t* counts, int W, int64_t rows_per_rank, int topk,
+                      int experts_per_rank, int64_t max_rows, int32_t* offsets, int32_t* pos, int32_t* src,
+                      void* workspace, size_t workspace_bytes, int32_t* device_status, void* stream);
+
+/*
+ * Rows by such an order; pos, counts, W, rows_per_rank, topk and max_rows as above.  Sorted rows past
+ * the last, and rows at or past counts[rank], are not written.  A position outside -1..max_rows-1 is
+ * recorded as EP_ERR_DEVICE_BOUNDS and skipped.
+ *
+ * ep_sorted_rows copies x [W][rows_per_rank] rows of row_bytes (a multiple of 16) and scales
+ * [W][rows_per_rank][scale_dim] to out [max_rows] and out_scales [max_rows][scale_dim].
+ *
+ * ep_return_rows: out[row] = sum over the row's slots, ascending, of weights[row][slot] * y[pos], in FP32,
+ * rounded to nearest even once; zeros for a row without a sorted slot.  y [max_rows][hidden], out
+ * [W][rows_per_rank][hidden], both EP_BF16 or EP_FP16, hidden a multiple of 8; weights FP32, or NULL
+ * for ones, which is also the gradient of ep_sorted_rows.
+ *
+ * ep_return_rows_backward: dy[pos] = weights[row][slot] * dout[row], rounded once; dweights[row][slot] =
+ * the dot product of y[pos] and dout[row] in FP32, 0 for a slot without a sorted row.
+ */
+int ep_sorted_rows(const void* x, const float* scales, const int32_t* pos, const int32_t* counts, int W,
+                   int64_t rows_per_rank, int topk, int64_t max_rows, int64_t row_bytes, int scale_dim, void* out,
+                   float* out_scales, int32_t* device_status, void* stream);
+int ep_return_rows(const void* y, const float* weights, const int32_t* pos, const int32_t* counts, int W,
+                   int64_t rows_per_rank, int topk, int64_t max_rows, int hidden, int dtype, void* out,
+                   int32_t* device_status, void* stream);
+int ep_return_rows_backward(const void* y, const float* weights, const void* dout, const int32_t* pos,
+                            const int32_t* counts, int W, int64_t rows_per_rank, int topk, int64_t max_rows,
+                            int hidden, int dtype, void* dy, float* dweights, int32_t* device_status, void* stream);
+
+/*
+ * e4m3 matrix product with block scales, dense or by expert:
+ *   out[i][n] = sum over 128-blocks kb of a_scales[i][kb] * b_scales[g][n/128][kb] * (sum over k in the
+ *               block of a[i][k] * b[g][n][k]),   in FP32
+ *   a, a_scales  [rows][inner] codes, [rows][ceil(inner/128)]
+ *   b, b_scales  [groups][columns][inner] codes, [groups][ceil(columns/128)][ceil(inner/128)]
+ *   offsets      [groups + 1] int32 on the device: rows offsets[g] .. offsets[g+1]-1 take b[g]; rows
+ *                outside every group are not written.  NULL with groups = 1: every row.
+ *   inner        a multiple of 16 up to 2^20;  groups up to 4096;  columns up to 2^20
+ * swiglu = 0: out [rows][columns], EP_BF16 or EP_FP16 by dtype, rounded once; out_scales is not used.
+ * swiglu = 1 (dtype EP_FP8_E4M3, columns a multiple of 32): the first half of b's columns is the gate,
+ * the second the up projection; z = gate * sigmoid(gate) * up in FP32 is quantised as by ep_rms_norm_fp8:
+ * out [rows][columns/2] codes, out_scales [rows][ceil(columns/256)].
+ * a, b and out are 16-byte aligned.
+ */
+int ep_matmul_fp8(const void* a, const float* a_scales, const void* b, const float* b_scales,
+                  const int32_t* offsets, int64_t rows, int groups, int columns, int inner, int swiglu, int dtype,
+                  void* out, float* out_scales, int32_t* device_status, void* stream);
+
 /* Static description of a status code ("unknown status" for any other value); never NULL.
  * With ep_last_error, the host side of the staging PR's caller contract ("refactor(EPv2):
  * replace per-module __device__ staging with shared buffer", section "Caller contract"): a
