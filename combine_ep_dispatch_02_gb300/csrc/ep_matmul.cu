@@ -8,7 +8,7 @@
 //
 // Products of e4m3 values are exact in FP32, so the block sums keep FP32 accuracy and the scales
 // enter once per block.
-#include "ep_layer.cuh"
+#include "ep_tcgen05.cuh"
 
 namespace ep {
 namespace {
@@ -26,8 +26,9 @@ struct MatmulArgs {
     int* status;
     int64_t rows;
     int groups, N, K, kb;     // N: output columns of a row (swiglu: half the rows of b)
-    int nb;                   // 128-row blocks of b in one group
+    int columns, nb;          // rows of b in one group, and their 128-row blocks
     int swiglu, dtype;
+    int vec;                  // 16-bit rows take 32-byte (2) or 16-byte (1) stores
 };
 
 // First and last row of group g, clamped to the buffer.
@@ -38,121 +39,355 @@ __device__ __forceinline__ void group_rows(const MatmulArgs& p, int g, int& lo, 
     hi = max(lo, min(p.offsets[g + 1], (int)p.rows));
 }
 
-constexpr int kTileM = 32, kTileN = 128, kTileK = 32, kThreads = 256;
+// ---- tiles of 128 rows
+//
+// A CTA keeps one SM and walks output tiles of 128 rows by 256 rows of b (with SwiGLU: 128 gate rows and
+// the 128 up rows that belong to them).  Warp 0 loads 128-byte wide K blocks of both operands by TMA
+// into kStages shared-memory stages; warp 1 multiplies each block on the tensor cores into one of two
+// 256-column accumulators in tensor memory; eight warps add each block's sums, times its scales,
+// to FP32 registers while the next block is multiplied.  The scales differ from block to block of
+// K, so the sums cannot stay in tensor memory over a tile.
+//
+// Tensor-core time of a block: 128*256*128 products at 8192 a cycle, 512 cycles.  In that time the eight
+// warps read 256 columns of 128 lanes (256 cycles at 512 bytes a cycle) and issue 32768 FMAs (256
+// cycles), so the scaling hides behind the products.
 
-__device__ __forceinline__ float2 codes2(uint32_t c) { return e4m3x2_to_float2(c & 0xFFFFu); }
+constexpr int kTileRows = 128, kTileCols = 256, kBlockK = 128;
+constexpr int kStages = 4;
+constexpr int kStageBytes = (kTileRows + kTileCols) * kBlockK;
+constexpr int kProductThreads = 384;   // load, multiply, two spare warps; eight scaling warps
+constexpr int kScaleThreads = 256;
+constexpr int kChunkTiles = 16;        // row tiles that share b's columns before the next columns
+
+struct Tile {
+    int g, m0, m1, n0;   // group, first row, end of the group's rows, first output column
+};
+
+__device__ __forceinline__ int row_tiles(const MatmulArgs& p, int g)
+{
+    int lo, hi;
+    group_rows(p, g, lo, hi);
+    return (hi - lo + kTileRows - 1) / kTileRows;
+}
+
+// Exclusive prefix of the groups' tile counts, by one warp.
+__device__ __forceinline__ void scan_tiles(const MatmulArgs& p, int* first, int col_tiles, int lane)
+{
+    int carry = 0;
+    for (int b = 0; b < p.groups; b += 32) {
+        const int n = b + lane < p.groups ? row_tiles(p, b + lane) * col_tiles : 0;
+        int s = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += u;
+        }
+        if (b + lane < p.groups) first[b + lane] = carry + s - n;
+        carry += __shfl_sync(0xffffffffu, s, 31);
+    }
+    if (lane == 0) first[p.groups] = carry;
+}
+
+// Tile t: groups in order; within a group, chunks of kChunkTiles row tiles, whose rows and the group's
+// weights stay in L2 while the chunk is done; within a chunk, row tiles before columns.
+__device__ __forceinline__ Tile find_tile(const MatmulArgs& p, const int* first, int col_tiles, int cols, int t)
+{
+    int lo = 0, hi = p.groups;   // first[lo] <= t < first[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    Tile x;
+    x.g = lo;
+    int r0;
+    group_rows(p, lo, r0, x.m1);
+    const int tiles = (x.m1 - r0 + kTileRows - 1) / kTileRows;
+    const int in = t - first[lo];
+    const int chunk = in / (kChunkTiles * col_tiles), rest = in - chunk * kChunkTiles * col_tiles;
+    const int wide = min(kChunkTiles, tiles - chunk * kChunkTiles);
+    const int col = rest / wide;
+    x.m0 = r0 + (chunk * kChunkTiles + rest - col * wide) * kTileRows;
+    x.n0 = col * cols;
+    return x;
+}
+
+// 32 accumulator columns times the scale, added to 32 of a thread's sums.
+__device__ __forceinline__ void add_scaled(float* acc, const uint32_t (&r)[32], float s)
+{
+#pragma unroll
+    for (int i = 0; i < 32; ++i) acc[i] = fmaf(__uint_as_float(r[i]), s, acc[i]);
+}
+
+__device__ __forceinline__ void add_scaled(float* acc, const uint32_t (&r)[32], float lo, float hi, int split)
+{
+#pragma unroll
+    for (int i = 0; i < 32; ++i) acc[i] = fmaf(__uint_as_float(r[i]), i < split ? lo : hi, acc[i]);
+}
+
+// 128 consecutive columns of one output row, 16-bit; n of them exist.
+template <bool FP16>
+__device__ __forceinline__ void store_row(uint8_t* out, const float (&acc)[128], int n, int vec)
+{
+#pragma unroll
+    for (int c = 0; c < 128; c += 16) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = pack2<FP16>(acc[c + 2 * i], acc[c + 2 * i + 1]);
+        if (vec == 2 && c + 16 <= n) {
+            st_v8(out + 2 * c, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
+        } else if (vec >= 1 && c + 16 <= n) {
+            st_v4(out + 2 * c, make_uint4(w[0], w[1], w[2], w[3]));
+            st_v4(out + 2 * c + 16, make_uint4(w[4], w[5], w[6], w[7]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (c + i < n) reinterpret_cast<uint16_t*>(out)[c + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+        }
+    }
+}
 
 template <bool SWIGLU>
-__global__ void __launch_bounds__(kThreads) ep_matmul_kernel(const MatmulArgs p)
+__global__ void __launch_bounds__(kProductThreads, 1)
+ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap map_a,
+                       const __grid_constant__ CUtensorMap map_b)
 {
-    constexpr int kHalves = SWIGLU ? 2 : 1;
-    __shared__ float sa[kTileK][kTileM + 1];
-    __shared__ float sb[kHalves][kTileK][kTileN + 1];
-    __shared__ int found[3];
-    if (threadIdx.x == 0) {   // the row tile this CTA takes
-        int t = blockIdx.x;
-        found[0] = -1;
-        for (int g = 0; g < p.groups; ++g) {
-            int lo, hi;
-            group_rows(p, g, lo, hi);
-            const int n = (hi - lo + kTileM - 1) / kTileM;
-            if (t < n) {
-                found[0] = g;
-                found[1] = lo + t * kTileM;
-                found[2] = hi;
-                break;
-            }
-            t -= n;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 6];
+    __shared__ float tops[2][2][kTileRows];   // [tile parity][half][row]: largest |z|
+    __shared__ uint32_t tmem_slot;
+    __shared__ int gave_up;
+    const uint32_t stages = (smem_u32(raw) + 1023u) & ~1023u;
+    int* first = reinterpret_cast<int*>(raw + (stages - smem_u32(raw)) + kStages * kStageBytes);
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
+                   acc_empty = acc_full + 16, drained = acc_empty + 16, topped = drained + 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Giveup giveup{&gave_up, p.status};
+    constexpr int kCols = SWIGLU ? kTileCols / 2 : kTileCols;   // output columns of a tile
+    const int col_tiles = (p.N + kCols - 1) / kCols;
+    const int kb = p.kb;
+
+    if (threadIdx.x == 0) {
+        gave_up = 0;
+        for (int i = 0; i < kStages; ++i) {
+            bar_init(full + 8 * i, 1);
+            bar_init(empty + 8 * i, 1);
         }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(acc_full + 8 * i, 1);
+            bar_init(acc_empty + 8 * i, kScaleThreads / 32);
+        }
+        bar_init(drained, 1);
+        bar_init(topped, kScaleThreads / 32);
+        fence_barrier_init();
+        prefetch_map(&map_a);
+        prefetch_map(&map_b);
     }
+    if (warp == 1) scan_tiles(p, first, col_tiles, lane);
+    if (warp == 2) tmem_alloc(smem_u32(&tmem_slot), 512);
+    tmem_fence_before();
     __syncthreads();
-    const int g = found[0], m0 = found[1], m1 = found[2];
-    if (g < 0) return;
-    const int n0 = blockIdx.y * kTileN;
-    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;   // 4 rows x (4 columns, 32 apart)
-    const int64_t bn = SWIGLU ? 2 * (int64_t)p.N : p.N;
-    float acc[kHalves][4][4] = {}, blk[kHalves][4][4] = {};
-    for (int k0 = 0; k0 < p.kb * 128; k0 += kTileK) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < kTileM * kTileK / 2; i += kThreads) {
-            const int r = i / (kTileK / 2), k = i % (kTileK / 2) * 2;
-            float2 v = make_float2(0.0f, 0.0f);
-            if (m0 + r < m1 && k0 + k < p.K)
-                v = codes2(*reinterpret_cast<const uint16_t*>(p.a + (int64_t)(m0 + r) * p.K + k0 + k));
-            sa[k][r] = v.x;
-            sa[k + 1][r] = v.y;
-        }
-        for (int i = threadIdx.x; i < kHalves * kTileN * kTileK / 2; i += kThreads) {
-            const int h = i / (kTileN * kTileK / 2), j = i % (kTileN * kTileK / 2);
-            const int n = j / (kTileK / 2), k = j % (kTileK / 2) * 2;
-            float2 v = make_float2(0.0f, 0.0f);
-            if (n0 + n < p.N && k0 + k < p.K)
-                v = codes2(*reinterpret_cast<const uint16_t*>(p.b + (g * bn + (int64_t)h * p.N + n0 + n) * p.K + k0 + k));
-            sb[h][k][n] = v.x;
-            sb[h][k + 1][n] = v.y;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kTileK; ++k) {
-            float av[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) av[i] = sa[k][4 * ty + i];
-#pragma unroll
-            for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float bv = sb[h][k][tx + 32 * j];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) blk[h][i][j] = fmaf(av[i], bv, blk[h][i][j]);
+    tmem_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const int tiles = first[p.groups];
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0 && lane == 0) {
+            uint32_t n = 0;   // blocks loaded
+            bool ok = true;
+            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                const Tile x = find_tile(p, first, col_tiles, kCols, t);
+                const int64_t b_rows = (int64_t)x.g * p.columns;
+                const int y0 = (int)(b_rows + x.n0), y1 = (int)(b_rows + (SWIGLU ? p.N + x.n0 : x.n0 + 128));
+                for (int k = 0; k < kb; ++k, ++n) {
+                    const uint32_t s = n % kStages, use = n / kStages;
+                    if (use > 0 && !bar_wait(empty + 8 * s, (use - 1) & 1, giveup)) { ok = false; break; }
+                    const uint32_t dst = stages + s * kStageBytes, bar = full + 8 * s;
+                    bar_expect(bar, kStageBytes);
+                    tma_load(dst, &map_a, k * kBlockK, x.m0, bar);
+                    tma_load(dst + kTileRows * kBlockK, &map_b, k * kBlockK, y0, bar);
+                    tma_load(dst + (kTileRows + 128) * kBlockK, &map_b, k * kBlockK, y1, bar);
                 }
+            }
+            if (!ok)   // its loads in flight
+                for (uint32_t i = n < kStages ? 0 : n - kStages; i < n; ++i) bar_drain(full + 8 * (i % kStages), (i / kStages) & 1);
+        } else if (warp == 1 && lane == 0) {
+            constexpr uint32_t instruction = mma_instruction(kTileRows, kTileCols);
+            uint32_t n = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                for (int k = 0; k < kb; ++k, ++n) {
+                    const uint32_t s = n % kStages, buf = n & 1, use = n >> 1;
+                    if (use > 0 && !bar_wait(acc_empty + 8 * buf, (use - 1) & 1, giveup)) { ok = false; break; }
+                    if (!bar_wait(full + 8 * s, (n / kStages) & 1, giveup)) { ok = false; break; }
+                    tmem_fence_after();
+                    const uint64_t a = mma_descriptor(stages + s * kStageBytes);
+                    const uint64_t b = mma_descriptor(stages + s * kStageBytes + kTileRows * kBlockK);
+#pragma unroll
+                    for (int i = 0; i < kBlockK / 32; ++i)
+                        mma_e4m3(tmem + buf * kTileCols, a + 2 * i, b + 2 * i, instruction, i == 0);
+                    mma_commit(empty + 8 * s);
+                    mma_commit(acc_full + 8 * buf);
+                }
+            }
+            mma_commit(drained);   // tensor memory is freed only after its last product
+            bar_drain(drained, 0);
         }
-        if ((k0 + kTileK) % 128 == 0) {
-            const int kb = k0 / 128;
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int half = (warp - 4) >> 2;                 // this warp's columns: 128 of the 256
+        const int row = (warp & 3) * 32 + lane;
+        // plain: columns half*128 ..; SwiGLU: gate columns half*64 .. (of 128), then their up columns
+        const uint32_t col0 = SWIGLU ? half * 64 : half * 128;
+        const uint32_t col1 = SWIGLU ? 128 + half * 64 : col0 + 64;
+        const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        uint32_t n = 0;
+        bool ok = true;
+        int parity = 0;
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, parity ^= 1) {
+            const Tile x = find_tile(p, first, col_tiles, kCols, t);
+            const int m = min(x.m0 + row, x.m1 - 1);
+            const float* as = p.as + (int64_t)m * kb;
+            const float* bs = p.bs + (int64_t)x.g * p.nb * kb;
+            // scale rows of b: of the first 64 columns, and of the last 64 before and from `split`
+            const int last = p.nb - 1;
+            const int b0 = min((x.n0 + (SWIGLU ? 0 : half * 128)) / 128, last);
+            const int up = p.N + x.n0 + half * 64;
+            const int b1 = SWIGLU ? min(up / 128, last) : b0, b2 = SWIGLU ? min(up / 128 + 1, last) : b0;
+            const int split = SWIGLU ? 128 - up % 128 : 64;   // a multiple of 16
+            float acc[128];
 #pragma unroll
-            for (int h = 0; h < kHalves; ++h)
+            for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
+            float sa = as[0], s0 = bs[(int64_t)b0 * kb], s1 = bs[(int64_t)b1 * kb], s2 = bs[(int64_t)b2 * kb];
+            for (int k = 0; k < kb; ++k, ++n) {
+                const uint32_t buf = n & 1;
+                const float f0 = sa * s0, f1 = sa * s1, f2 = sa * s2;
+                if (k + 1 < kb) {
+                    sa = as[k + 1];
+                    s0 = bs[(int64_t)b0 * kb + k + 1];
+                    if (SWIGLU) { s1 = bs[(int64_t)b1 * kb + k + 1]; s2 = bs[(int64_t)b2 * kb + k + 1]; }
+                }
+                ok = bar_wait(acc_full + 8 * buf, (n >> 1) & 1, giveup);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tmem_fence_after();
+                const uint32_t c = taddr + buf * kTileCols;
+                uint32_t r0[32], r1[32];
+                tmem_load32(r0, c + col0);
+                tmem_wait(r0);
+                tmem_load32(r1, c + col0 + 32);
+                add_scaled(acc, r0, f0);
+                tmem_wait(r1);
+                tmem_load32(r0, c + col1);
+                add_scaled(acc + 32, r1, f0);
+                tmem_wait(r0);
+                tmem_load32(r1, c + col1 + 32);
+                if (SWIGLU) add_scaled(acc + 64, r0, f1, f2, split);
+                else add_scaled(acc + 64, r0, f0);
+                tmem_wait(r1);
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(acc_empty + 8 * buf);
+                if (SWIGLU) add_scaled(acc + 96, r1, f1, f2, split - 32);
+                else add_scaled(acc + 96, r1, f0);
+            }
+            const bool present = x.m0 + row < x.m1;
+            if constexpr (!SWIGLU) {
+                const int n0 = x.n0 + half * 128;
+                if (ok && present && n0 < p.N) {
+                    uint8_t* out = (uint8_t*)p.out + 2 * ((int64_t)(x.m0 + row) * p.N + n0);
+                    if (p.dtype == EP_FP16) store_row<true>(out, acc, p.N - n0, p.vec);
+                    else store_row<false>(out, acc, p.N - n0, p.vec);
+                }
+            } else {
+                const int n0 = x.n0 + half * 64;
+                float top = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int m = min(m0 + 4 * ty + i, m1 - 1);
-                    const float s = p.as[(int64_t)m * p.kb + kb];
+                for (int i = 0; i < 64; ++i) {
+                    const float gate = acc[i];
+                    acc[i] = __fdividef(gate, 1.0f + __expf(-gate)) * acc[64 + i];
+                    top = fmaxf(top, n0 + i < p.N ? fabsf(acc[i]) : 0.0f);
+                }
+                tops[parity][half][row] = top;
+                // the other half's maximum; a parity's words are rewritten two tiles later, which no warp
+                // reaches before all have passed the tile between
+                __syncwarp();
+                if (lane == 0) bar_arrive(topped);
+                ok = __all_sync(0xffffffffu, ok && bar_wait(topped, parity, giveup));
+                const float scale = e4m3_block_scale(fmaxf(top, tops[parity][half ^ 1][row]));
+                const float inv = __frcp_rn(scale);
+                if (ok && present) {
+                    if (half == 0) p.out_scales[(int64_t)(x.m0 + row) * ((p.N + 127) / 128) + x.n0 / 128] = scale;
+                    uint8_t* out = (uint8_t*)p.out + (int64_t)(x.m0 + row) * p.N + n0;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int64_t row = min(n0 + tx + 32 * j, p.N - 1) + (int64_t)h * p.N;
-                        const float bs = p.bs[(g * (int64_t)p.nb + row / 128) * p.kb + kb];
-                        acc[h][i][j] = fmaf(blk[h][i][j], s * bs, acc[h][i][j]);
-                        blk[h][i][j] = 0.0f;
+                    for (int i = 0; i < 64; i += 16) {   // N is a multiple of 16
+                        if (n0 + i >= p.N) continue;
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            w[j] = e4m3x4_scaled(acc[i + 4 * j], acc[i + 4 * j + 1], acc[i + 4 * j + 2],
+                                                 acc[i + 4 * j + 3], scale, inv);
+                        st_v4(out + i, make_uint4(w[0], w[1], w[2], w[3]));
                     }
                 }
-        }
-    }
-    if constexpr (!SWIGLU) {
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) {
-                const int m = m0 + 4 * ty + i, n = n0 + tx + 32 * j;
-                if (m >= m1 || n >= p.N) continue;
-                const int64_t at = (int64_t)m * p.N + n;
-                if (p.dtype == EP_FP16) ((__half*)p.out)[at] = __float2half_rn(acc[0][i][j]);
-                else ((__nv_bfloat16*)p.out)[at] = __float2bfloat16_rn(acc[0][i][j]);
-            }
-    } else {
-        float z[4][4];
-        for (int i = 0; i < 4; ++i) {
-            float m = 0.0f;
-            for (int j = 0; j < 4; ++j) {
-                const float gate = acc[0][i][j];
-                z[i][j] = gate / (1.0f + expf(-gate)) * acc[1][i][j];
-                if (n0 + tx + 32 * j < p.N) m = fmaxf(m, fabsf(z[i][j]));
-            }
-            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float scale = e4m3_block_scale(m);
-            const int row = m0 + 4 * ty + i;
-            if (row >= m1) continue;
-            if (tx == 0) p.out_scales[(int64_t)row * ((p.N + 127) / 128) + blockIdx.y] = scale;
-            for (int j = 0; j < 4; ++j) {
-                const int n = n0 + tx + 32 * j;
-                if (n < p.N) ((uint8_t*)p.out)[(int64_t)row * p.N + n] = (uint8_t)e4m3x2(__fdiv_rn(z[i][j], scale), 0.0f);
             }
         }
     }
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tmem_fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+// ---- tensor maps
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled()
+{
+    static const EncodeTiled fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return (EncodeTiled)f;
+    }();
+    return fn;
+}
+
+// Map of [rows][K] codes with boxes of box_rows x 128 bytes, swizzled by 128 bytes; elements past either
+// end read as zero codes.
+int make_map(CUtensorMap* m, const char* what, const void* base, int64_t rows, int K, int box_rows)
+{
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return layer_fail(EP_ERR_CUDA, "ep_matmul_fp8: the driver has no cuTensorMapEncodeTiled");
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, pitch[1] = {(cuuint64_t)K};
+    const cuuint32_t box[2] = {kBlockK, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, pitch, box, step,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return layer_fail(EP_ERR_CUDA, "ep_matmul_fp8: tensor map of %s: CUresult %d", what, (int)r);
+    return EP_OK;
+}
+
+template <bool SWIGLU>
+cudaError_t launch_product_rows(const MatmulArgs& p, const CUtensorMap& ma, const CUtensorMap& mb, int sms,
+                                cudaStream_t s)
+{
+    const int cols = SWIGLU ? kTileCols / 2 : kTileCols;
+    const int64_t most = (p.rows / kTileRows + p.groups) * ((p.N + cols - 1) / cols);   // tiles, at most
+    const size_t smem = 1024 + kStages * kStageBytes + (p.groups + 1) * sizeof(int);
+    cudaError_t e = cudaFuncSetAttribute(ep_product_rows_kernel<SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem);
+    if (e != cudaSuccess) return e;
+    ep_product_rows_kernel<SWIGLU><<<(unsigned)(most < sms ? most : sms), kProductThreads, smem, s>>>(p, ma, mb);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -191,9 +426,15 @@ extern "C" int ep_matmul_fp8(const void* a, const float* a_scales, const void* b
     p.out = out; p.out_scales = out_scales; p.status = device_status; p.rows = rows; p.groups = groups;
     p.K = inner; p.kb = (inner + 127) / 128; p.N = swiglu ? columns / 2 : columns; p.nb = (columns + 127) / 128;
     p.swiglu = swiglu; p.dtype = dtype;
-    const dim3 grid((unsigned)(rows / kTileM + groups + 1), (unsigned)((p.N + kTileN - 1) / kTileN));
+    p.columns = columns;
+    p.vec = columns % 16 == 0 && layer_aligned(out, 32) ? 2 : columns % 8 == 0 ? 1 : 0;
+    const int sms = layer_num_sms();
+    if (sms == 0) return layer_fail(EP_ERR_CUDA, "%s: cannot tell the current device's multiprocessors", who);
+    CUtensorMap ma, mb;
+    if (int rc = make_map(&ma, "a", a, rows, inner, kTileRows)) return rc;
+    if (int rc = make_map(&mb, "b", b, (int64_t)groups * columns, inner, 128)) return rc;
     cudaStream_t s = (cudaStream_t)stream;
-    if (swiglu) ep_matmul_kernel<true><<<grid, kThreads, 0, s>>>(p);
-    else ep_matmul_kernel<false><<<grid, kThreads, 0, s>>>(p);
-    return layer_cuda(cudaGetLastError(), "ep_matmul_fp8: launch");
+    const cudaError_t e = swiglu ? launch_product_rows<true>(p, ma, mb, sms, s)
+                                 : launch_product_rows<false>(p, ma, mb, sms, s);
+    return layer_cuda(e, "ep_matmul_fp8: launch");
 }
