@@ -31,12 +31,12 @@ struct MatmulArgs {
     int vec;                  // 16-bit rows take 32-byte (2) or 16-byte (1) stores
 };
 
-// First and last row of group g, clamped to the buffer.
-__device__ __forceinline__ void group_rows(const MatmulArgs& p, int g, int& lo, int& hi)
+// First and last row of group g, clamped to the buffer; off is p.offsets or a copy of it.
+__device__ __forceinline__ void group_rows(const MatmulArgs& p, const int32_t* off, int g, int& lo, int& hi)
 {
-    if (!p.offsets) { lo = 0; hi = (int)p.rows; return; }
-    lo = max(0, min(p.offsets[g], (int)p.rows));
-    hi = max(lo, min(p.offsets[g + 1], (int)p.rows));
+    if (!off) { lo = 0; hi = (int)p.rows; return; }
+    lo = max(0, min(off[g], (int)p.rows));
+    hi = max(lo, min(off[g + 1], (int)p.rows));
 }
 
 // ---- tiles of 128 rows
@@ -44,38 +44,44 @@ __device__ __forceinline__ void group_rows(const MatmulArgs& p, int g, int& lo, 
 // A CTA keeps one SM and walks output tiles of 128 rows by 256 rows of b (with SwiGLU: 128 gate rows and
 // the 128 up rows that belong to them).  Warp 0 loads 128-byte wide K blocks of both operands by TMA
 // into kStages shared-memory stages; warp 1 multiplies each block on the tensor cores into one of two
-// 256-column accumulators in tensor memory; eight warps add each block's sums, times its scales,
-// to FP32 registers while the next block is multiplied.  The scales differ from block to block of
-// K, so the sums cannot stay in tensor memory over a tile.
+// 256-column accumulators in tensor memory; warps 2 and 3 multiply the block's row and column scales
+// into a shared-memory ring; eight warps add each block's sums, times those factors, to FP32
+// registers while the next block is multiplied.  The scales differ from block to block of K, so the
+// sums cannot stay in tensor memory over a tile.
 //
 // Tensor-core time of a block: 128*256*128 products at 8192 a cycle, 512 cycles.  In that time the eight
 // warps read 256 columns of 128 lanes (256 cycles at 512 bytes a cycle) and issue 32768 FMAs (256
-// cycles), so the scaling hides behind the products.
+// cycles).  What sets the pace is the way of an accumulator: multiply, tell the scaling warps, read,
+// give back.  A hop over an mbarrier takes about 300 cycles here, so an accumulator is given back over
+// a named barrier (bar.arrive by the readers, bar.sync by the multiplying warp).
 
 constexpr int kTileRows = 128, kTileCols = 256, kBlockK = 128;
-constexpr int kStages = 4;
+constexpr int kStages = 4;             // even: a stage always goes to the same accumulator
 constexpr int kStageBytes = (kTileRows + kTileCols) * kBlockK;
-constexpr int kProductThreads = 384;   // load, multiply, two spare warps; eight scaling warps
+constexpr int kProductThreads = 384;   // load, multiply, two factor warps; eight scaling warps
 constexpr int kScaleThreads = 256;
 constexpr int kChunkTiles = 16;        // row tiles that share b's columns before the next columns
+constexpr int kFactors = 3;            // factors of a row and block: per half, or gate and two up blocks
+constexpr int kRing = 8;               // blocks of factors: a block is written when the block kStages before it has
+                                       // been multiplied, while those up to kStages + 1 before it may be unread
+constexpr int kRingFloats = kRing * kFactors * kTileRows;
+constexpr int kSharedOffsets = 512;    // groups whose offsets are copied to shared memory
 
 struct Tile {
     int g, m0, m1, n0;   // group, first row, end of the group's rows, first output column
 };
-
-__device__ __forceinline__ int row_tiles(const MatmulArgs& p, int g)
-{
-    int lo, hi;
-    group_rows(p, g, lo, hi);
-    return (hi - lo + kTileRows - 1) / kTileRows;
-}
 
 // Exclusive prefix of the groups' tile counts, by one warp.
 __device__ __forceinline__ void scan_tiles(const MatmulArgs& p, int* first, int col_tiles, int lane)
 {
     int carry = 0;
     for (int b = 0; b < p.groups; b += 32) {
-        const int n = b + lane < p.groups ? row_tiles(p, b + lane) * col_tiles : 0;
+        int n = 0;
+        if (b + lane < p.groups) {
+            int lo, hi;
+            group_rows(p, p.offsets, b + lane, lo, hi);
+            n = (hi - lo + kTileRows - 1) / kTileRows * col_tiles;
+        }
         int s = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -90,7 +96,8 @@ __device__ __forceinline__ void scan_tiles(const MatmulArgs& p, int* first, int 
 
 // Tile t: groups in order; within a group, chunks of kChunkTiles row tiles, whose rows and the group's
 // weights stay in L2 while the chunk is done; within a chunk, row tiles before columns.
-__device__ __forceinline__ Tile find_tile(const MatmulArgs& p, const int* first, int col_tiles, int cols, int t)
+__device__ __forceinline__ Tile find_tile(const MatmulArgs& p, const int32_t* off, const int* first, int col_tiles,
+                                          int cols, int t)
 {
     int lo = 0, hi = p.groups;   // first[lo] <= t < first[hi]
     while (hi - lo > 1) {
@@ -101,7 +108,7 @@ __device__ __forceinline__ Tile find_tile(const MatmulArgs& p, const int* first,
     Tile x;
     x.g = lo;
     int r0;
-    group_rows(p, lo, r0, x.m1);
+    group_rows(p, off, lo, r0, x.m1);
     const int tiles = (x.m1 - r0 + kTileRows - 1) / kTileRows;
     const int in = t - first[lo];
     const int chunk = in / (kChunkTiles * col_tiles), rest = in - chunk * kChunkTiles * col_tiles;
@@ -112,28 +119,34 @@ __device__ __forceinline__ Tile find_tile(const MatmulArgs& p, const int* first,
     return x;
 }
 
-// 32 accumulator columns times the scale, added to 32 of a thread's sums.
-__device__ __forceinline__ void add_scaled(float* acc, const uint32_t (&r)[32], float s)
+// 32 accumulator columns times the factor, added to 32 of a thread's sums.
+__device__ __forceinline__ void add_scaled(float2* acc, const uint32_t (&r)[32], float s)
 {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) acc[i] = fmaf(__uint_as_float(r[i]), s, acc[i]);
+    for (int i = 0; i < 16; ++i)
+        fma2(acc[i], make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), make_float2(s, s));
 }
 
-__device__ __forceinline__ void add_scaled(float* acc, const uint32_t (&r)[32], float lo, float hi, int split)
+// The same where columns from `split` on, an even number, take another factor (an up block that ends
+// inside the tile).
+__device__ __forceinline__ void add_scaled(float2* acc, const uint32_t (&r)[32], float lo, float hi, int split)
 {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) acc[i] = fmaf(__uint_as_float(r[i]), i < split ? lo : hi, acc[i]);
+    for (int i = 0; i < 16; ++i) {
+        const float s = 2 * i < split ? lo : hi;
+        fma2(acc[i], make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), make_float2(s, s));
+    }
 }
 
 // 128 consecutive columns of one output row, 16-bit; n of them exist.
 template <bool FP16>
-__device__ __forceinline__ void store_row(uint8_t* out, const float (&acc)[128], int n, int vec)
+__device__ __forceinline__ void store_row(uint8_t* out, const float2 (&acc)[64], int n, int vec)
 {
 #pragma unroll
     for (int c = 0; c < 128; c += 16) {
         uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = pack2<FP16>(acc[c + 2 * i], acc[c + 2 * i + 1]);
+        for (int i = 0; i < 8; ++i) w[i] = pack2<FP16>(acc[c / 2 + i].x, acc[c / 2 + i].y);
         if (vec == 2 && c + 16 <= n) {
             st_v8(out + 2 * c, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
         } else if (vec >= 1 && c + 16 <= n) {
@@ -147,21 +160,36 @@ __device__ __forceinline__ void store_row(uint8_t* out, const float (&acc)[128],
     }
 }
 
-template <bool SWIGLU>
+// Named barriers 1 and 2: an accumulator has been read.  Every scaling warp arrives once per block, in
+// every case; the multiplying warp waits before it writes that accumulator again.
+constexpr int kReadThreads = kScaleThreads + 32;
+__device__ __forceinline__ void read_arrive(uint32_t buf)
+{
+    asm volatile("bar.arrive %0, %1;" :: "r"(1 + buf), "n"(kReadThreads) : "memory");
+}
+__device__ __forceinline__ void read_wait(uint32_t buf)
+{
+    asm volatile("bar.sync %0, %1;" :: "r"(1 + buf), "n"(kReadThreads) : "memory");
+}
+
+// SPLIT: with SwiGLU, an up block of 128 scales may end inside a tile (N is no multiple of 128).
+template <bool SWIGLU, bool SPLIT>
 __global__ void __launch_bounds__(kProductThreads, 1)
 ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap map_a,
                        const __grid_constant__ CUtensorMap map_b)
 {
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kStages + 6];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 2];
     __shared__ float tops[2][2][kTileRows];   // [tile parity][half][row]: largest |z|
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
     const uint32_t stages = (smem_u32(raw) + 1023u) & ~1023u;
-    int* first = reinterpret_cast<int*>(raw + (stages - smem_u32(raw)) + kStages * kStageBytes);
-    const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
-                   acc_empty = acc_full + 16, drained = acc_empty + 16, topped = drained + 8;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float* ring = reinterpret_cast<float*>(raw + (stages - smem_u32(raw)) + kStages * kStageBytes);
+    int* first = reinterpret_cast<int*>(ring + kRingFloats);
+    int32_t* off_copy = first + p.groups + 1;
+    const uint32_t full = smem_u32(bars), done = full + 8 * kStages, drained = done + 8 * kStages,
+                   topped = drained + 8;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const Giveup giveup{&gave_up, p.status};
     constexpr int kCols = SWIGLU ? kTileCols / 2 : kTileCols;   // output columns of a tile
     const int col_tiles = (p.N + kCols - 1) / kCols;
@@ -170,12 +198,8 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
     if (threadIdx.x == 0) {
         gave_up = 0;
         for (int i = 0; i < kStages; ++i) {
-            bar_init(full + 8 * i, 1);
-            bar_init(empty + 8 * i, 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            bar_init(acc_full + 8 * i, 1);
-            bar_init(acc_empty + 8 * i, kScaleThreads / 32);
+            bar_init(full + 8 * i, 3);   // the loads and two warps' factors
+            bar_init(done + 8 * i, 1);
         }
         bar_init(drained, 1);
         bar_init(topped, kScaleThreads / 32);
@@ -183,26 +207,30 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
         prefetch_map(&map_a);
         prefetch_map(&map_b);
     }
+    const bool copied = p.offsets != nullptr && p.groups <= kSharedOffsets;
+    if (copied)
+        for (int i = threadIdx.x; i <= p.groups; i += kProductThreads) off_copy[i] = p.offsets[i];
+    const int32_t* off = copied ? off_copy : p.offsets;
     if (warp == 1) scan_tiles(p, first, col_tiles, lane);
     if (warp == 2) tmem_alloc(smem_u32(&tmem_slot), 512);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = tmem_slot;
-    const int tiles = first[p.groups];
+    const int tiles = uniform(first[p.groups]);
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 0 && lane == 0) {
             uint32_t n = 0;   // blocks loaded
             bool ok = true;
             for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                const Tile x = find_tile(p, first, col_tiles, kCols, t);
+                const Tile x = find_tile(p, off, first, col_tiles, kCols, t);
                 const int64_t b_rows = (int64_t)x.g * p.columns;
                 const int y0 = (int)(b_rows + x.n0), y1 = (int)(b_rows + (SWIGLU ? p.N + x.n0 : x.n0 + 128));
                 for (int k = 0; k < kb; ++k, ++n) {
                     const uint32_t s = n % kStages, use = n / kStages;
-                    if (use > 0 && !bar_wait(empty + 8 * s, (use - 1) & 1, giveup)) { ok = false; break; }
+                    if (use > 0 && !bar_wait(done + 8 * s, (use - 1) & 1, giveup)) { ok = false; break; }
                     const uint32_t dst = stages + s * kStageBytes, bar = full + 8 * s;
                     bar_expect(bar, kStageBytes);
                     tma_load(dst, &map_a, k * kBlockK, x.m0, bar);
@@ -212,27 +240,87 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
             }
             if (!ok)   // its loads in flight
                 for (uint32_t i = n < kStages ? 0 : n - kStages; i < n; ++i) bar_drain(full + 8 * (i % kStages), (i / kStages) & 1);
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp == 1) {
             constexpr uint32_t instruction = mma_instruction(kTileRows, kTileCols);
+            const uint64_t a0 = mma_descriptor(stages), b0 = mma_descriptor(stages + kTileRows * kBlockK);
+            const uint32_t mine = tiles > (int)blockIdx.x ? (tiles - blockIdx.x - 1) / gridDim.x + 1 : 0;
+            const uint32_t blocks = mine * kb;
+            const bool leader = elect_one();
+            // After a wait that gave up the products go on, on whatever the stages hold: the others have
+            // left or are leaving, no result is stored, and every barrier still gets its arrivals.
+            for (uint32_t n = 0, phase = 0; n < blocks; n += kStages, phase ^= 1) {
+#pragma unroll
+                for (int s = 0; s < kStages; ++s) {
+                    if (n + s >= blocks) break;
+                    bar_wait(full + 8 * s, phase, giveup);
+                    if (n + s >= 2) read_wait(s & 1);
+                    if (leader) {
+                        tmem_fence_after();
+#pragma unroll
+                        for (int i = 0; i < kBlockK / 32; ++i)
+                            mma_e4m3(tmem + (s & 1) * kTileCols, a0 + (s * (kStageBytes >> 4) + 2 * i),
+                                     b0 + (s * (kStageBytes >> 4) + 2 * i), instruction, i == 0);
+                        mma_commit(done + 8 * s);
+                    }
+                    __syncwarp();
+                }
+            }
+            for (uint32_t n = blocks < 2 ? 0 : blocks - 2; n < blocks; ++n) read_wait(n & 1);
+            if (leader) {
+                mma_commit(drained);   // tensor memory is freed only after its last product
+                bar_drain(drained, 0);
+            }
+            __syncwarp();
+        } else if (warp >= 2) {
+            // factors: as[row][k] * bs[.][k] for rows r and r + 64; loaded kAhead blocks ahead
+            const int r = threadIdx.x - 64;
+            const int last = p.nb - 1;
             uint32_t n = 0;
             bool ok = true;
             for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                for (int k = 0; k < kb; ++k, ++n) {
-                    const uint32_t s = n % kStages, buf = n & 1, use = n >> 1;
-                    if (use > 0 && !bar_wait(acc_empty + 8 * buf, (use - 1) & 1, giveup)) { ok = false; break; }
-                    if (!bar_wait(full + 8 * s, (n / kStages) & 1, giveup)) { ok = false; break; }
-                    tmem_fence_after();
-                    const uint64_t a = mma_descriptor(stages + s * kStageBytes);
-                    const uint64_t b = mma_descriptor(stages + s * kStageBytes + kTileRows * kBlockK);
+                const Tile x = find_tile(p, off, first, col_tiles, kCols, t);
+                const float* as0 = p.as + (int64_t)min(x.m0 + r, x.m1 - 1) * kb;
+                const float* as1 = p.as + (int64_t)min(x.m0 + r + 64, x.m1 - 1) * kb;
+                const float* bs = p.bs + (int64_t)x.g * p.nb * kb;
+                const int up = (SWIGLU ? p.N + x.n0 : x.n0 + 128) / 128;
+                const float* bs0 = bs + (int64_t)min(x.n0 / 128, last) * kb;
+                const float* bs1 = bs + (int64_t)min(up, last) * kb;
+                const float* bs2 = bs + (int64_t)min(up + 1, last) * kb;
+                constexpr int kAhead = 4;
+                float a0[kAhead], a1[kAhead], b0[kAhead], b1[kAhead], b2[kAhead];
+                auto load = [&](int i, int k) {
+                    k = min(k, kb - 1);
+                    a0[i] = as0[k];
+                    a1[i] = as1[k];
+                    b0[i] = bs0[k];
+                    b1[i] = bs1[k];
+                    if (SPLIT) b2[i] = bs2[k];
+                };
 #pragma unroll
-                    for (int i = 0; i < kBlockK / 32; ++i)
-                        mma_e4m3(tmem + buf * kTileCols, a + 2 * i, b + 2 * i, instruction, i == 0);
-                    mma_commit(empty + 8 * s);
-                    mma_commit(acc_full + 8 * buf);
+                for (int i = 0; i < kAhead; ++i) load(i, i);
+                for (int k0 = 0; k0 < kb && ok; k0 += kAhead) {
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i) {
+                        if (k0 + i >= kb) break;
+                        const uint32_t s = n % kStages, use = n / kStages;
+                        if (use > 0) ok = ok && bar_wait(done + 8 * s, (use - 1) & 1, giveup);
+                        __syncwarp();
+                        float* f = ring + (n % kRing) * (kFactors * kTileRows) + r;
+                        f[0] = a0[i] * b0[i];
+                        f[64] = a1[i] * b0[i];
+                        f[kTileRows] = a0[i] * b1[i];
+                        f[kTileRows + 64] = a1[i] * b1[i];
+                        if (SPLIT) {
+                            f[2 * kTileRows] = a0[i] * b2[i];
+                            f[2 * kTileRows + 64] = a1[i] * b2[i];
+                        }
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(full + 8 * s);
+                        ++n;
+                        load(i, k0 + kAhead + i);
+                    }
                 }
             }
-            mma_commit(drained);   // tensor memory is freed only after its last product
-            bar_drain(drained, 0);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -242,55 +330,59 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
         const uint32_t col0 = SWIGLU ? half * 64 : half * 128;
         const uint32_t col1 = SWIGLU ? 128 + half * 64 : col0 + 64;
         const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        uint32_t n = 0;
         bool ok = true;
         int parity = 0;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, parity ^= 1) {
-            const Tile x = find_tile(p, first, col_tiles, kCols, t);
-            const int m = min(x.m0 + row, x.m1 - 1);
-            const float* as = p.as + (int64_t)m * kb;
-            const float* bs = p.bs + (int64_t)x.g * p.nb * kb;
-            // scale rows of b: of the first 64 columns, and of the last 64 before and from `split`
-            const int last = p.nb - 1;
-            const int b0 = min((x.n0 + (SWIGLU ? 0 : half * 128)) / 128, last);
-            const int up = p.N + x.n0 + half * 64;
-            const int b1 = SWIGLU ? min(up / 128, last) : b0, b2 = SWIGLU ? min(up / 128 + 1, last) : b0;
-            const int split = SWIGLU ? 128 - up % 128 : 64;   // a multiple of 16
-            float acc[128];
+        uint32_t n = 0;
+        for (int t = blockIdx.x; t < tiles; t += gridDim.x, parity ^= 1) {
+            const Tile x = find_tile(p, off, first, col_tiles, kCols, t);
+            // up columns of this half that share the tile's first up block
+            const int split = 128 - (p.N + x.n0) % 128 - half * 64;
+            float2 acc[64];
 #pragma unroll
-            for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
-            float sa = as[0], s0 = bs[(int64_t)b0 * kb], s1 = bs[(int64_t)b1 * kb], s2 = bs[(int64_t)b2 * kb];
+            for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.0f, 0.0f);
+            // a wait that gave up ends nothing here: what follows works on whatever is there, every barrier
+            // gets its arrivals, and the rows are not stored
+            float f0, f1, f2;
+            auto factors = [&](uint32_t i) {
+                const float* f = ring + (i % kRing) * (kFactors * kTileRows) + row;
+                f0 = f[SWIGLU ? 0 : half * kTileRows];
+                f1 = SWIGLU ? f[kTileRows] : f0;
+                f2 = SPLIT ? f[2 * kTileRows] : f1;
+            };
+            uint32_t r0[32], r1[32];
+            ok &= bar_wait(done + 8 * (n % kStages), (n / kStages) & 1, giveup);
+            __syncwarp();
+            tmem_fence_after();
+            tmem_load32(r0, taddr + (n & 1) * kTileCols + col0);
+            factors(n);
+            // 32 columns are read while the 32 before them are added, across the ends of blocks too
             for (int k = 0; k < kb; ++k, ++n) {
-                const uint32_t buf = n & 1;
-                const float f0 = sa * s0, f1 = sa * s1, f2 = sa * s2;
-                if (k + 1 < kb) {
-                    sa = as[k + 1];
-                    s0 = bs[(int64_t)b0 * kb + k + 1];
-                    if (SWIGLU) { s1 = bs[(int64_t)b1 * kb + k + 1]; s2 = bs[(int64_t)b2 * kb + k + 1]; }
-                }
-                ok = bar_wait(acc_full + 8 * buf, (n >> 1) & 1, giveup);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tmem_fence_after();
-                const uint32_t c = taddr + buf * kTileCols;
-                uint32_t r0[32], r1[32];
-                tmem_load32(r0, c + col0);
+                const uint32_t d = taddr + (n & 1) * kTileCols;
                 tmem_wait(r0);
-                tmem_load32(r1, c + col0 + 32);
+                tmem_load32(r1, d + col0 + 32);
                 add_scaled(acc, r0, f0);
                 tmem_wait(r1);
-                tmem_load32(r0, c + col1);
-                add_scaled(acc + 32, r1, f0);
+                tmem_load32(r0, d + col1);
+                const uint32_t next = done + 8 * ((n + 1) % kStages), phase = ((n + 1) / kStages) & 1;
+                const bool ready = bar_test(next, phase);
+                add_scaled(acc + 16, r1, f0);
                 tmem_wait(r0);
-                tmem_load32(r1, c + col1 + 32);
-                if (SWIGLU) add_scaled(acc + 64, r0, f1, f2, split);
-                else add_scaled(acc + 64, r0, f0);
+                tmem_load32(r1, d + col1 + 32);
+                if (SPLIT) add_scaled(acc + 32, r0, f1, f2, split);
+                else add_scaled(acc + 32, r0, f1);
                 tmem_wait(r1);
                 tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive(acc_empty + 8 * buf);
-                if (SWIGLU) add_scaled(acc + 96, r1, f1, f2, split - 32);
-                else add_scaled(acc + 96, r1, f0);
+                read_arrive(n & 1);
+                const float g1 = f1, g2 = f2;
+                if (k + 1 < kb) {
+                    if (!ready) ok &= bar_wait(next, phase, giveup);
+                    __syncwarp();
+                    tmem_fence_after();
+                    tmem_load32(r0, taddr + ((n + 1) & 1) * kTileCols + col0);
+                    factors(n + 1);
+                }
+                if (SPLIT) add_scaled(acc + 48, r1, g1, g2, split - 32);
+                else add_scaled(acc + 48, r1, g1);
             }
             const bool present = x.m0 + row < x.m1;
             if constexpr (!SWIGLU) {
@@ -303,18 +395,19 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
             } else {
                 const int n0 = x.n0 + half * 64;
                 float top = 0.0f;
+                float z[64];
 #pragma unroll
                 for (int i = 0; i < 64; ++i) {
-                    const float gate = acc[i];
-                    acc[i] = __fdividef(gate, 1.0f + __expf(-gate)) * acc[64 + i];
-                    top = fmaxf(top, n0 + i < p.N ? fabsf(acc[i]) : 0.0f);
+                    const float gate = i & 1 ? acc[i / 2].y : acc[i / 2].x, up = i & 1 ? acc[32 + i / 2].y : acc[32 + i / 2].x;
+                    z[i] = __fdividef(gate, 1.0f + __expf(-gate)) * up;
+                    top = fmaxf(top, n0 + i < p.N ? fabsf(z[i]) : 0.0f);
                 }
                 tops[parity][half][row] = top;
                 // the other half's maximum; a parity's words are rewritten two tiles later, which no warp
                 // reaches before all have passed the tile between
                 __syncwarp();
                 if (lane == 0) bar_arrive(topped);
-                ok = __all_sync(0xffffffffu, ok && bar_wait(topped, parity, giveup));
+                ok &= bar_wait(topped, parity, giveup);
                 const float scale = e4m3_block_scale(fmaxf(top, tops[parity][half ^ 1][row]));
                 const float inv = __frcp_rn(scale);
                 if (ok && present) {
@@ -326,8 +419,7 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
                         uint32_t w[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            w[j] = e4m3x4_scaled(acc[i + 4 * j], acc[i + 4 * j + 1], acc[i + 4 * j + 2],
-                                                 acc[i + 4 * j + 3], scale, inv);
+                            w[j] = e4m3x4_scaled(z[i + 4 * j], z[i + 4 * j + 1], z[i + 4 * j + 2], z[i + 4 * j + 3], scale, inv);
                         st_v4(out + i, make_uint4(w[0], w[1], w[2], w[3]));
                     }
                 }
@@ -376,17 +468,18 @@ int make_map(CUtensorMap* m, const char* what, const void* base, int64_t rows, i
     return EP_OK;
 }
 
-template <bool SWIGLU>
+template <bool SWIGLU, bool SPLIT>
 cudaError_t launch_product_rows(const MatmulArgs& p, const CUtensorMap& ma, const CUtensorMap& mb, int sms,
                                 cudaStream_t s)
 {
     const int cols = SWIGLU ? kTileCols / 2 : kTileCols;
     const int64_t most = (p.rows / kTileRows + p.groups) * ((p.N + cols - 1) / cols);   // tiles, at most
-    const size_t smem = 1024 + kStages * kStageBytes + (p.groups + 1) * sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(ep_product_rows_kernel<SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    const size_t smem = 1024 + kStages * kStageBytes + kRingFloats * sizeof(float) + (p.groups + 1) * sizeof(int) +
+                        (p.offsets && p.groups <= kSharedOffsets ? (p.groups + 1) * sizeof(int32_t) : 0);
+    cudaError_t e = cudaFuncSetAttribute(ep_product_rows_kernel<SWIGLU, SPLIT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    ep_product_rows_kernel<SWIGLU><<<(unsigned)(most < sms ? most : sms), kProductThreads, smem, s>>>(p, ma, mb);
+    ep_product_rows_kernel<SWIGLU, SPLIT><<<(unsigned)(most < sms ? most : sms), kProductThreads, smem, s>>>(p, ma, mb);
     return cudaGetLastError();
 }
 
@@ -434,7 +527,8 @@ extern "C" int ep_matmul_fp8(const void* a, const float* a_scales, const void* b
     if (int rc = make_map(&ma, "a", a, rows, inner, kTileRows)) return rc;
     if (int rc = make_map(&mb, "b", b, (int64_t)groups * columns, inner, 128)) return rc;
     cudaStream_t s = (cudaStream_t)stream;
-    const cudaError_t e = swiglu ? launch_product_rows<true>(p, ma, mb, sms, s)
-                                 : launch_product_rows<false>(p, ma, mb, sms, s);
+    const cudaError_t e = !swiglu            ? launch_product_rows<false, false>(p, ma, mb, sms, s)
+                          : p.N % 128 == 0 ? launch_product_rows<true, false>(p, ma, mb, sms, s)
+                                           : launch_product_rows<true, true>(p, ma, mb, sms, s);
     return layer_cuda(e, "ep_matmul_fp8: launch");
 }

@@ -15,7 +15,22 @@ namespace ep {
 // a second and a half at 2 GHz; the longest legitimate wait is a tile's, under a millisecond
 constexpr long long kWaitCycles = 3ll << 30;
 
+// a thread that waits sleeps for up to this long before it looks again: polling slows the barriers down
+constexpr uint32_t kSuspendNs = 1000000;
+
 #ifdef __CUDACC__
+
+// One lane of a converged warp, in a form the compiler knows to be one lane.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t e;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(e));
+    return e != 0;
+}
+
+// A value that is the same in every lane, told to the compiler: descriptors and loop counts made from it
+// stay in uniform registers, which the tensor-core instructions read.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -37,7 +52,16 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
-    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok) : "r"(bar), "r"(parity), "r"(kSuspendNs) : "memory");
+    return ok != 0;
+}
+
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
                  : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
@@ -51,7 +75,7 @@ struct Giveup {
 // Wait until the barrier's phase of this parity has completed; false if the wait gave up.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Giveup& g)
 {
-    if (bar_try(bar, parity)) return true;
+    if (bar_test(bar, parity)) return true;
     const long long t0 = clock64();
     while (!bar_try(bar, parity)) {
         if (*g.flag) return false;
@@ -119,12 +143,18 @@ __device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t addr)
 // The registers are tied to the wait, so that no use of them can be scheduled before it.
 __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32])
 {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-                 :: "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// d += a * b for two floats each, one instruction: rounded as two fused multiply-adds.  Kept in the
+// order it is written in, between the loads that it is meant to overlap.
+__device__ __forceinline__ void fma2(float2& d, const float2& a, const float2& b)
+{
+    asm volatile("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%0, %1};\n\t"
+        "fma.rn.f32x2 z, x, y, z; mov.b64 {%0, %1}, z; }"
+        : "+f"(d.x), "+f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
 }
 
 // ---- matrix multiply-accumulate
