@@ -8,6 +8,8 @@
 //
 // Products of e4m3 values are exact in FP32, so the block sums keep FP32 accuracy and the scales
 // enter once per block.
+#include <cstdlib>
+
 #include "ep_tcgen05.cuh"
 
 namespace ep {
@@ -72,6 +74,7 @@ struct Tile {
 };
 
 // Exclusive prefix of the groups' tile counts, by one warp.
+template <int ROWS>
 __device__ __forceinline__ void scan_tiles(const MatmulArgs& p, int* first, int col_tiles, int lane)
 {
     int carry = 0;
@@ -80,7 +83,7 @@ __device__ __forceinline__ void scan_tiles(const MatmulArgs& p, int* first, int 
         if (b + lane < p.groups) {
             int lo, hi;
             group_rows(p, p.offsets, b + lane, lo, hi);
-            n = (hi - lo + kTileRows - 1) / kTileRows * col_tiles;
+            n = (hi - lo + ROWS - 1) / ROWS * col_tiles;
         }
         int s = n;
 #pragma unroll
@@ -96,8 +99,9 @@ __device__ __forceinline__ void scan_tiles(const MatmulArgs& p, int* first, int 
 
 // Tile t: groups in order; within a group, chunks of kChunkTiles row tiles, whose rows and the group's
 // weights stay in L2 while the chunk is done; within a chunk, row tiles before columns.
+template <int ROWS, int COLS>
 __device__ __forceinline__ Tile find_tile(const MatmulArgs& p, const int32_t* off, const int* first, int col_tiles,
-                                          int cols, int t)
+                                          int t)
 {
     int lo = 0, hi = p.groups;   // first[lo] <= t < first[hi]
     while (hi - lo > 1) {
@@ -109,13 +113,13 @@ __device__ __forceinline__ Tile find_tile(const MatmulArgs& p, const int32_t* of
     x.g = lo;
     int r0;
     group_rows(p, off, lo, r0, x.m1);
-    const int tiles = (x.m1 - r0 + kTileRows - 1) / kTileRows;
+    const int tiles = (x.m1 - r0 + ROWS - 1) / ROWS;
     const int in = t - first[lo];
     const int chunk = in / (kChunkTiles * col_tiles), rest = in - chunk * kChunkTiles * col_tiles;
     const int wide = min(kChunkTiles, tiles - chunk * kChunkTiles);
     const int col = rest / wide;
-    x.m0 = r0 + (chunk * kChunkTiles + rest - col * wide) * kTileRows;
-    x.n0 = col * cols;
+    x.m0 = r0 + (chunk * kChunkTiles + rest - col * wide) * ROWS;
+    x.n0 = col * COLS;
     return x;
 }
 
@@ -211,7 +215,7 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
     if (copied)
         for (int i = threadIdx.x; i <= p.groups; i += kProductThreads) off_copy[i] = p.offsets[i];
     const int32_t* off = copied ? off_copy : p.offsets;
-    if (warp == 1) scan_tiles(p, first, col_tiles, lane);
+    if (warp == 1) scan_tiles<kTileRows>(p, first, col_tiles, lane);
     if (warp == 2) tmem_alloc(smem_u32(&tmem_slot), 512);
     tmem_fence_before();
     __syncthreads();
@@ -225,7 +229,7 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
             uint32_t n = 0;   // blocks loaded
             bool ok = true;
             for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                const Tile x = find_tile(p, off, first, col_tiles, kCols, t);
+                const Tile x = find_tile<kTileRows, kCols>(p, off, first, col_tiles, t);
                 const int64_t b_rows = (int64_t)x.g * p.columns;
                 const int y0 = (int)(b_rows + x.n0), y1 = (int)(b_rows + (SWIGLU ? p.N + x.n0 : x.n0 + 128));
                 for (int k = 0; k < kb; ++k, ++n) {
@@ -278,7 +282,7 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
             uint32_t n = 0;
             bool ok = true;
             for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                const Tile x = find_tile(p, off, first, col_tiles, kCols, t);
+                const Tile x = find_tile<kTileRows, kCols>(p, off, first, col_tiles, t);
                 const float* as0 = p.as + (int64_t)min(x.m0 + r, x.m1 - 1) * kb;
                 const float* as1 = p.as + (int64_t)min(x.m0 + r + 64, x.m1 - 1) * kb;
                 const float* bs = p.bs + (int64_t)x.g * p.nb * kb;
@@ -334,7 +338,7 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
         int parity = 0;
         uint32_t n = 0;
         for (int t = blockIdx.x; t < tiles; t += gridDim.x, parity ^= 1) {
-            const Tile x = find_tile(p, off, first, col_tiles, kCols, t);
+            const Tile x = find_tile<kTileRows, kCols>(p, off, first, col_tiles, t);
             // up columns of this half that share the tile's first up block
             const int split = 128 - (p.N + x.n0) % 128 - half * 64;
             float2 acc[64];
@@ -434,6 +438,293 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
     }
 }
 
+// ---- few rows
+//
+// With few rows to a group the time is that of reading b once.  Here b's rows are the 128 lanes of the
+// accumulator and the T <= 64 rows of a tile its columns: a CTA takes 128 output columns (with SwiGLU
+// also their 128 up rows) and T rows, and streams b through as many stages as shared memory holds
+// (130-180 KB in flight on an SM; the rows' codes come from L2).  Tiles are small enough to spread the
+// weights evenly, and where there are too few of them for the SMs a cluster of CTAs splits K: each
+// leaves its sums in its shared memory, and each adds up, in the order of the CTAs, the rows of T
+// that it finishes.  Roles as above, with four scaling warps: a thread owns one output column.
+
+constexpr int kFewThreads = 256;
+constexpr int kFewCols = 128;
+constexpr int kFewRing = 16;          // blocks of factors: at least stages + accumulators
+constexpr int kFewMaxStages = 12;
+constexpr int kFewReadThreads = 128 + 32;
+constexpr int kMaxSplit = 8;
+
+template <int T, bool SWIGLU>
+struct FewShape {
+    static constexpr int kHalves = SWIGLU ? 2 : 1;
+    static constexpr int kWeightBytes = kFewCols * kBlockK;
+    static constexpr int kStageBytes = kHalves * kWeightBytes + T * kBlockK;
+    static constexpr int kBufferCols = kHalves * T;
+    // accumulators: no more than stages, so that a stage's barrier is never a whole phase ahead of a reader
+    static constexpr int kBuffers = kBufferCols > 64 ? 2 : 4;
+    static constexpr int kTmemCols = kBuffers * kBufferCols < 32 ? 32 : kBuffers * kBufferCols;
+    static constexpr int kFactorRows = SWIGLU ? 3 : 1;   // gate, and the two up blocks a tile can touch
+    static constexpr int kRingFloats = kFewRing * kFactorRows * T;
+    static constexpr int kSumFloats = kHalves * T * kFewCols;
+};
+
+template <int T, bool SWIGLU>
+__global__ void __launch_bounds__(kFewThreads, 1)
+ep_product_few_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap map_a,
+                      const __grid_constant__ CUtensorMap map_b, const int stage_count, const int split_k)
+{
+    using S = FewShape<T, SWIGLU>;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t bars[2 * kFewMaxStages + 3];
+    __shared__ float tops[2][4][T];   // [tile parity][warp][row]: largest |z|
+    __shared__ uint32_t tmem_slot;
+    __shared__ int gave_up;
+    const uint32_t stages = (smem_u32(raw) + 1023u) & ~1023u;
+    float* sums = reinterpret_cast<float*>(raw + (stages - smem_u32(raw)) + stage_count * S::kStageBytes);
+    float* ring = sums + S::kSumFloats;
+    int* first = reinterpret_cast<int*>(ring + S::kRingFloats);
+    int32_t* off_copy = first + p.groups + 1;
+    const uint32_t full = smem_u32(bars), done = full + 8 * kFewMaxStages, drained = done + 8 * kFewMaxStages,
+                   summed = drained + 8, taken = summed + 8;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const Giveup giveup{&gave_up, p.status};
+    const int col_tiles = (p.N + kFewCols - 1) / kFewCols;
+    const uint32_t rank = split_k > 1 ? cluster_rank() : 0;
+    const int k_lo = (int)((int64_t)p.kb * rank / split_k), k_hi = (int)((int64_t)p.kb * (rank + 1) / split_k);
+    const int t_first = blockIdx.x / split_k, t_step = gridDim.x / split_k;
+
+    if (threadIdx.x == 0) {
+        gave_up = 0;
+        for (int i = 0; i < stage_count; ++i) {
+            bar_init(full + 8 * i, 3);   // the loads and two warps' factors
+            bar_init(done + 8 * i, 1);
+        }
+        bar_init(drained, 1);
+        bar_init(summed, 4 * split_k);
+        bar_init(taken, 4 * split_k);
+        fence_barrier_init();
+        prefetch_map(&map_a);
+        prefetch_map(&map_b);
+    }
+    const bool copied = p.offsets != nullptr && p.groups <= kSharedOffsets;
+    if (copied)
+        for (int i = threadIdx.x; i <= p.groups; i += kFewThreads) off_copy[i] = p.offsets[i];
+    const int32_t* off = copied ? off_copy : p.offsets;
+    if (warp == 1) scan_tiles<T>(p, first, col_tiles, lane);
+    if (warp == 2) tmem_alloc(smem_u32(&tmem_slot), S::kTmemCols);
+    tmem_fence_before();
+    __syncthreads();
+    if (split_k > 1) cluster_sync();   // the peers' barriers exist
+    tmem_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const int tiles = uniform(first[p.groups]);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t n = 0, s = 0, phase = 1;
+            bool ok = true;
+            for (int t = t_first; t < tiles && ok; t += t_step) {
+                const Tile x = find_tile<T, kFewCols>(p, off, first, col_tiles, t);
+                const int y = (int)((int64_t)x.g * p.columns + x.n0);
+                for (int k = k_lo; k < k_hi; ++k, ++n) {
+                    if (n >= (uint32_t)stage_count && !bar_wait(done + 8 * s, phase, giveup)) { ok = false; break; }
+                    const uint32_t dst = stages + s * S::kStageBytes, bar = full + 8 * s;
+                    bar_expect(bar, S::kStageBytes);
+                    tma_load(dst, &map_b, k * kBlockK, y, bar);
+                    if (SWIGLU) tma_load(dst + S::kWeightBytes, &map_b, k * kBlockK, y + p.N, bar);
+                    tma_load(dst + S::kHalves * S::kWeightBytes, &map_a, k * kBlockK, x.m0, bar);
+                    if (++s == (uint32_t)stage_count) { s = 0; phase ^= 1; }
+                }
+            }
+            if (!ok)   // its loads in flight
+                for (uint32_t i = n < (uint32_t)stage_count ? 0 : n - stage_count; i < n; ++i)
+                    bar_drain(full + 8 * (i % stage_count), (i / stage_count) & 1);
+        }
+    } else if (warp == 1) {
+        constexpr uint32_t instruction = mma_instruction(kFewCols, T);
+        const uint64_t d0 = mma_descriptor(stages);
+        const uint32_t mine = tiles > t_first ? (tiles - t_first - 1) / t_step + 1 : 0;
+        const uint32_t blocks = mine * (k_hi - k_lo);
+        const bool leader = elect_one();
+        // after a wait that gave up the products go on, on whatever the stages hold (see above)
+        for (uint32_t n = 0, s = 0, phase = 0; n < blocks; ++n) {
+            const uint32_t buf = n % S::kBuffers;
+            bar_wait(full + 8 * s, phase, giveup);
+            if (n >= S::kBuffers) asm volatile("bar.sync %0, %1;" :: "r"(1 + buf), "n"(kFewReadThreads) : "memory");
+            if (leader) {
+                tmem_fence_after();
+                const uint64_t w = d0 + s * (uint32_t)(S::kStageBytes >> 4);
+                const uint64_t r = w + S::kHalves * (S::kWeightBytes >> 4);
+#pragma unroll
+                for (int h = 0; h < S::kHalves; ++h)
+#pragma unroll
+                    for (int i = 0; i < kBlockK / 32; ++i)
+                        mma_e4m3(tmem + buf * S::kBufferCols + h * T, w + h * (S::kWeightBytes >> 4) + 2 * i, r + 2 * i,
+                                 instruction, i == 0);
+                mma_commit(done + 8 * s);
+            }
+            __syncwarp();
+            if (++s == (uint32_t)stage_count) { s = 0; phase ^= 1; }
+        }
+        for (uint32_t n = blocks < S::kBuffers ? 0 : blocks - S::kBuffers; n < blocks; ++n)
+            asm volatile("bar.sync %0, %1;" :: "r"(1 + n % S::kBuffers), "n"(kFewReadThreads) : "memory");
+        if (leader) {
+            mma_commit(drained);   // tensor memory is freed only after its last product
+            bar_drain(drained, 0);
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        // factors of row c of the tile: as[row][k] * bs[.][k]; loaded kAhead blocks ahead
+        const int c = threadIdx.x - 64;
+        const int last = p.nb - 1;
+        uint32_t n = 0, s = 0, phase = 1;
+        bool ok = true;
+        for (int t = t_first; t < tiles && ok; t += t_step) {
+            const Tile x = find_tile<T, kFewCols>(p, off, first, col_tiles, t);
+            const float* as = p.as + (int64_t)min(x.m0 + c, x.m1 - 1) * p.kb;
+            const float* bs = p.bs + (int64_t)x.g * p.nb * p.kb;
+            const int up = (p.N + x.n0) / 128;
+            const float* bs0 = bs + (int64_t)min(x.n0 / 128, last) * p.kb;
+            const float* bs1 = bs + (int64_t)min(up, last) * p.kb;
+            const float* bs2 = bs + (int64_t)min(up + 1, last) * p.kb;
+            constexpr int kAhead = 4;
+            float a[kAhead], b0[kAhead], b1[kAhead], b2[kAhead];
+            auto load = [&](int i, int k) {
+                if (c >= T || k >= k_hi) return;
+                a[i] = as[k];
+                b0[i] = bs0[k];
+                if (SWIGLU) { b1[i] = bs1[k]; b2[i] = bs2[k]; }
+            };
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) load(i, k_lo + i);
+            for (int k0 = k_lo; k0 < k_hi && ok; k0 += kAhead) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    if (k0 + i >= k_hi) break;
+                    if (n >= (uint32_t)stage_count) ok = ok && bar_wait(done + 8 * s, phase, giveup);
+                    __syncwarp();
+                    if (c < T) {
+                        float* f = ring + (n % kFewRing) * (S::kFactorRows * T) + c;
+                        f[0] = a[i] * b0[i];
+                        if (SWIGLU) { f[T] = a[i] * b1[i]; f[2 * T] = a[i] * b2[i]; }
+                    }
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(full + 8 * s);
+                    ++n;
+                    if (++s == (uint32_t)stage_count) { s = 0; phase ^= 1; }
+                    load(i, k0 + kAhead + i);
+                }
+            }
+        }
+    } else {
+        const int col = threadIdx.x - 128;
+        const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t my_sums = smem_u32(sums) + 4 * col;
+        bool ok = true;
+        uint32_t n = 0, s = 0, phase = 0, parity = 0;
+        const int c_lo = T * rank / split_k, c_hi = T * (rank + 1) / split_k;   // the rows this CTA finishes
+        for (int t = t_first; t < tiles; t += t_step, parity ^= 1) {
+            const Tile x = find_tile<T, kFewCols>(p, off, first, col_tiles, t);
+            const int up_row = (p.N + x.n0 + col) / 128 - (p.N + x.n0) / 128;   // 0 or 1: this column's up block
+            float2 acc[S::kHalves][T / 2];
+#pragma unroll
+            for (int h = 0; h < S::kHalves; ++h)
+#pragma unroll
+                for (int i = 0; i < T / 2; ++i) acc[h][i] = make_float2(0.0f, 0.0f);
+            for (int k = k_lo; k < k_hi; ++k, ++n) {
+                const uint32_t buf = n % S::kBuffers;
+                ok &= bar_wait(done + 8 * s, phase, giveup);
+                __syncwarp();
+                tmem_fence_after();
+                const float* f = ring + (n % kFewRing) * (S::kFactorRows * T);
+#pragma unroll
+                for (int h = 0; h < S::kHalves; ++h) {
+                    const float* fh = f + (h ? (1 + up_row) * T : 0);
+#pragma unroll
+                    for (int i = 0; i < T; i += 16) {
+                        uint32_t r[16];
+                        tmem_load16(r, taddr + buf * S::kBufferCols + h * T + i);
+                        tmem_wait(r);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 v = *reinterpret_cast<const float4*>(fh + i + j);
+                            fma2(acc[h][(i + j) / 2], make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
+                                 make_float2(v.x, v.y));
+                            fma2(acc[h][(i + j) / 2 + 1],
+                                 make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), make_float2(v.z, v.w));
+                        }
+                    }
+                }
+                tmem_fence_before();
+                asm volatile("bar.arrive %0, %1;" :: "r"(1 + buf), "n"(kFewReadThreads) : "memory");
+                if (++s == (uint32_t)stage_count) { s = 0; phase ^= 1; }
+            }
+            // this CTA's sums; before they are replaced every CTA has taken the last tile's
+            if (split_k > 1 && t != t_first) ok &= peer_wait(taken, parity ^ 1, giveup);
+#pragma unroll
+            for (int h = 0; h < S::kHalves; ++h)
+#pragma unroll
+                for (int i = 0; i < T / 2; ++i) {
+                    sums[(h * T + 2 * i) * kFewCols + col] = acc[h][i].x;
+                    sums[(h * T + 2 * i + 1) * kFewCols + col] = acc[h][i].y;
+                }
+            if (split_k > 1) {
+                __syncwarp();
+                if (lane < split_k) peer_arrive(peer_smem(summed, lane));
+                ok &= peer_wait(summed, parity, giveup);
+            }
+            auto total = [&](int j) {   // sums of row j (of gate rows, then up rows) over the cluster
+                if (split_k == 1) return sums[j * kFewCols + col];
+                float v = 0.0f;
+                for (int q = 0; q < split_k; ++q) v += peer_load(peer_smem(my_sums + j * kFewCols * 4, q));
+                return v;
+            };
+            const int rows = min(x.m1 - x.m0, c_hi);
+            const bool in = x.n0 + col < p.N;
+            if constexpr (!SWIGLU) {
+                for (int c = c_lo; c < rows; ++c) {
+                    const float v = total(c);
+                    if (!ok || !in) continue;
+                    const int64_t at = (int64_t)(x.m0 + c) * p.N + x.n0 + col;
+                    if (p.dtype == EP_FP16) ((__half*)p.out)[at] = __float2half_rn(v);
+                    else ((__nv_bfloat16*)p.out)[at] = __float2bfloat16_rn(v);
+                }
+            } else {
+                for (int c = c_lo; c < rows; ++c) {
+                    const float gate = total(c), up = total(T + c);
+                    const float z = __fdiv_rn(gate, 1.0f + expf(-gate)) * up;
+                    sums[c * kFewCols + col] = z;   // only this thread reads it from now on
+                    // whole-number order is that of magnitudes; fmaxf turns NaN into 0
+                    const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(in ? fmaxf(fabsf(z), 0.0f) : 0.0f));
+                    if (lane == 0) tops[parity][warp & 3][c] = __uint_as_float(top);
+                }
+                asm volatile("bar.sync 7, 128;" ::: "memory");
+                for (int c = c_lo; c < rows; ++c) {
+                    const float* w = &tops[parity][0][c];
+                    const float scale = e4m3_block_scale(fmaxf(fmaxf(w[0], w[T]), fmaxf(w[2 * T], w[3 * T])));
+                    if (!ok) continue;
+                    if (col == 0) p.out_scales[(int64_t)(x.m0 + c) * ((p.N + 127) / 128) + x.n0 / 128] = scale;
+                    if (in)
+                        ((uint8_t*)p.out)[(int64_t)(x.m0 + c) * p.N + x.n0 + col] =
+                            (uint8_t)e4m3x2(__fdiv_rn(sums[c * kFewCols + col], scale), 0.0f);
+                }
+            }
+            if (split_k > 1) {
+                __syncwarp();
+                if (lane < split_k) peer_arrive(peer_smem(taken, lane));
+            }
+        }
+    }
+    tmem_fence_before();
+    __syncthreads();
+    if (split_k > 1) cluster_sync();
+    if (warp == 2) {
+        tmem_fence_after();
+        tmem_free(tmem, S::kTmemCols);
+    }
+}
+
 // ---- tensor maps
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -483,6 +774,51 @@ cudaError_t launch_product_rows(const MatmulArgs& p, const CUtensorMap& ma, cons
     return cudaGetLastError();
 }
 
+template <int T, bool SWIGLU>
+cudaError_t launch_product_few(const MatmulArgs& p, const CUtensorMap& ma, const CUtensorMap& mb, int sms,
+                               cudaStream_t s)
+{
+    using S = FewShape<T, SWIGLU>;
+    const int64_t groups = p.groups < p.rows ? p.groups : p.rows;   // that can hold a row
+    const int64_t most = ((p.rows - groups) / T + groups) * ((p.N + kFewCols - 1) / kFewCols);   // tiles, at most
+    int split = 1;
+    while (split < kMaxSplit && most * split * 2 <= sms && split * 2 <= p.kb) split *= 2;
+    const size_t rest = 1024 + (S::kSumFloats + S::kRingFloats) * sizeof(float) + (p.groups + 1) * sizeof(int) +
+                        (p.offsets && p.groups <= kSharedOffsets ? (p.groups + 1) * sizeof(int32_t) : 0);
+    constexpr size_t kMost = 227 * 1024 - 4096;   // less the static part
+    int stages = (int)((kMost - rest) / S::kStageBytes);
+    if (stages > kFewMaxStages) stages = kFewMaxStages;
+    if (stages < S::kBuffers) return cudaErrorInvalidConfiguration;   // not reached: 3 stages at the least
+    const size_t smem = rest + (size_t)stages * S::kStageBytes;
+    auto* kernel = ep_product_few_kernel<T, SWIGLU>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int64_t clusters = most < sms / split ? most : sms / split;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(clusters * split));
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p, ma, mb, stages, split);
+}
+
+// Rows of a tile of the kernel for few rows, from the mean rows of a group, or 0 for the other kernel.
+int few_rows_tile(const MatmulArgs& p, int sms)
+{
+    (void)sms;
+    const int64_t groups = p.groups < p.rows ? p.groups : p.rows;
+    const int64_t mean = p.rows / (groups > 0 ? groups : 1);
+    const char* f = getenv("FEW");
+    if (f) return atoi(f);
+    return mean <= 10 ? 16 : mean <= 24 ? 32 : mean <= 64 ? 64 : 0;
+}
+
 }  // namespace
 }  // namespace ep
 
@@ -523,12 +859,18 @@ extern "C" int ep_matmul_fp8(const void* a, const float* a_scales, const void* b
     p.vec = columns % 16 == 0 && layer_aligned(out, 32) ? 2 : columns % 8 == 0 ? 1 : 0;
     const int sms = layer_num_sms();
     if (sms == 0) return layer_fail(EP_ERR_CUDA, "%s: cannot tell the current device's multiprocessors", who);
+    // rows of a tile of the kernel for few rows, or 0 for the kernel of 128-row tiles
+    const int few = few_rows_tile(p, sms);
     CUtensorMap ma, mb;
-    if (int rc = make_map(&ma, "a", a, rows, inner, kTileRows)) return rc;
+    if (int rc = make_map(&ma, "a", a, rows, inner, few ? few : kTileRows)) return rc;
     if (int rc = make_map(&mb, "b", b, (int64_t)groups * columns, inner, 128)) return rc;
     cudaStream_t s = (cudaStream_t)stream;
-    const cudaError_t e = !swiglu            ? launch_product_rows<false, false>(p, ma, mb, sms, s)
-                          : p.N % 128 == 0 ? launch_product_rows<true, false>(p, ma, mb, sms, s)
-                                           : launch_product_rows<true, true>(p, ma, mb, sms, s);
+    cudaError_t e;
+    if (few == 16) e = swiglu ? launch_product_few<16, true>(p, ma, mb, sms, s) : launch_product_few<16, false>(p, ma, mb, sms, s);
+    else if (few == 32) e = swiglu ? launch_product_few<32, true>(p, ma, mb, sms, s) : launch_product_few<32, false>(p, ma, mb, sms, s);
+    else if (few == 64) e = swiglu ? launch_product_few<64, true>(p, ma, mb, sms, s) : launch_product_few<64, false>(p, ma, mb, sms, s);
+    else if (!swiglu) e = launch_product_rows<false, false>(p, ma, mb, sms, s);
+    else if (p.N % 128 == 0) e = launch_product_rows<true, false>(p, ma, mb, sms, s);
+    else e = launch_product_rows<true, true>(p, ma, mb, sms, s);
     return layer_cuda(e, "ep_matmul_fp8: launch");
 }

@@ -95,6 +95,51 @@ __device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity)
     while (!bar_try(bar, parity) && clock64() - t0 < kWaitCycles) {}
 }
 
+// ---- between the CTAs of a cluster
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// The address in CTA `rank` of the cluster that corresponds to this CTA's shared-memory address.
+__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ float peer_load(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Arrive on a peer's barrier; this thread's earlier writes, and those ordered before them, are visible to
+// whoever waits for the phase with peer_wait().
+__device__ __forceinline__ void peer_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool peer_wait(uint32_t bar, uint32_t parity, const Giveup& g)
+{
+    const bool ok = bar_wait(bar, parity, g);
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    return ok;
+}
+
+// No CTA of the cluster leaves while another may still reach its shared memory.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Barrier initialisations become visible to the asynchronous units.
 __device__ __forceinline__ void fence_barrier_init() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
 
@@ -140,12 +185,23 @@ __device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t addr)
                  : "r"(addr));
 }
 
+// 16 consecutive columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_load16(uint32_t (&r)[16], uint32_t addr)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(addr));
+}
+
 // The registers are tied to the wait, so that no use of them can be scheduled before it.
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32])
+template <int N>
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[N])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 // d += a * b for two floats each, one instruction: rounded as two fused multiply-adds.  Kept in the
