@@ -101,6 +101,15 @@ __device__ __forceinline__ uint32_t e4m3x4_scaled(float a, float b, float c, flo
            (e4m3x2(__fdiv_rn(c, scale), __fdiv_rn(d, scale)) << 16);
 }
 
+// The same by a multiplication with the reciprocal, for values that are themselves off by more than the
+// half unit in the last place that this may add.
+__device__ __forceinline__ uint32_t e4m3x4_near(float a, float b, float c, float d, float scale, float inv)
+{
+    if (scale >= 0x1p-100f) return e4m3x2(a * inv, b * inv) | (e4m3x2(c * inv, d * inv) << 16);
+    return e4m3x2(__fdiv_rn(a, scale), __fdiv_rn(b, scale)) |
+           (e4m3x2(__fdiv_rn(c, scale), __fdiv_rn(d, scale)) << 16);
+}
+
 #endif  // __CUDACC__
 
 }  // namespace ep

@@ -30,7 +30,7 @@ struct MatmulArgs {
     int groups, N, K, kb;     // N: output columns of a row (swiglu: half the rows of b)
     int columns, nb;          // rows of b in one group, and their 128-row blocks
     int swiglu, dtype;
-    int vec;                  // 16-bit rows take 32-byte (2) or 16-byte (1) stores
+    int vec;                  // rows take 32-byte (2) or 16-byte (1) stores, or neither
 };
 
 // First and last row of group g, clamped to the buffer; off is p.offsets or a copy of it.
@@ -60,8 +60,10 @@ __device__ __forceinline__ void group_rows(const MatmulArgs& p, const int32_t* o
 constexpr int kTileRows = 128, kTileCols = 256, kBlockK = 128;
 constexpr int kStages = 4;             // even: a stage always goes to the same accumulator
 constexpr int kStageBytes = (kTileRows + kTileCols) * kBlockK;
-constexpr int kProductThreads = 384;   // load, multiply, two factor warps; eight scaling warps
-constexpr int kScaleThreads = 256;
+constexpr int kScaleWarps = 8;         // two to a quarter of the lanes, 128 columns each
+constexpr int kScaleThreads = 32 * kScaleWarps;
+constexpr int kProductThreads = 128 + kScaleThreads;   // load, multiply, two factor warps; the scaling warps
+constexpr int kInfo = 8;               // tiles the loading warp may be ahead of the scaling warps: kStages + 2 at most
 constexpr int kChunkTiles = 16;        // row tiles that share b's columns before the next columns
 constexpr int kFactors = 3;            // factors of a row and block: per half, or gate and two up blocks
 constexpr int kRing = 8;               // blocks of factors: a block is written when the block kStages before it has
@@ -164,9 +166,24 @@ __device__ __forceinline__ void store_row(uint8_t* out, const float2 (&acc)[64],
     }
 }
 
+// gate * sigmoid(gate) * up.  The exponential's argument is split so that its error stays a few units in
+// the last place at any magnitude (the product with log2 e alone would be off by |gate| units); the two
+// approximate units add two more.  Below -88 the exponential is held at 2^127, whose reciprocal is 0; an
+// infinite gate's split is not a number, which fminf turns into one that changes neither 0 nor 2^127's 0.
+__device__ __forceinline__ float swiglu(float gate, float up)
+{
+    const float t = -1.4426950408889634f * gate;
+    const float rest = fminf(fmaf(-1.4426950408889634f, gate, -t), 1.0f);   // what rounding t dropped
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fminf(t, 127.0f)));
+    e = fmaf(e * 0.6931471805599453f, rest, e);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return gate * up * r;
+}
+
 // Named barriers 1 and 2: an accumulator has been read.  Every scaling warp arrives once per block, in
 // every case; the multiplying warp waits before it writes that accumulator again.
-constexpr int kReadThreads = kScaleThreads + 32;
+constexpr int kReadThreads = kScaleThreads + 32;   // 544
 __device__ __forceinline__ void read_arrive(uint32_t buf)
 {
     asm volatile("bar.arrive %0, %1;" :: "r"(1 + buf), "n"(kReadThreads) : "memory");
@@ -184,7 +201,8 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
 {
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t bars[2 * kStages + 2];
-    __shared__ float tops[2][2][kTileRows];   // [tile parity][half][row]: largest |z|
+    __shared__ float tops[2][kScaleWarps / 4][kTileRows];   // [tile parity][column half][row]: largest |z|
+    __shared__ int4 info[kInfo];              // m0, end of the group's rows, n0 of the tiles being worked on
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
     const uint32_t stages = (smem_u32(raw) + 1023u) & ~1023u;
@@ -206,7 +224,7 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
             bar_init(done + 8 * i, 1);
         }
         bar_init(drained, 1);
-        bar_init(topped, kScaleThreads / 32);
+        bar_init(topped, kScaleWarps);
         fence_barrier_init();
         prefetch_map(&map_a);
         prefetch_map(&map_b);
@@ -226,10 +244,11 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 0 && lane == 0) {
-            uint32_t n = 0;   // blocks loaded
+            uint32_t n = 0, i = 0;   // blocks loaded, tiles
             bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++i) {
                 const Tile x = find_tile<kTileRows, kCols>(p, off, first, col_tiles, t);
+                info[i % kInfo] = make_int4(x.m0, x.m1, x.n0, 0);   // seen by whoever sees the block's products
                 const int64_t b_rows = (int64_t)x.g * p.columns;
                 const int y0 = (int)(b_rows + x.n0), y1 = (int)(b_rows + (SWIGLU ? p.N + x.n0 : x.n0 + 128));
                 for (int k = 0; k < kb; ++k, ++n) {
@@ -328,46 +347,50 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        const int half = (warp - 4) >> 2;                 // this warp's columns: 128 of the 256
+        const int part = (warp - 4) >> 2;                 // this warp's half of the columns
         const int row = (warp & 3) * 32 + lane;
-        // plain: columns half*128 ..; SwiGLU: gate columns half*64 .. (of 128), then their up columns
-        const uint32_t col0 = SWIGLU ? half * 64 : half * 128;
-        const uint32_t col1 = SWIGLU ? 128 + half * 64 : col0 + 64;
-        const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        // plain: columns part*128 ..; SwiGLU: gate columns part*64 .. (of 128), then their up columns
+        const uint32_t col0 = SWIGLU ? part * 64 : part * 128;
+        const uint32_t col1 = SWIGLU ? 128 + part * 64 : col0 + 64;
+        // up columns of this part that share a tile's first up block
+        const int split = 128 - p.N % 128 - part * 64;
         bool ok = true;
         int parity = 0;
-        uint32_t n = 0;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x, parity ^= 1) {
-            const Tile x = find_tile<kTileRows, kCols>(p, off, first, col_tiles, t);
-            // up columns of this half that share the tile's first up block
-            const int split = 128 - (p.N + x.n0) % 128 - half * 64;
+        uint32_t i = 0;
+        // of the next block: its products' barrier, that barrier's phase, its accumulator, its factors
+        uint32_t next = done, phase = 0, d = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        uint32_t f = smem_u32(ring) + 4 * (row + (SWIGLU ? 0 : part * kTileRows));
+        const uint32_t f_end = f + kRing * kFactors * kTileRows * 4;
+        for (int t = blockIdx.x; t < tiles; t += gridDim.x, parity ^= 1, ++i) {
             float2 acc[64];
 #pragma unroll
-            for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.0f, 0.0f);
+            for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.0f, 0.0f);
             // a wait that gave up ends nothing here: what follows works on whatever is there, every barrier
             // gets its arrivals, and the rows are not stored
             float f0, f1, f2;
-            auto factors = [&](uint32_t i) {
-                const float* f = ring + (i % kRing) * (kFactors * kTileRows) + row;
-                f0 = f[SWIGLU ? 0 : half * kTileRows];
-                f1 = SWIGLU ? f[kTileRows] : f0;
-                f2 = SPLIT ? f[2 * kTileRows] : f1;
-            };
             uint32_t r0[32], r1[32];
-            ok &= bar_wait(done + 8 * (n % kStages), (n / kStages) & 1, giveup);
-            __syncwarp();
-            tmem_fence_after();
-            tmem_load32(r0, taddr + (n & 1) * kTileCols + col0);
-            factors(n);
+            // the block's first columns and its factors, once its products are there
+            auto begin = [&](bool ready) {
+                if (!ready) ok &= bar_wait(next, phase, giveup);
+                __syncwarp();
+                tmem_fence_after();
+                tmem_load32(r0, d + col0);
+                f0 = smem_load(f);
+                f1 = SWIGLU ? smem_load(f + 4 * kTileRows) : f0;
+                f2 = SPLIT ? smem_load(f + 8 * kTileRows) : f1;
+                next += 8;
+                if (next == done + 8 * kStages) { next = done; phase ^= 1; }
+                f += 4 * kFactors * kTileRows;
+                if (f == f_end) f -= kRing * kFactors * kTileRows * 4;
+            };
+            begin(false);
             // 32 columns are read while the 32 before them are added, across the ends of blocks too
-            for (int k = 0; k < kb; ++k, ++n) {
-                const uint32_t d = taddr + (n & 1) * kTileCols;
+            for (int k = kb; k > 0; --k) {
                 tmem_wait(r0);
                 tmem_load32(r1, d + col0 + 32);
                 add_scaled(acc, r0, f0);
                 tmem_wait(r1);
                 tmem_load32(r0, d + col1);
-                const uint32_t next = done + 8 * ((n + 1) % kStages), phase = ((n + 1) / kStages) & 1;
                 const bool ready = bar_test(next, phase);
                 add_scaled(acc + 16, r1, f0);
                 tmem_wait(r0);
@@ -376,55 +399,57 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
                 else add_scaled(acc + 32, r0, f1);
                 tmem_wait(r1);
                 tmem_fence_before();
-                read_arrive(n & 1);
+                read_arrive((d >> 8) & 1);   // tensor memory starts at column 0: it is allocated whole
+                d ^= kTileCols;
                 const float g1 = f1, g2 = f2;
-                if (k + 1 < kb) {
-                    if (!ready) ok &= bar_wait(next, phase, giveup);
-                    __syncwarp();
-                    tmem_fence_after();
-                    tmem_load32(r0, taddr + ((n + 1) & 1) * kTileCols + col0);
-                    factors(n + 1);
-                }
+                if (k > 1) begin(ready);
                 if (SPLIT) add_scaled(acc + 48, r1, g1, g2, split - 32);
                 else add_scaled(acc + 48, r1, g1);
             }
-            const bool present = x.m0 + row < x.m1;
+            const int4 x = info[i % kInfo];
+            const bool present = x.x + row < x.y;
             if constexpr (!SWIGLU) {
-                const int n0 = x.n0 + half * 128;
+                const int n0 = x.z + part * 128;
                 if (ok && present && n0 < p.N) {
-                    uint8_t* out = (uint8_t*)p.out + 2 * ((int64_t)(x.m0 + row) * p.N + n0);
+                    uint8_t* out = (uint8_t*)p.out + 2 * ((int64_t)(x.x + row) * p.N + n0);
                     if (p.dtype == EP_FP16) store_row<true>(out, acc, p.N - n0, p.vec);
                     else store_row<false>(out, acc, p.N - n0, p.vec);
                 }
             } else {
-                const int n0 = x.n0 + half * 64;
+                const int n0 = x.z + part * 64;
                 float top = 0.0f;
-                float z[64];
 #pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    const float gate = i & 1 ? acc[i / 2].y : acc[i / 2].x, up = i & 1 ? acc[32 + i / 2].y : acc[32 + i / 2].x;
-                    z[i] = __fdividef(gate, 1.0f + __expf(-gate)) * up;
-                    top = fmaxf(top, n0 + i < p.N ? fabsf(z[i]) : 0.0f);
+                for (int j = 0; j < 32; ++j) {
+                    acc[j].x = swiglu(acc[j].x, acc[32 + j].x);
+                    acc[j].y = swiglu(acc[j].y, acc[32 + j].y);
+                    if (!SPLIT || n0 + 2 * j < p.N) top = fmaxf(top, fmaxf(fabsf(acc[j].x), fabsf(acc[j].y)));
                 }
-                tops[parity][half][row] = top;
-                // the other half's maximum; a parity's words are rewritten two tiles later, which no warp
+                tops[parity][part][row] = top;
+                // the other part's maximum; a parity's words are rewritten two tiles later, which no warp
                 // reaches before all have passed the tile between
                 __syncwarp();
                 if (lane == 0) bar_arrive(topped);
                 ok &= bar_wait(topped, parity, giveup);
-                const float scale = e4m3_block_scale(fmaxf(top, tops[parity][half ^ 1][row]));
+                const float scale = e4m3_block_scale(fmaxf(top, tops[parity][part ^ 1][row]));
                 const float inv = __frcp_rn(scale);
                 if (ok && present) {
-                    if (half == 0) p.out_scales[(int64_t)(x.m0 + row) * ((p.N + 127) / 128) + x.n0 / 128] = scale;
-                    uint8_t* out = (uint8_t*)p.out + (int64_t)(x.m0 + row) * p.N + n0;
+                    if (part == 0) p.out_scales[(int64_t)(x.x + row) * ((p.N + 127) / 128) + x.z / 128] = scale;
+                    uint8_t* out = (uint8_t*)p.out + (int64_t)(x.x + row) * p.N + n0;
 #pragma unroll
-                    for (int i = 0; i < 64; i += 16) {   // N is a multiple of 16
-                        if (n0 + i >= p.N) continue;
-                        uint32_t w[4];
+                    for (int b = 0; b < 2; ++b) {
+                        uint32_t c[8];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            w[j] = e4m3x4_scaled(z[i + 4 * j], z[i + 4 * j + 1], z[i + 4 * j + 2], z[i + 4 * j + 3], scale, inv);
-                        st_v4(out + i, make_uint4(w[0], w[1], w[2], w[3]));
+                        for (int j = 0; j < 8; ++j)
+                            c[j] = e4m3x4_near(acc[16 * b + 2 * j].x, acc[16 * b + 2 * j].y, acc[16 * b + 2 * j + 1].x,
+                                               acc[16 * b + 2 * j + 1].y, scale, inv);
+                        const uint4 lo = make_uint4(c[0], c[1], c[2], c[3]), hi = make_uint4(c[4], c[5], c[6], c[7]);
+                        const int left = p.N - n0 - 32 * b;   // columns; a multiple of 16
+                        if (p.vec == 2 && left >= 32) {
+                            st_v8(out + 32 * b, lo, hi);
+                        } else {
+                            if (left > 0) st_v4(out + 32 * b, lo);
+                            if (left > 16) st_v4(out + 32 * b + 16, hi);
+                        }
                     }
                 }
             }
@@ -693,7 +718,7 @@ ep_product_few_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap ma
             } else {
                 for (int c = c_lo; c < rows; ++c) {
                     const float gate = total(c), up = total(T + c);
-                    const float z = __fdiv_rn(gate, 1.0f + expf(-gate)) * up;
+                    const float z = swiglu(gate, up);
                     sums[c * kFewCols + col] = z;   // only this thread reads it from now on
                     // whole-number order is that of magnitudes; fmaxf turns NaN into 0
                     const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(in ? fmaxf(fabsf(z), 0.0f) : 0.0f));
@@ -856,7 +881,8 @@ extern "C" int ep_matmul_fp8(const void* a, const float* a_scales, const void* b
     p.K = inner; p.kb = (inner + 127) / 128; p.N = swiglu ? columns / 2 : columns; p.nb = (columns + 127) / 128;
     p.swiglu = swiglu; p.dtype = dtype;
     p.columns = columns;
-    p.vec = columns % 16 == 0 && layer_aligned(out, 32) ? 2 : columns % 8 == 0 ? 1 : 0;
+    p.vec = swiglu ? (p.N % 32 == 0 && layer_aligned(out, 32) ? 2 : 1)
+                   : columns % 16 == 0 && layer_aligned(out, 32) ? 2 : columns % 8 == 0 ? 1 : 0;
     const int sms = layer_num_sms();
     if (sms == 0) return layer_fail(EP_ERR_CUDA, "%s: cannot tell the current device's multiprocessors", who);
     // rows of a tile of the kernel for few rows, or 0 for the kernel of 128-row tiles

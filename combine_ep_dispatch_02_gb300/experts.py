@@ -41,15 +41,15 @@ def _bad(msg: str):
 
 def _arg(t: torch.Tensor, what: str, dtype, shape, device) -> int:
     """Address of a tensor that has to be contiguous, of this type and shape, on this device."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device:
+        return t.data_ptr()
     if t.device != device:
         _bad(f"{what} is on {t.device}, the call runs on {device}")
     if t.dtype != dtype:
         _bad(f"{what} is {t.dtype}, the call takes {dtype}")
     if tuple(t.shape) != tuple(shape):
         _bad(f"{what} has shape {tuple(t.shape)}, the call takes {tuple(shape)}")
-    if not t.is_contiguous():
-        _bad(f"{what} is not contiguous")
-    return t.data_ptr()
+    _bad(f"{what} is not contiguous")
 
 
 def _device(t: torch.Tensor, what: str) -> torch.device:
@@ -104,8 +104,12 @@ def _place(device: torch.device, stream):
     return _other_place(device, stream)
 
 
+# the current stream's handle without building a torch.cuda.Stream around it: 2 us less per call
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _raw_stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    return _current_raw_stream(device.index)
 
 
 def rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,

@@ -399,6 +399,17 @@ def test_product_swiglu(rows, K, N, groups):
     _check_product(*args, _edges(rows, groups, g) if groups else None, swiglu=True)
 
 
+@pytest.mark.parametrize("rows", [5, 700])
+def test_product_swiglu_of_gates_far_from_zero(rows):
+    """Gates from single digits to past 1000, where the sigmoid is 0 or 1 to every digit."""
+    g = _gen(rows)
+    a, sa, b, sb = _product_inputs(g, rows, 256, 256, 1)
+    sa *= torch.logspace(0, 2.5, rows, device=DEV)[:, None]
+    z, _ = _product64(a, sa, b[0], sb[0])
+    assert z[:, :128].max() > 100 and z[:, :128].min() < -100
+    _check_product(a, sa, b, sb, None, swiglu=True)
+
+
 @pytest.mark.parametrize("rows", [2, 20, 60, 100, 140, 1000])
 def test_product_all_rows_in_one_of_many_groups(rows):
     g = _gen(rows)
