@@ -8,8 +8,6 @@
 //
 // Products of e4m3 values are exact in FP32, so the block sums keep FP32 accuracy and the scales
 // enter once per block.
-#include <cstdlib>
-
 #include "ep_tcgen05.cuh"
 
 namespace ep {
@@ -701,8 +699,12 @@ ep_product_few_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap ma
             }
             auto total = [&](int j) {   // sums of row j (of gate rows, then up rows) over the cluster
                 if (split_k == 1) return sums[j * kFewCols + col];
-                float v = 0.0f;
-                for (int q = 0; q < split_k; ++q) v += peer_load(peer_smem(my_sums + j * kFewCols * 4, q));
+                float part[kMaxSplit], v = 0.0f;   // all loads on their way before the first is added
+#pragma unroll
+                for (int q = 0; q < kMaxSplit; ++q)
+                    part[q] = q < split_k ? peer_load(peer_smem(my_sums + j * kFewCols * 4, q)) : 0.0f;
+#pragma unroll
+                for (int q = 0; q < kMaxSplit; ++q) v += part[q];
                 return v;
             };
             const int rows = min(x.m1 - x.m0, c_hi);
@@ -806,8 +808,11 @@ cudaError_t launch_product_few(const MatmulArgs& p, const CUtensorMap& ma, const
     using S = FewShape<T, SWIGLU>;
     const int64_t groups = p.groups < p.rows ? p.groups : p.rows;   // that can hold a row
     const int64_t most = ((p.rows - groups) / T + groups) * ((p.N + kFewCols - 1) / kFewCols);   // tiles, at most
+    // K split in up to 4 while the CTAs fit the SMs; in 8 only for a few tiles, because a GPC's 16 to 20 SMs
+    // hold two clusters of 8 at most and 16 clusters do not all run at once (one row, 7168 x 4096 with
+    // SwiGLU: 13.7 us in 8, 9.2 in 4, 13.1 in 2)
     int split = 1;
-    while (split < kMaxSplit && most * split * 2 <= sms && split * 2 <= p.kb) split *= 2;
+    while (split < (most <= 8 ? 8 : 4) && most * split * 2 <= sms && split * 2 <= p.kb) split *= 2;
     const size_t rest = 1024 + (S::kSumFloats + S::kRingFloats) * sizeof(float) + (p.groups + 1) * sizeof(int) +
                         (p.offsets && p.groups <= kSharedOffsets ? (p.groups + 1) * sizeof(int32_t) : 0);
     constexpr size_t kMost = 227 * 1024 - 4096;   // less the static part
@@ -833,15 +838,19 @@ cudaError_t launch_product_few(const MatmulArgs& p, const CUtensorMap& ma, const
     return cudaLaunchKernelEx(&cfg, kernel, p, ma, mb, stages, split);
 }
 
-// Rows of a tile of the kernel for few rows, from the mean rows of a group, or 0 for the other kernel.
-int few_rows_tile(const MatmulArgs& p, int sms)
+// Rows of a tile of the kernel for few rows, or 0 for the kernel of 128-row tiles.  Measured, us, few rows
+// against 128-row tiles, at 7168 x 4096 with SwiGLU:
+//   one group     1 row 9.2 : 24.2   32 rows 11.4 : 24.2   64 rows 13.4 : 24.5   100 rows 18.8 : 24.7
+//   32 groups     of 8 rows 145 : 152   of 16 rows 152 : 153   of 24 rows 167 : 153
+// One group has only col_tiles tiles of 128 rows, which leave most SMs idle; several groups have enough of
+// them, and a group whose rows pass the tile reads its weights twice.  Two tiles of 16 rows or 32 run side
+// by side and finish before one of twice the rows.
+int few_rows_tile(const MatmulArgs& p)
 {
-    (void)sms;
-    const int64_t groups = p.groups < p.rows ? p.groups : p.rows;
-    const int64_t mean = p.rows / (groups > 0 ? groups : 1);
-    const char* f = getenv("FEW");
-    if (f) return atoi(f);
-    return mean <= 10 ? 16 : mean <= 24 ? 32 : mean <= 64 ? 64 : 0;
+    if (p.groups == 1) return p.rows <= 32 ? 16 : p.rows <= 64 ? 32 : p.rows <= 128 ? 64 : 0;
+    const int64_t groups = p.groups < p.rows ? p.groups : p.rows;   // that can hold a row
+    const int64_t mean = p.rows / groups;
+    return mean <= 8 ? 16 : mean <= 16 ? 32 : 0;
 }
 
 }  // namespace
@@ -886,7 +895,7 @@ extern "C" int ep_matmul_fp8(const void* a, const float* a_scales, const void* b
     const int sms = layer_num_sms();
     if (sms == 0) return layer_fail(EP_ERR_CUDA, "%s: cannot tell the current device's multiprocessors", who);
     // rows of a tile of the kernel for few rows, or 0 for the kernel of 128-row tiles
-    const int few = few_rows_tile(p, sms);
+    const int few = few_rows_tile(p);
     CUtensorMap ma, mb;
     if (int rc = make_map(&ma, "a", a, rows, inner, few ? few : kTileRows)) return rc;
     if (int rc = make_map(&mb, "b", b, (int64_t)groups * columns, inner, 128)) return rc;
