@@ -1,13 +1,15 @@
 """Build libep.so (the CUDA dispatch / combine library) in-tree with nvcc for sm_103a.
 
 Each .cu file compiles in its own nvcc process (in parallel), then one shared link.  The
-library links the shared CUDA runtime so it shares the process's runtime with PyTorch.
+library links the shared CUDA runtime so it shares the process's runtime with PyTorch.  The
+native half of the Python binding, _ep_binding.so, compiles beside them with g++.
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +20,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libep.so")
 SOURCES = ("ep_api.cu", "ep_route.cu", "ep_scatter.cu", "ep_combine.cu", "ep_noalloc.cu",
            "ep_fp8wire.cu", "ep_grouped.cu", "ep_norm.cu", "ep_sort.cu", "ep_matmul.cu")
+BINDING = os.path.join(PKG, "_ep_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -28,20 +31,40 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libep.so")
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB):
+def _stale(lib: str = LIB) -> bool:
+    if not os.path.exists(lib):
         return True
-    t = os.path.getmtime(LIB)
+    t = os.path.getmtime(lib)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + \
            [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] + [__file__]
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def build_binding() -> None:
+    """Compile csrc/ep_binding.cpp against the installed PyTorch; it calls libep.so through addresses it
+    is given, so it links nothing of it."""
+    import torch
+    home = os.path.dirname(torch.__file__)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-isystem", os.path.join(home, "include"),
+           "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "ep_binding.cpp"), "-o", tmp, "-L", os.path.join(home, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on ep_binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
           defines=(), lib_path: str = LIB, build_dir: str = BUILD_DIR) -> str:
     """Compile libep.so; `defines` (e.g. ["EP_COMBINE_STAGES=4"]) and a separate lib_path /
     build_dir let a caller build tuning variants side by side."""
-    if not force and lib_path == LIB and not defines and not _stale():
+    product = lib_path == LIB and not defines
+    if not force and product and not _stale() and not _stale(BINDING):
         return LIB
     os.makedirs(build_dir, exist_ok=True)
     cc = nvcc()
@@ -60,8 +83,11 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
             print(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(build_binding) if product else None
         objs = list(ex.map(compile_one, SOURCES))
+        if binding:
+            binding.result()
     tmp = lib_path + f".tmp{os.getpid()}"
     cmd = [cc, "-shared", *ARCH, "-cudart", "shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -10,20 +10,48 @@ Every call runs on the device of its first tensor, enqueues on the current strea
 returns without waiting.  Outputs and workspaces come from PyTorch's allocator on that stream.
 Arguments are checked before any launch (``EpError`` with ``EP_ERR_ARG``); what only the device can
 see is recorded in one status word per device, read and cleared by ``op_status``.
+
+The checks and allocations are native (``_ep_binding``, csrc/ep_binding.cpp): these calls are often one
+token's, and marshalling in Python would take longer than the kernels.
 """
 from __future__ import annotations
 
-import contextlib
+import ctypes
 import dataclasses
-from typing import Optional, Tuple
+import importlib.util
+import os
+from typing import Optional
 
 import torch
 
-from . import EP_BF16, EP_ERR_ARG, EP_FP16, EP_FP8_E4M3, EpError, _check, load_library
+from . import EP_BF16, EP_ERR_ARG, EP_FP16, EP_FP8_E4M3, EpError, _PKG, load_library
 
-_HALF_CODES = {torch.bfloat16: EP_BF16, torch.float16: EP_FP16}
-_OUT_TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
+BINDING_PATH = os.path.join(_PKG, "_ep_binding.so")
+_OUT_CODES = {"bf16": EP_BF16, "fp16": EP_FP16}
+# the C ABI functions the binding calls, in the order of its bind()
+_BOUND = ("ep_rms_norm_fp8", "ep_sort_workspace_bytes", "ep_sort_by_expert", "ep_sorted_rows", "ep_return_rows",
+          "ep_return_rows_backward", "ep_matmul_fp8", "ep_strerror", "ep_last_error")
 _status_words = {}
+_binding = None
+_bound_to = None
+
+
+def _native():
+    """The native binding, calling whichever build of libep.so the package has loaded."""
+    global _binding, _bound_to
+    lib = load_library()
+    if lib is not _bound_to:
+        if _binding is None:
+            if not os.path.exists(BINDING_PATH):
+                raise RuntimeError(f"_ep_binding.so not found at {BINDING_PATH}: build it with "
+                                   "combine_ep_dispatch_02_gb300.build.build()")
+            spec = importlib.util.spec_from_file_location("_ep_binding", BINDING_PATH)
+            _binding = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(_binding)
+        _binding.bind(EpError, _status_address,
+                      *(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _BOUND))
+        _bound_to = lib
+    return _binding
 
 
 @dataclasses.dataclass
@@ -35,29 +63,6 @@ class ExpertOrder:
     counts: Optional[torch.Tensor] = None    # [W] int32: rows held by each rank (None: all of them)
 
 
-def _bad(msg: str):
-    raise EpError(EP_ERR_ARG, msg)
-
-
-def _arg(t: torch.Tensor, what: str, dtype, shape, device) -> int:
-    """Address of a tensor that has to be contiguous, of this type and shape, on this device."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device:
-        return t.data_ptr()
-    if t.device != device:
-        _bad(f"{what} is on {t.device}, the call runs on {device}")
-    if t.dtype != dtype:
-        _bad(f"{what} is {t.dtype}, the call takes {dtype}")
-    if tuple(t.shape) != tuple(shape):
-        _bad(f"{what} has shape {tuple(t.shape)}, the call takes {tuple(shape)}")
-    _bad(f"{what} is not contiguous")
-
-
-def _device(t: torch.Tensor, what: str) -> torch.device:
-    if not t.is_cuda:
-        _bad(f"{what} is on {t.device}, not a CUDA device")
-    return t.device
-
-
 def _status_word(device: torch.device) -> torch.Tensor:
     w = _status_words.get(device.index)
     if w is None:
@@ -66,6 +71,10 @@ def _status_word(device: torch.device) -> torch.Tensor:
             torch.cuda.synchronize(device)   # other streams may be the first to use it
         _status_words[device.index] = w
     return w
+
+
+def _status_address(index: int) -> int:
+    return _status_word(torch.device("cuda", index)).data_ptr()
 
 
 def op_status(device=None) -> int:
@@ -83,33 +92,12 @@ def op_status(device=None) -> int:
     return v
 
 
-@contextlib.contextmanager
-def _other_place(device, stream):
-    with torch.cuda.device(device):
-        if stream is None:
-            yield
-        else:
-            with torch.cuda.stream(stream):
-                yield
-
-
-_here = contextlib.nullcontext()
-
-
-def _place(device: torch.device, stream):
-    """Context in which outputs are allocated and the call is enqueued: the tensors' device and the
-    caller's stream, so that the allocator ties the memory to the stream that uses it."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return _here
-    return _other_place(device, stream)
-
-
-# the current stream's handle without building a torch.cuda.Stream around it: 2 us less per call
-_current_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _raw_stream(device: torch.device) -> int:
-    return _current_raw_stream(device.index)
+def _on(stream, call, *args):
+    """The call on the current stream, or on the caller's, where its outputs are then allocated too."""
+    if stream is None:
+        return call(*args)
+    with torch.cuda.stream(stream):
+        return call(*args)
 
 
 def rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -119,41 +107,7 @@ def rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
     BF16 or FP16, hidden a multiple of 16, rows any multiple of 8 elements apart; weight [hidden] of
     x's type or FP32.  Returns (q [rows][hidden] float8_e4m3fn, scales [rows][ceil(hidden/128)],
     h [rows][hidden] or None without a residual, y [rows][hidden] or None unless want_y)."""
-    dev = _device(x, "x")
-    code = _HALF_CODES.get(x.dtype)
-    if code is None:
-        _bad(f"x is {x.dtype}, the call takes bfloat16 or float16")
-    if x.dim() != 2:
-        _bad(f"x has {x.dim()} dimensions, the call takes [rows][hidden]")
-    rows, hidden = x.shape
-    if x.stride(1) != 1 and hidden > 1:
-        _bad("x: the elements of a row are not consecutive")
-    rp, rs = None, 0
-    if residual is not None:
-        if residual.device != dev or residual.dtype != x.dtype or residual.shape != x.shape:
-            _bad(f"residual is {residual.dtype} {tuple(residual.shape)} on {residual.device}, x is {x.dtype} "
-                 f"{tuple(x.shape)} on {dev}")
-        if residual.stride(1) != 1 and hidden > 1:
-            _bad("residual: the elements of a row are not consecutive")
-        rp, rs = residual.data_ptr(), residual.stride(0) if rows > 1 else hidden
-    if weight.dtype != x.dtype and weight.dtype != torch.float32:
-        _bad(f"weight is {weight.dtype}, the call takes {x.dtype} or float32")
-    wp = _arg(weight, "weight", weight.dtype, (hidden,), dev)
-    with _place(dev, stream):
-        q = torch.empty((rows, hidden), dtype=torch.float8_e4m3fn, device=dev)
-        scales = torch.empty((rows, -(-hidden // 128)), dtype=torch.float32, device=dev)
-        h = torch.empty((rows, hidden), dtype=x.dtype, device=dev) if residual is not None else None
-        y = torch.empty((rows, hidden), dtype=x.dtype, device=dev) if want_y else None
-        _check(load_library().ep_rms_norm_fp8(
-            x.data_ptr(), x.stride(0) if rows > 1 else hidden, rp, rs, wp, weight.dtype == torch.float32, code, rows,
-            hidden, eps, q.data_ptr(), scales.data_ptr(), h.data_ptr() if h is not None else None,
-            y.data_ptr() if y is not None else None, _raw_stream(dev)))
-    return q, scales, h, y
-
-
-def _rows_shape(shape) -> Tuple[int, int]:
-    """(W, rows per rank) of the leading dimensions [rows] or [W][rows]."""
-    return (1, shape[0]) if len(shape) == 1 else (shape[0], shape[1])
+    return _on(stream, _native().rms_norm_fp8, x, weight, residual, eps, want_y)
 
 
 def sort_by_expert(indices: torch.Tensor, experts: int, max_rows: Optional[int] = None,
@@ -163,69 +117,14 @@ def sort_by_expert(indices: torch.Tensor, experts: int, max_rows: Optional[int] 
     (r + 1) * experts - 1); other ids, -1 among them, are left out.  counts [W] int32 on the device: rows
     held by each rank (``Dispatched.recv_count``).  max_rows bounds the sorted rows (default: every
     pair); pairs past it are left out and recorded (``op_status``)."""
-    dev = _device(indices, "indices")
-    if indices.dim() not in (2, 3):
-        _bad(f"indices has {indices.dim()} dimensions, the call takes [rows][k] or [W][rows][k]")
-    W, rows = _rows_shape(indices.shape[:-1])
-    k = indices.shape[-1]
-    ip = _arg(indices, "indices", torch.int32, indices.shape, dev)
-    cp = None if counts is None else _arg(counts, "counts", torch.int32, (W,), dev)
-    if max_rows is None:
-        max_rows = W * rows * k
-    if max_rows < 0:
-        _bad(f"max_rows={max_rows} < 0")
-    lib = load_library()
-    status = _status_word(dev)
-    with _place(dev, stream):
-        need = lib.ep_sort_workspace_bytes(W, rows, k, experts)
-        work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        offsets = torch.empty(max(0, W * experts) + 1, dtype=torch.int32, device=dev)
-        pos = torch.empty_like(indices)
-        src = torch.empty(max_rows, dtype=torch.int32, device=dev)
-        _check(lib.ep_sort_by_expert(ip, cp, W, rows, k, experts, max_rows, offsets.data_ptr(), pos.data_ptr(),
-                                     src.data_ptr(), work.data_ptr() if need else None, need, status.data_ptr(),
-                                     _raw_stream(dev)))
-    return ExpertOrder(offsets, pos, src, counts)
-
-
-def _order_args(order: ExpertOrder, lead, dev):
-    """(W, rows, k, max_rows, pos, counts) of an order whose pairs belong to rows of shape ``lead``."""
-    if order.pos.dim() not in (2, 3) or tuple(order.pos.shape[:-1]) != tuple(lead):
-        _bad(f"order.pos has shape {tuple(order.pos.shape)}, the rows are {tuple(lead)}")
-    W, rows = _rows_shape(lead)
-    pp = _arg(order.pos, "order.pos", torch.int32, order.pos.shape, dev)
-    cp = None if order.counts is None else _arg(order.counts, "order.counts", torch.int32, (W,), dev)
-    return W, rows, order.pos.shape[-1], order.src.shape[0], pp, cp
+    return ExpertOrder(*_on(stream, _native().sort_by_expert, indices, experts, max_rows, counts), counts)
 
 
 def sorted_rows(order: ExpertOrder, x: torch.Tensor, scales: Optional[torch.Tensor] = None, stream=None):
     """x [rows][hidden] (or [W][rows][hidden]) in expert order: (x_sorted [max_rows][hidden], scales_sorted
     [max_rows][scale_dim] or None).  Any element type whose rows are a multiple of 16 bytes; scales
     FP32.  Rows past order.offsets[-1] hold unspecified data."""
-    dev = _device(x, "x")
-    lead = x.shape[:-1]
-    W, rows, k, max_rows, pp, cp = _order_args(order, lead, dev)
-    xp = _arg(x, "x", x.dtype, x.shape, dev)
-    sd, sp = 0, None
-    if scales is not None:
-        sd = scales.shape[-1]
-        sp = _arg(scales, "scales", torch.float32, (*lead, sd), dev)
-    status = _status_word(dev)
-    with _place(dev, stream):
-        out = torch.empty((max_rows, x.shape[-1]), dtype=x.dtype, device=dev)
-        out_s = torch.empty((max_rows, sd), dtype=torch.float32, device=dev) if scales is not None else None
-        _check(load_library().ep_sorted_rows(
-            xp, sp, pp, cp, W, rows, k, max_rows, x.shape[-1] * x.element_size(), sd, out.data_ptr(),
-            out_s.data_ptr() if sd else None, status.data_ptr(), _raw_stream(dev)))
-    return out, out_s
-
-
-def _sorted_arg(order, y, what, dev):
-    if y.dtype not in _HALF_CODES:
-        _bad(f"{what} is {y.dtype}, the call takes bfloat16 or float16")
-    if y.dim() != 2:
-        _bad(f"{what} has {y.dim()} dimensions, the call takes [max_rows][hidden]")
-    return _arg(y, what, y.dtype, (order.src.shape[0], y.shape[1]), dev), _HALF_CODES[y.dtype]
+    return _on(stream, _native().sorted_rows, order.pos, order.src, order.counts, x, scales)
 
 
 def return_rows(order: ExpertOrder, y: torch.Tensor, weights: Optional[torch.Tensor] = None,
@@ -233,17 +132,7 @@ def return_rows(order: ExpertOrder, y: torch.Tensor, weights: Optional[torch.Ten
     """Rows back from expert order: out[row] = sum over the row's slots, ascending, of weight * y[pos],
     in FP32, rounded once.  y [max_rows][hidden] BF16 or FP16; weights of order.pos's shape, FP32 (None:
     ones).  A row without a sorted slot becomes zeros; rows past order.counts are not written."""
-    dev = _device(y, "y")
-    yp, code = _sorted_arg(order, y, "y", dev)
-    lead = order.pos.shape[:-1]
-    W, rows, k, max_rows, pp, cp = _order_args(order, lead, dev)
-    wp = None if weights is None else _arg(weights, "weights", torch.float32, order.pos.shape, dev)
-    status = _status_word(dev)
-    with _place(dev, stream):
-        out = torch.empty((*lead, y.shape[1]), dtype=y.dtype, device=dev)
-        _check(load_library().ep_return_rows(yp, wp, pp, cp, W, rows, k, max_rows, y.shape[1], code, out.data_ptr(),
-                                             status.data_ptr(), _raw_stream(dev)))
-    return out
+    return _on(stream, _native().return_rows, order.pos, order.src, order.counts, y, weights)
 
 
 def sorted_rows_backward(order: ExpertOrder, dx_sorted: torch.Tensor, stream=None) -> torch.Tensor:
@@ -255,38 +144,7 @@ def return_rows_backward(order: ExpertOrder, y: torch.Tensor, weights: torch.Ten
     """Gradients of return_rows: (dy [max_rows][hidden] = weight * dout[row], rounded once; dweights of
     weights' shape = <y[pos], dout[row]> in FP32, 0 where a slot has no sorted row).  Rows of dy past
     order.offsets[-1], and dweights of rows past order.counts, hold unspecified data."""
-    dev = _device(y, "y")
-    yp, code = _sorted_arg(order, y, "y", dev)
-    lead = order.pos.shape[:-1]
-    W, rows, k, max_rows, pp, cp = _order_args(order, lead, dev)
-    wp = _arg(weights, "weights", torch.float32, order.pos.shape, dev)
-    dp = _arg(dout, "dout", y.dtype, (*lead, y.shape[1]), dev)
-    status = _status_word(dev)
-    with _place(dev, stream):
-        dy = torch.empty_like(y)
-        dw = torch.empty_like(weights)
-        _check(load_library().ep_return_rows_backward(
-            yp, wp, dp, pp, cp, W, rows, k, max_rows, y.shape[1], code, dy.data_ptr(), dw.data_ptr(),
-            status.data_ptr(), _raw_stream(dev)))
-    return dy, dw
-
-
-def _product_args(a, a_scales, b, b_scales, offsets):
-    dev = _device(a, "a")
-    f8, f32 = torch.float8_e4m3fn, torch.float32
-    if a.dim() != 2:
-        _bad(f"a has {a.dim()} dimensions, the call takes [rows][inner]")
-    rows, inner = a.shape
-    if b.dim() != (2 if offsets is None else 3) or b.shape[-1] != inner:
-        _bad(f"b has shape {tuple(b.shape)}, the call takes "
-             f"{'[columns]' if offsets is None else '[groups][columns]'}[{inner}]")
-    groups = 1 if offsets is None else b.shape[0]
-    columns, kb = b.shape[-2], -(-inner // 128)
-    scale_shape = (-(-columns // 128), kb) if offsets is None else (groups, -(-columns // 128), kb)
-    args = (_arg(a, "a", f8, a.shape, dev), _arg(a_scales, "a_scales", f32, (rows, kb), dev),
-            _arg(b, "b", f8, b.shape, dev), _arg(b_scales, "b_scales", f32, scale_shape, dev),
-            None if offsets is None else _arg(offsets, "offsets", torch.int32, (groups + 1,), dev))
-    return dev, args, rows, groups, columns, inner
+    return _on(stream, _native().return_rows_backward, order.pos, order.src, order.counts, y, weights, dout)
 
 
 def matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
@@ -296,16 +154,10 @@ def matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scale
     [ceil(columns/128)][ceil(inner/128)].  With offsets [groups + 1] int32 on the device, b and b_scales
     have a leading [groups] and rows offsets[g] .. offsets[g + 1] - 1 take b[g]; rows outside every group
     are not written.  inner must be a multiple of 16."""
-    dev, args, rows, groups, columns, inner = _product_args(a, a_scales, b, b_scales, offsets)
-    t = _OUT_TYPES.get(out_dtype)
-    if t is None:
-        _bad(f"out_dtype={out_dtype!r} is neither 'bf16' nor 'fp16'")
-    status = _status_word(dev)
-    with _place(dev, stream):
-        out = torch.empty((rows, columns), dtype=t, device=dev)
-        _check(load_library().ep_matmul_fp8(*args, rows, groups, columns, inner, 0, _HALF_CODES[t], out.data_ptr(),
-                                            None, status.data_ptr(), _raw_stream(dev)))
-    return out
+    code = _OUT_CODES.get(out_dtype)
+    if code is None:
+        raise EpError(EP_ERR_ARG, f"out_dtype={out_dtype!r} is neither 'bf16' nor 'fp16'")
+    return _on(stream, _native().matmul_fp8, a, a_scales, b, b_scales, offsets, code)
 
 
 def matmul_fp8_swiglu(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
@@ -314,11 +166,4 @@ def matmul_fp8_swiglu(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, 
     projection; z = gate * sigmoid(gate) * up in FP32.  Returns (q [rows][columns/2] float8_e4m3fn,
     scales [rows][ceil(columns/256)]), the a and a_scales of a following matmul_fp8.  Arguments as
     matmul_fp8; columns must be a multiple of 32."""
-    dev, args, rows, groups, columns, inner = _product_args(a, a_scales, b, b_scales, offsets)
-    status = _status_word(dev)
-    with _place(dev, stream):
-        q = torch.empty((rows, columns // 2), dtype=torch.float8_e4m3fn, device=dev)
-        scales = torch.empty((rows, -(-(columns // 2) // 128)), dtype=torch.float32, device=dev)
-        _check(load_library().ep_matmul_fp8(*args, rows, groups, columns, inner, 1, EP_FP8_E4M3, q.data_ptr(),
-                                            scales.data_ptr(), status.data_ptr(), _raw_stream(dev)))
-    return q, scales
+    return _on(stream, _native().matmul_fp8, a, a_scales, b, b_scales, offsets, EP_FP8_E4M3)

@@ -475,6 +475,60 @@ def test_product_is_deterministic(rows):
         assert torch.equal(one, ep.matmul_fp8(a, sa, b, sb, offsets=offsets))
 
 
+# ------------------------------------------------------------------------------------------- refusals
+
+def _zeros(shape, dtype):
+    t = torch.zeros(shape, dtype=torch.uint8 if dtype == F8 else dtype, device=DEV)
+    return t.view(F8) if dtype == F8 else t
+
+
+def test_binding_names_the_argument_at_fault():
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    x = _zeros((4, 256), bf)
+    order = ep.ExpertOrder(_zeros((5,), i32), _zeros((4, 2), i32), _zeros((8,), i32))
+    y, w = _zeros((8, 256), bf), _zeros((4, 2), f32)
+    a, sa, b, sb = _zeros((4, 128), F8), _zeros((4, 1), f32), _zeros((64, 128), F8), _zeros((1, 1), f32)
+    many = (_zeros((3, 64, 128), F8), _zeros((3, 1, 1), f32))
+    cases = [
+        (lambda: ep.rms_norm_fp8(_zeros((4, 256), f32), _zeros((256,), f32)), "x is Float"),
+        (lambda: ep.rms_norm_fp8(x[0], x[0]), "x has 1 dimensions"),
+        (lambda: ep.rms_norm_fp8(x.t(), _zeros((4,), bf)), "not consecutive"),
+        (lambda: ep.rms_norm_fp8(x, _zeros((128,), bf)), "weight has shape"),
+        (lambda: ep.rms_norm_fp8(x, _zeros((256,), torch.float16)), "weight is Half"),
+        (lambda: ep.rms_norm_fp8(x, x[0], residual=_zeros((4, 128), bf)), "residual is"),
+        (lambda: ep.rms_norm_fp8(x[:, :24].contiguous(), x[0, :24].contiguous()), "hidden=24"),
+        (lambda: ep.rms_norm_fp8(x[:, 4:132], x[0, :128].contiguous()), "16-byte aligned"),
+        (lambda: ep.sort_by_expert(_zeros((4, 2), torch.int64), 4), "indices is Long"),
+        (lambda: ep.sort_by_expert(_zeros((4,), i32), 4), "indices has 1 dimensions"),
+        (lambda: ep.sort_by_expert(_zeros((2, 4, 2), i32), 4, counts=_zeros((3,), i32)), "counts has shape"),
+        (lambda: ep.sort_by_expert(_zeros((4, 2), i32), 0), "experts_per_rank"),
+        (lambda: ep.sort_by_expert(_zeros((4, 2), i32), 5000), "experts_per_rank"),
+        (lambda: ep.sort_by_expert(_zeros((4, 2), i32), 4, max_rows=-1), "max_rows"),
+        (lambda: ep.sort_by_expert(_zeros((4, 65), i32), 4), "topk=65"),
+        (lambda: ep.sort_by_expert(_zeros((4, 2), i32)[:, :1], 4), "indices is not contiguous"),
+        (lambda: ep.sorted_rows(order, _zeros((5, 256), bf)), "order.pos has shape"),
+        (lambda: ep.sorted_rows(order, _zeros((4, 12), bf)), "row of 24 bytes"),
+        (lambda: ep.sorted_rows(order, x, _zeros((4, 2), bf)), "scales is BFloat16"),
+        (lambda: ep.return_rows(order, x), "y has shape"),
+        (lambda: ep.return_rows(order, y, _zeros((4, 3), f32)), "weights has shape"),
+        (lambda: ep.return_rows(order, y.float()), "y is Float"),
+        (lambda: ep.return_rows_backward(order, y, None, x), "weights is a NoneType"),
+        (lambda: ep.return_rows_backward(order, y, w, x.half()), "dout is Half"),
+        (lambda: ep.matmul_fp8(a, sa, _zeros((64, 256), F8), sb), "b has shape"),
+        (lambda: ep.matmul_fp8(a, sa, b, _zeros((2, 1), f32)), "b_scales has shape"),
+        (lambda: ep.matmul_fp8(a, _zeros((4, 2), f32), b, sb), "a_scales has shape"),
+        (lambda: ep.matmul_fp8(a, sa, *many, offsets=_zeros((3,), i32)), "offsets has shape"),
+        (lambda: ep.matmul_fp8(a, sa, *many), "b has shape"),
+        (lambda: ep.matmul_fp8(a.view(torch.uint8), sa, b, sb), "a is Byte"),
+        (lambda: ep.matmul_fp8_swiglu(a, sa, _zeros((48, 128), F8), sb), "columns=48"),
+        (lambda: ep.matmul_fp8(a, sa, b.cpu(), sb), "b is on cpu"),
+    ]
+    for call, words in cases:
+        with pytest.raises(ep.EpError) as e:
+            call()
+        assert e.value.code == ep.EP_ERR_ARG and words in str(e.value), (words, str(e.value))
+
+
 # ------------------------------------------------------------------------------------------- together
 
 def test_dispatched_rows_through_the_experts():
