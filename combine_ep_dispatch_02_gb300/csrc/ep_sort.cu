@@ -6,8 +6,9 @@
 //   offsets[g]  sorted rows below group g            pos[pair]  the pair's sorted row, or -1
 //   src[i]      the pair of sorted row i, -1 past offsets[groups]
 //
-// Sorting indices takes one CTA up to kSortSmallPairs pairs.  Above that, tiles of kSortTile pairs
-// are counted, one CTA scans the counts (groups x tiles), and the tiles place their pairs.
+// Sorting indices takes one CTA up to kSortSmallPairs pairs.  Above that, tiles of 2048 pairs are counted
+// in one launch and placed in a second, whose CTAs each add up the counts of the tiles; above 64 tiles,
+// tiles of 8192 pairs, and one CTA scans the counts (groups x tiles) in a launch between the two.
 // Within a warp, __match_any_sync gives a pair's rank among equal groups; a warp's running counts
 // live in shared memory, so no step has an order that atomics could change.
 #include "ep_layer.cuh"
@@ -16,10 +17,11 @@ namespace ep {
 namespace {
 
 constexpr int kSortMaxGroups = 4096;
-constexpr int kSortTile = 2048;              // pairs of a tile: 8 warps x 8 steps of 32
 constexpr int kSortTileThreads = 256;
+constexpr int kSortSteps = 8, kSortLongSteps = 32;   // steps of 256 pairs of a tile
+constexpr int kSortShortTiles = 64;          // tiles of kSortSteps, at most; more pairs make longer tiles
 constexpr int kSortSmallThreads = 512;       // one CTA for the whole sort
-constexpr int kSortSmallSteps = 16;
+constexpr int kSortSmallSteps = 4;           // a step is 0.7 us in one CTA; the two launches take 6 to 9 us
 constexpr int kSortSmallPairs = kSortSmallThreads * kSortSmallSteps;
 constexpr int kSortSmallGroups = 2048;       // 16 warps' counts in 128 KB of shared memory
 
@@ -142,13 +144,14 @@ __global__ void __launch_bounds__(kSortSmallThreads) ep_sort_small_kernel(const 
     for (int64_t i = carry + threadIdx.x; i < a.max_rows; i += blockDim.x) a.src[i] = -1;
 }
 
-__global__ void __launch_bounds__(kSortTileThreads) ep_sort_count_kernel(const SortArgs a)
+__global__ void __launch_bounds__(kSortTileThreads) ep_sort_count_kernel(const SortArgs a, int tile_pairs)
 {
     extern __shared__ int counts[];   // [groups]
     for (int i = threadIdx.x; i < a.groups; i += blockDim.x) counts[i] = 0;
     __syncthreads();
-    const int64_t first = (int64_t)blockIdx.x * kSortTile;
-    for (int i = threadIdx.x; i < kSortTile; i += blockDim.x) {
+    const int64_t first = (int64_t)blockIdx.x * tile_pairs;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < tile_pairs; i += kSortTileThreads) {
         const int g = pair_group(a, first + i);
         if (g >= 0) atomicAdd(&counts[g], 1);   // whole numbers: the order does not matter
     }
@@ -209,14 +212,18 @@ __global__ void __launch_bounds__(kScanThreads) ep_sort_scan_kernel(const SortAr
     allow_dependents();
 }
 
+// SCANNED: tile_counts holds first positions and offsets is written; else tile_counts holds counts, and each
+// CTA adds them up for itself.
+template <int kSteps, bool SCANNED>
 __global__ void __launch_bounds__(kSortTileThreads) ep_sort_place_kernel(const SortArgs a)
 {
     extern __shared__ int counts[];   // [warps][groups]
-    constexpr int kWarps = kSortTileThreads / 32, kSteps = kSortTile / kSortTileThreads;
+    __shared__ int warp_sums[32];
+    constexpr int kWarps = kSortTileThreads / 32;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     for (int i = threadIdx.x; i < kWarps * a.groups; i += blockDim.x) counts[i] = 0;
     __syncthreads();
-    const int64_t first = (int64_t)blockIdx.x * kSortTile + w * kSteps * 32;
+    const int64_t first = ((int64_t)blockIdx.x * kWarps + w) * kSteps * 32;
     int g[kSteps], at[kSteps];
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) g[i] = pair_group(a, first + 32 * i + lane);
@@ -224,21 +231,43 @@ __global__ void __launch_bounds__(kSortTileThreads) ep_sort_place_kernel(const S
     for (int i = 0; i < kSteps; ++i) at[i] = warp_rank(g[i], counts + w * a.groups, lane);
     __syncthreads();
     wait_for_predecessor();
-    for (int e = threadIdx.x; e < a.groups; e += blockDim.x) {
-        int base = a.tile_counts[(int64_t)blockIdx.x * a.groups + e];
-        for (int v = 0; v < kWarps; ++v) {
-            const int c = counts[v * a.groups + e];
-            counts[v * a.groups + e] = base;
-            base += c;
+    int carry = 0;
+    for (int e0 = 0; e0 < a.groups; e0 += kSortTileThreads) {
+        const int e = e0 + threadIdx.x;
+        int base = 0;
+        if constexpr (SCANNED) {
+            if (e < a.groups) base = a.tile_counts[(int64_t)blockIdx.x * a.groups + e];
+        } else {
+            int all = 0, before = 0;
+            if (e < a.groups) {
+#pragma unroll 16
+                for (int t = 0; t < a.tiles; ++t) {
+                    const int c = a.tile_counts[(int64_t)t * a.groups + e];
+                    all += c;
+                    before += t < (int)blockIdx.x ? c : 0;
+                }
+            }
+            int total;
+            base = carry + cta_exclusive_scan(all, warp_sums, total);
+            if (blockIdx.x == 0 && e < a.groups) a.offsets[e] = clamp_rows(a, base);
+            base += before;
+            carry += total;
         }
+        if (e < a.groups)
+            for (int v = 0; v < kWarps; ++v) {
+                const int c = counts[v * a.groups + e];
+                counts[v * a.groups + e] = base;
+                base += c;
+            }
     }
+    if constexpr (SCANNED) carry = a.offsets[a.groups];
+    else if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[a.groups] = clamp_rows(a, carry);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kSteps; ++i)
         place_pair(a, first + 32 * i + lane, g[i], g[i] >= 0 ? counts[w * a.groups + g[i]] + at[i] : -1);
     const int64_t step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = a.offsets[a.groups] + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < a.max_rows; i += step)
-        a.src[i] = -1;
+    for (int64_t i = carry + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < a.max_rows; i += step) a.src[i] = -1;
 }
 
 // ---------------------------------------------------------------- rows to expert order and back
@@ -258,7 +287,7 @@ struct RowsArgs {
     int64_t rows, rows_per_rank, max_rows;
     int64_t row_bytes;
     int k, sd, vecs;          // vecs: 16-byte vectors of a row
-    int slices;               // warps a row is split over
+    int slices, slice_vecs;   // warps a row is split over, vectors each takes
 };
 
 __device__ __forceinline__ bool row_present(const RowsArgs& a, int64_t row)
@@ -279,7 +308,8 @@ __device__ __forceinline__ int64_t checked_pos(const RowsArgs& a, int64_t pair)
 }
 
 constexpr int kRowThreads = 256;
-constexpr int kRowVecs = 4;   // vectors of a lane's slice: a warp's unit is 2 KB of a row
+constexpr int kWarpRowVecs = 128;   // a row's gradient is one warp's up to this many vectors
+constexpr int kRowVecs = 4;   // vectors of a lane's slice at most: 2 KB of a row to a warp
 
 // x rows to their sorted rows: each row is read once and written to each of its pairs.
 __global__ void __launch_bounds__(kRowThreads) ep_sorted_rows_kernel(const RowsArgs a)
@@ -291,10 +321,10 @@ __global__ void __launch_bounds__(kRowThreads) ep_sorted_rows_kernel(const RowsA
     if (!row_present(a, row)) return;
     const uint8_t* x = a.in + row * a.row_bytes;
     uint4 v[kRowVecs];
-    const int v0 = slice * 32 * kRowVecs + lane;
+    const int v0 = slice * a.slice_vecs + lane, v1 = min(a.vecs, (slice + 1) * a.slice_vecs);
 #pragma unroll
     for (int i = 0; i < kRowVecs; ++i)
-        if (v0 + 32 * i < a.vecs) v[i] = ld_stream_v4(x + 16 * (int64_t)(v0 + 32 * i));
+        if (v0 + 32 * i < v1) v[i] = ld_stream_v4(x + 16 * (int64_t)(v0 + 32 * i));
     for (int jb = 0; jb < a.k; jb += 32) {
         const int64_t mine = jb + lane < a.k ? checked_pos(a, row * a.k + jb + lane) : -1;
         for (int j = 0; j < min(32, a.k - jb); ++j) {
@@ -303,41 +333,101 @@ __global__ void __launch_bounds__(kRowThreads) ep_sorted_rows_kernel(const RowsA
             uint8_t* out = a.out + to * a.row_bytes;
 #pragma unroll
             for (int i = 0; i < kRowVecs; ++i)
-                if (v0 + 32 * i < a.vecs) st_v4(out + 16 * (int64_t)(v0 + 32 * i), v[i]);
+                if (v0 + 32 * i < v1) st_v4(out + 16 * (int64_t)(v0 + 32 * i), v[i]);
             if (slice == 0)
                 for (int i = lane; i < a.sd; i += 32) a.out_scales[to * a.sd + i] = a.in_scales[row * a.sd + i];
         }
     }
 }
 
-// out[row] = round(sum over slots, ascending, of weight * y[pos]); FP32 sums.
-template <bool FP16>
-__global__ void __launch_bounds__(kRowThreads) ep_return_rows_kernel(const RowsArgs a)
+// out[row] = round(sum over slots, ascending, of weight * y[pos]); FP32 sums.  A warp takes a.slice_vecs
+// vectors of a row.  Reading HBM at full rate takes about 100 KB on their way to each SM: a lane loads
+// the next vector of up to kSlots rows before it adds the current ones, so 16 warps keep up to 128 KB
+// in flight without a gap.
+template <bool FP16, int kSlots>
+__global__ void __launch_bounds__(kRowThreads, 2) ep_return_rows_kernel(const RowsArgs a)
 {
     const int lane = threadIdx.x & 31;
     const int64_t unit = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
     const int64_t row = unit / a.slices;
     const int slice = (int)(unit - row * a.slices);
     if (!row_present(a, row)) return;
-    constexpr int kStep = 4;   // rows loaded together
-    const int v1 = min(a.vecs, (slice + 1) * 32 * kRowVecs);
-    for (int v = slice * 32 * kRowVecs + lane; v - lane < v1; v += 32) {
-        float acc[8] = {};
-        for (int jb = 0; jb < a.k; jb += kStep) {
-            uint4 y[kStep];
-            float w[kStep];
+    int mine = -1;
+    float weight = 0.0f;
+    if (lane < a.k) {
+        mine = (int)checked_pos(a, row * a.k + lane);
+        if (mine >= 0) weight = a.weights ? a.weights[row * a.k + lane] : 1.0f;
+    }
+    int from[kSlots];
+    float w[kSlots];
 #pragma unroll
-            for (int j = 0; j < kStep; ++j) {
-                const int64_t from = jb + j < a.k ? checked_pos(a, row * a.k + jb + j) : -1;
-                w[j] = 0.0f;
+    for (int j = 0; j < kSlots; ++j) {
+        from[j] = __shfl_sync(0xffffffffu, mine, j);
+        w[j] = __shfl_sync(0xffffffffu, weight, j);
+    }
+    const int v0 = slice * a.slice_vecs, v1 = min(a.vecs, v0 + a.slice_vecs);
+    auto load = [&](uint4 (&y)[kSlots], int v) {
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+            y[j] = make_uint4(0, 0, 0, 0);
+            if (from[j] >= 0 && v < v1) y[j] = ld_stream_v4(a.in + from[j] * a.row_bytes + 16 * (int64_t)v);
+        }
+    };
+    auto fold = [&](const uint4 (&y)[kSlots], int v) {
+        float acc[8] = {};
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+            float f[8];
+            unpack8<FP16>(y[j], f);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) acc[q] = fmaf(w[j], f[q], acc[q]);
+        }
+        if (v < v1) st_v4(a.out + row * a.row_bytes + 16 * (int64_t)v, pack8<FP16>(acc));
+    };
+    uint4 y0[kSlots], y1[kSlots];
+    int v = v0 + lane;
+    load(y0, v);
+    for (; v - lane < v1; v += 64) {
+        load(y1, v + 32);
+        fold(y0, v);
+        load(y0, v + 64);
+        fold(y1, v + 32);
+    }
+}
+
+// The same for more than 8 slots a row, 8 at a time.
+template <bool FP16>
+__global__ void __launch_bounds__(kRowThreads) ep_return_rows_many_kernel(const RowsArgs a)
+{
+    constexpr int kSlots = 8;
+    const int lane = threadIdx.x & 31;
+    const int64_t unit = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+    const int64_t row = unit / a.slices;
+    const int slice = (int)(unit - row * a.slices);
+    if (!row_present(a, row)) return;
+    const int v0 = slice * a.slice_vecs, v1 = min(a.vecs, v0 + a.slice_vecs);
+    int64_t from[2] = {-1, -1};   // of slots lane and lane + 32
+    float weight[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (32 * h + lane < a.k) {
+            from[h] = checked_pos(a, row * a.k + 32 * h + lane);
+            if (from[h] >= 0) weight[h] = a.weights ? a.weights[row * a.k + 32 * h + lane] : 1.0f;
+        }
+    for (int v = v0 + lane; v - lane < v1; v += 32) {
+        float acc[8] = {};
+        for (int jb = 0; jb < a.k; jb += kSlots) {
+            uint4 y[kSlots];
+            float w[kSlots];
+#pragma unroll
+            for (int j = 0; j < kSlots; ++j) {
+                const int64_t r = __shfl_sync(0xffffffffu, jb < 32 ? from[0] : from[1], (jb + j) & 31);
+                w[j] = __shfl_sync(0xffffffffu, jb < 32 ? weight[0] : weight[1], (jb + j) & 31);
                 y[j] = make_uint4(0, 0, 0, 0);
-                if (from >= 0 && v < v1) {
-                    y[j] = ld_stream_v4(a.in + from * a.row_bytes + 16 * (int64_t)v);
-                    w[j] = a.weights ? a.weights[row * a.k + jb + j] : 1.0f;
-                }
+                if (r >= 0 && v < v1) y[j] = ld_stream_v4(a.in + r * a.row_bytes + 16 * (int64_t)v);
             }
 #pragma unroll
-            for (int j = 0; j < kStep; ++j) {
+            for (int j = 0; j < kSlots; ++j) {
                 float f[8];
                 unpack8<FP16>(y[j], f);
 #pragma unroll
@@ -348,35 +438,35 @@ __global__ void __launch_bounds__(kRowThreads) ep_return_rows_kernel(const RowsA
     }
 }
 
-// Gradient of the weighted return: dy[pos] = round(weight * dout[row]), dw = <y[pos], dout[row]>.
-// A CTA takes a row, so that each dot product is summed in one place and in one order.
-constexpr int kBackSlots = 4;   // slots whose dot products run together
-template <bool FP16>
+// Gradient of the weighted return: dy[pos] = round(weight * dout[row]), dw = <y[pos], dout[row]>.  A row
+// is one warp's, or one CTA's, so that each dot product is summed in one place and in one order; the
+// products of kSlots slots run together.
+template <bool FP16, bool WARP, int kSlots>
 __global__ void __launch_bounds__(kRowThreads) ep_return_rows_backward_kernel(const RowsArgs a)
 {
-    __shared__ float part[kBackSlots][kRowThreads / 32];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int64_t row = blockIdx.x;
-    if (!row_present(a, row)) return;
+    __shared__ float part[kRowThreads / 32][kSlots];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = WARP ? (int64_t)blockIdx.x * (kRowThreads / 32) + warp : blockIdx.x;
+    if (!row_present(a, row)) return;   // whole warps, and whole CTAs where they synchronise
     const uint8_t* dout = a.dout + row * a.row_bytes;
-    for (int jb = 0; jb < a.k; jb += kBackSlots) {
-        int64_t at[kBackSlots];
-        float wt[kBackSlots], dot[kBackSlots];
+    for (int jb = 0; jb < a.k; jb += kSlots) {
+        int at[kSlots];
+        float wt[kSlots], dot[kSlots];
 #pragma unroll
-        for (int j = 0; j < kBackSlots; ++j) {
-            at[j] = jb + j < a.k ? checked_pos(a, row * a.k + jb + j) : -1;
+        for (int j = 0; j < kSlots; ++j) {
+            at[j] = jb + j < a.k ? (int)checked_pos(a, row * a.k + jb + j) : -1;
             wt[j] = at[j] >= 0 ? a.weights[row * a.k + jb + j] : 0.0f;
             dot[j] = 0.0f;
         }
-        for (int v = threadIdx.x; v < a.vecs; v += blockDim.x) {
-            uint4 y[kBackSlots];
+        for (int v = WARP ? lane : threadIdx.x; v < a.vecs; v += WARP ? 32 : kRowThreads) {
+            uint4 y[kSlots];
 #pragma unroll
-            for (int j = 0; j < kBackSlots; ++j)
+            for (int j = 0; j < kSlots; ++j)
                 if (at[j] >= 0) y[j] = ld_stream_v4(a.in + at[j] * a.row_bytes + 16 * (int64_t)v);
             float g[8];
             unpack8<FP16>(*reinterpret_cast<const uint4*>(dout + 16 * (int64_t)v), g);
 #pragma unroll
-            for (int j = 0; j < kBackSlots; ++j) {
+            for (int j = 0; j < kSlots; ++j) {
                 if (at[j] < 0) continue;
                 float f[8], o[8];
                 unpack8<FP16>(y[j], f);
@@ -389,19 +479,52 @@ __global__ void __launch_bounds__(kRowThreads) ep_return_rows_backward_kernel(co
             }
         }
 #pragma unroll
-        for (int j = 0; j < kBackSlots; ++j) {
+        for (int j = 0; j < kSlots; ++j) {
 #pragma unroll
             for (int o = 16; o; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
-            if (lane == 0) part[j][w] = dot[j];
+            if (lane == j) part[warp][j] = dot[j];
         }
-        __syncthreads();
-        if (threadIdx.x < kBackSlots && jb + (int)threadIdx.x < a.k) {
-            float s = 0.0f;
-            for (int i = 0; i < (int)(blockDim.x >> 5); ++i) s += part[threadIdx.x][i];
-            a.dw[row * a.k + jb + threadIdx.x] = s;
+        if constexpr (WARP) {
+            __syncwarp();
+            if (lane < kSlots && jb + lane < a.k) a.dw[row * a.k + jb + lane] = part[warp][lane];
+            __syncwarp();
+        } else {
+            __syncthreads();
+            if (threadIdx.x < kSlots && jb + (int)threadIdx.x < a.k) {
+                float s = 0.0f;
+                for (int i = 0; i < kRowThreads / 32; ++i) s += part[i][threadIdx.x];
+                a.dw[row * a.k + jb + threadIdx.x] = s;
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
+}
+
+template <bool FP16>
+cudaError_t launch_return(const RowsArgs& a, unsigned grid, cudaStream_t s)
+{
+    if (a.k <= 2) ep_return_rows_kernel<FP16, 2><<<grid, kRowThreads, 0, s>>>(a);
+    else if (a.k <= 4) ep_return_rows_kernel<FP16, 4><<<grid, kRowThreads, 0, s>>>(a);
+    else if (a.k <= 8) ep_return_rows_kernel<FP16, 8><<<grid, kRowThreads, 0, s>>>(a);
+    else ep_return_rows_many_kernel<FP16><<<grid, kRowThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <bool FP16>
+cudaError_t launch_return_backward(const RowsArgs& a, cudaStream_t s)
+{
+    if (a.vecs <= kWarpRowVecs) {
+        const unsigned grid = (unsigned)((a.rows + kRowThreads / 32 - 1) / (kRowThreads / 32));
+        if (a.k <= 4) ep_return_rows_backward_kernel<FP16, true, 4><<<grid, kRowThreads, 0, s>>>(a);
+        else ep_return_rows_backward_kernel<FP16, true, 8><<<grid, kRowThreads, 0, s>>>(a);
+    } else {
+        // 8 slots together shorten one row's chain of loads (64 rows of 7168: 9.2 -> 6.7 us); with every SM
+        // full their registers cost more (4096 rows: 4 slots 151.8 us, 8 slots 157.5)
+        const unsigned grid = (unsigned)a.rows;
+        if (a.k <= 4 || a.rows >= 1024) ep_return_rows_backward_kernel<FP16, false, 4><<<grid, kRowThreads, 0, s>>>(a);
+        else ep_return_rows_backward_kernel<FP16, false, 8><<<grid, kRowThreads, 0, s>>>(a);
+    }
+    return cudaGetLastError();
 }
 
 // The shape every call of this file shares.
@@ -430,20 +553,32 @@ int check_row_type(const char* who, int dtype, int hidden)
     return EP_OK;
 }
 
-int64_t sort_tiles(int64_t pairs) { return (pairs + kSortTile - 1) / kSortTile; }
+int sort_tile_pairs(int64_t pairs)
+{
+    return kSortTileThreads * (pairs <= (int64_t)kSortShortTiles * kSortTileThreads * kSortSteps ? kSortSteps : kSortLongSteps);
+}
+
+int64_t sort_tiles(int64_t pairs) { return (pairs + sort_tile_pairs(pairs) - 1) / sort_tile_pairs(pairs); }
 
 bool sort_is_small(int64_t pairs, int groups) { return pairs <= kSortSmallPairs && groups <= kSortSmallGroups; }
 
-// A row's 2 KB slices, and the CTAs of 8 warps that take one each.
-int set_slices(const char* who, RowsArgs& a, unsigned& grid)
+// Splits rows into slices of at most `most` steps of 32 vectors, no longer than it takes to give every SM 32
+// warps, all about as long; and the CTAs of 8 warps that take one each.
+int set_slices(const char* who, RowsArgs& a, int most, unsigned& grid)
 {
     a.vecs = (int)(a.row_bytes / 16);
-    a.slices = (a.vecs + 32 * kRowVecs - 1) / (32 * kRowVecs);
-    const int64_t ctas = (a.rows * a.slices + kRowThreads / 32 - 1) / (kRowThreads / 32);
-    if (ctas >= (int64_t)1 << 31)
+    const int64_t steps = (a.vecs + 31) / 32;
+    const int64_t least = (a.rows * ((steps + most - 1) / most) + kRowThreads / 32 - 1) / (kRowThreads / 32);
+    if (least >= (int64_t)1 << 31)
         return layer_fail(EP_ERR_ARG, "%s: %lld rows of %lld bytes need %lld CTAs, past 2^31-1", who, (long long)a.rows,
-                          (long long)a.row_bytes, (long long)ctas);
-    grid = (unsigned)ctas;
+                          (long long)a.row_bytes, (long long)least);
+    const int64_t warps = 32 * (int64_t)layer_num_sms();
+    if (warps == 0) return layer_fail(EP_ERR_CUDA, "%s: cannot tell the current device's multiprocessors", who);
+    int64_t take = (a.rows * steps + warps - 1) / warps;
+    take = take < 1 ? 1 : take > most ? most : take;
+    a.slices = (int)((steps + take - 1) / take);
+    a.slice_vecs = (int)((steps + a.slices - 1) / a.slices) * 32;
+    grid = (unsigned)((a.rows * a.slices + kRowThreads / 32 - 1) / (kRowThreads / 32));   // `least`, or under 2^20
     return EP_OK;
 }
 
@@ -503,15 +638,17 @@ int ep_sort_by_expert(const int32_t* indices, const int32_t* counts, int W, int6
         return layer_cuda(e, "ep_sort_by_expert: launch");
     }
     const size_t smem = (size_t)(kSortTileThreads / 32) * a.groups * sizeof(int);
+    const int tile_pairs = sort_tile_pairs(a.pairs);
+    const bool shorter = tile_pairs == kSortTileThreads * kSortSteps;
+    auto* place = shorter ? ep_sort_place_kernel<kSortSteps, false> : ep_sort_place_kernel<kSortLongSteps, true>;
     e = cudaSuccess;
-    if (smem > 48 * 1024)
-        e = cudaFuncSetAttribute(ep_sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem > 48 * 1024) e = cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess) {
-        ep_sort_count_kernel<<<a.tiles, kSortTileThreads, a.groups * sizeof(int), s>>>(a);
+        ep_sort_count_kernel<<<a.tiles, kSortTileThreads, a.groups * sizeof(int), s>>>(a, tile_pairs);
         e = cudaGetLastError();
     }
-    if (e == cudaSuccess) e = launch_dependent(ep_sort_scan_kernel, dim3(1), dim3(kScanThreads), 0, s, a);
-    if (e == cudaSuccess) e = launch_dependent(ep_sort_place_kernel, dim3(a.tiles), dim3(kSortTileThreads), smem, s, a);
+    if (e == cudaSuccess && !shorter) e = launch_dependent(ep_sort_scan_kernel, dim3(1), dim3(kScanThreads), 0, s, a);
+    if (e == cudaSuccess) e = launch_dependent(place, dim3(a.tiles), dim3(kSortTileThreads), smem, s, a);
     return layer_cuda(e, "ep_sort_by_expert: launch");
 }
 
@@ -537,7 +674,7 @@ int ep_sorted_rows(const void* x, const float* scales, const int32_t* pos, const
     a.out_scales = out_scales; a.status = device_status; a.rows = W * rows_per_rank; a.rows_per_rank = rows_per_rank;
     a.max_rows = max_rows; a.row_bytes = row_bytes; a.k = topk; a.sd = scale_dim;
     unsigned grid;
-    if (int rc = set_slices(who, a, grid)) return rc;
+    if (int rc = set_slices(who, a, kRowVecs, grid)) return rc;
     ep_sorted_rows_kernel<<<grid, kRowThreads, 0, (cudaStream_t)stream>>>(a);
     return layer_cuda(cudaGetLastError(), "ep_sorted_rows: launch");
 }
@@ -559,11 +696,10 @@ int ep_return_rows(const void* y, const float* weights, const int32_t* pos, cons
     a.status = device_status; a.rows = W * rows_per_rank; a.rows_per_rank = rows_per_rank; a.max_rows = max_rows;
     a.row_bytes = 2 * (int64_t)hidden; a.k = topk;
     unsigned grid;
-    if (int rc = set_slices(who, a, grid)) return rc;
+    if (int rc = set_slices(who, a, 8, grid)) return rc;
     cudaStream_t s = (cudaStream_t)stream;
-    if (dtype == EP_FP16) ep_return_rows_kernel<true><<<grid, kRowThreads, 0, s>>>(a);
-    else ep_return_rows_kernel<false><<<grid, kRowThreads, 0, s>>>(a);
-    return layer_cuda(cudaGetLastError(), "ep_return_rows: launch");
+    const cudaError_t e = dtype == EP_FP16 ? launch_return<true>(a, grid, s) : launch_return<false>(a, grid, s);
+    return layer_cuda(e, "ep_return_rows: launch");
 }
 
 int ep_return_rows_backward(const void* y, const float* weights, const void* dout, const int32_t* pos,
@@ -586,10 +722,8 @@ int ep_return_rows_backward(const void* y, const float* weights, const void* dou
     a.rows_per_rank = rows_per_rank; a.max_rows = max_rows; a.row_bytes = 2 * (int64_t)hidden; a.k = topk;
     a.vecs = hidden / 8;
     cudaStream_t s = (cudaStream_t)stream;
-    const unsigned grid = (unsigned)a.rows;
-    if (dtype == EP_FP16) ep_return_rows_backward_kernel<true><<<grid, kRowThreads, 0, s>>>(a);
-    else ep_return_rows_backward_kernel<false><<<grid, kRowThreads, 0, s>>>(a);
-    return layer_cuda(cudaGetLastError(), "ep_return_rows_backward: launch");
+    const cudaError_t e = dtype == EP_FP16 ? launch_return_backward<true>(a, s) : launch_return_backward<false>(a, s);
+    return layer_cuda(e, "ep_return_rows_backward: launch");
 }
 
 }  // extern "C"

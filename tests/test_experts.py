@@ -64,9 +64,11 @@ def test_sort_refusals(lib, change, word):
 
 
 def test_sort_workspace_sizes(lib):
-    assert lib.ep_sort_workspace_bytes(1, 1024, 8, 256) == 0            # one CTA sorts 8192 pairs
-    assert lib.ep_sort_workspace_bytes(1, 1025, 8, 256) == 5 * 256 * 4  # tiles of 2048 pairs
-    assert lib.ep_sort_workspace_bytes(8, 32768, 8, 32) == 1024 * 256 * 4
+    assert lib.ep_sort_workspace_bytes(1, 256, 8, 256) == 0             # one CTA sorts 2048 pairs
+    assert lib.ep_sort_workspace_bytes(1, 257, 8, 256) == 2 * 256 * 4   # tiles of 2048 pairs
+    assert lib.ep_sort_workspace_bytes(1, 16384, 8, 64) == 64 * 64 * 4  # 131072 pairs: the last such size
+    assert lib.ep_sort_workspace_bytes(1, 16385, 8, 64) == 17 * 64 * 4  # tiles of 8192 pairs
+    assert lib.ep_sort_workspace_bytes(8, 32768, 8, 32) == 256 * 256 * 4
     assert lib.ep_sort_workspace_bytes(1, 10, 8, 2049) == 2049 * 4      # many groups: the tiled form
     for bad in ((0, 8, 8, 8), (1, -1, 8, 8), (1, 8, 65, 8), (1, 8, 8, 4097), (1, 1 << 31, 1, 1), (32, 1 << 26, 1, 1)):
         assert lib.ep_sort_workspace_bytes(*bad) == 0

@@ -179,9 +179,11 @@ def _indices(g, W, R, k, E, bad=0.1):
 
 
 @pytest.mark.parametrize("W,R,k,E", [(1, 1, 1, 1), (1, 3, 8, 256), (1, 1000, 8, 32), (1, 1024, 8, 7), (1, 1025, 8, 7),
+                                     (1, 256, 8, 7), (1, 257, 8, 7), (1, 2047, 1, 40),
                                      (1, 1537, 6, 96), (1, 9000, 8, 256), (1, 700, 64, 4096), (1, 64, 2, 4096),
                                      (1, 20000, 1, 1), (2, 64, 2, 4), (4, 999, 9, 64), (8, 2048, 8, 32), (32, 5, 3, 2),
-                                     (1, 500, 4, 2048), (1, 500, 4, 2049), (1, 40000, 8, 129)])
+                                     (1, 500, 4, 2048), (1, 500, 4, 2049), (1, 40000, 8, 129), (1, 16384, 8, 300),
+                                     (1, 16385, 8, 300), (2, 20001, 4, 700)])
 def test_sort_by_expert(W, R, k, E):
     g = _gen(W + 10 * R + k + E)
     idx = _indices(g, W, R, k, E)
@@ -240,7 +242,7 @@ def _return64(y, w, pos):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-@pytest.mark.parametrize("R,k,E,hidden", [(1, 1, 4, 8), (1, 8, 64, 7168), (513, 6, 96, 2056), (130, 33, 40, 264),
+@pytest.mark.parametrize("R,k,E,hidden", [(1100, 8, 24, 1040), (1, 1, 4, 8), (1, 8, 64, 7168), (513, 6, 96, 2056), (130, 33, 40, 264),
                                           (64, 64, 100, 1000), (1531, 2, 8, 512)])
 def test_return_rows_and_gradients(R, k, E, hidden, dtype):
     g, t = _gen(R + hidden), HALF[dtype]
