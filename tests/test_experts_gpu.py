@@ -602,3 +602,11 @@ def test_calls_replay_in_a_graph():
     x.copy_(x2)
     graph.replay()
     assert torch.equal(out, layer())
+
+
+def test_example_layer_agrees_with_fp32():
+    """The example's layer quantises the rows twice; see the bound of the test above."""
+    from combine_ep_dispatch_02_gb300 import expert_layer
+    assert expert_layer.main(["--tokens-per-rank", "33", "--hidden", "512", "--inner", "272", "--passes", "2"]) <= 2.0 ** -3
+    assert expert_layer.main(["--ranks", "1", "--experts-per-rank", "4", "--topk", "2", "--tokens-per-rank", "1",
+                              "--hidden", "256", "--passes", "1"]) <= 2.0 ** -3
