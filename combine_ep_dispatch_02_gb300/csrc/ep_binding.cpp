@@ -7,7 +7,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -111,7 +111,7 @@ int half_code(const at::Tensor& t, const char* what)
 
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, at::Device device)
 {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(device));
+    return at::detail::empty_cuda(shape, type, device, std::nullopt);
 }
 
 int32_t* status(at::Device device)

@@ -227,12 +227,13 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
         prefetch_map(&map_a);
         prefetch_map(&map_b);
     }
+    if (warp == 2) tmem_alloc(smem_u32(&tmem_slot), 512);
+    follow_predecessor();
     const bool copied = p.offsets != nullptr && p.groups <= kSharedOffsets;
     if (copied)
         for (int i = threadIdx.x; i <= p.groups; i += kProductThreads) off_copy[i] = p.offsets[i];
     const int32_t* off = copied ? off_copy : p.offsets;
     if (warp == 1) scan_tiles<kTileRows>(p, first, col_tiles, lane);
-    if (warp == 2) tmem_alloc(smem_u32(&tmem_slot), 512);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
@@ -530,12 +531,13 @@ ep_product_few_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap ma
         prefetch_map(&map_a);
         prefetch_map(&map_b);
     }
+    if (warp == 2) tmem_alloc(smem_u32(&tmem_slot), S::kTmemCols);
+    follow_predecessor();
     const bool copied = p.offsets != nullptr && p.groups <= kSharedOffsets;
     if (copied)
         for (int i = threadIdx.x; i <= p.groups; i += kFewThreads) off_copy[i] = p.offsets[i];
     const int32_t* off = copied ? off_copy : p.offsets;
     if (warp == 1) scan_tiles<T>(p, first, col_tiles, lane);
-    if (warp == 2) tmem_alloc(smem_u32(&tmem_slot), S::kTmemCols);
     tmem_fence_before();
     __syncthreads();
     if (split_k > 1) cluster_sync();   // the peers' barriers exist
@@ -797,8 +799,8 @@ cudaError_t launch_product_rows(const MatmulArgs& p, const CUtensorMap& ma, cons
     cudaError_t e = cudaFuncSetAttribute(ep_product_rows_kernel<SWIGLU, SPLIT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    ep_product_rows_kernel<SWIGLU, SPLIT><<<(unsigned)(most < sms ? most : sms), kProductThreads, smem, s>>>(p, ma, mb);
-    return cudaGetLastError();
+    return launch_dependent(ep_product_rows_kernel<SWIGLU, SPLIT>, dim3((unsigned)(most < sms ? most : sms)),
+                            dim3(kProductThreads), smem, s, p, ma, mb);
 }
 
 template <int T, bool SWIGLU>
@@ -829,12 +831,14 @@ cudaError_t launch_product_few(const MatmulArgs& p, const CUtensorMap& ma, const
     cfg.blockDim = dim3(kFewThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = split;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // as launch_dependent
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = split > 1 ? 1 : 0;
+    cfg.numAttrs = split > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, p, ma, mb, stages, split);
 }
 

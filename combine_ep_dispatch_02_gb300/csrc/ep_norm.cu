@@ -41,6 +41,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarpsPerCta : kNormMaxThreads
     const int t = WARP ? lane : threadIdx.x;
     const int stride = WARP ? 32 : blockDim.x;
     const int64_t row = WARP ? (int64_t)blockIdx.x * kNormWarpsPerCta + (threadIdx.x >> 5) : blockIdx.x;
+    follow_predecessor();
     if (WARP && row >= a.rows) return;
     const uint8_t* x = a.x + row * a.x_pitch;
     float f[VPT][8];
@@ -127,12 +128,11 @@ cudaError_t launch_norm(const NormArgs& a, int vpt, int threads, cudaStream_t s)
 {
     const unsigned grid = (unsigned)(WARP ? (a.rows + kNormWarpsPerCta - 1) / kNormWarpsPerCta : a.rows);
     switch (vpt) {
-    case 1: ep_norm_kernel<FP16, WARP, 1><<<grid, threads, 0, s>>>(a); break;
-    case 2: ep_norm_kernel<FP16, WARP, 2><<<grid, threads, 0, s>>>(a); break;
-    case 4: ep_norm_kernel<FP16, WARP, 4><<<grid, threads, 0, s>>>(a); break;
-    default: ep_norm_kernel<FP16, WARP, 8><<<grid, threads, 0, s>>>(a); break;
+    case 1: return launch_dependent(ep_norm_kernel<FP16, WARP, 1>, dim3(grid), dim3(threads), 0, s, a);
+    case 2: return launch_dependent(ep_norm_kernel<FP16, WARP, 2>, dim3(grid), dim3(threads), 0, s, a);
+    case 4: return launch_dependent(ep_norm_kernel<FP16, WARP, 4>, dim3(grid), dim3(threads), 0, s, a);
+    default: return launch_dependent(ep_norm_kernel<FP16, WARP, 8>, dim3(grid), dim3(threads), 0, s, a);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace

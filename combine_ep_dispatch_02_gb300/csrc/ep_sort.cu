@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(kSortSmallThreads) ep_sort_small_kernel(const 
     constexpr int kWarps = kSortSmallThreads / 32;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     for (int i = threadIdx.x; i < kWarps * a.groups; i += blockDim.x) counts[i] = 0;
+    follow_predecessor();
     __syncthreads();
     const int steps = (int)((a.pairs + kSortSmallThreads - 1) / kSortSmallThreads);
     const int64_t first = (int64_t)w * steps * 32;   // a warp's pairs are consecutive
@@ -148,6 +149,7 @@ __global__ void __launch_bounds__(kSortTileThreads) ep_sort_count_kernel(const S
 {
     extern __shared__ int counts[];   // [groups]
     for (int i = threadIdx.x; i < a.groups; i += blockDim.x) counts[i] = 0;
+    follow_predecessor();
     __syncthreads();
     const int64_t first = (int64_t)blockIdx.x * tile_pairs;
 #pragma unroll 8
@@ -158,7 +160,6 @@ __global__ void __launch_bounds__(kSortTileThreads) ep_sort_count_kernel(const S
     __syncthreads();
     for (int i = threadIdx.x; i < a.groups; i += blockDim.x)
         a.tile_counts[(int64_t)blockIdx.x * a.groups + i] = counts[i];
-    allow_dependents();
 }
 
 // Counts to first positions: tile_counts[t][g] becomes the sorted row of tile t's first pair of g.
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(kScanThreads) ep_sort_scan_kernel(const SortAr
 {
     constexpr int kCols = kScanThreads / kScanParts;
     __shared__ int sums[kScanParts][kCols], warp_sums[32];
-    wait_for_predecessor();
+    follow_predecessor();
     const int col = threadIdx.x % kCols, part = threadIdx.x / kCols;
     const int per = (a.tiles + kScanParts - 1) / kScanParts;
     const int t0 = min(part * per, a.tiles), t1 = min(t0 + per, a.tiles);
@@ -209,7 +210,6 @@ __global__ void __launch_bounds__(kScanThreads) ep_sort_scan_kernel(const SortAr
         __syncthreads();
     }
     if (threadIdx.x == 0) a.offsets[a.groups] = clamp_rows(a, carry);
-    allow_dependents();
 }
 
 // SCANNED: tile_counts holds first positions and offsets is written; else tile_counts holds counts, and each
@@ -224,13 +224,14 @@ __global__ void __launch_bounds__(kSortTileThreads) ep_sort_place_kernel(const S
     for (int i = threadIdx.x; i < kWarps * a.groups; i += blockDim.x) counts[i] = 0;
     __syncthreads();
     const int64_t first = ((int64_t)blockIdx.x * kWarps + w) * kSteps * 32;
+    // the kernel before this one let it start after its own predecessor: the indices are complete
     int g[kSteps], at[kSteps];
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) g[i] = pair_group(a, first + 32 * i + lane);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) at[i] = warp_rank(g[i], counts + w * a.groups, lane);
     __syncthreads();
-    wait_for_predecessor();
+    follow_predecessor();
     int carry = 0;
     for (int e0 = 0; e0 < a.groups; e0 += kSortTileThreads) {
         const int e = e0 + threadIdx.x;
@@ -318,6 +319,7 @@ __global__ void __launch_bounds__(kRowThreads) ep_sorted_rows_kernel(const RowsA
     const int64_t unit = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
     const int64_t row = unit / a.slices;
     const int slice = (int)(unit - row * a.slices);
+    follow_predecessor();
     if (!row_present(a, row)) return;
     const uint8_t* x = a.in + row * a.row_bytes;
     uint4 v[kRowVecs];
@@ -351,6 +353,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) ep_return_rows_kernel(const Ro
     const int64_t unit = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
     const int64_t row = unit / a.slices;
     const int slice = (int)(unit - row * a.slices);
+    follow_predecessor();
     if (!row_present(a, row)) return;
     int mine = -1;
     float weight = 0.0f;
@@ -404,6 +407,7 @@ __global__ void __launch_bounds__(kRowThreads) ep_return_rows_many_kernel(const 
     const int64_t unit = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
     const int64_t row = unit / a.slices;
     const int slice = (int)(unit - row * a.slices);
+    follow_predecessor();
     if (!row_present(a, row)) return;
     const int v0 = slice * a.slice_vecs, v1 = min(a.vecs, v0 + a.slice_vecs);
     int64_t from[2] = {-1, -1};   // of slots lane and lane + 32
@@ -447,6 +451,7 @@ __global__ void __launch_bounds__(kRowThreads) ep_return_rows_backward_kernel(co
     __shared__ float part[kRowThreads / 32][kSlots];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = WARP ? (int64_t)blockIdx.x * (kRowThreads / 32) + warp : blockIdx.x;
+    follow_predecessor();
     if (!row_present(a, row)) return;   // whole warps, and whole CTAs where they synchronise
     const uint8_t* dout = a.dout + row * a.row_bytes;
     for (int jb = 0; jb < a.k; jb += kSlots) {
@@ -503,28 +508,25 @@ __global__ void __launch_bounds__(kRowThreads) ep_return_rows_backward_kernel(co
 template <bool FP16>
 cudaError_t launch_return(const RowsArgs& a, unsigned grid, cudaStream_t s)
 {
-    if (a.k <= 2) ep_return_rows_kernel<FP16, 2><<<grid, kRowThreads, 0, s>>>(a);
-    else if (a.k <= 4) ep_return_rows_kernel<FP16, 4><<<grid, kRowThreads, 0, s>>>(a);
-    else if (a.k <= 8) ep_return_rows_kernel<FP16, 8><<<grid, kRowThreads, 0, s>>>(a);
-    else ep_return_rows_many_kernel<FP16><<<grid, kRowThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    auto* kernel = a.k <= 2   ? ep_return_rows_kernel<FP16, 2>
+                   : a.k <= 4 ? ep_return_rows_kernel<FP16, 4>
+                   : a.k <= 8 ? ep_return_rows_kernel<FP16, 8>
+                              : ep_return_rows_many_kernel<FP16>;
+    return launch_dependent(kernel, dim3(grid), dim3(kRowThreads), 0, s, a);
 }
 
 template <bool FP16>
 cudaError_t launch_return_backward(const RowsArgs& a, cudaStream_t s)
 {
-    if (a.vecs <= kWarpRowVecs) {
-        const unsigned grid = (unsigned)((a.rows + kRowThreads / 32 - 1) / (kRowThreads / 32));
-        if (a.k <= 4) ep_return_rows_backward_kernel<FP16, true, 4><<<grid, kRowThreads, 0, s>>>(a);
-        else ep_return_rows_backward_kernel<FP16, true, 8><<<grid, kRowThreads, 0, s>>>(a);
-    } else {
-        // 8 slots together shorten one row's chain of loads (64 rows of 7168: 9.2 -> 6.7 us); with every SM
-        // full their registers cost more (4096 rows: 4 slots 151.8 us, 8 slots 157.5)
-        const unsigned grid = (unsigned)a.rows;
-        if (a.k <= 4 || a.rows >= 1024) ep_return_rows_backward_kernel<FP16, false, 4><<<grid, kRowThreads, 0, s>>>(a);
-        else ep_return_rows_backward_kernel<FP16, false, 8><<<grid, kRowThreads, 0, s>>>(a);
-    }
-    return cudaGetLastError();
+    const bool warp = a.vecs <= kWarpRowVecs;
+    const unsigned grid = (unsigned)(warp ? (a.rows + kRowThreads / 32 - 1) / (kRowThreads / 32) : a.rows);
+    // 8 slots together shorten one row's chain of loads (64 rows of 7168: 9.2 -> 6.7 us); with every SM
+    // full their registers cost more (4096 rows: 4 slots 151.8 us, 8 slots 157.5)
+    auto* kernel = warp ? (a.k <= 4 ? ep_return_rows_backward_kernel<FP16, true, 4>
+                                    : ep_return_rows_backward_kernel<FP16, true, 8>)
+                        : (a.k <= 4 || a.rows >= 1024 ? ep_return_rows_backward_kernel<FP16, false, 4>
+                                                      : ep_return_rows_backward_kernel<FP16, false, 8>);
+    return launch_dependent(kernel, dim3(grid), dim3(kRowThreads), 0, s, a);
 }
 
 // The shape every call of this file shares.
@@ -631,10 +633,7 @@ int ep_sort_by_expert(const int32_t* indices, const int32_t* counts, int W, int6
         e = cudaSuccess;
         if (smem > 48 * 1024)
             e = cudaFuncSetAttribute(ep_sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e == cudaSuccess) {
-            ep_sort_small_kernel<<<1, kSortSmallThreads, smem, s>>>(a);
-            e = cudaGetLastError();
-        }
+        if (e == cudaSuccess) e = launch_dependent(ep_sort_small_kernel, dim3(1), dim3(kSortSmallThreads), smem, s, a);
         return layer_cuda(e, "ep_sort_by_expert: launch");
     }
     const size_t smem = (size_t)(kSortTileThreads / 32) * a.groups * sizeof(int);
@@ -643,10 +642,9 @@ int ep_sort_by_expert(const int32_t* indices, const int32_t* counts, int W, int6
     auto* place = shorter ? ep_sort_place_kernel<kSortSteps, false> : ep_sort_place_kernel<kSortLongSteps, true>;
     e = cudaSuccess;
     if (smem > 48 * 1024) e = cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess) {
-        ep_sort_count_kernel<<<a.tiles, kSortTileThreads, a.groups * sizeof(int), s>>>(a, tile_pairs);
-        e = cudaGetLastError();
-    }
+    if (e == cudaSuccess)
+        e = launch_dependent(ep_sort_count_kernel, dim3(a.tiles), dim3(kSortTileThreads), a.groups * sizeof(int), s, a,
+                             tile_pairs);
     if (e == cudaSuccess && !shorter) e = launch_dependent(ep_sort_scan_kernel, dim3(1), dim3(kScanThreads), 0, s, a);
     if (e == cudaSuccess) e = launch_dependent(place, dim3(a.tiles), dim3(kSortTileThreads), smem, s, a);
     return layer_cuda(e, "ep_sort_by_expert: launch");
@@ -675,8 +673,8 @@ int ep_sorted_rows(const void* x, const float* scales, const int32_t* pos, const
     a.max_rows = max_rows; a.row_bytes = row_bytes; a.k = topk; a.sd = scale_dim;
     unsigned grid;
     if (int rc = set_slices(who, a, kRowVecs, grid)) return rc;
-    ep_sorted_rows_kernel<<<grid, kRowThreads, 0, (cudaStream_t)stream>>>(a);
-    return layer_cuda(cudaGetLastError(), "ep_sorted_rows: launch");
+    return layer_cuda(launch_dependent(ep_sorted_rows_kernel, dim3(grid), dim3(kRowThreads), 0, (cudaStream_t)stream, a),
+                      "ep_sorted_rows: launch");
 }
 
 int ep_return_rows(const void* y, const float* weights, const int32_t* pos, const int32_t* counts, int W,
