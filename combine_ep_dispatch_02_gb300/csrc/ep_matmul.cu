@@ -164,6 +164,49 @@ __device__ __forceinline__ void store_row(uint8_t* out, const float2 (&acc)[64],
     }
 }
 
+// The same for a warp's 32 rows, m of which exist (row by lane, rows `pitch` bytes apart), where all 128
+// columns exist and rows are 32-byte aligned.  A store of 32 bytes by every lane to a row of its own
+// visits 32 lines, two cycles each, 4000 for a tile.  So four lanes first trade 32-byte pieces, two
+// exchanges of half of them, until lane q of the four holds piece q (then q + 4) of all four rows: a
+// store then writes 128 bytes each of 8 rows.
+template <bool FP16>
+__device__ __forceinline__ void store_rows(uint8_t* out, int64_t pitch, const float2 (&acc)[64], int m)
+{
+    const int lane = threadIdx.x & 31, q = lane & 3;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t w[4][8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 v = acc[32 * h + 8 * c + i];
+                w[c][i] = pack2<FP16>(v.x, v.y);
+            }
+#pragma unroll
+        for (int bit = 1; bit <= 2; bit *= 2) {
+            const bool upper = q & bit;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (c & bit) continue;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? w[c][i] : w[c | bit][i], bit);
+                    if (upper) w[c][i] = got;
+                    else w[c | bit][i] = got;
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = (lane & ~3) + r;
+            if (row < m)
+                st_v8(out + row * pitch + 128 * h + 32 * q, make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]),
+                      make_uint4(w[r][4], w[r][5], w[r][6], w[r][7]));
+        }
+    }
+}
+
 // gate * sigmoid(gate) * up.  The exponential's argument is split so that its error stays a few units in
 // the last place at any magnitude (the product with log2 e alone would be off by |gate| units); the two
 // approximate units add two more.  Below -88 the exponential is held at 2^127, whose reciprocal is 0; an
@@ -406,13 +449,17 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
                 else add_scaled(acc + 48, r1, g1);
             }
             const int4 x = info[i % kInfo];
-            const bool present = x.x + row < x.y;
             if constexpr (!SWIGLU) {
-                const int n0 = x.z + part * 128;
-                if (ok && present && n0 < p.N) {
-                    uint8_t* out = (uint8_t*)p.out + 2 * ((int64_t)(x.x + row) * p.N + n0);
-                    if (p.dtype == EP_FP16) store_row<true>(out, acc, p.N - n0, p.vec);
-                    else store_row<false>(out, acc, p.N - n0, p.vec);
+                const int n0 = x.z + part * 128, m = x.y - x.x - (warp & 3) * 32;   // rows of this warp's 32 that exist
+                const int64_t pitch = 2 * (int64_t)p.N;
+                uint8_t* out = (uint8_t*)p.out + (int64_t)(x.x + (warp & 3) * 32) * pitch + 2 * n0;
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok && p.vec == 2 && n0 + 128 <= p.N) {
+                    if (p.dtype == EP_FP16) store_rows<true>(out, pitch, acc, m);
+                    else store_rows<false>(out, pitch, acc, m);
+                } else if (ok && lane < m && n0 < p.N) {
+                    if (p.dtype == EP_FP16) store_row<true>(out + lane * pitch, acc, p.N - n0, p.vec);
+                    else store_row<false>(out + lane * pitch, acc, p.N - n0, p.vec);
                 }
             } else {
                 const int n0 = x.z + part * 64;
@@ -431,7 +478,7 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
                 ok &= bar_wait(topped, parity, giveup);
                 const float scale = e4m3_block_scale(fmaxf(top, tops[parity][part ^ 1][row]));
                 const float inv = __frcp_rn(scale);
-                if (ok && present) {
+                if (ok && x.x + row < x.y) {
                     if (part == 0) p.out_scales[(int64_t)(x.x + row) * ((p.N + 127) / 128) + x.z / 128] = scale;
                     uint8_t* out = (uint8_t*)p.out + (int64_t)(x.x + row) * p.N + n0;
 #pragma unroll
