@@ -295,7 +295,8 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
                 const int y0 = (int)(b_rows + x.n0), y1 = (int)(b_rows + (SWIGLU ? p.N + x.n0 : x.n0 + 128));
                 for (int k = 0; k < kb; ++k, ++n) {
                     const uint32_t s = n % kStages, use = n / kStages;
-                    if (use > 0 && !bar_wait(done + 8 * s, (use - 1) & 1, giveup)) { ok = false; break; }
+                    if (use > 0 && !bar_wait(done + 8 * s, (use - 1) & 1, giveup)) ok = false;
+                    if (n == kWithheldBlock || !ok) { ok = false; break; }
                     const uint32_t dst = stages + s * kStageBytes, bar = full + 8 * s;
                     bar_expect(bar, kStageBytes);
                     tma_load(dst, &map_a, k * kBlockK, x.m0, bar);
@@ -600,7 +601,8 @@ ep_product_few_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap ma
                 const Tile x = find_tile<T, kFewCols>(p, off, first, col_tiles, t);
                 const int y = (int)((int64_t)x.g * p.columns + x.n0);
                 for (int k = k_lo; k < k_hi; ++k, ++n) {
-                    if (n >= (uint32_t)stage_count && !bar_wait(done + 8 * s, phase, giveup)) { ok = false; break; }
+                    if (n >= (uint32_t)stage_count && !bar_wait(done + 8 * s, phase, giveup)) ok = false;
+                    if (n == kWithheldBlock || !ok) { ok = false; break; }
                     const uint32_t dst = stages + s * S::kStageBytes, bar = full + 8 * s;
                     bar_expect(bar, S::kStageBytes);
                     tma_load(dst, &map_b, k * kBlockK, y, bar);

@@ -13,7 +13,18 @@
 namespace ep {
 
 // a second and a half at 2 GHz; the longest legitimate wait is a tile's, under a millisecond
-constexpr long long kWaitCycles = 3ll << 30;
+#ifndef EP_WAIT_CYCLES
+#define EP_WAIT_CYCLES (3ll << 30)
+#endif
+constexpr long long kWaitCycles = EP_WAIT_CYCLES;
+
+// Test builds (EP_TEST_WITHHOLD_LOAD): block 2 of every loading warp is never loaded, so that the waits
+// for it run out.
+#ifdef EP_TEST_WITHHOLD_LOAD
+constexpr uint32_t kWithheldBlock = 2;
+#else
+constexpr uint32_t kWithheldBlock = ~0u;
+#endif
 
 // a thread that waits sleeps for up to this long before it looks again: polling slows the barriers down
 constexpr uint32_t kSuspendNs = 1000000;
