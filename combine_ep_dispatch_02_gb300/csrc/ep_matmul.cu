@@ -67,6 +67,8 @@ constexpr int kFactors = 3;            // factors of a row and block: per half, 
 constexpr int kRing = 8;               // blocks of factors: a block is written when the block kStages before it has
                                        // been multiplied, while those up to kStages + 1 before it may be unread
 constexpr int kRingFloats = kRing * kFactors * kTileRows;
+constexpr int kSharedBlocks = 24;     // blocks of K from which CTAs may share a tile of 128 rows
+constexpr int kMaxSplit = 8;          // CTAs that share a tile's K, at most: 1, 2, 4 or 8
 constexpr int kSharedOffsets = 512;    // groups whose offsets are copied to shared memory
 
 struct Tile {
@@ -234,8 +236,82 @@ __device__ __forceinline__ void read_wait(uint32_t buf)
     asm volatile("bar.sync %0, %1;" :: "r"(1 + buf), "n"(kReadThreads) : "memory");
 }
 
+// 4 consecutive 16-bit outputs at element `at`, `left` of which exist.
+__device__ __forceinline__ void store4(const MatmulArgs& p, int64_t at, const float4& v, int left)
+{
+    uint2 w;
+    if (p.dtype == EP_FP16) w = make_uint2(pack2<true>(v.x, v.y), pack2<true>(v.z, v.w));
+    else w = make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
+    uint16_t* out = (uint16_t*)p.out + at;
+    if (p.vec >= 1 && left >= 4) {
+        *reinterpret_cast<uint2*>(out) = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < left) out[i] = (uint16_t)((i < 2 ? w.x : w.y) >> (16 * (i & 1)));
+    }
+}
+
+// A tile whose K the S CTAs of a cluster shared: this CTA finishes rows r .. r_end - 1 of those that are
+// kScaleWarps apart, from every CTA's sums at address `sums`, added in the CTAs' order.  A lane takes 4
+// columns and the 4 that are 128 further on; 16 loads are on their way before the first is added, from all
+// CTAs alike, so that no CTA's shared memory is asked by all of them at once.
+template <bool SWIGLU, int S>
+__device__ __forceinline__ void finish_rows(const MatmulArgs& p, const Tile& x, uint32_t sums, int r, int r_end)
+{
+    constexpr int kRows = 8 / S;
+    const int lane = threadIdx.x & 31;
+    for (; r < r_end; r += kRows * kScaleWarps) {
+        float4 part[kRows][S][2];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int row = min(r + i * kScaleWarps, r_end - 1);
+#pragma unroll
+            for (int q = 0; q < S; ++q)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    part[i][q][c] = peer_load4(peer_smem(sums, q) + row * (4 * kTileCols) + (((32 * c + lane) ^ (row & 7)) << 4));
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int row = r + i * kScaleWarps;
+            if (row >= r_end) break;
+            float4 v[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                v[c] = part[i][0][c];
+#pragma unroll
+                for (int q = 1; q < S; ++q) {
+                    v[c].x += part[i][q][c].x;
+                    v[c].y += part[i][q][c].y;
+                    v[c].z += part[i][q][c].z;
+                    v[c].w += part[i][q][c].w;
+                }
+            }
+            const int64_t at = (int64_t)(x.m0 + row) * p.N + x.n0 + 4 * lane;
+            const int left = p.N - x.n0 - 4 * lane;
+            if constexpr (!SWIGLU) {
+                store4(p, at, v[0], left);
+                store4(p, at + 128, v[1], left - 128);
+            } else {   // left is a multiple of 4: N is one of 16
+                const float z[4] = {swiglu(v[0].x, v[1].x), swiglu(v[0].y, v[1].y), swiglu(v[0].z, v[1].z),
+                                    swiglu(v[0].w, v[1].w)};
+                float top = left > 0 ? fmaxf(fmaxf(fabsf(z[0]), fabsf(z[1])), fmaxf(fabsf(z[2]), fabsf(z[3]))) : 0.0f;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float scale = e4m3_block_scale(top);
+                if (lane == 0) p.out_scales[(int64_t)(x.m0 + row) * ((p.N + 127) / 128) + x.n0 / 128] = scale;
+                if (left > 0)
+                    *reinterpret_cast<uint32_t*>((uint8_t*)p.out + at) =
+                        e4m3x4_near(z[0], z[1], z[2], z[3], scale, __frcp_rn(scale));
+            }
+        }
+    }
+}
+
 // SPLIT: with SwiGLU, an up block of 128 scales may end inside a tile (N is no multiple of 128).
-template <bool SWIGLU, bool SPLIT>
+// KSPLIT: the CTAs of a cluster share one tile, a part of K each, and each finishes a part of its rows.
+template <bool SWIGLU, bool SPLIT, bool KSPLIT>
 __global__ void __launch_bounds__(kProductThreads, 1)
 ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap map_a,
                        const __grid_constant__ CUtensorMap map_b)
@@ -256,7 +332,10 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
     const Giveup giveup{&gave_up, p.status};
     constexpr int kCols = SWIGLU ? kTileCols / 2 : kTileCols;   // output columns of a tile
     const int col_tiles = (p.N + kCols - 1) / kCols;
-    const int kb = p.kb;
+    const int ctas = KSPLIT ? cluster_size() : 1, rank = KSPLIT ? cluster_rank() : 0;
+    const int t_first = KSPLIT ? blockIdx.x / ctas : blockIdx.x, t_step = KSPLIT ? gridDim.x / ctas : gridDim.x;
+    const int k_lo = KSPLIT ? p.kb * rank / ctas : 0, k_hi = KSPLIT ? p.kb * (rank + 1) / ctas : p.kb;
+    const int kb = k_hi - k_lo;   // blocks of this CTA; one at least
 
     if (threadIdx.x == 0) {
         gave_up = 0;
@@ -281,19 +360,20 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = tmem_slot;
-    const int tiles = uniform(first[p.groups]);
+    // with KSPLIT there is a cluster for every tile, unless the offsets overlap
+    const int tiles = uniform(KSPLIT ? min(first[p.groups], t_step) : first[p.groups]);
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 0 && lane == 0) {
             uint32_t n = 0, i = 0;   // blocks loaded, tiles
             bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++i) {
+            for (int t = t_first; t < tiles && ok; t += t_step, ++i) {
                 const Tile x = find_tile<kTileRows, kCols>(p, off, first, col_tiles, t);
                 info[i % kInfo] = make_int4(x.m0, x.m1, x.n0, 0);   // seen by whoever sees the block's products
                 const int64_t b_rows = (int64_t)x.g * p.columns;
                 const int y0 = (int)(b_rows + x.n0), y1 = (int)(b_rows + (SWIGLU ? p.N + x.n0 : x.n0 + 128));
-                for (int k = 0; k < kb; ++k, ++n) {
+                for (int k = k_lo; k < k_hi; ++k, ++n) {
                     const uint32_t s = n % kStages, use = n / kStages;
                     if (use > 0 && !bar_wait(done + 8 * s, (use - 1) & 1, giveup)) ok = false;
                     if (n == kWithheldBlock || !ok) { ok = false; break; }
@@ -309,7 +389,7 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
         } else if (warp == 1) {
             constexpr uint32_t instruction = mma_instruction(kTileRows, kTileCols);
             const uint64_t a0 = mma_descriptor(stages), b0 = mma_descriptor(stages + kTileRows * kBlockK);
-            const uint32_t mine = tiles > (int)blockIdx.x ? (tiles - blockIdx.x - 1) / gridDim.x + 1 : 0;
+            const uint32_t mine = tiles > t_first ? (tiles - t_first - 1) / t_step + 1 : 0;
             const uint32_t blocks = mine * kb;
             const bool leader = elect_one();
             // After a wait that gave up the products go on, on whatever the stages hold: the others have
@@ -343,15 +423,15 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
             const int last = p.nb - 1;
             uint32_t n = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (int t = t_first; t < tiles && ok; t += t_step) {
                 const Tile x = find_tile<kTileRows, kCols>(p, off, first, col_tiles, t);
-                const float* as0 = p.as + (int64_t)min(x.m0 + r, x.m1 - 1) * kb;
-                const float* as1 = p.as + (int64_t)min(x.m0 + r + 64, x.m1 - 1) * kb;
-                const float* bs = p.bs + (int64_t)x.g * p.nb * kb;
+                const float* as0 = p.as + (int64_t)min(x.m0 + r, x.m1 - 1) * p.kb + k_lo;
+                const float* as1 = p.as + (int64_t)min(x.m0 + r + 64, x.m1 - 1) * p.kb + k_lo;
+                const float* bs = p.bs + (int64_t)x.g * p.nb * p.kb + k_lo;
                 const int up = (SWIGLU ? p.N + x.n0 : x.n0 + 128) / 128;
-                const float* bs0 = bs + (int64_t)min(x.n0 / 128, last) * kb;
-                const float* bs1 = bs + (int64_t)min(up, last) * kb;
-                const float* bs2 = bs + (int64_t)min(up + 1, last) * kb;
+                const float* bs0 = bs + (int64_t)min(x.n0 / 128, last) * p.kb;
+                const float* bs1 = bs + (int64_t)min(up, last) * p.kb;
+                const float* bs2 = bs + (int64_t)min(up + 1, last) * p.kb;
                 constexpr int kAhead = 4;
                 float a0[kAhead], a1[kAhead], b0[kAhead], b1[kAhead], b2[kAhead];
                 auto load = [&](int i, int k) {
@@ -404,7 +484,7 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
         uint32_t next = done, phase = 0, d = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         uint32_t f = smem_u32(ring) + 4 * (row + (SWIGLU ? 0 : part * kTileRows));
         const uint32_t f_end = f + kRing * kFactors * kTileRows * 4;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x, parity ^= 1, ++i) {
+        for (int t = t_first; t < tiles; t += t_step, parity ^= 1, ++i) {
             float2 acc[64];
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.0f, 0.0f);
@@ -450,7 +530,16 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
                 else add_scaled(acc + 48, r1, g1);
             }
             const int4 x = info[i % kInfo];
-            if constexpr (!SWIGLU) {
+            if constexpr (KSPLIT) {
+                // the cluster's only tile: every load has arrived and been multiplied, so the stages hold the
+                // sums, [row][256 columns], 16-byte pieces exchanged so that neither side meets a bank twice
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const uint32_t piece = ((j < 16 ? col0 : col1 - 64) >> 2) + j;
+                    smem_store4(stages + row * (4 * kTileCols) + ((piece ^ (row & 7)) << 4), acc[2 * j], acc[2 * j + 1]);
+                }
+                if (!ok) gave_up = 1;
+            } else if constexpr (!SWIGLU) {
                 const int n0 = x.z + part * 128, m = x.y - x.x - (warp & 3) * 32;   // rows of this warp's 32 that exist
                 const int64_t pitch = 2 * (int64_t)p.N;
                 uint8_t* out = (uint8_t*)p.out + (int64_t)(x.x + (warp & 3) * 32) * pitch + 2 * n0;
@@ -504,6 +593,18 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
     }
     tmem_fence_before();
     __syncthreads();
+    if constexpr (KSPLIT) {
+        cluster_sync();   // the sums of every CTA are there
+        if (warp >= 4 && t_first < tiles && !gave_up) {
+            const Tile x = find_tile<kTileRows, kCols>(p, off, first, col_tiles, t_first);
+            const int per = kTileRows / ctas;   // rows this CTA finishes, a warp every eighth
+            const int r = rank * per + warp - 4, r_end = min((rank + 1) * per, x.m1 - x.m0);
+            if (ctas == 2) finish_rows<SWIGLU, 2>(p, x, stages, r, r_end);
+            else if (ctas == 4) finish_rows<SWIGLU, 4>(p, x, stages, r, r_end);
+            else finish_rows<SWIGLU, 8>(p, x, stages, r, r_end);
+        }
+        cluster_sync();   // every CTA has taken what it needs of this one's sums
+    }
     if (warp == 2) {
         tmem_fence_after();
         tmem_free(tmem, 512);
@@ -513,7 +614,7 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
 // ---- few rows
 //
 // With few rows to a group the time is that of reading b once.  Here b's rows are the 128 lanes of the
-// accumulator and the T <= 64 rows of a tile its columns: a CTA takes 128 output columns (with SwiGLU
+// accumulator and the T rows of a tile, 16 or 32, its columns: a CTA takes 128 output columns (with SwiGLU
 // also their 128 up rows) and T rows, and streams b through as many stages as shared memory holds
 // (130-180 KB in flight on an SM; the rows' codes come from L2).  Tiles are small enough to spread the
 // weights evenly, and where there are too few of them for the SMs a cluster of CTAs splits K: each
@@ -525,7 +626,6 @@ constexpr int kFewCols = 128;
 constexpr int kFewRing = 16;          // blocks of factors: at least stages + accumulators
 constexpr int kFewMaxStages = 12;
 constexpr int kFewReadThreads = 128 + 32;
-constexpr int kMaxSplit = 8;
 
 template <int T, bool SWIGLU>
 struct FewShape {
@@ -534,7 +634,7 @@ struct FewShape {
     static constexpr int kStageBytes = kHalves * kWeightBytes + T * kBlockK;
     static constexpr int kBufferCols = kHalves * T;
     // accumulators: no more than stages, so that a stage's barrier is never a whole phase ahead of a reader
-    static constexpr int kBuffers = kBufferCols > 64 ? 2 : 4;
+    static constexpr int kBuffers = 4;
     static constexpr int kTmemCols = kBuffers * kBufferCols < 32 ? 32 : kBuffers * kBufferCols;
     static constexpr int kFactorRows = SWIGLU ? 3 : 1;   // gate, and the two up blocks a tile can touch
     static constexpr int kRingFloats = kFewRing * kFactorRows * T;
@@ -837,19 +937,58 @@ int make_map(CUtensorMap* m, const char* what, const void* base, int64_t rows, i
     return EP_OK;
 }
 
+template <typename... Params, typename... Args>
+cudaError_t launch_cluster(void (*k)(Params...), unsigned grid, int threads, size_t smem, int ctas, cudaStream_t s,
+                           const Args&... args)   // launch_dependent with clusters of `ctas`
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+// Tiles, at most, of `rows` rows in groups: every group that holds a row can end inside a tile.
+int64_t most_tiles(const MatmulArgs& p, int rows, int cols)
+{
+    const int64_t groups = p.groups < p.rows ? p.groups : p.rows;
+    return ((p.rows - groups) / rows + groups) * ((p.N + cols - 1) / cols);
+}
+
+// CTAs that share a tile's K, each at least `least` blocks: 1, 2 or 4 while they fit the SMs; 8 only for a few
+// tiles, because a GPC's 16 to 20 SMs hold two clusters of 8 at most and 16 clusters do not all run at once
+// (one row, 7168 x 4096 with SwiGLU: 13.7 us in 8, 9.2 in 4, 13.1 in 2).
+int split_of(const MatmulArgs& p, int64_t tiles, int least, int sms)
+{
+    int split = 1;
+    while (split < (tiles <= 8 ? kMaxSplit : 4) && tiles * split * 2 <= sms && split * 2 * least <= p.kb) split *= 2;
+    return split;
+}
+
 template <bool SWIGLU, bool SPLIT>
 cudaError_t launch_product_rows(const MatmulArgs& p, const CUtensorMap& ma, const CUtensorMap& mb, int sms,
                                 cudaStream_t s)
 {
-    const int cols = SWIGLU ? kTileCols / 2 : kTileCols;
-    const int64_t most = (p.rows / kTileRows + p.groups) * ((p.N + cols - 1) / cols);   // tiles, at most
+    const int64_t most = most_tiles(p, kTileRows, SWIGLU ? kTileCols / 2 : kTileCols);
+    // The sums' exchange costs what half a dozen blocks do.  256 rows, us, whole against shared: 7168 x 2048
+    // 22.1 : 12.8 in 4, 4096 x 1024 14.2 : 10.6 in 4, 2048 x 7168 (16 blocks) 9.4 : 10.8 in 2.
+    const int split = p.kb < kSharedBlocks ? 1 : split_of(p, most, 7, sms);
     const size_t smem = 1024 + kStages * kStageBytes + kRingFloats * sizeof(float) + (p.groups + 1) * sizeof(int) +
                         (p.offsets && p.groups <= kSharedOffsets ? (p.groups + 1) * sizeof(int32_t) : 0);
-    cudaError_t e = cudaFuncSetAttribute(ep_product_rows_kernel<SWIGLU, SPLIT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    auto* kernel = split > 1 ? ep_product_rows_kernel<SWIGLU, SPLIT, true> : ep_product_rows_kernel<SWIGLU, SPLIT, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(ep_product_rows_kernel<SWIGLU, SPLIT>, dim3((unsigned)(most < sms ? most : sms)),
-                            dim3(kProductThreads), smem, s, p, ma, mb);
+    const int64_t grid = split > 1 ? most * split : most < sms ? most : sms;
+    return launch_cluster(kernel, (unsigned)grid, kProductThreads, smem, split, s, p, ma, mb);
 }
 
 template <int T, bool SWIGLU>
@@ -857,53 +996,38 @@ cudaError_t launch_product_few(const MatmulArgs& p, const CUtensorMap& ma, const
                                cudaStream_t s)
 {
     using S = FewShape<T, SWIGLU>;
-    const int64_t groups = p.groups < p.rows ? p.groups : p.rows;   // that can hold a row
-    const int64_t most = ((p.rows - groups) / T + groups) * ((p.N + kFewCols - 1) / kFewCols);   // tiles, at most
-    // K split in up to 4 while the CTAs fit the SMs; in 8 only for a few tiles, because a GPC's 16 to 20 SMs
-    // hold two clusters of 8 at most and 16 clusters do not all run at once (one row, 7168 x 4096 with
-    // SwiGLU: 13.7 us in 8, 9.2 in 4, 13.1 in 2)
-    int split = 1;
-    while (split < (most <= 8 ? 8 : 4) && most * split * 2 <= sms && split * 2 <= p.kb) split *= 2;
+    const int64_t most = most_tiles(p, T, kFewCols);
+    const int split = split_of(p, most, 1, sms);
     const size_t rest = 1024 + (S::kSumFloats + S::kRingFloats) * sizeof(float) + (p.groups + 1) * sizeof(int) +
                         (p.offsets && p.groups <= kSharedOffsets ? (p.groups + 1) * sizeof(int32_t) : 0);
     constexpr size_t kMost = 227 * 1024 - 4096;   // less the static part
     int stages = (int)((kMost - rest) / S::kStageBytes);
     if (stages > kFewMaxStages) stages = kFewMaxStages;
-    if (stages < S::kBuffers) return cudaErrorInvalidConfiguration;   // not reached: 3 stages at the least
+    if (stages < S::kBuffers) return cudaErrorInvalidConfiguration;   // not reached: 4 stages at the least
     const size_t smem = rest + (size_t)stages * S::kStageBytes;
     auto* kernel = ep_product_few_kernel<T, SWIGLU>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t clusters = most < sms / split ? most : sms / split;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(clusters * split));
-    cfg.blockDim = dim3(kFewThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // as launch_dependent
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = split;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p, ma, mb, stages, split);
+    return launch_cluster(kernel, (unsigned)(clusters * split), kFewThreads, smem, split, s, p, ma, mb, stages, split);
 }
 
 // Rows of a tile of the kernel for few rows, or 0 for the kernel of 128-row tiles.  Measured, us, few rows
-// against 128-row tiles, at 7168 x 4096 with SwiGLU:
-//   one group     1 row 9.2 : 24.2   32 rows 11.4 : 24.2   64 rows 13.4 : 24.5   100 rows 18.8 : 24.7
-//   32 groups     of 8 rows 145 : 152   of 16 rows 152 : 153   of 24 rows 167 : 153
-// One group has only col_tiles tiles of 128 rows, which leave most SMs idle; several groups have enough of
-// them, and a group whose rows pass the tile reads its weights twice.  Two tiles of 16 rows or 32 run side
-// by side and finish before one of twice the rows.
-int few_rows_tile(const MatmulArgs& p)
+// against 128-row tiles:
+//   one group, 7168 x 4096 with SwiGLU     1 row 8.5 : 11.9   32 rows 11.0 : 13.2   64 rows 12.9 : 13.5
+//                                          96 rows 18.3 : 13.9
+//   4 groups, 7168 x 2048                  of 4 rows 14.8 : 16.4   of 8 rows 16.1 : 15.7   of 16 rows 18.8 : 16.5
+//   32 groups, 7168 x 4096 with SwiGLU     of 8 rows 145 : 152   of 16 rows 152 : 153   of 24 rows 167 : 153
+// The 128-row tiles multiply rows that are not there, which costs them nothing while the weights' bytes or
+// the tiles' number set the time; a group whose rows pass a tile of few reads its weights twice.
+int few_rows_tile(const MatmulArgs& p, int sms)
 {
-    if (p.groups == 1) return p.rows <= 32 ? 16 : p.rows <= 64 ? 32 : p.rows <= 128 ? 64 : 0;
+    if (p.groups == 1) return p.rows <= 32 ? 16 : p.rows <= 64 ? 32 : 0;
     const int64_t groups = p.groups < p.rows ? p.groups : p.rows;   // that can hold a row
     const int64_t mean = p.rows / groups;
-    return mean <= 8 ? 16 : mean <= 16 ? 32 : 0;
+    // with K shared, 128-row tiles win from 8 rows a group on; without, from 16
+    const bool shared = 2 * most_tiles(p, kTileRows, p.swiglu ? kTileCols / 2 : kTileCols) <= sms && p.kb >= kSharedBlocks;
+    return mean < 8 || (mean == 8 && !shared) ? 16 : mean <= 16 && !shared ? 32 : 0;
 }
 
 }  // namespace
@@ -948,7 +1072,7 @@ extern "C" int ep_matmul_fp8(const void* a, const float* a_scales, const void* b
     const int sms = layer_num_sms();
     if (sms == 0) return layer_fail(EP_ERR_CUDA, "%s: cannot tell the current device's multiprocessors", who);
     // rows of a tile of the kernel for few rows, or 0 for the kernel of 128-row tiles
-    const int few = few_rows_tile(p);
+    const int few = few_rows_tile(p, sms);
     CUtensorMap ma, mb;
     if (int rc = make_map(&ma, "a", a, rows, inner, few ? few : kTileRows)) return rc;
     if (int rc = make_map(&mb, "b", b, (int64_t)groups * columns, inner, 128)) return rc;
@@ -956,7 +1080,6 @@ extern "C" int ep_matmul_fp8(const void* a, const float* a_scales, const void* b
     cudaError_t e;
     if (few == 16) e = swiglu ? launch_product_few<16, true>(p, ma, mb, sms, s) : launch_product_few<16, false>(p, ma, mb, sms, s);
     else if (few == 32) e = swiglu ? launch_product_few<32, true>(p, ma, mb, sms, s) : launch_product_few<32, false>(p, ma, mb, sms, s);
-    else if (few == 64) e = swiglu ? launch_product_few<64, true>(p, ma, mb, sms, s) : launch_product_few<64, false>(p, ma, mb, sms, s);
     else if (!swiglu) e = launch_product_rows<false, false>(p, ma, mb, sms, s);
     else if (p.N % 128 == 0) e = launch_product_rows<true, false>(p, ma, mb, sms, s);
     else e = launch_product_rows<true, true>(p, ma, mb, sms, s);

@@ -52,6 +52,11 @@ __device__ __forceinline__ float smem_load(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ void smem_store4(uint32_t addr, const float2& lo, const float2& hi)
+{
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "f"(lo.x), "f"(lo.y), "f"(hi.x), "f"(hi.y) : "memory");
+}
+
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count)
 {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(count) : "memory");
@@ -122,6 +127,13 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t n;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    return n;
+}
+
 // The address in CTA `rank` of the cluster that corresponds to this CTA's shared-memory address.
 __device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank)
 {
@@ -134,6 +146,14 @@ __device__ __forceinline__ float peer_load(uint32_t addr)
 {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 peer_load4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
 }
 
@@ -154,6 +174,7 @@ __device__ __forceinline__ bool peer_wait(uint32_t bar, uint32_t parity, const G
 // No CTA of the cluster leaves while another may still reach its shared memory.
 __device__ __forceinline__ void cluster_sync()
 {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
