@@ -340,8 +340,10 @@ int ep_probe_read(ep_plan* p, uint64_t* ns_host, int n_words);
  * Expert-layer operators: the steps of a mixture-of-experts layer around dispatch and combine.  They
  * take caller-owned memory only (outputs, workspace, status word), run on the current device, enqueue
  * on `stream` and return without waiting.  device_status is one int32 on the device: the first problem
- * only the GPU can see is recorded there and the work it concerns is skipped; no call clears it.
- * Arrays are dense and row-major unless a stride is given.  Scales are FP32, one per 128 elements of
+ * only the GPU can see is recorded there and the work it concerns is skipped; no call clears it.  Their
+ * kernels are launched as programmatic dependents of what precedes them on the stream (set-up overlaps
+ * its tail, no memory is touched before it has completed): results and stream order are those of plain
+ * launches.  Arrays are dense and row-major unless a stride is given.  Scales are FP32, one per 128 elements of
  * a row (the last block may be shorter): ceil(n / 128) per row of n.
  *
  * ep_rms_norm_fp8: the residual's addition and the RMS norm, quantised to the rows and scales an
@@ -419,9 +421,11 @@ int ep_return_rows_backward(const void* y, const float* weights, const void* dou
  *   inner        a multiple of 16 up to 2^20;  groups up to 4096;  columns up to 2^20
  * swiglu = 0: out [rows][columns], EP_BF16 or EP_FP16 by dtype, rounded once; out_scales is not used.
  * swiglu = 1 (dtype EP_FP8_E4M3, columns a multiple of 32): the first half of b's columns is the gate,
- * the second the up projection; z = gate * sigmoid(gate) * up in FP32 is quantised as by ep_rms_norm_fp8:
- * out [rows][columns/2] codes, out_scales [rows][ceil(columns/256)].
- * a, b and out are 16-byte aligned.
+ * the second the up projection; z = gate * sigmoid(gate) * up in FP32 is quantised as by ep_rms_norm_fp8,
+ * by the scale's reciprocal: out [rows][columns/2] codes, out_scales [rows][ceil(columns/256)].
+ * a, b and out are 16-byte aligned.  The result does not depend on timing: sums are added in a fixed order.
+ * A bounded wait that runs out on the GPU is recorded as EP_ERR_DEVICE_TIMEOUT; out is then not valid.
+ * The first call on a device looks up a driver entry point and should come before any stream capture.
  */
 int ep_matmul_fp8(const void* a, const float* a_scales, const void* b, const float* b_scales,
                   const int32_t* offsets, int64_t rows, int groups, int columns, int inner, int swiglu, int dtype,
