@@ -106,27 +106,38 @@ __device__ __forceinline__ void scan_tiles(const MatmulArgs& p, int* first, int 
     if (lane == 0) first[p.groups] = carry;
 }
 
-// Tile t: groups in order; within a group, chunks of kChunkTiles row tiles, whose rows and the group's
-// weights stay in L2 while the chunk is done; within a chunk, row tiles before columns.
+// a / b for whole numbers, b > 0, without an integer division where a is small: (a + 0.5) / b is at least
+// 0.5 / b away from a whole number, and below 2^21 the float quotient is off by less.
+__device__ __forceinline__ int quick_div(int a, int b)
+{
+    if (a < 1 << 21) return (int)__fdividef((float)a + 0.5f, (float)b);
+    return a / b;
+}
+
+// Tile t, by a converged warp: groups in order; within a group, chunks of kChunkTiles row tiles, whose rows and
+// the group's weights stay in L2 while the chunk is done; within a chunk, row tiles before columns.
 template <int ROWS, int COLS>
 __device__ __forceinline__ Tile find_tile(const MatmulArgs& p, const int32_t* off, const int* first, int col_tiles,
                                           int t)
 {
-    int lo = 0, hi = p.groups;   // first[lo] <= t < first[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first[mid] <= t) lo = mid;
-        else hi = mid;
+    // the last group whose first tile is not past t, 32 candidates at a time
+    int lo = 0;
+    for (int n = p.groups; n > 1;) {
+        const int step = (n + 31) >> 5, at = lo + (int)(threadIdx.x & 31) * step;
+        const unsigned m = __ballot_sync(0xffffffffu, at < lo + n && first[min(at, p.groups)] <= t);
+        const int skip = (__popc(m) - 1) * step;
+        lo += skip;
+        n = min(step, n - skip);
     }
     Tile x;
     x.g = lo;
     int r0;
     group_rows(p, off, lo, r0, x.m1);
     const int tiles = (x.m1 - r0 + ROWS - 1) / ROWS;
-    const int in = t - first[lo];
-    const int chunk = in / (kChunkTiles * col_tiles), rest = in - chunk * kChunkTiles * col_tiles;
+    const int in = t - first[lo], wide_tiles = kChunkTiles * col_tiles;
+    const int chunk = quick_div(in, wide_tiles), rest = in - chunk * wide_tiles;
     const int wide = min(kChunkTiles, tiles - chunk * kChunkTiles);
-    const int col = rest / wide;
+    const int col = quick_div(rest, wide);
     x.m0 = r0 + (chunk * kChunkTiles + rest - col * wide) * ROWS;
     x.n0 = col * COLS;
     return x;
@@ -151,35 +162,13 @@ __device__ __forceinline__ void add_scaled(float2* acc, const uint32_t (&r)[32],
     }
 }
 
-// 128 consecutive columns of one output row, 16-bit; n of them exist.
+// 128 consecutive columns, n of which exist, of a warp's 32 rows, m of which exist (row by lane, rows `pitch`
+// bytes apart), 16-bit.  A store of 32 bytes by every lane to a row of its own visits 32 lines, two
+// cycles each, 4000 for a tile.  So four lanes first trade 32-byte pieces, two exchanges of half of
+// them, until lane q of the four holds piece q (then q + 4) of all four rows: a store then writes 128
+// bytes each of 8 rows.
 template <bool FP16>
-__device__ __forceinline__ void store_row(uint8_t* out, const float2 (&acc)[64], int n, int vec)
-{
-#pragma unroll
-    for (int c = 0; c < 128; c += 16) {
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = pack2<FP16>(acc[c / 2 + i].x, acc[c / 2 + i].y);
-        if (vec == 2 && c + 16 <= n) {
-            st_v8(out + 2 * c, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
-        } else if (vec >= 1 && c + 16 <= n) {
-            st_v4(out + 2 * c, make_uint4(w[0], w[1], w[2], w[3]));
-            st_v4(out + 2 * c + 16, make_uint4(w[4], w[5], w[6], w[7]));
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (c + i < n) reinterpret_cast<uint16_t*>(out)[c + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
-        }
-    }
-}
-
-// The same for a warp's 32 rows, m of which exist (row by lane, rows `pitch` bytes apart), where all 128
-// columns exist and rows are 32-byte aligned.  A store of 32 bytes by every lane to a row of its own
-// visits 32 lines, two cycles each, 4000 for a tile.  So four lanes first trade 32-byte pieces, two
-// exchanges of half of them, until lane q of the four holds piece q (then q + 4) of all four rows: a
-// store then writes 128 bytes each of 8 rows.
-template <bool FP16>
-__device__ __forceinline__ void store_rows(uint8_t* out, int64_t pitch, const float2 (&acc)[64], int m)
+__device__ __forceinline__ void store_rows(uint8_t* out, int64_t pitch, const float2 (&acc)[64], int m, int n, int vec)
 {
     const int lane = threadIdx.x & 31, q = lane & 3;
 #pragma unroll
@@ -206,12 +195,22 @@ __device__ __forceinline__ void store_rows(uint8_t* out, int64_t pitch, const fl
                 }
             }
         }
+        const int left = n - (64 * h + 16 * q);   // columns of this lane's pieces that exist
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int row = (lane & ~3) + r;
-            if (row < m)
-                st_v8(out + row * pitch + 128 * h + 32 * q, make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]),
-                      make_uint4(w[r][4], w[r][5], w[r][6], w[r][7]));
+            if (row >= m) break;
+            uint8_t* to = out + row * pitch + 128 * h + 32 * q;
+            if (vec == 2 && left >= 16) {
+                st_v8(to, make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]), make_uint4(w[r][4], w[r][5], w[r][6], w[r][7]));
+            } else if (vec == 1 && left >= 16) {
+                st_v4(to, make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]));
+                st_v4(to + 16, make_uint4(w[r][4], w[r][5], w[r][6], w[r][7]));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (i < left) reinterpret_cast<uint16_t*>(to)[i] = (uint16_t)(w[r][i / 2] >> (16 * (i & 1)));
+            }
         }
     }
 }
@@ -372,28 +371,33 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == 0 && lane == 0) {
+        if (warp == 0) {
             uint32_t n = 0, i = 0;   // blocks loaded, tiles
+            const bool leader = elect_one();
             bool ok = true;
             for (int t = t_first; t < tiles && ok; t += t_step, ++i) {
                 const Tile x = find_tile<kTileRows, kCols>(p, off, first, col_tiles, t);
-                info[i % kInfo] = make_int4(x.m0, x.m1, x.n0, 0);   // seen by whoever sees the block's products
-                const int64_t b_rows = (int64_t)x.g * p.columns;
-                const int y0 = (int)(b_rows + x.n0), y1 = (int)(b_rows + (SWIGLU ? p.N + x.n0 : x.n0 + 128));
-                for (int k = k_lo; k < k_hi; ++k, ++n) {
-                    const uint32_t s = n % kStages, use = n / kStages;
-                    if (use > 0 && !bar_wait(done + 8 * s, (use - 1) & 1, giveup)) ok = false;
-                    if (n == kWithheldBlock || !ok) { ok = false; break; }
-                    const uint32_t dst = stages + s * kStageBytes, bar = full + 8 * s;
-                    bar_expect(bar, kStageBytes);
-                    tma_load(dst, &map_a, k * kBlockK, x.m0, bar);
-                    tma_load(dst + kTileRows * kBlockK, &map_b, k * kBlockK, y0, bar);
-                    tma_load(dst + (kTileRows + 128) * kBlockK, &map_b, k * kBlockK, y1, bar);
+                if (leader) {
+                    info[i % kInfo] = make_int4(x.m0, x.m1, x.n0, 0);   // seen by whoever sees the block's products
+                    const int64_t b_rows = (int64_t)x.g * p.columns;
+                    const int y0 = (int)(b_rows + x.n0), y1 = (int)(b_rows + (SWIGLU ? p.N + x.n0 : x.n0 + 128));
+                    for (int k = k_lo; k < k_hi; ++k, ++n) {
+                        const uint32_t s = n % kStages, use = n / kStages;
+                        if (use > 0 && !bar_wait(done + 8 * s, (use - 1) & 1, giveup)) ok = false;
+                        if (n == kWithheldBlock || !ok) { ok = false; break; }
+                        const uint32_t dst = stages + s * kStageBytes, bar = full + 8 * s;
+                        bar_expect(bar, kStageBytes);
+                        tma_load(dst, &map_a, k * kBlockK, x.m0, bar);
+                        tma_load(dst + kTileRows * kBlockK, &map_b, k * kBlockK, y0, bar);
+                        tma_load(dst + (kTileRows + 128) * kBlockK, &map_b, k * kBlockK, y1, bar);
+                    }
                 }
+                ok = __all_sync(0xffffffffu, ok);
             }
-            if (!ok)   // its loads in flight
+            if (leader && !ok)   // its loads in flight
                 for (uint32_t j = n < kStages ? 0 : n - kStages; j < n; ++j)
                     bar_drain(full + 8 * (j % kStages), (j / kStages) & 1);
+            __syncwarp();
         } else if (warp == 1) {
             constexpr uint32_t instruction = mma_instruction(kTileRows, kTileCols);
             const uint64_t a0 = mma_descriptor(stages), b0 = mma_descriptor(stages + kTileRows * kBlockK);
@@ -432,6 +436,7 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
             uint32_t n = 0;
             bool ok = true;
             for (int t = t_first; t < tiles && ok; t += t_step) {
+                __syncwarp();
                 const Tile x = find_tile<kTileRows, kCols>(p, off, first, col_tiles, t);
                 const float* as0 = p.as + (int64_t)min(x.m0 + r, x.m1 - 1) * p.kb + k_lo;
                 const float* as1 = p.as + (int64_t)min(x.m0 + r + 64, x.m1 - 1) * p.kb + k_lo;
@@ -551,13 +556,9 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
                 const int n0 = x.z + part * 128, m = x.y - x.x - (warp & 3) * 32;   // rows of this warp's 32 that exist
                 const int64_t pitch = 2 * (int64_t)p.N;
                 uint8_t* out = (uint8_t*)p.out + (int64_t)(x.x + (warp & 3) * 32) * pitch + 2 * n0;
-                ok = __all_sync(0xffffffffu, ok);
-                if (ok && p.vec == 2 && n0 + 128 <= p.N) {
-                    if (p.dtype == EP_FP16) store_rows<true>(out, pitch, acc, m);
-                    else store_rows<false>(out, pitch, acc, m);
-                } else if (ok && lane < m && n0 < p.N) {
-                    if (p.dtype == EP_FP16) store_row<true>(out + lane * pitch, acc, p.N - n0, p.vec);
-                    else store_row<false>(out + lane * pitch, acc, p.N - n0, p.vec);
+                if (__all_sync(0xffffffffu, ok) && n0 < p.N) {
+                    if (p.dtype == EP_FP16) store_rows<true>(out, pitch, acc, m, p.N - n0, p.vec);
+                    else store_rows<false>(out, pitch, acc, m, p.N - n0, p.vec);
                 }
             } else {
                 const int n0 = x.z + part * 64;
@@ -604,7 +605,7 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
     if constexpr (KSPLIT) {
         cluster_sync();   // the sums of every CTA are there
         if (warp >= 4 && t_first < tiles && !gave_up) {
-            const Tile x = find_tile<kTileRows, kCols>(p, off, first, col_tiles, t_first);
+            const Tile x = find_tile<kTileRows, kCols>(p, off, first, col_tiles, t_first);   // whole warps
             const int per = kTileRows / ctas;   // rows this CTA finishes, a warp every eighth
             const int r = rank * per + warp - 4, r_end = min((rank + 1) * per, x.m1 - x.m0);
             if (ctas == 2) finish_rows<SWIGLU, 2>(p, x, stages, r, r_end);
@@ -706,11 +707,12 @@ ep_product_few_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap ma
     const int tiles = uniform(first[p.groups]);
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t n = 0, s = 0, phase = 1;
-            bool ok = true;
-            for (int t = t_first; t < tiles && ok; t += t_step) {
-                const Tile x = find_tile<T, kFewCols>(p, off, first, col_tiles, t);
+        uint32_t n = 0, s = 0, phase = 1;
+        const bool leader = elect_one();
+        bool ok = true;
+        for (int t = t_first; t < tiles && ok; t += t_step) {
+            const Tile x = find_tile<T, kFewCols>(p, off, first, col_tiles, t);
+            if (leader) {
                 const int y = (int)((int64_t)x.g * p.columns + x.n0);
                 for (int k = k_lo; k < k_hi; ++k, ++n) {
                     if (n >= (uint32_t)stage_count && !bar_wait(done + 8 * s, phase, giveup)) ok = false;
@@ -723,10 +725,12 @@ ep_product_few_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap ma
                     if (++s == (uint32_t)stage_count) { s = 0; phase ^= 1; }
                 }
             }
-            if (!ok)   // its loads in flight
-                for (uint32_t i = n < (uint32_t)stage_count ? 0 : n - stage_count; i < n; ++i)
-                    bar_drain(full + 8 * (i % stage_count), (i / stage_count) & 1);
+            ok = __all_sync(0xffffffffu, ok);
         }
+        if (leader && !ok)   // its loads in flight
+            for (uint32_t i = n < (uint32_t)stage_count ? 0 : n - stage_count; i < n; ++i)
+                bar_drain(full + 8 * (i % stage_count), (i / stage_count) & 1);
+        __syncwarp();
     } else if (warp == 1) {
         constexpr uint32_t instruction = mma_instruction(kFewCols, T);
         const uint64_t d0 = mma_descriptor(stages);
@@ -767,6 +771,7 @@ ep_product_few_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap ma
         uint32_t n = 0, s = 0, phase = 1;
         bool ok = true;
         for (int t = t_first; t < tiles && ok; t += t_step) {
+            __syncwarp();
             const Tile x = find_tile<T, kFewCols>(p, off, first, col_tiles, t);
             const float* as = p.as + (int64_t)min(x.m0 + c, x.m1 - 1) * p.kb;
             const float* bs = p.bs + (int64_t)x.g * p.nb * p.kb;
@@ -811,6 +816,7 @@ ep_product_few_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap ma
         uint32_t n = 0, s = 0, phase = 0, parity = 0;
         const int c_lo = T * rank / split_k, c_hi = T * (rank + 1) / split_k;   // the rows this CTA finishes
         for (int t = t_first; t < tiles; t += t_step, parity ^= 1) {
+            __syncwarp();
             const Tile x = find_tile<T, kFewCols>(p, off, first, col_tiles, t);
             const int up_row = (p.N + x.n0 + col) / 128 - (p.N + x.n0) / 128;   // 0 or 1: this column's up block
             float2 acc[S::kHalves][T / 2];
