@@ -93,11 +93,16 @@ def op_status(device=None) -> int:
 
 
 def _on(stream, call, *args):
-    """The call on the current stream, or on the caller's, where its outputs are then allocated too."""
+    """The call on the current stream, or on the caller's, where its outputs are then allocated too; memory of
+    its inputs that is freed is not reused before that stream is done with them."""
     if stream is None:
         return call(*args)
     with torch.cuda.stream(stream):
-        return call(*args)
+        out = call(*args)
+        for a in args:
+            if isinstance(a, torch.Tensor) and a.is_cuda:
+                a.record_stream(stream)
+        return out
 
 
 def rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,

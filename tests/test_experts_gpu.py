@@ -479,6 +479,59 @@ def test_product_is_deterministic(rows):
         assert torch.equal(one, ep.matmul_fp8(a, sa, b, sb, offsets=offsets))
 
 
+# ------------------------------------------------------------------------------------------- past 32 bits
+
+def test_norm_past_32_bits():
+    rows, hidden = 300000, 8192                                     # 2.46e9 elements
+    x = torch.empty(rows, hidden, dtype=torch.bfloat16, device=DEV)
+    x[-3:] = _randn(_gen(1), 3, hidden).to(x.dtype)
+    w = torch.ones(hidden, device=DEV)
+    q, s, h, _ = ep.rms_norm_fp8(x, w, residual=x)
+    q2, s2, h2, _ = ep.rms_norm_fp8(x[-3:], w, residual=x[-3:])
+    assert torch.equal(q[-3:].view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s[-3:], s2) and torch.equal(h[-3:], h2)
+
+
+def test_sorted_rows_and_return_past_32_bits():
+    R, k, E, H = 40000, 8, 16, 4096                                 # 320000 sorted rows of 8 KB: 2.6 GB
+    g = _gen(2)
+    idx = torch.rand(R, E, generator=g, device=DEV).topk(k, 1).indices.int()
+    x = _randn(g, R, H).to(torch.bfloat16)
+    order = ep.sort_by_expert(idx, E)
+    xs, _ = ep.sorted_rows(order, x)
+    last = order.src[-50:].long()
+    assert torch.equal(xs[-50:], x[last // k])
+    w = torch.softmax(_randn(g, R, k), 1)
+    rows = last // k                                                # rows with a slot at the far end
+    out = ep.return_rows(order, xs, w)
+    want = (x[rows].double()[:, None] * w[rows].double()[..., None])
+    _within(out[rows], want.sum(1), _half_bound(out.dtype, want.sum(1)) + 2 * 9 * U * want.abs().sum(1), "return")
+    dout = _randn(g, R, H).to(torch.bfloat16)
+    dy, dw = ep.return_rows_backward(order, xs, w, dout)
+    assert torch.equal(dy[-50:], (w.reshape(-1)[last][:, None] * dout[rows].float()).to(dy.dtype))
+    dots = x[rows].double() * dout[rows].double()
+    _within(dw[rows], dots.sum(1)[:, None].expand(-1, k), (H * U * dots.abs().sum(1))[:, None], "dweights")
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_product_past_32_bits(swiglu):
+    rows, K, N = 530000, 64, 8192                                   # 4.3e9 outputs, 2.2e9 with SwiGLU
+    g = _gen(3)
+    a, sa = _fp8_rows(g, rows, K)
+    b = (100 * _randn(g, 2, N, K)).clamp(-448, 448).to(F8)
+    sb = torch.rand(2, _blocks(N), 1, generator=g, device=DEV) * 1e-3
+    cut = rows - 200                                                # the last group is the last 200 rows
+    offsets = torch.tensor([0, cut, rows], dtype=torch.int32, device=DEV)
+    one = torch.tensor([0, 200, 200], dtype=torch.int32, device=DEV)
+    if swiglu:
+        q, s = ep.matmul_fp8_swiglu(a, sa, b, sb, offsets=offsets)
+        q2, s2 = ep.matmul_fp8_swiglu(a[cut:], sa[cut:], b.flip(0), sb.flip(0), offsets=one)
+        assert torch.equal(q[cut:].view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s[cut:], s2)
+        return
+    out = ep.matmul_fp8(a, sa, b, sb, offsets=offsets)
+    z, mag = _product64(a[cut:], sa[cut:], b[1], sb[1])
+    _within(out[cut:], z, _half_bound(out.dtype, z) + 2.02 * 131 * U * mag, "the last group")
+
+
 # ------------------------------------------------------------------------------------------- refusals
 
 def _zeros(shape, dtype):
@@ -612,3 +665,41 @@ def test_example_layer_agrees_with_fp32():
     assert expert_layer.main(["--tokens-per-rank", "33", "--hidden", "512", "--inner", "272", "--passes", "2"]) <= 2.0 ** -3
     assert expert_layer.main(["--ranks", "1", "--experts-per-rank", "4", "--topk", "2", "--tokens-per-rank", "1",
                               "--hidden", "256", "--passes", "1"]) <= 2.0 ** -3
+
+
+def test_back_to_back_calls_touch_nothing_early():
+    """A call's kernels are set up while the kernel before them still runs; their memory is the allocator's
+    and so often what that kernel reads.  Results of a stream of calls are those of calls one by one."""
+    g = _gen(21)
+    H, E, R, k = 512, 8, 24, 4
+    w = (1 + 0.1 * _randn(g, H)).to(torch.bfloat16)
+    _, _, b, sb = _product_inputs(g, 1, H, 2 * H, E)
+    _, _, b2, sb2 = _product_inputs(g, 1, H, H, E)
+    base = _randn(g, R, H).to(torch.bfloat16)
+    idx = torch.rand(R, E, generator=g, device=DEV).topk(k, 1).indices.int()
+    wt = torch.softmax(_randn(g, R, k), 1)
+
+    def passes(wait):
+        x, i, done = base.clone(), idx.clone(), []
+        step = torch.cuda.synchronize if wait else (lambda: None)
+        for _ in range(60):
+            q, s, h, y = ep.rms_norm_fp8(x, w, residual=x, want_y=True)
+            step()
+            i = (i + 1) % E
+            order = ep.sort_by_expert(i, E)
+            step()
+            xs, ss = ep.sorted_rows(order, q, s)
+            step()
+            z, zs = ep.matmul_fp8_swiglu(xs, ss, b, sb, offsets=order.offsets)
+            step()
+            o = ep.matmul_fp8(z, zs, b2, sb2, offsets=order.offsets)
+            step()
+            out = ep.return_rows(order, o, wt)
+            dy, dw = ep.return_rows_backward(order, o, wt, y)
+            step()
+            x = (0.5 * y.float() + 0.05 * out.float().tanh()).to(torch.bfloat16)
+            done += [x, dw, dy[:3].clone()]
+        torch.cuda.synchronize()
+        return done
+    for a, c in zip(passes(True), passes(False)):
+        assert torch.equal(a, c)
