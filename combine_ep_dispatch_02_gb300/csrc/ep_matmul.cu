@@ -64,15 +64,15 @@ __device__ __forceinline__ void group_rows(const MatmulArgs& p, const int32_t* o
 
 constexpr int kTileRows = 128, kTileCols = 256, kBlockK = 128;
 constexpr int kStages = 4;             // even: a stage always goes to the same accumulator
-constexpr int kStageBytes = (kTileRows + kTileCols) * kBlockK;
+__host__ __device__ constexpr int stage_bytes(int cols) { return (kTileRows + cols) * kBlockK; }
 constexpr int kScaleWarps = 8;         // two to a quarter of the lanes, 128 columns each
 constexpr int kScaleThreads = 32 * kScaleWarps;
 constexpr int kProductThreads = 128 + kScaleThreads;   // load, multiply, two factor warps; the scaling warps
-constexpr int kInfo = 8;               // tiles the loading warp may be ahead of the scaling warps: kStages + 2 at most
+constexpr int kInfo = 16;              // more tiles than the loading warp can be ahead of the scaling warps: 8
 constexpr int kChunkTiles = 16;        // row tiles that share b's columns before the next columns
 constexpr int kFactors = 3;            // factors of a row and block: per half, or gate and two up blocks
 constexpr int kRing = 8;               // blocks of factors: a block is written when the block kStages before it has
-                                       // been multiplied, while those up to kStages + 1 before it may be unread
+                                       // been multiplied, while up to kStages + 3 before it may be unread
 constexpr int kRingFloats = kRing * kFactors * kTileRows;
 constexpr int kSharedBlocks = 24;     // blocks of K from which CTAs may share a tile of 128 rows
 constexpr int kMaxSplit = 8;          // CTAs that share a tile's K, at most: 1, 2, 4 or 8
@@ -162,17 +162,17 @@ __device__ __forceinline__ void add_scaled(float2* acc, const uint32_t (&r)[32],
     }
 }
 
-// 128 consecutive columns, n of which exist, of a warp's 32 rows, m of which exist (row by lane, rows `pitch`
+// 2 * PAIRS consecutive columns, n of which exist, of a warp's 32 rows, m of which exist (row by lane, rows `pitch`
 // bytes apart), 16-bit.  A store of 32 bytes by every lane to a row of its own visits 32 lines, two
 // cycles each, 4000 for a tile.  So four lanes first trade 32-byte pieces, two exchanges of half of
 // them, until lane q of the four holds piece q (then q + 4) of all four rows: a store then writes 128
 // bytes each of 8 rows.
-template <bool FP16>
-__device__ __forceinline__ void store_rows(uint8_t* out, int64_t pitch, const float2 (&acc)[64], int m, int n, int vec)
+template <bool FP16, int PAIRS>
+__device__ __forceinline__ void store_rows(uint8_t* out, int64_t pitch, const float2 (&acc)[PAIRS], int m, int n, int vec)
 {
     const int lane = threadIdx.x & 31, q = lane & 3;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < PAIRS / 32; ++h) {
         uint32_t w[4][8];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -230,7 +230,7 @@ __device__ __forceinline__ float swiglu(float gate, float up)
     return gate * up * r;
 }
 
-// Named barriers 1 and 2: an accumulator has been read.  Every scaling warp arrives once per block, in
+// Named barriers 1 to 4: an accumulator has been read.  Every scaling warp arrives once per block, in
 // every case; the multiplying warp waits before it writes that accumulator again.
 constexpr int kReadThreads = kScaleThreads + 32;   // 544
 __device__ __forceinline__ void read_arrive(uint32_t buf)
@@ -317,11 +317,15 @@ __device__ __forceinline__ void finish_rows(const MatmulArgs& p, const Tile& x, 
 
 // SPLIT: with SwiGLU, an up block of 128 scales may end inside a tile (N is no multiple of 128).
 // KSPLIT: the CTAs of a cluster share one tile, a part of K each, and each finishes a part of its rows.
-template <bool SWIGLU, bool SPLIT, bool KSPLIT>
+// TC: columns of a tile, 256 or, with four accumulators and a 16-bit output only, 128.
+template <bool SWIGLU, bool SPLIT, bool KSPLIT, int TC>
 __global__ void __launch_bounds__(kProductThreads, 1)
 ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap map_a,
                        const __grid_constant__ CUtensorMap map_b)
 {
+    static_assert(TC == kTileCols || (TC == 128 && !SWIGLU && !KSPLIT), "the narrow tile is the plain product's");
+    constexpr int kStageBytes = stage_bytes(TC), kBuffers = 512 / TC;
+    static_assert(kStages % kBuffers == 0, "a stage always goes to the same accumulator");
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t bars[2 * kStages + 2];
     __shared__ float tops[2][kScaleWarps / 4][kTileRows];   // [tile parity][column half][row]: largest |z|
@@ -336,7 +340,7 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
                    topped = drained + 8;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const Giveup giveup{&gave_up, p.status};
-    constexpr int kCols = SWIGLU ? kTileCols / 2 : kTileCols;   // output columns of a tile
+    constexpr int kCols = SWIGLU ? TC / 2 : TC;   // output columns of a tile
     const int col_tiles = (p.N + kCols - 1) / kCols;
     const int ctas = KSPLIT ? cluster_size() : 1, rank = KSPLIT ? cluster_rank() : 0;
     const int t_first = KSPLIT ? blockIdx.x / ctas : blockIdx.x, t_step = KSPLIT ? gridDim.x / ctas : gridDim.x;
@@ -389,7 +393,7 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
                         bar_expect(bar, kStageBytes);
                         tma_load(dst, &map_a, k * kBlockK, x.m0, bar);
                         tma_load(dst + kTileRows * kBlockK, &map_b, k * kBlockK, y0, bar);
-                        tma_load(dst + (kTileRows + 128) * kBlockK, &map_b, k * kBlockK, y1, bar);
+                        if (TC > 128) tma_load(dst + (kTileRows + 128) * kBlockK, &map_b, k * kBlockK, y1, bar);
                     }
                 }
                 ok = __all_sync(0xffffffffu, ok);
@@ -399,7 +403,7 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
                     bar_drain(full + 8 * (j % kStages), (j / kStages) & 1);
             __syncwarp();
         } else if (warp == 1) {
-            constexpr uint32_t instruction = mma_instruction(kTileRows, kTileCols);
+            constexpr uint32_t instruction = mma_instruction(kTileRows, TC);
             const uint64_t a0 = mma_descriptor(stages), b0 = mma_descriptor(stages + kTileRows * kBlockK);
             const uint32_t mine = tiles > t_first ? (tiles - t_first - 1) / t_step + 1 : 0;
             const uint32_t blocks = mine * kb;
@@ -411,19 +415,19 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
                 for (int s = 0; s < kStages; ++s) {
                     if (n + s >= blocks) break;
                     bar_wait(full + 8 * s, phase, giveup);
-                    if (n + s >= 2) read_wait(s & 1);
+                    if (n + s >= kBuffers) read_wait(s % kBuffers);
                     if (leader) {
                         tmem_fence_after();
 #pragma unroll
                         for (int i = 0; i < kBlockK / 32; ++i)
-                            mma_e4m3(tmem + (s & 1) * kTileCols, a0 + (s * (kStageBytes >> 4) + 2 * i),
+                            mma_e4m3(tmem + (s % kBuffers) * TC, a0 + (s * (kStageBytes >> 4) + 2 * i),
                                      b0 + (s * (kStageBytes >> 4) + 2 * i), instruction, i == 0);
                         mma_commit(done + 8 * s);
                     }
                     __syncwarp();
                 }
             }
-            for (uint32_t n = blocks < 2 ? 0 : blocks - 2; n < blocks; ++n) read_wait(n & 1);
+            for (uint32_t n = blocks < kBuffers ? 0 : blocks - kBuffers; n < blocks; ++n) read_wait(n % kBuffers);
             if (leader) {
                 mma_commit(drained);   // tensor memory is freed only after its last product
                 bar_drain(drained, 0);
@@ -467,8 +471,10 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
                         float* f = ring + (n % kRing) * (kFactors * kTileRows) + r;
                         f[0] = a0[i] * b0[i];
                         f[64] = a1[i] * b0[i];
-                        f[kTileRows] = a0[i] * b1[i];
-                        f[kTileRows + 64] = a1[i] * b1[i];
+                        if (TC > 128) {
+                            f[kTileRows] = a0[i] * b1[i];
+                            f[kTileRows + 64] = a1[i] * b1[i];
+                        }
                         if (SPLIT) {
                             f[2 * kTileRows] = a0[i] * b2[i];
                             f[2 * kTileRows + 64] = a1[i] * b2[i];
@@ -485,8 +491,8 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int part = (warp - 4) >> 2;                 // this warp's half of the columns
         const int row = (warp & 3) * 32 + lane;
-        // plain: columns part*128 ..; SwiGLU: gate columns part*64 .. (of 128), then their up columns
-        const uint32_t col0 = SWIGLU ? part * 64 : part * 128;
+        // plain: columns part*TC/2 ..; SwiGLU: gate columns part*64 .. (of 128), then their up columns
+        const uint32_t col0 = SWIGLU ? part * 64 : part * (TC / 2);
         const uint32_t col1 = SWIGLU ? 128 + part * 64 : col0 + 64;
         // up columns of this part that share a tile's first up block
         const int split = 128 - p.N % 128 - part * 64;
@@ -495,12 +501,12 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
         uint32_t i = 0;
         // of the next block: its products' barrier, that barrier's phase, its accumulator, its factors
         uint32_t next = done, phase = 0, d = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        uint32_t f = smem_u32(ring) + 4 * (row + (SWIGLU ? 0 : part * kTileRows));
+        uint32_t f = smem_u32(ring) + 4 * (row + (SWIGLU || TC == 128 ? 0 : part * kTileRows));
         const uint32_t f_end = f + kRing * kFactors * kTileRows * 4;
         for (int t = t_first; t < tiles; t += t_step, parity ^= 1, ++i) {
-            float2 acc[64];
+            float2 acc[TC / 4];
 #pragma unroll
-            for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.0f, 0.0f);
+            for (int j = 0; j < TC / 4; ++j) acc[j] = make_float2(0.0f, 0.0f);
             // a wait that gave up ends nothing here: what follows works on whatever is there, every barrier
             // gets its arrivals, and the rows are not stored
             float f0, f1, f2;
@@ -522,25 +528,29 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
             begin(false);
             // 32 columns are read while the 32 before them are added, across the ends of blocks too
             for (int k = kb; k > 0; --k) {
+                bool ready;
                 tmem_wait(r0);
                 tmem_load32(r1, d + col0 + 32);
+                if constexpr (TC == 128) ready = bar_test(next, phase);
                 add_scaled(acc, r0, f0);
-                tmem_wait(r1);
-                tmem_load32(r0, d + col1);
-                const bool ready = bar_test(next, phase);
-                add_scaled(acc + 16, r1, f0);
-                tmem_wait(r0);
-                tmem_load32(r1, d + col1 + 32);
-                if (SPLIT) add_scaled(acc + 32, r0, f1, f2, split);
-                else add_scaled(acc + 32, r0, f1);
+                if constexpr (TC > 128) {
+                    tmem_wait(r1);
+                    tmem_load32(r0, d + col1);
+                    ready = bar_test(next, phase);
+                    add_scaled(acc + 16, r1, f0);
+                    tmem_wait(r0);
+                    tmem_load32(r1, d + col1 + 32);
+                    if (SPLIT) add_scaled(acc + 32, r0, f1, f2, split);
+                    else add_scaled(acc + 32, r0, f1);
+                }
                 tmem_wait(r1);
                 tmem_fence_before();
-                read_arrive((d >> 8) & 1);   // tensor memory starts at column 0: it is allocated whole
-                d ^= kTileCols;
-                const float g1 = f1, g2 = f2;
+                read_arrive((d & 511) / TC);   // tensor memory starts at column 0: it is allocated whole
+                d = (d & ~511u) | ((d + TC) & 511);
+                const float g1 = TC > 128 ? f1 : f0, g2 = f2;
                 if (k > 1) begin(ready);
-                if (SPLIT) add_scaled(acc + 48, r1, g1, g2, split - 32);
-                else add_scaled(acc + 48, r1, g1);
+                if (SPLIT) add_scaled(acc + TC / 4 - 16, r1, g1, g2, split - 32);
+                else add_scaled(acc + TC / 4 - 16, r1, g1);
             }
             const int4 x = info[i % kInfo];
             if constexpr (KSPLIT) {
@@ -553,12 +563,12 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
                 }
                 if (!ok) gave_up = 1;
             } else if constexpr (!SWIGLU) {
-                const int n0 = x.z + part * 128, m = x.y - x.x - (warp & 3) * 32;   // rows of this warp's 32 that exist
+                const int n0 = x.z + part * (TC / 2), m = x.y - x.x - (warp & 3) * 32;   // rows of this warp's 32 that exist
                 const int64_t pitch = 2 * (int64_t)p.N;
                 uint8_t* out = (uint8_t*)p.out + (int64_t)(x.x + (warp & 3) * 32) * pitch + 2 * n0;
                 if (__all_sync(0xffffffffu, ok) && n0 < p.N) {
-                    if (p.dtype == EP_FP16) store_rows<true>(out, pitch, acc, m, p.N - n0, p.vec);
-                    else store_rows<false>(out, pitch, acc, m, p.N - n0, p.vec);
+                    if (p.dtype == EP_FP16) store_rows<true, TC / 4>(out, pitch, acc, m, p.N - n0, p.vec);
+                    else store_rows<false, TC / 4>(out, pitch, acc, m, p.N - n0, p.vec);
                 }
             } else {
                 const int n0 = x.z + part * 64;
@@ -992,6 +1002,18 @@ int split_of(const MatmulArgs& p, int64_t tiles, int least, int sms)
     return split;
 }
 
+using RowsKernel = void(const MatmulArgs, const CUtensorMap, const CUtensorMap);
+cudaError_t launch_tiles(RowsKernel* kernel, const MatmulArgs& p, const CUtensorMap& ma, const CUtensorMap& mb, int stage,
+                         int64_t tiles, int split, int sms, cudaStream_t s)
+{
+    const size_t smem = 1024 + kStages * stage + kRingFloats * sizeof(float) + (p.groups + 1) * sizeof(int) +
+                        (p.offsets && p.groups <= kSharedOffsets ? (p.groups + 1) * sizeof(int32_t) : 0);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = split > 1 ? tiles * split : tiles < sms ? tiles : sms;
+    return launch_cluster(kernel, (unsigned)grid, kProductThreads, smem, split, s, p, ma, mb);
+}
+
 template <bool SWIGLU, bool SPLIT>
 cudaError_t launch_product_rows(const MatmulArgs& p, const CUtensorMap& ma, const CUtensorMap& mb, int sms,
                                 cudaStream_t s)
@@ -1000,13 +1022,15 @@ cudaError_t launch_product_rows(const MatmulArgs& p, const CUtensorMap& ma, cons
     // The sums' exchange costs what half a dozen blocks do.  256 rows, us, whole against shared: 7168 x 2048
     // 22.1 : 12.8 in 4, 4096 x 1024 14.2 : 10.6 in 4, 2048 x 7168 (16 blocks) 9.4 : 10.8 in 2.
     const int split = p.kb < kSharedBlocks ? 1 : split_of(p, most, 7, sms);
-    const size_t smem = 1024 + kStages * kStageBytes + kRingFloats * sizeof(float) + (p.groups + 1) * sizeof(int) +
-                        (p.offsets && p.groups <= kSharedOffsets ? (p.groups + 1) * sizeof(int32_t) : 0);
-    auto* kernel = split > 1 ? ep_product_rows_kernel<SWIGLU, SPLIT, true> : ep_product_rows_kernel<SWIGLU, SPLIT, false>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    const int64_t grid = split > 1 ? most * split : most < sms ? most : sms;
-    return launch_cluster(kernel, (unsigned)grid, kProductThreads, smem, split, s, p, ma, mb);
+    // Half as wide while the tiles still fit the SMs at once, which shortens a tile's blocks and its end.  us, 256
+    // against 128 columns: 200 rows of 2048 x 2048 9.2 : 6.3, 1777 rows of 1040 x 520 in 6 groups 10.4 : 7.9; past
+    // the SMs, 512 rows of 2048 x 7168 (112 : 224 tiles) 11.0 : 12.2.
+    const int64_t narrow = most_tiles(p, kTileRows, 128);
+    if (!SWIGLU && split == 1 && narrow <= sms)
+        return launch_tiles(ep_product_rows_kernel<false, false, false, 128>, p, ma, mb, stage_bytes(128), narrow, 1, sms, s);
+    auto* kernel = split > 1 ? ep_product_rows_kernel<SWIGLU, SPLIT, true, kTileCols>
+                             : ep_product_rows_kernel<SWIGLU, SPLIT, false, kTileCols>;
+    return launch_tiles(kernel, p, ma, mb, stage_bytes(kTileCols), most, split, sms, s);
 }
 
 template <int T, bool SWIGLU>
@@ -1032,20 +1056,25 @@ cudaError_t launch_product_few(const MatmulArgs& p, const CUtensorMap& ma, const
 
 // Rows of a tile of the kernel for few rows, or 0 for the kernel of 128-row tiles.  Measured, us, few rows
 // against 128-row tiles:
-//   one group, 7168 x 4096 with SwiGLU     1 row 8.5 : 11.9   32 rows 11.0 : 13.2   64 rows 12.9 : 13.5
-//                                          96 rows 18.3 : 13.9
-//   4 groups, 7168 x 2048                  of 4 rows 14.8 : 16.4   of 8 rows 16.1 : 15.7   of 16 rows 18.8 : 16.5
-//   32 groups, 7168 x 4096 with SwiGLU     of 8 rows 145 : 152   of 16 rows 152 : 153   of 24 rows 167 : 153
+//   one group, 7168 x 4096 with SwiGLU   1 row 8.5 : 11.9   32 rows 11.0 : 13.2   64 rows 12.9 : 13.5   96 rows 18.3 : 13.9
+//   one group, 2048 x 2048               1 row 4.6 : 5.7    32 rows 5.8 : 5.9     64 rows 6.9 : 5.9
+//   one group, 1024 x 1024               1 row 4.3 : 4.2    32 rows 5.1 : 4.3
+//   4 groups, 7168 x 2048                of 4 rows 14.8 : 16.4   of 8 rows 16.1 : 15.7   of 16 rows 18.8 : 16.5
+//   32 groups, 7168 x 4096 with SwiGLU   of 8 rows 145 : 152     of 16 rows 152 : 153    of 24 rows 167 : 153
 // The 128-row tiles multiply rows that are not there, which costs them nothing while the weights' bytes or
 // the tiles' number set the time; a group whose rows pass a tile of few reads its weights twice.
 int few_rows_tile(const MatmulArgs& p, int sms)
 {
-    if (p.groups == 1) return p.rows <= 32 ? 16 : p.rows <= 64 ? 32 : 0;
+    // whether the wide tiles leave half of the SMs to narrower ones or to parts of K
+    const bool idle = 2 * most_tiles(p, kTileRows, p.swiglu ? kTileCols / 2 : kTileCols) <= sms;
+    if (p.groups == 1) {
+        if (p.rows > 64 || (p.kb <= 8 && (!p.swiglu || p.rows > 32))) return 0;
+        if (p.rows <= 32) return 16;
+        return !p.swiglu && p.kb < kSharedBlocks && idle ? 0 : 32;
+    }
     const int64_t groups = p.groups < p.rows ? p.groups : p.rows;   // that can hold a row
     const int64_t mean = p.rows / groups;
-    // with K shared, 128-row tiles win from 8 rows a group on; without, from 16
-    const bool shared = 2 * most_tiles(p, kTileRows, p.swiglu ? kTileCols / 2 : kTileCols) <= sms && p.kb >= kSharedBlocks;
-    return mean < 8 || (mean == 8 && !shared) ? 16 : mean <= 16 && !shared ? 32 : 0;
+    return mean < 8 || (mean == 8 && !idle) ? 16 : mean <= 16 && !idle ? 32 : 0;
 }
 
 }  // namespace

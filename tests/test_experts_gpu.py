@@ -385,7 +385,8 @@ SHAPES = [(1, 16, 8, 0), (1, 7168, 512, 0), (3, 144, 24, 0), (65, 128, 129, 0), 
           (4000, 256, 512, 9), (17, 4096, 7, 0), (520, 144, 1, 2), (50, 640, 288, 0), (64, 2064, 1184, 0),
           (100, 272, 192, 8), (96, 128, 2048, 0), (31, 1024, 20000, 0), (700, 64, 40, 600), (12000, 32, 16, 600),
           (9000, 16, 32, 4096), (66, 4096, 512, 0), (130, 3088, 1000, 0), (200, 7168, 2048, 0), (300, 3600, 1312, 0),
-          (90, 4096, 544, 5), (129, 3200, 257, 2), (1000, 4096, 96, 0)]
+          (90, 4096, 544, 5), (129, 3200, 257, 2), (1000, 4096, 96, 0), (20, 1536, 528, 0), (40, 3200, 640, 0), (64, 1536, 96, 8),
+          (2000, 1040, 712, 0), (777, 144, 300, 3)]
 
 
 @pytest.mark.parametrize("rows,K,N,groups", SHAPES)
