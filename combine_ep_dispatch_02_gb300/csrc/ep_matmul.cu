@@ -56,7 +56,8 @@ __device__ __forceinline__ void group_rows(const MatmulArgs& p, const int32_t* o
 // 1340 cycles at first: descriptors and loop counts in uniform registers; an accumulator given back over
 // a named barrier, because a hop over an mbarrier takes 300 cycles; factors made ahead by idle warps;
 // 32 columns read while the 32 before are added, across the ends of blocks.  256 columns, because a
-// 128-column product takes 68 cycles where half of a 256-column one takes 64, and reads the rows again.
+// 128-column product takes 68 cycles where half of a 256-column one takes 64, and reads the rows again;
+// where tiles are too few for the SMs, tiles of 128 columns, or a tile's K by several CTAs, are shorter.
 //
 // 32768 rows in 32 groups, 7168 x 4096 with SwiGLU: 690 us, 2790 TFLOP/s (0.73 of twice the measured BF16
 // rate), and 805 us once the card holds its power limit, at 1545 MHz.  2048 x 7168: 400 us, whose 16 blocks

@@ -315,7 +315,7 @@ constexpr int kWarpRowVecs = 128;   // a row's gradient is one warp's up to this
 constexpr int kRowVecs = 4;   // vectors of a lane's slice at most: 2 KB of a row to a warp
 
 // x rows to their sorted rows: each row is read once and written to each of its pairs.  HBM-bound by its
-// stores: 8192 rows of 7168 BF16 to 65536 take 160 us, 6.6 TB/s, at HBM's 0.99 GB of algorithmic bytes.
+// stores: 8192 rows of 7168 BF16 to 65536 take 157 us, 6.7 TB/s.
 __global__ void __launch_bounds__(kRowThreads) ep_sorted_rows_kernel(const RowsArgs a)
 {
     const int lane = threadIdx.x & 31;
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kRowThreads) ep_sorted_rows_kernel(const RowsA
 // out[row] = round(sum over slots, ascending, of weight * y[pos]); FP32 sums.  A warp takes a.slice_vecs
 // vectors of a row.  Reading HBM at full rate takes about 100 KB on their way to each SM: a lane loads
 // the next vector of up to kSlots rows before it adds the current ones, so 16 warps keep up to 128 KB
-// in flight without a gap: 8192 rows of 7168 BF16 from 65536, 162 us, 6.5 TB/s (192 us without).
+// in flight without a gap: 8192 rows of 7168 BF16 from 65536, 164 us, 6.4 TB/s (192 us without).
 template <bool FP16, int kSlots>
 __global__ void __launch_bounds__(kRowThreads, 2) ep_return_rows_kernel(const RowsArgs a)
 {
