@@ -49,15 +49,16 @@ __device__ __forceinline__ void group_rows(const MatmulArgs& p, const int32_t* o
 // registers while the next block is multiplied.  The scales differ from block to block of K, so the
 // sums cannot stay in tensor memory over a tile.
 //
-// What bounds it.  A block's products take 512 cycles (128*256*128 at 8192 a cycle; 528 measured alone).
-// In that time shared memory takes in 48 KB from TMA and gives 48 KB to the tensor cores, which at 128
-// bytes a cycle is 750; products and loads together measure 750, the whole loop 690.  The scaling keeps
-// up: 256 columns of 128 lanes read and 32768 FMAs are 256 cycles each.  What it took to get there, of
-// 1340 cycles at first: descriptors and loop counts in uniform registers; an accumulator given back over
-// a named barrier, because a hop over an mbarrier takes 300 cycles; factors made ahead by idle warps;
-// 32 columns read while the 32 before are added, across the ends of blocks.  256 columns, because a
-// 128-column product takes 68 cycles where half of a 256-column one takes 64, and reads the rows again;
-// where tiles are too few for the SMs, tiles of 128 columns, or a tile's K by several CTAs, are shorter.
+// What bounds it.  A block takes 690 cycles, of which its products need 512 (128*256*128 at 8192 a cycle; 528
+// measured alone).  The rest is the way of an accumulator: multiplied in 512 cycles, 300 until the scaling
+// warps are told and the multiplying warp is told back, 400 until they have read it, 1220 for each of
+// two.  Tensor memory holds no third.  Loading half of b's bytes takes a block to 664 cycles, none to 650.
+// What it took to get there, of 1340 cycles at first: descriptors and loop counts in uniform registers; an
+// accumulator given back over a named barrier, because a hop over an mbarrier takes 300 cycles; factors
+// made ahead by idle warps; 32 columns read while the 32 before are added, across the ends of blocks.
+// 256 columns, because a 128-column product takes 68 cycles where half of a 256-column one takes 64, and
+// reads the rows again; where tiles are too few for the SMs, tiles of 128 columns, or a tile's K by
+// several CTAs, are shorter.
 //
 // 32768 rows in 32 groups, 7168 x 4096 with SwiGLU: 690 us, 2790 TFLOP/s (0.73 of twice the measured BF16
 // rate), and 805 us once the card holds its power limit, at 1545 MHz.  2048 x 7168: 400 us, whose 16 blocks
