@@ -232,9 +232,9 @@ __device__ __forceinline__ float swiglu(float gate, float up)
     return gate * up * r;
 }
 
-// Named barriers 1 to 4: an accumulator has been read.  Every scaling warp arrives once per block, in
-// every case; the multiplying warp waits before it writes that accumulator again.
-constexpr int kReadThreads = kScaleThreads + 32;   // 544
+// Named barriers 1 to 4, one to an accumulator: it has been read.  Every scaling warp arrives once per block,
+// in every case; the multiplying warp waits before it writes that accumulator again.
+constexpr int kReadThreads = kScaleThreads + 32;
 __device__ __forceinline__ void read_arrive(uint32_t buf)
 {
     asm volatile("bar.arrive %0, %1;" :: "r"(1 + buf), "n"(kReadThreads) : "memory");
@@ -458,7 +458,7 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
                     a0[i] = as0[k];
                     a1[i] = as1[k];
                     b0[i] = bs0[k];
-                    b1[i] = bs1[k];
+                    if (TC > 128) b1[i] = bs1[k];
                     if (SPLIT) b2[i] = bs2[k];
                 };
 #pragma unroll

@@ -20,11 +20,14 @@ import ctypes
 import dataclasses
 import importlib.util
 import os
+import sys
 from typing import Optional
 
 import torch
 
 from . import EP_BF16, EP_ERR_ARG, EP_FP16, EP_FP8_E4M3, EpError, _PKG, load_library
+
+_package = sys.modules[__package__]
 
 BINDING_PATH = os.path.join(_PKG, "_ep_binding.so")
 _OUT_CODES = {"bf16": EP_BF16, "fp16": EP_FP16}
@@ -39,6 +42,8 @@ _bound_to = None
 def _native():
     """The native binding, calling whichever build of libep.so the package has loaded."""
     global _binding, _bound_to
+    if _bound_to is not None and _package._lib is _bound_to:   # the usual case, without a call
+        return _binding
     lib = load_library()
     if lib is not _bound_to:
         if _binding is None:
