@@ -400,9 +400,11 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
                 }
                 ok = __all_sync(0xffffffffu, ok);
             }
-            if (leader && !ok)   // its loads in flight
+            if (leader && !ok) {   // its loads in flight
+                const long long t0 = clock64();
                 for (uint32_t j = n < kStages ? 0 : n - kStages; j < n; ++j)
-                    bar_drain(full + 8 * (j % kStages), (j / kStages) & 1);
+                    bar_drain(full + 8 * (j % kStages), (j / kStages) & 1, t0);
+            }
             __syncwarp();
         } else if (warp == 1) {
             constexpr uint32_t instruction = mma_instruction(kTileRows, TC);
@@ -410,13 +412,14 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
             const uint32_t mine = tiles > t_first ? (tiles - t_first - 1) / t_step + 1 : 0;
             const uint32_t blocks = mine * kb;
             const bool leader = elect_one();
-            // After a wait that gave up the products go on, on whatever the stages hold: the others have
-            // left or are leaving, no result is stored, and every barrier still gets its arrivals.
+            // after a wait that gave up the products go on, at most kSuspendNs a block, on whatever the stages
+            // hold: the scaling warps need every block's arrival
             for (uint32_t n = 0, phase = 0; n < blocks; n += kStages, phase ^= 1) {
 #pragma unroll
                 for (int s = 0; s < kStages; ++s) {
                     if (n + s >= blocks) break;
                     bar_wait(full + 8 * s, phase, giveup);
+                    __syncwarp();
                     if (n + s >= kBuffers) read_wait(s % kBuffers);
                     if (leader) {
                         tmem_fence_after();
@@ -432,7 +435,7 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
             for (uint32_t n = blocks < kBuffers ? 0 : blocks - kBuffers; n < blocks; ++n) read_wait(n % kBuffers);
             if (leader) {
                 mma_commit(drained);   // tensor memory is freed only after its last product
-                bar_drain(drained, 0);
+                bar_drain(drained, 0, clock64());
             }
             __syncwarp();
         } else if (warp >= 2) {
@@ -468,8 +471,8 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
                     for (int i = 0; i < kAhead; ++i) {
                         if (k0 + i >= kb) break;
                         const uint32_t s = n % kStages, use = n / kStages;
-                        if (use > 0) ok = ok && bar_wait(done + 8 * s, (use - 1) & 1, giveup);
-                        __syncwarp();
+                        // one answer for the warp, whose lanes have to leave together
+                        if (use > 0) ok = __all_sync(0xffffffffu, ok && bar_wait(done + 8 * s, (use - 1) & 1, giveup));
                         float* f = ring + (n % kRing) * (kFactors * kTileRows) + r;
                         f[0] = a0[i] * b0[i];
                         f[64] = a1[i] * b0[i];
@@ -498,7 +501,6 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
         const uint32_t col1 = SWIGLU ? 128 + part * 64 : col0 + 64;
         // up columns of this part that share a tile's first up block
         const int split = 128 - p.N % 128 - part * 64;
-        bool ok = true;
         int parity = 0;
         uint32_t i = 0;
         // of the next block: its products' barrier, that barrier's phase, its accumulator, its factors
@@ -509,13 +511,13 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
             float2 acc[TC / 4];
 #pragma unroll
             for (int j = 0; j < TC / 4; ++j) acc[j] = make_float2(0.0f, 0.0f);
-            // a wait that gave up ends nothing here: what follows works on whatever is there, every barrier
-            // gets its arrivals, and the rows are not stored
+            // another warp's giving up ends nothing here: what follows works on whatever is there, and the rows
+            // are not stored
             float f0, f1, f2;
             uint32_t r0[32], r1[32];
             // the block's first columns and its factors, once its products are there
             auto begin = [&](bool ready) {
-                if (!ready) ok &= bar_wait(next, phase, giveup);
+                if (!ready) products_wait(next, phase, giveup);
                 __syncwarp();
                 tmem_fence_after();
                 tmem_load32(r0, d + col0);
@@ -563,12 +565,11 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
                     const uint32_t piece = ((j < 16 ? col0 : col1 - 64) >> 2) + j;
                     smem_store4(stages + row * (4 * kTileCols) + ((piece ^ (row & 7)) << 4), acc[2 * j], acc[2 * j + 1]);
                 }
-                if (!ok) gave_up = 1;
             } else if constexpr (!SWIGLU) {
                 const int n0 = x.z + part * (TC / 2), m = x.y - x.x - (warp & 3) * 32;   // rows of this warp's 32 that exist
                 const int64_t pitch = 2 * (int64_t)p.N;
                 uint8_t* out = (uint8_t*)p.out + (int64_t)(x.x + (warp & 3) * 32) * pitch + 2 * n0;
-                if (__all_sync(0xffffffffu, ok) && n0 < p.N) {
+                if (!__any_sync(0xffffffffu, *giveup.flag) && n0 < p.N) {
                     if (p.dtype == EP_FP16) store_rows<true, TC / 4>(out, pitch, acc, m, p.N - n0, p.vec);
                     else store_rows<false, TC / 4>(out, pitch, acc, m, p.N - n0, p.vec);
                 }
@@ -586,7 +587,7 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
                 // reaches before all have passed the tile between
                 __syncwarp();
                 if (lane == 0) bar_arrive(topped);
-                ok &= bar_wait(topped, parity, giveup);
+                const bool ok = bar_wait(topped, parity, giveup) && !*giveup.flag;
                 const float scale = e4m3_block_scale(fmaxf(top, tops[parity][part ^ 1][row]));
                 const float inv = __frcp_rn(scale);
                 if (ok && x.x + row < x.y) {
@@ -739,9 +740,11 @@ ep_product_few_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap ma
             }
             ok = __all_sync(0xffffffffu, ok);
         }
-        if (leader && !ok)   // its loads in flight
+        if (leader && !ok) {   // its loads in flight
+            const long long t0 = clock64();
             for (uint32_t i = n < (uint32_t)stage_count ? 0 : n - stage_count; i < n; ++i)
-                bar_drain(full + 8 * (i % stage_count), (i / stage_count) & 1);
+                bar_drain(full + 8 * (i % stage_count), (i / stage_count) & 1, t0);
+        }
         __syncwarp();
     } else if (warp == 1) {
         constexpr uint32_t instruction = mma_instruction(kFewCols, T);
@@ -753,6 +756,7 @@ ep_product_few_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap ma
         for (uint32_t n = 0, s = 0, phase = 0; n < blocks; ++n) {
             const uint32_t buf = n % S::kBuffers;
             bar_wait(full + 8 * s, phase, giveup);
+            __syncwarp();
             if (n >= S::kBuffers) asm volatile("bar.sync %0, %1;" :: "r"(1 + buf), "n"(kFewReadThreads) : "memory");
             if (leader) {
                 tmem_fence_after();
@@ -773,7 +777,7 @@ ep_product_few_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap ma
             asm volatile("bar.sync %0, %1;" :: "r"(1 + n % S::kBuffers), "n"(kFewReadThreads) : "memory");
         if (leader) {
             mma_commit(drained);   // tensor memory is freed only after its last product
-            bar_drain(drained, 0);
+            bar_drain(drained, 0, clock64());
         }
         __syncwarp();
     } else if (warp < 4) {
@@ -805,8 +809,8 @@ ep_product_few_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap ma
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
                     if (k0 + i >= k_hi) break;
-                    if (n >= (uint32_t)stage_count) ok = ok && bar_wait(done + 8 * s, phase, giveup);
-                    __syncwarp();
+                    // one answer for the warp, whose lanes have to leave together
+                    if (n >= (uint32_t)stage_count) ok = __all_sync(0xffffffffu, ok && bar_wait(done + 8 * s, phase, giveup));
                     if (c < T) {
                         float* f = ring + (n % kFewRing) * (S::kFactorRows * T) + c;
                         f[0] = a[i] * b0[i];
@@ -838,8 +842,7 @@ ep_product_few_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap ma
                 for (int i = 0; i < T / 2; ++i) acc[h][i] = make_float2(0.0f, 0.0f);
             for (int k = k_lo; k < k_hi; ++k, ++n) {
                 const uint32_t buf = n % S::kBuffers;
-                ok &= bar_wait(done + 8 * s, phase, giveup);
-                __syncwarp();
+                products_wait(done + 8 * s, phase, giveup);
                 tmem_fence_after();
                 const float* f = ring + (n % kFewRing) * (S::kFactorRows * T);
 #pragma unroll

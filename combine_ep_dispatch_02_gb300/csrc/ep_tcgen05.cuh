@@ -2,8 +2,10 @@
 // bounded waits, tiled TMA loads, and the fifth-generation tensor cores with their tensor memory.
 //
 // Bounded waits.  Every wait gives up after kWaitCycles clock cycles (or as soon as another thread of
-// the CTA gave up), records EP_ERR_DEVICE_TIMEOUT and returns false; the roles of a kernel then leave
-// their loops, wait for what they have in flight (bounded again), free tensor memory and return.
+// the CTA gave up), records EP_ERR_DEVICE_TIMEOUT and returns false.  The warps that load and those that
+// make factors then leave; the multiplying and the scaling warps go through all their blocks, on whatever
+// is there, because named barriers, whose waits have no limit, need every warp's arrivals in step.  What
+// is in flight is waited for (bounded again), tensor memory is freed, and the kernel returns.
 #pragma once
 
 #include <cuda.h>
@@ -111,10 +113,28 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Gi
     return true;
 }
 
-// The wait of a role that is leaving early for its own operations in flight: bounded, records nothing.
-__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity)
+// A scaling warp's wait for a block's products, by a whole warp.  The multiplying warp issues every block,
+// the latest when its own wait for the loads has given up, so this one does not end when another gave
+// up: a scaling warp that ran ahead would arrive twice where the others arrive once, and the multiplying
+// warp could wait at its named barrier for ever.  The limit is that of a tensor core that has stopped.
+__device__ __forceinline__ void products_wait(uint32_t bar, uint32_t parity, const Giveup& g)
 {
-    const long long t0 = clock64();
+    if (!bar_test(bar, parity)) {
+        const long long t0 = clock64();
+        while (!bar_try(bar, parity)) {
+            if (clock64() - t0 > 8 * kWaitCycles) {
+                *g.flag = 1;
+                record_status(g.status, EP_ERR_DEVICE_TIMEOUT);
+                break;
+            }
+        }
+    }
+    __syncwarp();
+}
+
+// The wait of a role that is leaving early for its own operations in flight, since t0: bounded, records nothing.
+__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity, long long t0)
+{
     while (!bar_try(bar, parity) && clock64() - t0 < kWaitCycles) {}
 }
 

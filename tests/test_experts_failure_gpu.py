@@ -53,3 +53,32 @@ def test_withheld_load_reports_timeout_and_context_survives(withheld_lib, monkey
         assert (out[0].float() == 448).all() and torch.allclose(out[1] * 448, z.to(dev).expand_as(out[1]), rtol=2.0 ** -20)
     else:
         assert (out == 1).all()
+
+
+# several tiles to a CTA: the roles that go on after a wait has given up stay in step over all of them
+@pytest.mark.parametrize("rows,columns,groups,swiglu", [
+    (16384, 1024, 0, False), (16384, 1024, 0, True), (256, 4096, 32, False), (256, 4096, 32, True)])
+def test_withheld_load_with_many_tiles_returns(withheld_lib, monkeypatch, rows, columns, groups, swiglu):
+    dev = torch.device("cuda", 0)
+    lead = (groups,) if groups else ()
+    a = torch.full((rows, 1024), 0x38, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)      # 1.0
+    b = torch.full((*lead, columns, 1024), 0x38, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+    sa = torch.full((rows, 8), 2.0 ** -5, device=dev)
+    sb = torch.full((*lead, columns // 128, 8), 2.0 ** -5, device=dev)
+    offsets = torch.arange(groups + 1, dtype=torch.int32, device=dev) * (rows // groups) if groups else None
+
+    def run():
+        call = ep.matmul_fp8_swiglu if swiglu else ep.matmul_fp8
+        return call(a, sa, b, sb, offsets=offsets)
+    assert ep.op_status(dev) == 0
+    with monkeypatch.context() as m:
+        m.setattr(ep, "_lib", withheld_lib)
+        for _ in range(3):
+            run()
+        assert ep.op_status(dev) == ep.EP_ERR_DEVICE_TIMEOUT
+    out = run()
+    assert ep.op_status(dev) == 0
+    if swiglu:                                        # 1024 ones times 2^-10: gate = up = 1
+        assert (out[0].float() == 448).all()
+    else:
+        assert (out == 1).all()
