@@ -1091,8 +1091,8 @@ extern "C" int ep_matmul_fp8(const void* a, const float* a_scales, const void* b
 {
     using namespace ep;
     const char* who = "ep_matmul_fp8";
-    if (rows < 0 || rows >= (int64_t)1 << 31)
-        return layer_fail(EP_ERR_ARG, "%s: rows=%lld outside 0..2^31-1", who, (long long)rows);
+    if (rows < 0 || rows > INT32_MAX - kTileRows)   // a tile's last row is counted in 32 bits
+        return layer_fail(EP_ERR_ARG, "%s: rows=%lld outside 0..2^31-1-%d", who, (long long)rows, kTileRows);
     if (groups < 1 || groups > kMaxMatmulGroups || (!offsets && groups != 1))
         return layer_fail(EP_ERR_ARG, "%s: groups=%d outside 1..%d, or several without offsets", who, groups,
                           kMaxMatmulGroups);

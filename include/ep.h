@@ -418,7 +418,7 @@ int ep_return_rows_backward(const void* y, const float* weights, const void* dou
  *   b, b_scales  [groups][columns][inner] codes, [groups][ceil(columns/128)][ceil(inner/128)]
  *   offsets      [groups + 1] int32 on the device: rows offsets[g] .. offsets[g+1]-1 take b[g]; rows
  *                outside every group are not written.  NULL with groups = 1: every row.
- *   inner        a multiple of 16 up to 2^20;  groups up to 4096;  columns up to 2^20
+ *   inner        a multiple of 16 up to 2^20;  groups up to 4096;  columns up to 2^20;  rows up to 2^31-129
  * swiglu = 0: out [rows][columns], EP_BF16 or EP_FP16 by dtype, rounded once; out_scales is not used.
  * swiglu = 1 (dtype EP_FP8_E4M3, columns a multiple of 32): the first half of b's columns is the gate,
  * the second the up projection; z = gate * sigmoid(gate) * up in FP32 is quantised as by ep_rms_norm_fp8,

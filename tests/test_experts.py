@@ -108,6 +108,10 @@ def test_product_refusals(lib, change, word):
     _refused(lib, lib.ep_matmul_fp8(*{**MUL, **change}.values()), "ep_matmul_fp8", word)
 
 
+def test_product_rows_stay_in_32_bits_to_the_end_of_the_last_tile(lib):
+    _refused(lib, lib.ep_matmul_fp8(*{**MUL, "rows": (1 << 31) - 128}.values()), "ep_matmul_fp8", "rows")
+
+
 def test_empty_calls_succeed_without_a_gpu(lib):
     assert lib.ep_rms_norm_fp8(*{**NORM, "rows": 0, "x": None, "q": None}.values()) == ep.EP_OK
     assert lib.ep_sorted_rows(*{**ROWS, "R": 0, "x": None}.values()) == ep.EP_OK
