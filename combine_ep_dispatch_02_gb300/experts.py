@@ -9,7 +9,8 @@
 Every call runs on the device of its first tensor, enqueues on the current stream (or ``stream``) and
 returns without waiting.  Outputs and workspaces come from PyTorch's allocator on that stream.
 Arguments are checked before any launch (``EpError`` with ``EP_ERR_ARG``); what only the device can
-see is recorded in one status word per device, read and cleared by ``op_status``.
+see is recorded in one status word per device, read and cleared by ``op_status``.  The first call on a
+device makes that word and waits for it, so a call comes before a graph's capture.
 
 The checks and allocations are native (``_ep_binding``, csrc/ep_binding.cpp): these calls are often one
 token's, and marshalling in Python would take longer than the kernels.
@@ -87,7 +88,8 @@ def op_status(device=None) -> int:
     read (0 for none), clearing it: EP_ERR_CAPACITY (more sorted rows than max_rows; the rest were
     left out), EP_ERR_DEVICE_BOUNDS (a position outside its buffer; skipped) or
     EP_ERR_DEVICE_TIMEOUT (a bounded wait of the product ran out; its output is not valid)."""
-    dev = torch.device("cuda", torch.cuda.current_device() if device is None else torch.device(device).index or 0)
+    index = None if device is None else torch.device(device).index
+    dev = torch.device("cuda", torch.cuda.current_device() if index is None else index)
     w = _status_word(dev)
     torch.cuda.synchronize(dev)
     v = int(w.item())
