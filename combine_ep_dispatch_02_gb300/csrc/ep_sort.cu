@@ -563,7 +563,11 @@ int sort_tile_pairs(int64_t pairs)
     return kSortTileThreads * (pairs <= (int64_t)kSortShortTiles * kSortTileThreads * kSortSteps ? kSortSteps : kSortLongSteps);
 }
 
-int64_t sort_tiles(int64_t pairs) { return (pairs + sort_tile_pairs(pairs) - 1) / sort_tile_pairs(pairs); }
+// One at least: no pairs in more groups than one CTA counts still leave offsets and src to write.
+int64_t sort_tiles(int64_t pairs)
+{
+    return pairs == 0 ? 1 : (pairs + sort_tile_pairs(pairs) - 1) / sort_tile_pairs(pairs);
+}
 
 bool sort_is_small(int64_t pairs, int groups) { return pairs <= kSortSmallPairs && groups <= kSortSmallGroups; }
 

@@ -74,6 +74,12 @@ def test_sort_workspace_sizes(lib):
         assert lib.ep_sort_workspace_bytes(*bad) == 0
 
 
+def test_sort_of_no_rows_with_many_groups_takes_one_tile(lib):
+    assert lib.ep_sort_workspace_bytes(1, 0, 8, 2048) == 0
+    assert lib.ep_sort_workspace_bytes(1, 0, 8, 2049) == 2049 * 4
+    assert lib.ep_sort_workspace_bytes(2, 0, 4, 1500) == 3000 * 4
+
+
 @pytest.mark.parametrize("change,word", COMMON + [
     (dict(row_bytes=0), "row of"), (dict(row_bytes=24), "row of"), (dict(row_bytes=1 << 31), "row of"),
     (dict(sd=-1), "scale_dim"), (dict(sd=65537), "scale_dim"), (dict(sd=3), "scales"), (dict(x=P + 8), "x, out"),

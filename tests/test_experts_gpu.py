@@ -198,6 +198,14 @@ def test_sort_nothing_and_one_expert_for_all():
     _check_sort(torch.zeros((2, 50, 4), dtype=torch.int32, device=DEV), 16, counts=[0, 0])
 
 
+@pytest.mark.parametrize("W,E", [(1, 2049), (1, 4096), (2, 1500)])
+def test_sort_of_no_rows_with_many_groups(W, E):
+    shape = (W, 0, 4) if W > 1 else (0, 4)
+    order = ep.sort_by_expert(torch.zeros(shape, dtype=torch.int32, device=DEV), E, max_rows=37)
+    assert order.offsets.shape == (W * E + 1,) and not order.offsets.any()
+    assert order.pos.shape == shape and (order.src == -1).all()
+
+
 @pytest.mark.parametrize("R", [100, 4000])
 def test_sort_past_capacity_is_recorded_and_left_out(R):
     idx = _indices(_gen(R), 1, R, 8, 16, bad=0)
