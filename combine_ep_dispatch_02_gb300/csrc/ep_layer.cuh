@@ -6,6 +6,7 @@
 // recorded in the caller's status word.
 #pragma once
 
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cuda_bf16.h>
@@ -38,15 +39,38 @@ inline bool layer_aligned(const void* p, size_t a) { return p != nullptr && ((ui
 // SMs of the current device, 0 if it cannot be told (looked up once per device)
 inline int layer_num_sms()
 {
-    static int sms[64] = {};
+    static std::atomic<int> sms[64] = {};
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (sms[dev] == 0 && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return sms[dev];
+    int n = sms[dev].load(std::memory_order_relaxed);
+    if (n != 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    sms[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 #ifdef __CUDACC__
+
+// Lets launches of K take all the shared memory a CTA can have.  The limit is one per kernel and device, and
+// host threads share it: it is raised once to the most there is, never to one call's size, which another
+// thread's smaller call could lower again before the launch.  Two threads may both raise it, to the same value.
+template <auto* K>
+cudaError_t allow_all_shared()
+{
+    static std::atomic<uint64_t> raised{0};   // a bit per device
+    int dev = -1, most = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
+    if (raised.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    cudaFuncAttributes f;
+    e = cudaFuncGetAttributes(&f, K);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)f.sharedSizeBytes);
+    if (e == cudaSuccess) raised.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // Every kernel of these operators is launched as a programmatic dependent (launch_dependent), whatever
 // precedes it on the stream, and starts with this: its launch and set-up overlap the tail of the kernel

@@ -1007,16 +1007,16 @@ int split_of(const MatmulArgs& p, int64_t tiles, int least, int sms)
     return split;
 }
 
-using RowsKernel = void(const MatmulArgs, const CUtensorMap, const CUtensorMap);
-cudaError_t launch_tiles(RowsKernel* kernel, const MatmulArgs& p, const CUtensorMap& ma, const CUtensorMap& mb, int stage,
-                         int64_t tiles, int split, int sms, cudaStream_t s)
+template <auto* K>
+cudaError_t launch_tiles(const MatmulArgs& p, const CUtensorMap& ma, const CUtensorMap& mb, int stage, int64_t tiles,
+                         int split, int sms, cudaStream_t s)
 {
     const size_t smem = 1024 + kStages * stage + kRingFloats * sizeof(float) + (p.groups + 1) * sizeof(int) +
                         (p.offsets && p.groups <= kSharedOffsets ? (p.groups + 1) * sizeof(int32_t) : 0);
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_all_shared<K>();
     if (e != cudaSuccess) return e;
     const int64_t grid = split > 1 ? tiles * split : tiles < sms ? tiles : sms;
-    return launch_cluster(kernel, (unsigned)grid, kProductThreads, smem, split, s, p, ma, mb);
+    return launch_cluster(K, (unsigned)grid, kProductThreads, smem, split, s, p, ma, mb);
 }
 
 template <bool SWIGLU, bool SPLIT>
@@ -1032,10 +1032,11 @@ cudaError_t launch_product_rows(const MatmulArgs& p, const CUtensorMap& ma, cons
     // the SMs, 512 rows of 2048 x 7168 (112 : 224 tiles) 11.0 : 12.2.
     const int64_t narrow = most_tiles(p, kTileRows, 128);
     if (!SWIGLU && split == 1 && narrow <= sms)
-        return launch_tiles(ep_product_rows_kernel<false, false, false, 128>, p, ma, mb, stage_bytes(128), narrow, 1, sms, s);
-    auto* kernel = split > 1 ? ep_product_rows_kernel<SWIGLU, SPLIT, true, kTileCols>
-                             : ep_product_rows_kernel<SWIGLU, SPLIT, false, kTileCols>;
-    return launch_tiles(kernel, p, ma, mb, stage_bytes(kTileCols), most, split, sms, s);
+        return launch_tiles<ep_product_rows_kernel<false, false, false, 128>>(p, ma, mb, stage_bytes(128), narrow, 1, sms, s);
+    constexpr int kStage = stage_bytes(kTileCols);
+    if (split > 1)
+        return launch_tiles<ep_product_rows_kernel<SWIGLU, SPLIT, true, kTileCols>>(p, ma, mb, kStage, most, split, sms, s);
+    return launch_tiles<ep_product_rows_kernel<SWIGLU, SPLIT, false, kTileCols>>(p, ma, mb, kStage, most, 1, sms, s);
 }
 
 template <int T, bool SWIGLU>
@@ -1052,11 +1053,11 @@ cudaError_t launch_product_few(const MatmulArgs& p, const CUtensorMap& ma, const
     if (stages > kFewMaxStages) stages = kFewMaxStages;
     if (stages < S::kBuffers) return cudaErrorInvalidConfiguration;   // not reached: 4 stages at the least
     const size_t smem = rest + (size_t)stages * S::kStageBytes;
-    auto* kernel = ep_product_few_kernel<T, SWIGLU>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_all_shared<ep_product_few_kernel<T, SWIGLU>>();
     if (e != cudaSuccess) return e;
     const int64_t clusters = most < sms / split ? most : sms / split;
-    return launch_cluster(kernel, (unsigned)(clusters * split), kFewThreads, smem, split, s, p, ma, mb, stages, split);
+    return launch_cluster(ep_product_few_kernel<T, SWIGLU>, (unsigned)(clusters * split), kFewThreads, smem, split, s, p,
+                          ma, mb, stages, split);
 }
 
 // Rows of a tile of the kernel for few rows, or 0 for the kernel of 128-row tiles.  Measured, us, few rows

@@ -645,9 +645,7 @@ int ep_sort_by_expert(const int32_t* indices, const int32_t* counts, int W, int6
     cudaError_t e;
     if (sort_is_small(a.pairs, a.groups)) {
         const size_t smem = (size_t)(kSortSmallThreads / 32) * a.groups * sizeof(int);
-        e = cudaSuccess;
-        if (smem > 48 * 1024)
-            e = cudaFuncSetAttribute(ep_sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = allow_all_shared<ep_sort_small_kernel>();
         if (e == cudaSuccess) e = launch_dependent(ep_sort_small_kernel, dim3(1), dim3(kSortSmallThreads), smem, s, a);
         return layer_cuda(e, "ep_sort_by_expert: launch");
     }
@@ -655,8 +653,8 @@ int ep_sort_by_expert(const int32_t* indices, const int32_t* counts, int W, int6
     const int tile_pairs = sort_tile_pairs(a.pairs);
     const bool shorter = tile_pairs == kSortTileThreads * kSortSteps;
     auto* place = shorter ? ep_sort_place_kernel<kSortSteps, false> : ep_sort_place_kernel<kSortLongSteps, true>;
-    e = cudaSuccess;
-    if (smem > 48 * 1024) e = cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = shorter ? allow_all_shared<ep_sort_place_kernel<kSortSteps, false>>()
+                : allow_all_shared<ep_sort_place_kernel<kSortLongSteps, true>>();
     if (e == cudaSuccess)
         e = launch_dependent(ep_sort_count_kernel, dim3(a.tiles), dim3(kSortTileThreads), a.groups * sizeof(int), s, a,
                              tile_pairs);

@@ -6,6 +6,8 @@ truncate instead of round); a 16-bit output adds half a unit in its last place (
 BF16, 2^-11 for FP16, or half the smallest subnormal, 2^-25, for FP16); an e4m3 code is within 2^-4
 relative or 2^-10 absolute of the value it rounds.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -712,3 +714,61 @@ def test_back_to_back_calls_touch_nothing_early():
         return done
     for a, c in zip(passes(True), passes(False)):
         assert torch.equal(a, c)
+
+
+# ------------------------------------------------------------------------------------------- host threads
+
+def _on_two_threads(calls, passes):
+    """Each call `passes` times on a thread and a stream of its own: the messages of those that were refused."""
+    failed, start = [[] for _ in calls], threading.Barrier(len(calls))
+
+    def work(i):
+        with torch.cuda.device(DEV):
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                torch.zeros(1, device=DEV)     # the thread has used the device before
+            start.wait()
+            for _ in range(passes):
+                if calls[i](s.cuda_stream) != ep.EP_OK:
+                    failed[i].append(ep.load_library().ep_last_error())
+            s.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    return failed
+
+
+@pytest.mark.parametrize("dense,grouped,groups,K", [(4, 1600, 400, 2048), (160, 2400, 100, 128)])
+def test_products_of_two_host_threads_do_not_disturb_each_other(dense, grouped, groups, K):
+    """ctypes releases the interpreter's lock, so the calls run at the same time; their kernel is the same, the
+    shared memory that their numbers of groups take is not."""
+    lib, calls, keep = ep.load_library(), [], []
+    for n, G in ((dense, 1), (grouped, groups)):
+        a, sa, b, sb = _product_inputs(_gen(n), n, K, 16, G)
+        offsets = torch.linspace(0, n, G + 1, device=DEV).int()
+        out, word = torch.empty(n, 16, dtype=torch.bfloat16, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+        keep.append((a, sa, b, sb, offsets, out, word))
+        calls.append(lambda s, p=[t.data_ptr() for t in keep[-1]], n=n, G=G: lib.ep_matmul_fp8(
+            p[0], p[1], p[2], p[3], p[4], n, G, 16, K, 0, ep.EP_BF16, p[5], None, p[6], s))
+    torch.cuda.synchronize()
+    assert _on_two_threads(calls, 4000) == [[], []]
+
+
+@pytest.mark.parametrize("rows", [64, 4096])
+def test_sorts_of_two_host_threads_do_not_disturb_each_other(rows):
+    lib, g = ep.load_library(), _gen(rows)
+    calls, keep = [], []
+    for E in (1600, 2048):
+        idx = _indices(g, 1, rows, 4, E)
+        n = rows * 4
+        ws = max(4, lib.ep_sort_workspace_bytes(1, rows, 4, E))
+        bufs = [idx] + [torch.empty(m, dtype=torch.int32, device=DEV) for m in (E + 1, n, n, ws // 4)] + \
+            [torch.zeros(1, dtype=torch.int32, device=DEV)]
+        keep.append(bufs)
+        p = [t.data_ptr() for t in bufs]
+        calls.append(lambda s, p=p, E=E, n=n, ws=ws: lib.ep_sort_by_expert(
+            p[0], None, 1, rows, 4, E, n, p[1], p[2], p[3], p[4], ws, p[5], s))
+    torch.cuda.synchronize()
+    assert _on_two_threads(calls, 4000) == [[], []]
