@@ -963,9 +963,19 @@ int make_map(CUtensorMap* m, const char* what, const void* base, int64_t rows, i
     if (!encode) return layer_fail(EP_ERR_CUDA, "ep_matmul_fp8: the driver has no cuTensorMapEncodeTiled");
     const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, pitch[1] = {(cuuint64_t)K};
     const cuuint32_t box[2] = {kBlockK, (cuuint32_t)box_rows}, step[2] = {1, 1};
-    const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, pitch, box, step,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    auto make = [&] {
+        return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, pitch, box, step,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = make();
+    if (r == CUDA_ERROR_INVALID_CONTEXT) {   // a host thread's first call, which nothing has bound to the device yet
+        int dev = -1;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaSetDevice(dev);
+        if (e != cudaSuccess) return layer_cuda(e, "ep_matmul_fp8: binding the host thread to its device");
+        r = make();
+    }
     if (r != CUDA_SUCCESS) return layer_fail(EP_ERR_CUDA, "ep_matmul_fp8: tensor map of %s: CUresult %d", what, (int)r);
     return EP_OK;
 }

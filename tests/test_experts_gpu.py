@@ -772,3 +772,23 @@ def test_sorts_of_two_host_threads_do_not_disturb_each_other(rows):
             p[0], None, 1, rows, 4, E, n, p[1], p[2], p[3], p[4], ws, p[5], s))
     torch.cuda.synchronize()
     assert _on_two_threads(calls, 4000) == [[], []]
+
+
+@pytest.mark.parametrize("rows", [4, 160])
+def test_product_as_the_first_call_of_a_host_thread(rows):
+    """The allocator has memory of these sizes at hand, so nothing before the product binds the thread to the device."""
+    args = _product_inputs(_gen(rows), rows, 256, 128, 1)
+    a, sa, b, sb = args[0], args[1], args[2][0], args[3][0]
+    want, got = ep.matmul_fp8(a, sa, b, sb).clone(), []
+    torch.cuda.synchronize()
+
+    def work():
+        try:
+            got.append(ep.matmul_fp8(a, sa, b, sb))
+        except ep.EpError as e:
+            got.append(e)
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    assert isinstance(got[0], torch.Tensor), got[0]
+    assert torch.equal(got[0], want)
