@@ -9,8 +9,8 @@
 // Sorting indices takes one CTA up to kSortSmallPairs pairs.  Above that, tiles of 2048 pairs are counted
 // in one launch and placed in a second, whose CTAs each add up the counts of the tiles; above 64 tiles,
 // tiles of 8192 pairs, and one CTA scans the counts (groups x tiles) in a launch between the two.
-// 64 x 8 pairs and 256 groups take 2.4 us, 65536 pairs 6.5 us: two launches and a few trips to L2; 2 million
-// pairs 43 us, mostly the one CTA's scan.
+// 64 x 8 pairs and 256 groups take 2.5 us, 65536 pairs 8.2 us: two launches and a few trips to L2; 2 million
+// pairs 44 us, mostly the one CTA's scan.
 // Within a warp, __match_any_sync gives a pair's rank among equal groups; a warp's running counts
 // live in shared memory, so no step has an order that atomics could change.
 #include "ep_layer.cuh"
@@ -215,7 +215,9 @@ __global__ void __launch_bounds__(kScanThreads) ep_sort_scan_kernel(const SortAr
 }
 
 // SCANNED: tile_counts holds first positions and offsets is written; else tile_counts holds counts, and each
-// CTA adds them up for itself.
+// CTA adds them up for itself.  The indices, too, are read after the wait, although the kernel before this one
+// has waited for whoever wrote them: what another kernel wrote is visible to this one only after its own wait,
+// and the count may have left their lines in L1.  Ranking them during that kernel would take 1.5 us less of 8.
 template <int kSteps, bool SCANNED>
 __global__ void __launch_bounds__(kSortTileThreads) ep_sort_place_kernel(const SortArgs a)
 {
@@ -224,16 +226,15 @@ __global__ void __launch_bounds__(kSortTileThreads) ep_sort_place_kernel(const S
     constexpr int kWarps = kSortTileThreads / 32;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     for (int i = threadIdx.x; i < kWarps * a.groups; i += blockDim.x) counts[i] = 0;
+    follow_predecessor();
     __syncthreads();
     const int64_t first = ((int64_t)blockIdx.x * kWarps + w) * kSteps * 32;
-    // the kernel before this one let it start after its own predecessor: the indices are complete
     int g[kSteps], at[kSteps];
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) g[i] = pair_group(a, first + 32 * i + lane);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) at[i] = warp_rank(g[i], counts + w * a.groups, lane);
     __syncthreads();
-    follow_predecessor();
     int carry = 0;
     for (int e0 = 0; e0 < a.groups; e0 += kSortTileThreads) {
         const int e = e0 + threadIdx.x;

@@ -1,6 +1,8 @@
 """Refusals of the expert-layer operators that need no GPU: the C ABI rejects what the host can check
 before any CUDA call, and the binding rejects tensors of the wrong kind."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -146,3 +148,25 @@ def test_binding_takes_cuda_tensors_only(lib):
 
 def test_status_codes_have_messages(lib):
     assert ctypes.c_char_p(lib.ep_strerror(ep.EP_ERR_CAPACITY)).value
+
+
+@pytest.mark.parametrize("name,kernels", [("ep_norm.cu", 1), ("ep_sort.cu", 8), ("ep_matmul.cu", 2)])
+def test_kernels_read_no_memory_before_their_own_wait(name, kernels):
+    """Launched as programmatic dependents, they may run before what they read is visible to them: before
+    follow_predecessor() none names an array of its arguments or calls a function that reads one."""
+    with open(os.path.join(epbuild.CSRC, name)) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    arrays = set()
+    for struct in re.findall(r"struct \w+Args \{(.*?)\n\};", text, flags=re.S):
+        for line in re.findall(r"[^;]*\*[^;]*;", struct):
+            arrays |= set(re.findall(r"\*?\s*(\w+)\s*[,;]", line))
+    arrays -= {"status"}                                      # handed on as an address
+    assert {"x", "weight"} <= arrays or {"idx", "tile_counts", "pos"} <= arrays or {"a", "bs", "offsets"} <= arrays
+    readers = set(re.findall(r"__device__ __forceinline__ \w+ (\w+)\(const \w+Args& ", text))
+    bodies = re.findall(r"__global__ [^;{]*\{(.*?)\n\}", text, flags=re.S)
+    assert len(bodies) == kernels
+    for body in bodies:
+        before, wait, _ = body.partition("follow_predecessor();")
+        assert wait
+        used = set(re.findall(r"\b[ap]\.(\w+)", before)) & arrays | set(re.findall(r"\b(\w+)(?:<[^;()]*>)?\(", before)) & readers
+        assert not used, (name, used, before[-300:])

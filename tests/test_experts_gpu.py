@@ -716,6 +716,35 @@ def test_back_to_back_calls_touch_nothing_early():
         assert torch.equal(a, c)
 
 
+@pytest.mark.parametrize("W,R,k,E", [(1, 1500, 8, 40), (4, 4500, 8, 16)])
+def test_sorts_of_several_launches_read_nothing_early(W, R, k, E):
+    """The two- and three-launch sorts on indices and counts that the kernels just before them write, in memory
+    that an earlier pass has read: as calls one by one."""
+    g = _gen(R)
+    base = torch.stack([_indices(g, W, R, k, E, bad=0.05) for _ in range(2)])
+    held = torch.tensor([[R] * W, [R // (r + 2) for r in range(W)]], dtype=torch.int32, device=DEV)
+    idx, counts = torch.empty_like(base[0]), torch.empty_like(held[0])
+    view = idx if W > 1 else idx[0]
+
+    def passes(wait):
+        step, done = torch.cuda.synchronize if wait else (lambda: None), []
+        for i in range(40):
+            torch.add(base[i % 2], 0, out=idx)
+            torch.add(held[i // 2 % 2], 0, out=counts)
+            step()
+            order = ep.sort_by_expert(view, E, counts=counts)
+            step()
+            done += [order.offsets, order.pos, order.src]
+        torch.cuda.synchronize()
+        return done
+    for a, b in zip(passes(False), passes(True)):
+        assert torch.equal(a, b)
+    order = ep.sort_by_expert(view, E, counts=counts)      # the last pass's
+    want = _sort_np(base[1], E, held[1].tolist(), base[1].numel())
+    for name, w in zip(("offsets", "pos", "src"), want):
+        assert np.array_equal(getattr(order, name).cpu().numpy().reshape(w.shape), w), name
+
+
 # ------------------------------------------------------------------------------------------- host threads
 
 def _on_two_threads(calls, passes):
