@@ -32,7 +32,7 @@ VARIANTS = {"auto": 0, "whole_row": 1, "tiled_512": 2, "tiled_1024": 3}
 
 # every entry point include/ep.h declares
 EXPORTS = ("ep_plan_create", "ep_plan_destroy", "ep_plan_set_variant", "ep_plan_device_bytes",
-           "ep_dispatch", "ep_dispatch_route", "ep_dispatch_scatter", "ep_combine", "ep_reset",
+           "ep_dispatch", "ep_dispatch_route", "ep_dispatch_scatter", "ep_combine", "ep_reset", "ep_check_live",
            "ep_status", "ep_strerror", "ep_last_error", "ep_route_noalloc",
            "ep_quantize_received", "ep_combine_fp8", "ep_group_by_expert", "ep_ungroup_by_expert",
            "ep_dispatch_grouped", "ep_quantize_received_fp4", "ep_combine_fp4", "ep_probe_read",
@@ -77,6 +77,7 @@ def load_library(path: Optional[str] = None):
         "ep_dispatch_route": (I, [V, V, V, V, ctypes.POINTER(DispatchOut)]),
         "ep_dispatch_scatter": (I, [V, V, V, V, V, V]),
         "ep_combine": (I, [V, V, V, V, V, U64, V]),
+        "ep_check_live": (I, [V, U64]),
         "ep_reset": (I, [V, V]),
         "ep_status": (I, [V, ctypes.POINTER(I)]),
         "ep_strerror": (ctypes.c_char_p, [I]),
@@ -439,7 +440,8 @@ class Plan:
     def sort_received(self, d: Dispatched, max_rows: Optional[int] = None, stream=None) -> "ExpertOrder":
         """The live dispatch's received rows in compact expert order, every rank's experts in turn (see
         ``sort_by_expert``).  A routed token's slots are received once each, so max_rows defaults to
-        W * max_tok_per_rank * topk."""
+        W * max_tok_per_rank * topk.  A dispatch that is not live is refused (``EP_ERR_STATE``)."""
+        _check(self._lib.ep_check_live(self._h, ctypes.c_uint64(d.epoch)))
         return sort_by_expert(d.recv_idx, self.E, max_rows=self.rows * self.k if max_rows is None else max_rows,
                               counts=d.recv_count, stream=stream)
 

@@ -785,6 +785,15 @@ int ep_reset(ep_plan* p, void* stream)
     return EP_OK;
 }
 
+int ep_check_live(const ep_plan* p, uint64_t epoch)
+{
+    if (!p) return fail(EP_ERR_ARG, "plan is NULL");
+    if (!p->live || epoch != p->epoch)
+        return fail(EP_ERR_STATE, "epoch %llu is not the plan's live dispatch (live=%d, epoch %llu)",
+                    (unsigned long long)epoch, (int)p->live, (unsigned long long)p->epoch);
+    return EP_OK;
+}
+
 int ep_probe_read(ep_plan* p, uint64_t* ns_host, int n_words)
 {
     if (!p || !ns_host || n_words < 0) return fail(EP_ERR_ARG, "ep_probe_read: plan or ns_host is NULL, or n_words < 0");

@@ -286,6 +286,10 @@ int ep_dispatch_grouped(ep_plan* p, const void* x, const float* weights, const f
  * fails.  No device work is needed: the scan flags carry a per-call stamp. */
 int ep_reset(ep_plan* p, void* stream);
 
+/* EP_OK if epoch is the plan's live dispatch, whose views hold its rows, else EP_ERR_STATE: the check
+ * that the calls on an epoch make, for work on the views that goes past the plan (ep_sort_by_expert). */
+int ep_check_live(const ep_plan* p, uint64_t epoch);
+
 /* Wait for the device, store the plan's device status word (EP_OK or the first EP_ERR_INDEX /
  * EP_ERR_DEVICE_TIMEOUT recorded since the last call) in *device_status, and clear it.  Device
  * problems are recorded rather than trapped, as the staging PR's caller contract asks of the

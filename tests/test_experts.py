@@ -129,6 +129,10 @@ def test_empty_calls_succeed_without_a_gpu(lib):
     assert lib.ep_matmul_fp8(*{**MUL, "rows": 0, "a": None, "out": None}.values()) == ep.EP_OK
 
 
+def test_live_check_refuses_a_null_plan(lib):
+    assert lib.ep_check_live(None, 0) == ep.EP_ERR_ARG
+
+
 def test_binding_takes_cuda_tensors_only(lib):
     x = torch.zeros(4, 256, dtype=torch.bfloat16)
     i = torch.zeros(4, 2, dtype=torch.int32)

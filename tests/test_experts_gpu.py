@@ -636,6 +636,44 @@ def test_dispatched_rows_through_the_experts():
         assert not out[r, int(wl.n_tok[r]):].any()
 
 
+def test_sort_received_refuses_a_dispatch_that_is_not_live():
+    wl = wlmod.custom_workload(W=2, E=4, k=2, H=128, M=16, n_tok=[16, 9], seed=3)
+    idx = torch.from_numpy(wl.indices).to(DEV)
+    x = _randn(_gen(1), 2, 16, 128).to(torch.bfloat16)
+
+    def refused(plan, d):
+        with pytest.raises(ep.EpError) as e:
+            plan.sort_received(d)
+        assert e.value.code == ep.EP_ERR_STATE
+    with ep.Plan(2, 4, 2, 128, "bf16", 0, 16, device=DEV) as plan:
+        d = plan.dispatch(x, None, None, idx, wl.n_tok)
+        plan.sort_received(d)
+        d2 = plan.dispatch(x, None, None, idx, wl.n_tok)
+        refused(plan, d)
+        plan.sort_received(d2)
+        d3 = plan.dispatch_route(idx, wl.n_tok)
+        refused(plan, d3)                      # routed, but no row has arrived
+        plan.dispatch_scatter(x, None, None, idx)
+        plan.sort_received(d3)
+        plan.reset()
+        refused(plan, d3)
+
+
+def test_sort_received_of_many_rows():
+    """Above 131072 pairs, with the dispatch's own counts."""
+    wl = wlmod.custom_workload(W=4, E=8, k=8, H=128, M=1100, n_tok=[1100, 0, 1000, 7], seed=5)
+    idx = torch.from_numpy(wl.indices).to(DEV)
+    with ep.Plan(4, 8, 8, 128, "bf16", 0, 1100, device=DEV) as plan:
+        d = plan.dispatch(_randn(_gen(1), 4, 1100, 128).to(torch.bfloat16), None, None, idx, wl.n_tok)
+        assert d.recv_idx.numel() > 131072
+        order = plan.sort_received(d)
+        want = _sort_np(d.recv_idx, 8, d.recv_count.tolist(), 4 * 1100 * 8)
+        for name, w in zip(("offsets", "pos", "src"), want):
+            assert np.array_equal(getattr(order, name).cpu().numpy().reshape(w.shape), w), name
+        held = wl.indices[np.arange(1100)[None, :] < np.asarray(wl.n_tok)[:, None]]
+        assert int(order.offsets[-1]) == (held >= 0).sum()
+
+
 def test_calls_replay_in_a_graph():
     g = _gen(11)
     R, k, E, H = 40, 4, 8, 256
