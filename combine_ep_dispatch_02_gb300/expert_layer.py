@@ -37,7 +37,7 @@ class ExpertLayer:
 
     def __init__(self, W: int, experts_per_rank: int, topk: int, hidden: int, max_tok_per_rank: int, up, down,
                  norm_weight: torch.Tensor):
-        self.plan = ep.Plan(W, experts_per_rank, topk, hidden, "fp8", hidden // 128, max_tok_per_rank,
+        self.plan = ep.Plan(W, experts_per_rank, topk, hidden, "fp8", -(-hidden // 128), max_tok_per_rank,
                             device=norm_weight.device)
         self.up, self.down, self.norm_weight = up, down, norm_weight
 

@@ -716,6 +716,11 @@ def test_example_layer_agrees_with_fp32():
                               "--hidden", "256", "--passes", "1"]) <= 2.0 ** -3
 
 
+def test_example_layer_with_a_short_last_block_of_scales():
+    from combine_ep_dispatch_02_gb300 import expert_layer
+    assert expert_layer.main(["--tokens-per-rank", "20", "--hidden", "272", "--inner", "144", "--passes", "1"]) <= 2.0 ** -3
+
+
 def test_back_to_back_calls_touch_nothing_early():
     """A call's kernels are set up while the kernel before them still runs; their memory is the allocator's
     and so often what that kernel reads.  Results of a stream of calls are those of calls one by one."""
