@@ -37,7 +37,7 @@ EXPORTS = ("ep_plan_create", "ep_plan_destroy", "ep_plan_set_variant", "ep_plan_
            "ep_quantize_received", "ep_combine_fp8", "ep_group_by_expert", "ep_ungroup_by_expert",
            "ep_dispatch_grouped", "ep_quantize_received_fp4", "ep_combine_fp4", "ep_probe_read",
            "ep_rms_norm_fp8", "ep_sort_workspace_bytes", "ep_sort_by_expert", "ep_sorted_rows",
-           "ep_return_rows", "ep_return_rows_backward", "ep_matmul_fp8")
+           "ep_return_rows", "ep_return_rows_backward", "ep_matmul_fp8", "ep_take_status")
 
 
 class EpError(RuntimeError):
@@ -97,6 +97,7 @@ def load_library(path: Optional[str] = None):
         "ep_sorted_rows": (I, [V, V, V, V, I, L, I, L, L, I, V, V, V, V]),
         "ep_return_rows": (I, [V, V, V, V, I, L, I, L, I, I, V, V, V]),
         "ep_return_rows_backward": (I, [V, V, V, V, V, I, L, I, L, I, I, V, V, V, V]),
+        "ep_take_status": (I, [V, V, V]),
         "ep_matmul_fp8": (I, [V, V, V, V, V, L, I, I, I, I, I, V, V, V, V]),
     }
     for name, (res, args) in sig.items():

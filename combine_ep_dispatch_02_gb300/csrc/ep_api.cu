@@ -231,6 +231,10 @@ int check_units(int N, int chunks, const char* who)
     return EP_OK;
 }
 
+// A caller-owned status word to *taken and zero in its place: one step, so that nothing recorded is lost or
+// read twice, whichever streams and host threads take part.
+__global__ void take_status_kernel(int* status, int* taken) { *taken = atomicExch(status, 0); }
+
 }  // namespace
 
 namespace ep {
@@ -810,6 +814,16 @@ int ep_probe_read(ep_plan* p, uint64_t* ns_host, int n_words)
     for (int i = 0; i < n_words && i < 2 * kProbePhases; ++i) ns_host[i] = w[i];
     return EP_OK;
 #endif
+}
+
+int ep_take_status(int32_t* device_status, int32_t* taken, void* stream)
+{
+    if (!device_status || !aligned(device_status, 4) || !taken || !aligned(taken, 4))
+        return fail(EP_ERR_ARG, "ep_take_status: device_status or taken is NULL or not 4-byte aligned");
+    take_status_kernel<<<1, 1, 0, (cudaStream_t)stream>>>(device_status, taken);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "ep_take_status: launch");
+    return EP_OK;
 }
 
 int ep_status(ep_plan* p, int* device_status)

@@ -26,7 +26,7 @@ from typing import Optional
 
 import torch
 
-from . import EP_BF16, EP_ERR_ARG, EP_FP16, EP_FP8_E4M3, EpError, _PKG, load_library
+from . import EP_BF16, EP_ERR_ARG, EP_FP16, EP_FP8_E4M3, EpError, _PKG, _check, load_library
 
 _package = sys.modules[__package__]
 
@@ -87,16 +87,18 @@ def op_status(device=None) -> int:
     """Wait for the device and return the first status its expert-layer calls recorded since the last
     read (0 for none), clearing it: EP_ERR_CAPACITY (more sorted rows than max_rows; the rest were
     left out), EP_ERR_DEVICE_BOUNDS (a position outside its buffer; skipped) or
-    EP_ERR_DEVICE_TIMEOUT (a bounded wait of the product ran out; its output is not valid)."""
+    EP_ERR_DEVICE_TIMEOUT (a bounded wait of the product ran out; its output is not valid).  The word
+    is read and cleared in one step, so a status that another host thread's call records meanwhile stays for
+    the next read; but it is the device's, not the caller's: one thread's read takes what another's call
+    recorded."""
     index = None if device is None else torch.device(device).index
     dev = torch.device("cuda", torch.cuda.current_device() if index is None else index)
     w = _status_word(dev)
     torch.cuda.synchronize(dev)
-    v = int(w.item())
-    if v:
-        w.zero_()
-        torch.cuda.synchronize(dev)
-    return v
+    with torch.cuda.device(dev):
+        taken = torch.empty(1, dtype=torch.int32, device=dev)
+        _check(load_library().ep_take_status(w.data_ptr(), taken.data_ptr(), torch.cuda.current_stream().cuda_stream))
+        return int(taken.item())
 
 
 def _on(stream, call, *args):

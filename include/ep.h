@@ -344,7 +344,7 @@ int ep_probe_read(ep_plan* p, uint64_t* ns_host, int n_words);
  * Expert-layer operators: the steps of a mixture-of-experts layer around dispatch and combine.  They
  * take caller-owned memory only (outputs, workspace, status word), run on the current device, enqueue
  * on `stream` and return without waiting.  device_status is one int32 on the device: the first problem
- * only the GPU can see is recorded there and the work it concerns is skipped; no call clears it.  Their
+ * only the GPU can see is recorded there and the work it concerns is skipped; ep_take_status clears it.  Their
  * kernels are launched as programmatic dependents of what precedes them on the stream (set-up overlaps
  * its tail, no memory is touched before it has completed): results and stream order are those of plain
  * launches.  Arrays are dense and row-major unless a stride is given.  Scales are FP32, one per 128 elements of
@@ -365,6 +365,13 @@ int ep_probe_read(ep_plan* p, uint64_t* ns_host, int n_words);
 int ep_rms_norm_fp8(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
                     const void* weight, int weight_fp32, int dtype, int64_t rows, int hidden, float eps, void* q,
                     float* scales, void* h, void* y, void* stream);
+
+/*
+ * Reads and clears such a status word in one step: taken (one int32 that the GPU can write) receives what was
+ * recorded since the word was last cleared, 0 for nothing.  Of calls whose streams overlap it sees those that
+ * have recorded by then; what is recorded later stays in the word for the next call.
+ */
+int ep_take_status(int32_t* device_status, int32_t* taken, void* stream);
 
 /*
  * Received rows in compact expert order, and back.  The order of W ranks' rows [W][rows_per_rank] with

@@ -150,6 +150,11 @@ def test_binding_takes_cuda_tensors_only(lib):
         ep.matmul_fp8(f8, x, f8, x, out_dtype="fp32")
 
 
+def test_take_status_refusals(lib):
+    for args in ((None, P, None), (P, None, None), (P + 2, P, None), (P, P + 1, None)):
+        _refused(lib, lib.ep_take_status(*args), "ep_take_status", "4-byte aligned")
+
+
 def test_status_codes_have_messages(lib):
     assert ctypes.c_char_p(lib.ep_strerror(ep.EP_ERR_CAPACITY)).value
 

@@ -864,3 +864,30 @@ def test_product_as_the_first_call_of_a_host_thread(rows):
     t.join()
     assert isinstance(got[0], torch.Tensor), got[0]
     assert torch.equal(got[0], want)
+
+
+def test_each_recorded_status_is_read_once():
+    order = ep.ExpertOrder(torch.zeros(2, dtype=torch.int32, device=DEV),
+                           torch.full((1, 1), 7, dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV))
+    y = torch.ones(2, 16, dtype=torch.bfloat16, device=DEV)
+    done, other = threading.Event(), [0]
+
+    def reader():
+        while not done.is_set():
+            other[0] += ep.op_status(DEV) != 0
+    t = threading.Thread(target=reader)
+    t.start()
+    mine, passes = 0, 1500
+    for _ in range(passes):
+        ep.return_rows(order, y)               # one lane of one warp records EP_ERR_DEVICE_BOUNDS
+        mine += ep.op_status(DEV) != 0
+    done.set()
+    t.join()
+    assert mine + other[0] == passes
+
+
+def test_taking_a_status_clears_its_word():
+    lib, word, taken = ep.load_library(), torch.full((1,), -5, dtype=torch.int32, device=DEV), torch.ones(2, dtype=torch.int32, device=DEV)
+    for i in range(2):
+        assert lib.ep_take_status(word.data_ptr(), taken[i:].data_ptr(), torch.cuda.current_stream().cuda_stream) == ep.EP_OK
+    assert taken.tolist() == [-5, 0] and word.item() == 0
