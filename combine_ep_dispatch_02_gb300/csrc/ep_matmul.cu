@@ -217,10 +217,13 @@ __device__ __forceinline__ void store_rows(uint8_t* out, int64_t pitch, const fl
     }
 }
 
-// gate * sigmoid(gate) * up.  The exponential's argument is split so that its error stays a few units in
-// the last place at any magnitude (the product with log2 e alone would be off by |gate| units); the two
-// approximate units add two more.  Below -88 the exponential is held at 2^127, whose reciprocal is 0; an
-// infinite gate's split is not a number, which fminf turns into one that changes neither 0 nor 2^127's 0.
+// gate * sigmoid(gate) * up, in this order: gate * up could pass FP32's range where the result is far inside.
+// The exponential's argument is split, so that its rounding does not enter (the product with log2 e alone would
+// be off by |gate| units in the exponential's last place).  What stays is that of log2 e to FP32, 1.9e-8 of the
+// gate, and two units of each approximate instruction: in all 2 units at a gate of -10, 5 at -40, 11 at -87,
+// which the e4m3 code's 2^-4 hides.  Below -88 the exponential is held at 2^127, whose reciprocal is 0: a sigmoid
+// under FP32's smallest normal number counts as 0.  An infinite gate's split is not a number, which fminf turns
+// into one that changes neither 0 nor 2^127's 0.
 __device__ __forceinline__ float swiglu(float gate, float up)
 {
     const float t = -1.4426950408889634f * gate;
@@ -229,7 +232,7 @@ __device__ __forceinline__ float swiglu(float gate, float up)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fminf(t, 127.0f)));
     e = fmaf(e * 0.6931471805599453f, rest, e);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return gate * up * r;
+    return gate * r * up;
 }
 
 // Named barriers 1 to 4, one to an accumulator: it has been read.  Every scaling warp arrives once per block,

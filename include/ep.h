@@ -433,7 +433,8 @@ int ep_return_rows_backward(const void* y, const float* weights, const void* dou
  * swiglu = 0: out [rows][columns], EP_BF16 or EP_FP16 by dtype, rounded once; out_scales is not used.
  * swiglu = 1 (dtype EP_FP8_E4M3, columns a multiple of 32): the first half of b's columns is the gate,
  * the second the up projection; z = gate * sigmoid(gate) * up in FP32 is quantised as by ep_rms_norm_fp8,
- * by the scale's reciprocal: out [rows][columns/2] codes, out_scales [rows][ceil(columns/256)].
+ * by the scale's reciprocal: out [rows][columns/2] codes, out_scales [rows][ceil(columns/256)].  A sigmoid below
+ * FP32's smallest normal number, 2^-126, counts as 0.
  * a, b and out are 16-byte aligned.  The result does not depend on timing: sums are added in a fixed order.
  * A bounded wait that runs out on the GPU is recorded as EP_ERR_DEVICE_TIMEOUT; out is then not valid.
  * The first call on a device looks up a driver entry point and should come before any stream capture.

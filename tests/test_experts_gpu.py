@@ -426,6 +426,31 @@ def test_product_swiglu_of_gates_far_from_zero(rows):
     _check_product(a, sa, b, sb, None, swiglu=True)
 
 
+@pytest.mark.parametrize("rows,K", [(6, 256), (700, 256), (256, 4096)])
+def test_product_swiglu_of_small_sigmoids_times_large_values(rows, K):
+    """gate * up alone would pass FP32's range; with the sigmoid between them the product does not."""
+    one = torch.full((1, 1), 0x38, dtype=torch.uint8, device=DEV)                 # 1.0
+    a, b = one.expand(rows, K).contiguous().view(F8), one.expand(256, K).contiguous()
+    b[:128] = 0xB8                                                                # -1.0
+    sb = torch.full((2, K // 128), 80.0 / K, device=DEV)
+    sb[1] = 3e37 / K
+    f = torch.linspace(0.25, 1.05, rows, device=DEV)
+    sa = f[:, None].expand(rows, K // 128).contiguous()
+    q, s = ep.matmul_fp8_swiglu(a, sa, b.view(F8), sb)
+    z, _ = _product64(a, sa, b.view(F8), sb)
+    gate, up = z[:, :128], z[:, 128:]
+    assert (gate * up).abs().max() > 3.5e38 and gate.min() < -80
+    want = gate / (1 + torch.exp(-gate)) * up
+    # the sums' error in the gate enters by its own size (the exponential), the exponential's argument is off
+    # by less than 2^-25 |gate| (log2 e in FP32), and the rest by less than 32 u
+    err = want.abs() * (2 * (130 + K // 128) * U * (gate.abs() + 1) + 2.0 ** -25 * gate.abs() + 32 * U) * 1.01
+    _check_codes(q, s, want, err)
+    # a sigmoid below FP32's smallest normal number counts as zero
+    sa[:] = 1.25
+    q, s = ep.matmul_fp8_swiglu(a, sa, b.view(F8), sb)
+    assert not q.float().any() and (s == 1).all()
+
+
 @pytest.mark.parametrize("rows", [2, 20, 60, 100, 140, 1000])
 def test_product_all_rows_in_one_of_many_groups(rows):
     g = _gen(rows)
