@@ -136,7 +136,12 @@ __device__ __forceinline__ uint32_t e4m3x4_scaled(float a, float b, float c, flo
 }
 
 // The same by a multiplication with the reciprocal, for values that are themselves off by more than the
-// half unit in the last place that this may add.
+// half unit in the last place that this may add; by a division where the reciprocal would be too large.
+__device__ __forceinline__ float near_quotient(float v, float scale, float inv)
+{
+    return scale >= 0x1p-100f ? v * inv : __fdiv_rn(v, scale);
+}
+
 __device__ __forceinline__ uint32_t e4m3x4_near(float a, float b, float c, float d, float scale, float inv)
 {
     if (scale >= 0x1p-100f) return e4m3x2(a * inv, b * inv) | (e4m3x2(c * inv, d * inv) << 16);

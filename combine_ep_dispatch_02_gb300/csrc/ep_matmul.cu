@@ -921,7 +921,7 @@ ep_product_few_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap ma
                     if (col == 0) p.out_scales[(int64_t)(x.m0 + c) * ((p.N + 127) / 128) + x.n0 / 128] = scale;
                     if (in)
                         ((uint8_t*)p.out)[(int64_t)(x.m0 + c) * p.N + x.n0 + col] =
-                            (uint8_t)e4m3x2(__fdiv_rn(sums[c * kFewCols + col], scale), 0.0f);
+                            (uint8_t)e4m3x2(near_quotient(sums[c * kFewCols + col], scale, __frcp_rn(scale)), 0.0f);
                 }
             }
             if (split_k > 1) {

@@ -451,6 +451,20 @@ def test_product_swiglu_of_small_sigmoids_times_large_values(rows, K):
     assert not q.float().any() and (s == 1).all()
 
 
+def test_product_swiglu_codes_do_not_depend_on_the_number_of_rows():
+    """With one block of K and whole-number codes every kernel has the same sums, so the same codes."""
+    for seed in range(16):
+        g = _gen(seed)
+        a = torch.randint(-8, 9, (200, 128), generator=g, device=DEV).float().to(F8)
+        b = torch.randint(-8, 9, (131072, 128), generator=g, device=DEV).float().to(F8)
+        sa = 0.002 * torch.rand(200, 1, generator=g, device=DEV)
+        sb = torch.rand(1024, 1, generator=g, device=DEV)
+        q, s = ep.matmul_fp8_swiglu(a, sa, b, sb)
+        few, s_few = ep.matmul_fp8_swiglu(a[:32].contiguous(), sa[:32].contiguous(), b, sb)
+        assert torch.equal(s[:32], s_few)
+        assert torch.equal(q[:32].view(torch.uint8), few.view(torch.uint8)), seed
+
+
 @pytest.mark.parametrize("rows", [2, 20, 60, 100, 140, 1000])
 def test_product_all_rows_in_one_of_many_groups(rows):
     g = _gen(rows)
