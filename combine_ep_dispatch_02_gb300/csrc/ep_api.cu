@@ -61,6 +61,7 @@ int fail(int code, const char* fmt, ...)
 
 int cuda_fail(cudaError_t e, const char* what)
 {
+    cudaGetLastError();   // reported here: not once more to the next caller that asks the runtime
     return fail(EP_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 

@@ -31,6 +31,7 @@ inline int layer_fail(int code, const char* fmt, ...)
 inline int layer_cuda(cudaError_t e, const char* who)
 {
     if (e == cudaSuccess) return EP_OK;
+    cudaGetLastError();   // reported here: not once more to the next caller that asks the runtime
     return layer_fail(EP_ERR_CUDA, "%s: %s (%s)", who, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 

@@ -6,6 +6,7 @@ truncate instead of round); a 16-bit output adds half a unit in its last place (
 BF16, 2^-11 for FP16, or half the smallest subnormal, 2^-25, for FP16); an e4m3 code is within 2^-4
 relative or 2^-10 absolute of the value it rounds.
 """
+import ctypes
 import threading
 
 import numpy as np
@@ -634,6 +635,28 @@ def test_binding_names_the_argument_at_fault():
         with pytest.raises(ep.EpError) as e:
             call()
         assert e.value.code == ep.EP_ERR_ARG and words in str(e.value), (words, str(e.value))
+
+
+def test_a_refused_launch_is_reported_by_its_own_call_only():
+    """A launch into the legacy stream is refused while another stream captures.  The call returns that error; the
+    runtime's record of it, which the next caller's check would read, is clear."""
+    rt, lib = ctypes.CDLL("libcudart.so.13"), ep.load_library()
+    y, pos, out, word = _zeros((2, 16), torch.bfloat16), _zeros((1, 1), torch.int32), _zeros((1, 16), torch.bfloat16), \
+        ep.experts._status_word(DEV)
+    stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+    torch.cuda.synchronize()
+    assert rt.cudaStreamCreate(ctypes.byref(stream)) == 0
+    assert rt.cudaStreamBeginCapture(stream, 0) == 0
+    try:
+        rc = lib.ep_return_rows(y.data_ptr(), None, pos.data_ptr(), None, 1, 1, 1, 2, 16, ep.EP_BF16, out.data_ptr(),
+                                word.data_ptr(), None)
+        left = rt.cudaPeekAtLastError()
+    finally:
+        rt.cudaStreamEndCapture(stream, ctypes.byref(graph))
+        rt.cudaGetLastError()
+        rt.cudaStreamDestroy(stream)
+    assert rc == ep.EP_ERR_CUDA and b"Capture" in lib.ep_last_error()
+    assert left == 0
 
 
 # ------------------------------------------------------------------------------------------- together
