@@ -21,6 +21,7 @@ LIB = os.path.join(PKG, "libep.so")
 SOURCES = ("ep_api.cu", "ep_route.cu", "ep_scatter.cu", "ep_combine.cu", "ep_noalloc.cu",
            "ep_fp8wire.cu", "ep_grouped.cu", "ep_norm.cu", "ep_sort.cu", "ep_matmul.cu")
 BINDING = os.path.join(PKG, "_ep_binding.so")
+BINDING_STAMP = os.path.join(BUILD_DIR, "_ep_binding.stamp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -40,6 +41,19 @@ def _stale(lib: str = LIB) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_built_for() -> str:
+    """What the binding's binary depends on besides its sources: PyTorch's C++ layout and Python's C API."""
+    import torch
+    return f"torch {torch.__version__}, cxx11 abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, {sysconfig.get_config_var('SOABI')}\n"
+
+
+def _binding_stale() -> bool:
+    if _stale(BINDING) or not os.path.exists(BINDING_STAMP):
+        return True
+    with open(BINDING_STAMP) as f:
+        return f.read() != _binding_built_for()
+
+
 def build_binding() -> None:
     """Compile csrc/ep_binding.cpp against the installed PyTorch; it calls libep.so through addresses it
     is given, so it links nothing of it."""
@@ -57,6 +71,9 @@ def build_binding() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on ep_binding.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(_binding_built_for())
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
@@ -64,7 +81,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
     """Compile libep.so; `defines` (e.g. ["EP_COMBINE_STAGES=4"]) and a separate lib_path /
     build_dir let a caller build tuning variants side by side."""
     product = lib_path == LIB and not defines
-    if not force and product and not _stale() and not _stale(BINDING):
+    if not force and product and not _stale() and not _binding_stale():
         return LIB
     os.makedirs(build_dir, exist_ok=True)
     cc = nvcc()

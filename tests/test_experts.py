@@ -179,3 +179,16 @@ def test_kernels_read_no_memory_before_their_own_wait(name, kernels):
         assert wait
         used = set(re.findall(r"\b[ap]\.(\w+)", before)) & arrays | set(re.findall(r"\b(\w+)(?:<[^;()]*>)?\(", before)) & readers
         assert not used, (name, used, before[-300:])
+
+
+def test_binding_is_built_again_for_another_pytorch(lib, monkeypatch):
+    """Its binary holds PyTorch's C++ layout, so its sources' times alone do not tell whether it still fits."""
+    built = []
+    monkeypatch.setattr(epbuild, "build_binding", lambda: built.append(1))
+    monkeypatch.setattr(epbuild.subprocess, "run", lambda *a, **k: epbuild.subprocess.CompletedProcess(a, 0, "", ""))
+    monkeypatch.setattr(epbuild.os, "replace", lambda *a: None)
+    epbuild.build()
+    assert not built
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".other")
+    epbuild.build()
+    assert built
