@@ -49,10 +49,11 @@ __device__ __forceinline__ void group_rows(const MatmulArgs& p, const int32_t* o
 // registers while the next block is multiplied.  The scales differ from block to block of K, so the
 // sums cannot stay in tensor memory over a tile.
 //
-// What bounds it.  A block takes 690 cycles, of which its products need 512 (128*256*128 at 8192 a cycle; 528
-// measured alone).  The rest is the way of an accumulator: multiplied in 512 cycles, 300 until the scaling
-// warps are told and the multiplying warp is told back, 400 until they have read it, 1220 for each of
-// two.  Tensor memory holds no third.  Loading half of b's bytes takes a block to 664 cycles, none to 650.
+// What bounds it is not settled.  A block takes 690 cycles, of which its products need 512 (128*256*128 at 8192 a
+// cycle; 528 measured alone).  An accumulator's way takes 1220 (multiplied in 512, 300 until the scaling warps are
+// told and the multiplying warp is told back, 400 until they have read it), and tensor memory holds two: 610 a
+// block.  But shortening that way did not help: two 128-column products a block, with two accumulators each, took
+// 703 cycles (a is read twice).  Loading half of b's bytes takes a block to 664 cycles, none to 650.
 // What it took to get there, of 1340 cycles at first: descriptors and loop counts in uniform registers; an
 // accumulator given back over a named barrier, because a hop over an mbarrier takes 300 cycles; factors
 // made ahead by idle warps; 32 columns read while the 32 before are added, across the ends of blocks.
@@ -60,8 +61,8 @@ __device__ __forceinline__ void group_rows(const MatmulArgs& p, const int32_t* o
 // reads the rows again; where tiles are too few for the SMs, tiles of 128 columns, or a tile's K by
 // several CTAs, are shorter.
 //
-// 32768 rows in 32 groups, 7168 x 4096 with SwiGLU: 690 us, 2790 TFLOP/s (0.73 of twice the measured BF16
-// rate), and 805 us once the card holds its power limit, at 1545 MHz.  2048 x 7168: 400 us, whose 16 blocks
+// 32768 rows in 32 groups, 7168 x 4096 with SwiGLU: 690 to 706 us, 2790 TFLOP/s (0.73 of twice the measured BF16
+// rate), and 805 to 840 us once the card holds its power limit, at 1545 MHz.  2048 x 7168: 400 us, whose 16 blocks
 // a tile cannot hide the tile's end, 3000 cycles.
 
 constexpr int kTileRows = 128, kTileCols = 256, kBlockK = 128;
@@ -646,8 +647,8 @@ ep_product_rows_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap m
 // leaves its sums in its shared memory, and each adds up, in the order of the CTAs, the rows of T
 // that it finishes.  Roles as above, with four scaling warps: a thread owns one output column.
 //
-// 256 rows in 32 groups, 7168 x 4096 with SwiGLU: 140 us, 6.7 TB/s (0.99 of the measured copy), tensor cores
-// 4 % busy.  One row of 7168 x 2048: 7 us where the weights' bytes take 2.2; the rest is the launch, the
+// 256 rows in 32 groups, 7168 x 4096 with SwiGLU: 143 us, 6.6 TB/s (0.97 of the measured copy), tensor cores
+// 4 % busy.  One row of 7168 x 2048: 6 us where the weights' bytes take 2.2; the rest is the launch, the
 // first load's way from HBM and the cluster's exchange, each 1 to 2 us.
 
 constexpr int kFewThreads = 256;
@@ -1082,6 +1083,9 @@ cudaError_t launch_product_few(const MatmulArgs& p, const CUtensorMap& ma, const
 //   32 groups, 7168 x 4096 with SwiGLU   of 8 rows 145 : 152     of 16 rows 152 : 153    of 24 rows 167 : 153
 // The 128-row tiles multiply rows that are not there, which costs them nothing while the weights' bytes or
 // the tiles' number set the time; a group whose rows pass a tile of few reads its weights twice.
+// The host knows p.rows alone, not what the groups hold of them: a buffer far longer than its groups takes the
+// 128-row tiles (256 rows held of 262144, 32 groups, 7168 x 4096 with SwiGLU 151 us, against 143 in a buffer of
+// their length; 8 rows held 36.4 against 32.8; 256 held of 32768, 2048 x 7168 73 against 75).
 int few_rows_tile(const MatmulArgs& p, int sms)
 {
     // whether the wide tiles leave half of the SMs to narrower ones or to parts of K

@@ -10,7 +10,7 @@
 // in one launch and placed in a second, whose CTAs each add up the counts of the tiles; above 64 tiles,
 // tiles of 8192 pairs, and one CTA scans the counts (groups x tiles) in a launch between the two.
 // 64 x 8 pairs and 256 groups take 2.5 us, 65536 pairs 8.2 us: two launches and a few trips to L2; 2 million
-// pairs 44 us, mostly the one CTA's scan.
+// pairs 44 us (56 with a dispatch's counts), mostly the one CTA's scan.
 // Within a warp, __match_any_sync gives a pair's rank among equal groups; a warp's running counts
 // live in shared memory, so no step has an order that atomics could change.
 #include "ep_layer.cuh"
@@ -524,8 +524,10 @@ cudaError_t launch_return_backward(const RowsArgs& a, cudaStream_t s)
 {
     const bool warp = a.vecs <= kWarpRowVecs;
     const unsigned grid = (unsigned)(warp ? (a.rows + kRowThreads / 32 - 1) / (kRowThreads / 32) : a.rows);
-    // 8 slots together shorten one row's chain of loads (64 rows of 7168: 9.2 -> 6.7 us); with every SM
-    // full their registers cost more (4096 rows: 4 slots 151.8 us, 8 slots 157.5)
+    // 8 slots together shorten one row's chain of loads; with every SM full their registers cost more.  us, 4 slots
+    // against 8, rows of 8 slots: of 7168, 64 rows 9.3 : 6.9, 256 11.3 : 9.9, 512 17.4 : 18.4, 768 33.9 : 33.5,
+    // 1024 42.9 : 44.5, 4096 151.5 : 157.0; of 2048, 256 rows 5.1 : 4.7, 512 7.3 : 7.8, 1024 11.1 : 12.8, 4096
+    // 45.8 : 55.0.  Between 512 and 1024 rows neither is ahead at every width; the bound suits the widest.
     auto* kernel = warp ? (a.k <= 4 ? ep_return_rows_backward_kernel<FP16, true, 4>
                                     : ep_return_rows_backward_kernel<FP16, true, 8>)
                         : (a.k <= 4 || a.rows >= 1024 ? ep_return_rows_backward_kernel<FP16, false, 4>

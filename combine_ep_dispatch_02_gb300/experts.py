@@ -12,6 +12,9 @@ Arguments are checked before any launch (``EpError`` with ``EP_ERR_ARG``); what 
 see is recorded in one status word per device, read and cleared by ``op_status``.  The first call on a
 device makes that word and waits for it, so a call comes before a graph's capture.
 
+The gradients are calls of their own, for a training step or its ``torch.autograd.Function`` to make: no call
+here records itself for autograd, and its results never require a gradient.
+
 The checks and allocations are native (``_ep_binding``, csrc/ep_binding.cpp): these calls are often one
 token's, and marshalling in Python would take longer than the kernels.
 """
@@ -167,7 +170,8 @@ def matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scale
     a [rows][inner] with a_scales [rows][ceil(inner/128)]; b [columns][inner] with b_scales
     [ceil(columns/128)][ceil(inner/128)].  With offsets [groups + 1] int32 on the device, b and b_scales
     have a leading [groups] and rows offsets[g] .. offsets[g + 1] - 1 take b[g]; rows outside every group
-    are not written.  inner must be a multiple of 16."""
+    are not written.  inner must be a multiple of 16.  The kernel is chosen from a's rows, so a buffer cut to
+    about the rows that the groups hold can be faster than one of full capacity."""
     code = _OUT_CODES.get(out_dtype)
     if code is None:
         raise EpError(EP_ERR_ARG, f"out_dtype={out_dtype!r} is neither 'bf16' nor 'fp16'")

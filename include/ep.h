@@ -437,6 +437,9 @@ int ep_return_rows_backward(const void* y, const float* weights, const void* dou
  * FP32's smallest normal number, 2^-126, counts as 0.
  * a, b and out are 16-byte aligned.  The result does not depend on timing: sums are added in a fixed order.
  * A bounded wait that runs out on the GPU is recorded as EP_ERR_DEVICE_TIMEOUT; out is then not valid.
+ * The kernel and its split are chosen from rows, the buffer's length; what the groups hold of it only the GPU
+ * knows.  A buffer far longer than its groups runs the form for that length (up to a tenth slower for a few
+ * rows per group).
  * The first call on a device looks up a driver entry point and should come before any stream capture.
  */
 int ep_matmul_fp8(const void* a, const float* a_scales, const void* b, const float* b_scales,
