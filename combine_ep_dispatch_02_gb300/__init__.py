@@ -37,7 +37,10 @@ EXPORTS = ("ep_plan_create", "ep_plan_destroy", "ep_plan_set_variant", "ep_plan_
            "ep_quantize_received", "ep_combine_fp8", "ep_group_by_expert", "ep_ungroup_by_expert",
            "ep_dispatch_grouped", "ep_quantize_received_fp4", "ep_combine_fp4", "ep_probe_read",
            "ep_rms_norm_fp8", "ep_sort_workspace_bytes", "ep_sort_by_expert", "ep_sorted_rows",
-           "ep_return_rows", "ep_return_rows_backward", "ep_matmul_fp8", "ep_take_status")
+           "ep_return_rows", "ep_return_rows_backward", "ep_matmul_fp8", "ep_take_status",
+           "ep_rms_norm_join", "ep_rms_norm_join_workspace_bytes", "ep_rms_norm_join_backward", "ep_swiglu_saved",
+           "ep_swiglu_saved_backward")
+GATE_KINDS = {"none": 0, "row": 1, "channel": 2, "element": 3}
 
 
 class EpError(RuntimeError):
@@ -51,6 +54,15 @@ class DispatchOut(ctypes.Structure):
                 ("recv_w", ctypes.c_void_p), ("recv_scales", ctypes.c_void_p),
                 ("recv_count", ctypes.c_void_p), ("src_token_pos", ctypes.c_void_p),
                 ("rows_per_rank", ctypes.c_int64), ("epoch", ctypes.c_uint64)]
+
+
+class JoinArgs(ctypes.Structure):
+    """``ep_join``."""
+    _fields_ = [("y", ctypes.c_void_p), ("y_stride", ctypes.c_int64), ("post_weight", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_int64), ("pre_weight", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("hidden", ctypes.c_int), ("dtype", ctypes.c_int), ("post_fp32", ctypes.c_int),
+                ("pre_fp32", ctypes.c_int), ("gate_kind", ctypes.c_int), ("gate_fp32", ctypes.c_int),
+                ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -99,6 +111,11 @@ def load_library(path: Optional[str] = None):
         "ep_return_rows_backward": (I, [V, V, V, V, V, I, L, I, L, I, I, V, V, V, V]),
         "ep_take_status": (I, [V, V, V]),
         "ep_matmul_fp8": (I, [V, V, V, V, V, L, I, I, I, I, I, V, V, V, V]),
+        "ep_rms_norm_join": (I, [ctypes.POINTER(JoinArgs), V, L, V, V, V, V, V, V, V]),
+        "ep_rms_norm_join_workspace_bytes": (SZ, [L, I]),
+        "ep_rms_norm_join_backward": (I, [ctypes.POINTER(JoinArgs), V, V, V, V, L, V, L, V, V, V, V, V, V, SZ, V]),
+        "ep_swiglu_saved": (I, [V, L, I, L, I, V, V, V, V, V, V]),
+        "ep_swiglu_saved_backward": (I, [V, V, V, L, I, L, I, V, V, V, V, V]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -464,5 +481,6 @@ class Plan:
         return v.value
 
 
-from .experts import (ExpertOrder, matmul_fp8, matmul_fp8_swiglu, op_status, return_rows,  # noqa: E402
-                      return_rows_backward, rms_norm_fp8, sort_by_expert, sorted_rows, sorted_rows_backward)
+from .experts import (ExpertOrder, Joined, JoinGradients, matmul_fp8, matmul_fp8_swiglu, op_status,  # noqa: E402
+                      return_rows, return_rows_backward, rms_norm_fp8, rms_norm_join, rms_norm_join_backward,
+                      sort_by_expert, sorted_rows, sorted_rows_backward, swiglu_saved, swiglu_saved_backward)

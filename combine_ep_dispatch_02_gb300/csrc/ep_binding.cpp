@@ -15,6 +15,7 @@
 
 #include <cstdarg>
 #include <cstdio>
+#include <cstring>
 #include <string>
 
 #include "ep.h"
@@ -28,6 +29,11 @@ decltype(&ep_sorted_rows) g_rows;
 decltype(&ep_return_rows) g_return;
 decltype(&ep_return_rows_backward) g_back;
 decltype(&ep_matmul_fp8) g_matmul;
+decltype(&ep_rms_norm_join) g_join;
+decltype(&ep_rms_norm_join_workspace_bytes) g_join_bytes;
+decltype(&ep_rms_norm_join_backward) g_join_back;
+decltype(&ep_swiglu_saved) g_swiglu;
+decltype(&ep_swiglu_saved_backward) g_swiglu_back;
 decltype(&ep_strerror) g_strerror;
 decltype(&ep_last_error) g_last_error;
 PyObject* g_error;         // the package's EpError
@@ -373,6 +379,186 @@ PyObject* matmul(PyObject* const* v)
     return swiglu ? pack({out, scales}) : wrap(out);
 }
 
+// Address of a 2-D tensor of rows, of this type and shape on this device, whose rows may be a stride apart.
+void* row_data(const at::Tensor& t, const char* what, at::ScalarType type, at::IntArrayRef shape, at::Device device,
+               int64_t& stride)
+{
+    if (t.device() != device)
+        refuse("%s is on %s, the call runs on %s", what, t.device().str().c_str(), device.str().c_str());
+    if (t.scalar_type() != type) refuse("%s is %s, the call takes %s", what, type_text(t.scalar_type()), type_text(type));
+    if (t.sizes() != shape)
+        refuse("%s has shape %s, the call takes %s", what, shape_text(t.sizes()).c_str(), shape_text(shape).c_str());
+    if (t.size(1) > 1 && t.stride(1) != 1) refuse("%s: the elements of a row are not consecutive", what);
+    stride = t.size(0) > 1 ? t.stride(0) : t.size(1);
+    return t.data_ptr();
+}
+
+// A vector along the channels, of `type` or FP32; NULL for None.
+const void* channels(PyObject* o, const char* what, at::ScalarType type, int64_t hidden, at::Device dev, int& fp32)
+{
+    if (o == Py_None) return nullptr;
+    const at::Tensor& w = tensor(o, what);
+    fp32 = w.scalar_type() == at::kFloat;
+    return data(w, what, fp32 ? at::kFloat : type, {hidden}, dev);
+}
+
+double number(PyObject* o)
+{
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw Raised{};
+    return v;
+}
+
+// The arguments that the join and its gradient share.
+ep_join join_args(PyObject* y_o, PyObject* post_o, PyObject* gate_o, PyObject* pre_o, PyObject* scale_o)
+{
+    const at::Tensor& y = lead_tensor(y_o, "y");
+    ep_join j{};
+    j.dtype = half_code(y, "y");
+    if (y.dim() != 2) refuse("y has %lld dimensions, the call takes [rows][hidden]", (long long)y.dim());
+    const at::Device dev = y.device();
+    const int64_t hidden = y.size(1);
+    j.rows = y.size(0);
+    j.hidden = clamp_int(hidden);
+    j.y = row_data(y, "y", y.scalar_type(), y.sizes(), dev, j.y_stride);
+    j.post_weight = channels(post_o, "post_weight", y.scalar_type(), hidden, dev, j.post_fp32);
+    j.pre_weight = channels(pre_o, "pre_weight", y.scalar_type(), hidden, dev, j.pre_fp32);
+    j.residual_scale = (float)number(scale_o);
+    if (gate_o != Py_None) {
+        const at::Tensor& g = tensor(gate_o, "gate");
+        if (g.dim() == 1) {
+            j.gate_kind = EP_GATE_CHANNEL;
+            j.gate = channels(gate_o, "gate", y.scalar_type(), hidden, dev, j.gate_fp32);
+        } else if (g.dim() == 2 && g.size(1) == 1) {
+            j.gate_kind = EP_GATE_ROW;
+            j.gate = data(g, "gate", at::kFloat, {j.rows, 1}, dev);
+        } else {
+            j.gate_kind = EP_GATE_ELEMENT;
+            if (g.dim() != 2)
+                refuse("gate has shape %s, the call takes [hidden], [rows][1] or [rows][hidden]", shape_text(g.sizes()).c_str());
+            j.gate = row_data(g, "gate", y.scalar_type(), y.sizes(), dev, j.gate_stride);
+        }
+    }
+    return j;
+}
+
+bool truth(PyObject* o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Raised{};
+    return v != 0;
+}
+
+// (y, residual, post_weight, gate, pre_weight, residual_scale, eps, fp8, want_n)
+PyObject* join(PyObject* const* v)
+{
+    ep_join j = join_args(v[0], v[2], v[3], v[4], v[5]);
+    const at::Tensor& y = THPVariable_Unpack(v[0]);
+    const at::Device dev = y.device();
+    j.eps = (float)number(v[6]);
+    const bool fp8 = truth(v[7]), want_n = truth(v[8]);
+    if (!j.pre_weight && (fp8 || want_n)) refuse("n or its codes are wanted without pre_weight");
+    int64_t rs = 0;
+    const void* r = row_data(tensor(v[1], "residual"), "residual", y.scalar_type(), y.sizes(), dev, rs);
+    const c10::cuda::CUDAGuard guard(dev);
+    at::Tensor h = empty(y.sizes(), y.scalar_type(), dev), n, q, s, post, pre;
+    if (want_n) n = empty(y.sizes(), y.scalar_type(), dev);
+    if (fp8) {
+        q = empty(y.sizes(), at::kFloat8_e4m3fn, dev);
+        s = empty({j.rows, (y.size(1) + 127) / 128}, at::kFloat, dev);
+    }
+    if (j.post_weight) post = empty({j.rows}, at::kFloat, dev);
+    if (j.pre_weight) pre = empty({j.rows}, at::kFloat, dev);
+    check(g_join(&j, r, rs, h.data_ptr(), get(n), get(q), (float*)get(s), (float*)get(post), (float*)get(pre), stream(dev)));
+    return pack({h, n, q, s, post, pre});
+}
+
+// (y, h, post_rstd, pre_rstd, dh, dn, post_weight, gate, pre_weight, residual_scale)
+PyObject* join_backward(PyObject* const* v)
+{
+    const ep_join j = join_args(v[0], v[6], v[7], v[8], v[9]);
+    const at::Tensor& y = THPVariable_Unpack(v[0]);
+    const at::Device dev = y.device();
+    const at::ScalarType type = y.scalar_type();
+    int64_t dh_stride = 0, dn_stride = 0;
+    const void* dh = v[4] == Py_None ? nullptr : row_data(tensor(v[4], "dh"), "dh", type, y.sizes(), dev, dh_stride);
+    const void* dn = v[5] == Py_None ? nullptr : row_data(tensor(v[5], "dn"), "dn", type, y.sizes(), dev, dn_stride);
+    if ((v[5] != Py_None) != (v[8] != Py_None)) refuse("dn and pre_weight are not both given, nor both None");
+    if (v[4] == Py_None && v[5] == Py_None) refuse("neither dh nor dn is given");
+    const void *h = nullptr, *post = nullptr, *pre = nullptr;
+    if (j.pre_weight) {
+        h = data(tensor(v[1], "joined.h"), "joined.h", type, y.sizes(), dev);
+        pre = data(tensor(v[3], "joined.pre_rstd"), "joined.pre_rstd", at::kFloat, {j.rows}, dev);
+    }
+    if (j.post_weight) post = data(tensor(v[2], "joined.post_rstd"), "joined.post_rstd", at::kFloat, {j.rows}, dev);
+    const c10::cuda::CUDAGuard guard(dev);
+    at::Tensor dy = empty(y.sizes(), type, dev), dres = empty(y.sizes(), type, dev), dpost, dgate, dpre, work;
+    if (j.post_weight) dpost = empty({y.size(1)}, at::kFloat, dev);
+    if (j.pre_weight) dpre = empty({y.size(1)}, at::kFloat, dev);
+    if (j.gate_kind != EP_GATE_NONE)
+        dgate = empty(THPVariable_Unpack(v[7]).sizes(), j.gate_kind == EP_GATE_ELEMENT ? type : at::kFloat, dev);
+    const size_t need = g_join_bytes(j.rows, j.hidden);
+    if (need) work = empty({(int64_t)need}, at::kByte, dev);
+    check(g_join_back(&j, h, (const float*)post, (const float*)pre, dh, dh_stride, dn, dn_stride, dy.data_ptr(),
+                      dres.data_ptr(), (float*)get(dpost), get(dgate), (float*)get(dpre), get(work), need, stream(dev)));
+    return pack({dy, dres, dpost, dgate, dpre});
+}
+
+// The last of a sort's offsets, past which a buffer's rows hold nothing; NULL for None.
+const int32_t* rows_end(PyObject* offsets, at::Device dev)
+{
+    if (offsets == Py_None) return nullptr;
+    const at::Tensor& t = tensor(offsets, "offsets");
+    if (t.dim() != 1 || t.size(0) < 1) refuse("offsets has shape %s, the call takes [groups + 1]", shape_text(t.sizes()).c_str());
+    return (const int32_t*)data(t, "offsets", at::kInt, t.sizes(), dev) + t.size(0) - 1;
+}
+
+// (gate_up, offsets)
+PyObject* swiglu_saved(PyObject* const* v)
+{
+    const at::Tensor& x = lead_tensor(v[0], "gate_up");
+    const int code = half_code(x, "gate_up");
+    if (x.dim() != 2 || x.size(1) % 2 != 0)
+        refuse("gate_up has shape %s, the call takes [rows][2 * inner]", shape_text(x.sizes()).c_str());
+    const at::Device dev = x.device();
+    const int64_t rows = x.size(0), inner = x.size(1) / 2;
+    int64_t stride = 0;
+    const void* xp = row_data(x, "gate_up", x.scalar_type(), x.sizes(), dev, stride);
+    const int32_t* end = rows_end(v[1], dev);
+    const c10::cuda::CUDAGuard guard(dev);
+    at::Tensor q = empty({rows, inner}, at::kFloat8_e4m3fn, dev), s = empty({rows, (inner + 127) / 128}, at::kFloat, dev),
+               saved = empty({rows, 2 * inner}, at::kFloat8_e4m3fn, dev),
+               saved_s = empty({rows, (2 * inner + 127) / 128}, at::kFloat, dev);
+    check(g_swiglu(xp, stride, code, rows, clamp_int(inner), end, q.data_ptr(), (float*)s.data_ptr(), saved.data_ptr(),
+                   (float*)saved_s.data_ptr(), stream(dev)));
+    return pack({q, s, saved, saved_s});
+}
+
+// (saved, saved_scales, dz, offsets, fp8)
+PyObject* swiglu_saved_backward(PyObject* const* v)
+{
+    const at::Tensor& dz = lead_tensor(v[2], "dz");
+    const int code = half_code(dz, "dz");
+    if (dz.dim() != 2) refuse("dz has %lld dimensions, the call takes [rows][inner]", (long long)dz.dim());
+    const at::Device dev = dz.device();
+    const int64_t rows = dz.size(0), inner = dz.size(1), blocks = (2 * inner + 127) / 128;
+    const void* saved = data(tensor(v[0], "saved"), "saved", at::kFloat8_e4m3fn, {rows, 2 * inner}, dev);
+    const void* saved_s = data(tensor(v[1], "saved_scales"), "saved_scales", at::kFloat, {rows, blocks}, dev);
+    int64_t stride = 0;
+    const void* dp = row_data(dz, "dz", dz.scalar_type(), dz.sizes(), dev, stride);
+    const int32_t* end = rows_end(v[3], dev);
+    const bool fp8 = truth(v[4]);
+    const c10::cuda::CUDAGuard guard(dev);
+    at::Tensor d = empty({rows, 2 * inner}, dz.scalar_type(), dev), q, s;
+    if (fp8) {
+        q = empty({rows, 2 * inner}, at::kFloat8_e4m3fn, dev);
+        s = empty({rows, blocks}, at::kFloat, dev);
+    }
+    check(g_swiglu_back(saved, (const float*)saved_s, dp, stride, code, rows, clamp_int(inner), end, d.data_ptr(), get(q),
+                        (float*)get(s), stream(dev)));
+    return pack({d, q, s});
+}
+
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n)
 {
@@ -389,19 +575,30 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// bind(EpError, make_status, addresses of the C ABI functions in the order below)
+// The C ABI functions that bind() takes, in its order.
+struct Bound {
+    const char* name;
+    void* target;
+};
+#define EP_BOUND(variable) {#variable, &variable}
+const Bound g_bound[] = {EP_BOUND(g_norm), EP_BOUND(g_sort_bytes), EP_BOUND(g_sort), EP_BOUND(g_rows), EP_BOUND(g_return),
+                         EP_BOUND(g_back), EP_BOUND(g_matmul), EP_BOUND(g_join), EP_BOUND(g_join_bytes), EP_BOUND(g_join_back),
+                         EP_BOUND(g_swiglu), EP_BOUND(g_swiglu_back), EP_BOUND(g_strerror), EP_BOUND(g_last_error)};
+constexpr int kBound = sizeof g_bound / sizeof g_bound[0];
+
+// bind(EpError, make_status, addresses of the C ABI functions in the order above)
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n)
 {
-    void* f[9];
-    if (n != 11) {
-        PyErr_SetString(PyExc_TypeError, "bind takes EpError, make_status and nine addresses");
+    void* f[kBound];
+    if (n != 2 + kBound) {
+        PyErr_Format(PyExc_TypeError, "bind takes EpError, make_status and %d addresses", kBound);
         return nullptr;
     }
-    for (int i = 0; i < 9; ++i) {
+    for (int i = 0; i < kBound; ++i) {
         f[i] = PyLong_AsVoidPtr(args[2 + i]);
         if (PyErr_Occurred()) return nullptr;
         if (!f[i]) {
-            PyErr_SetString(PyExc_ValueError, "bind: a function's address is 0");
+            PyErr_Format(PyExc_ValueError, "bind: the address of %s is 0", g_bound[i].name);
             return nullptr;
         }
     }
@@ -409,15 +606,7 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n)
     Py_XDECREF(g_make_status);
     g_error = Py_NewRef(args[0]);
     g_make_status = Py_NewRef(args[1]);
-    g_norm = (decltype(g_norm))f[0];
-    g_sort_bytes = (decltype(g_sort_bytes))f[1];
-    g_sort = (decltype(g_sort))f[2];
-    g_rows = (decltype(g_rows))f[3];
-    g_return = (decltype(g_return))f[4];
-    g_back = (decltype(g_back))f[5];
-    g_matmul = (decltype(g_matmul))f[6];
-    g_strerror = (decltype(g_strerror))f[7];
-    g_last_error = (decltype(g_last_error))f[8];
+    for (int i = 0; i < kBound; ++i) memcpy(g_bound[i].target, &f[i], sizeof f[i]);
     Py_RETURN_NONE;
 }
 
@@ -429,6 +618,10 @@ PyMethodDef g_methods[] = {
     {"return_rows", (PyCFunction)(void (*)())entry<return_rows, 5>, METH_FASTCALL, nullptr},
     {"return_rows_backward", (PyCFunction)(void (*)())entry<return_rows_backward, 6>, METH_FASTCALL, nullptr},
     {"matmul_fp8", (PyCFunction)(void (*)())entry<matmul, 6>, METH_FASTCALL, nullptr},
+    {"rms_norm_join", (PyCFunction)(void (*)())entry<join, 9>, METH_FASTCALL, nullptr},
+    {"rms_norm_join_backward", (PyCFunction)(void (*)())entry<join_backward, 10>, METH_FASTCALL, nullptr},
+    {"swiglu_saved", (PyCFunction)(void (*)())entry<swiglu_saved, 2>, METH_FASTCALL, nullptr},
+    {"swiglu_saved_backward", (PyCFunction)(void (*)())entry<swiglu_saved_backward, 5>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ep_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

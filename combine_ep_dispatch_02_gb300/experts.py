@@ -4,7 +4,10 @@
   ``"fp8"`` plan's dispatch;
 * ``sort_by_expert``, ``sorted_rows``, ``return_rows`` and the gradients ``sorted_rows_backward`` and
   ``return_rows_backward``: received rows in compact expert order, and back with routing weights;
-* ``matmul_fp8`` and ``matmul_fp8_swiglu``: the block-scaled e4m3 product, dense or by expert.
+* ``matmul_fp8`` and ``matmul_fp8_swiglu``: the block-scaled e4m3 product, dense or by expert;
+* ``rms_norm_join`` and its gradient: the norm after a block, its gate, the scaled residual and the norm before the
+  next block;
+* ``swiglu_saved`` and its gradient: SwiGLU between two products for training, its input kept as e4m3.
 
 Every call runs on the device of its first tensor, enqueues on the current stream (or ``stream``) and
 returns without waiting.  Outputs and workspaces come from PyTorch's allocator on that stream.
@@ -37,7 +40,8 @@ BINDING_PATH = os.path.join(_PKG, "_ep_binding.so")
 _OUT_CODES = {"bf16": EP_BF16, "fp16": EP_FP16}
 # the C ABI functions the binding calls, in the order of its bind()
 _BOUND = ("ep_rms_norm_fp8", "ep_sort_workspace_bytes", "ep_sort_by_expert", "ep_sorted_rows", "ep_return_rows",
-          "ep_return_rows_backward", "ep_matmul_fp8", "ep_strerror", "ep_last_error")
+          "ep_return_rows_backward", "ep_matmul_fp8", "ep_rms_norm_join", "ep_rms_norm_join_workspace_bytes",
+          "ep_rms_norm_join_backward", "ep_swiglu_saved", "ep_swiglu_saved_backward", "ep_strerror", "ep_last_error")
 _status_words = {}
 _binding = None
 _bound_to = None
@@ -185,3 +189,67 @@ def matmul_fp8_swiglu(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, 
     scales [rows][ceil(columns/256)]), the a and a_scales of a following matmul_fp8.  Arguments as
     matmul_fp8; columns must be a multiple of 32."""
     return _on(stream, _native().matmul_fp8, a, a_scales, b, b_scales, offsets, EP_FP8_E4M3)
+
+
+@dataclasses.dataclass
+class Joined:
+    """What ``rms_norm_join`` returns; its gradient takes h and the roots that it made."""
+    h: Optional[torch.Tensor]                     # [rows][hidden]: the residual stream
+    n: Optional[torch.Tensor] = None              # [rows][hidden]: its norm
+    q: Optional[torch.Tensor] = None              # [rows][hidden] float8_e4m3fn: the norm's codes
+    scales: Optional[torch.Tensor] = None         # [rows][ceil(hidden/128)] FP32
+    post_rstd: Optional[torch.Tensor] = None      # [rows] FP32: 1 / sqrt(mean(y^2) + eps)
+    pre_rstd: Optional[torch.Tensor] = None       # [rows] FP32: 1 / sqrt(mean(h^2) + eps)
+
+
+@dataclasses.dataclass
+class JoinGradients:
+    """What ``rms_norm_join_backward`` returns; None for what the call was not given."""
+    dy: torch.Tensor
+    dresidual: torch.Tensor
+    dpost_weight: Optional[torch.Tensor]          # FP32
+    dgate: Optional[torch.Tensor]                 # of the gate's shape; FP32 unless that is [rows][hidden]
+    dpre_weight: Optional[torch.Tensor]           # FP32
+
+
+def rms_norm_join(y: torch.Tensor, residual: torch.Tensor, post_weight: Optional[torch.Tensor] = None,
+                  gate: Optional[torch.Tensor] = None, pre_weight: Optional[torch.Tensor] = None,
+                  residual_scale: float = 1.0, eps: float = 1e-6, fp8: bool = False, want_n: Optional[bool] = None,
+                  stream=None) -> Joined:
+    """A block's output joined to the residual stream, and the next block's input: u = y / sqrt(mean(y^2) + eps) *
+    post_weight (y itself without post_weight); h = residual_scale * residual + gate * u; n = h / sqrt(mean(h^2) +
+    eps) * pre_weight, only with pre_weight, from the unrounded h.  y and residual [rows][hidden] BF16 or FP16, hidden a
+    multiple of 16 up to 32768, rows any multiple of 8 elements apart; weights [hidden] of y's type or FP32; gate
+    [hidden] (of y's type or FP32), [rows][1] (FP32) or [rows][hidden] (of y's type).  fp8: n as e4m3 codes and block
+    scales, as ``rms_norm_fp8`` writes them.  want_n: n in 16 bits (by default where the codes are not wanted)."""
+    if want_n is None:
+        want_n = pre_weight is not None and not fp8
+    return Joined(*_on(stream, _native().rms_norm_join, y, residual, post_weight, gate, pre_weight, residual_scale, eps,
+                       fp8, want_n))
+
+
+def rms_norm_join_backward(joined: Joined, y: torch.Tensor, dh: Optional[torch.Tensor] = None,
+                           dn: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None,
+                           gate: Optional[torch.Tensor] = None, pre_weight: Optional[torch.Tensor] = None,
+                           residual_scale: float = 1.0, stream=None) -> JoinGradients:
+    """Gradients of rms_norm_join from those for h and n ([rows][hidden] of y's type; dh None for zeros, dn given if
+    pre_weight is), for the 16-bit h that it returned.  Other arguments as there, hidden up to 8192.  Sums over rows are
+    in FP32, in an order that the shape fixes."""
+    return JoinGradients(*_on(stream, _native().rms_norm_join_backward, y, joined.h, joined.post_rstd, joined.pre_rstd, dh,
+                              dn, post_weight, gate, pre_weight, residual_scale))
+
+
+def swiglu_saved(gate_up: torch.Tensor, offsets: Optional[torch.Tensor] = None, stream=None):
+    """z = gate * sigmoid(gate) * up of gate_up [rows][2 * inner] (``matmul_fp8``'s output: gate, then up; rows any
+    multiple of 8 elements apart), as e4m3 codes and block scales, with gate_up itself kept the same way for the
+    gradient: (q [rows][inner], scales, saved [rows][2 * inner], saved_scales).  inner must be a multiple of 16.  With
+    offsets (an order's), rows past the last are neither read nor written."""
+    return _on(stream, _native().swiglu_saved, gate_up, offsets)
+
+
+def swiglu_saved_backward(saved: torch.Tensor, saved_scales: torch.Tensor, dz: torch.Tensor,
+                          offsets: Optional[torch.Tensor] = None, fp8: bool = False, stream=None):
+    """Gradient of swiglu_saved for gate_up, at the saved values: (d [rows][2 * inner] of dz's type, q, scales), the
+    latter the same as e4m3 codes and block scales if fp8, else None: the a of a ``matmul_fp8`` with the transposed
+    weights.  dz [rows][inner] BF16 or FP16; the quantiser of z passes it unchanged."""
+    return _on(stream, _native().swiglu_saved_backward, saved, saved_scales, dz, offsets, fp8)

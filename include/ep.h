@@ -446,6 +446,86 @@ int ep_matmul_fp8(const void* a, const float* a_scales, const void* b, const flo
                   const int32_t* offsets, int64_t rows, int groups, int columns, int inner, int swiglu, int dtype,
                   void* out, float* out_scales, int32_t* device_status, void* stream);
 
+/*
+ * The norm after a block, joined through a gate to the scaled residual, with the norm before the next block.  Per row,
+ * in FP32, rs(v) = 1 / sqrt(mean(v^2) + eps):
+ *   u = y * rs(y) * post_weight    (u = y without post_weight)
+ *   h = residual_scale * residual + gate * u
+ *   n = h * rs(h) * pre_weight     (only with pre_weight; the norm takes the unrounded h)
+ * The arguments that the forward call and its gradient share:
+ */
+enum { EP_GATE_NONE = 0,      /* no gate: 1 */
+       EP_GATE_ROW = 1,       /* [rows] FP32 */
+       EP_GATE_CHANNEL = 2,   /* [hidden] of dtype, or FP32 if gate_fp32 is not 0 */
+       EP_GATE_ELEMENT = 3    /* [rows][hidden] of dtype, rows gate_stride elements apart */ };
+
+typedef struct ep_join {
+    const void* y;             /* [rows][hidden] of dtype: the block's output */
+    int64_t y_stride;          /* elements between rows; every row stride is a multiple of 8, its array 16-byte aligned */
+    const void* post_weight;   /* [hidden] of dtype, or FP32 if post_fp32 is not 0; 16-byte aligned; may be NULL */
+    const void* gate;
+    int64_t gate_stride;
+    const void* pre_weight;    /* [hidden] of dtype, or FP32 if pre_fp32 is not 0; 16-byte aligned; may be NULL */
+    int64_t rows;
+    int hidden;                /* a multiple of 16 in 16..32768 (8192 for the gradient) */
+    int dtype;                 /* EP_BF16 or EP_FP16 */
+    int post_fp32, pre_fp32, gate_kind, gate_fp32;
+    float residual_scale, eps; /* eps >= 0 */
+} ep_join;
+
+/*
+ *   residual     [rows][hidden] of dtype, rows residual_stride elements apart
+ *   h, n         [rows][hidden] of dtype, dense; n may be NULL
+ *   q, scales    n as e4m3 codes [rows][hidden] and FP32 scales [rows][ceil(hidden/128)], quantised as by
+ *                ep_rms_norm_fp8: the input of an EP_FP8_E4M3 dispatch or of ep_matmul_fp8; both may be NULL
+ *   post_rstd, pre_rstd  [rows] FP32: rs(y) and rs(h), for the gradient; each is written if its weight is given
+ * h may be y or residual itself, if that is dense.
+ */
+int ep_rms_norm_join(const ep_join* join, const void* residual, int64_t residual_stride, void* h, void* n, void* q,
+                     float* scales, float* post_rstd, float* pre_rstd, void* stream);
+
+/*
+ * Its gradient, from the 16-bit h and the roots that the forward call left; dh and dn are the gradients for h and n
+ * ([rows][hidden] of dtype, rows dh_stride and dn_stride elements apart).  dh may be NULL (zeros); dn is given if
+ * pre_weight is.  e4m3 codes are taken for the values that they round.
+ *   D = dh + rs(h) * (g - x * mean(g * x)),  g = dn * pre_weight,  x = h * rs(h)
+ *   dresidual    [rows][hidden] of dtype: residual_scale * D; may be NULL
+ *   dy           [rows][hidden] of dtype: rs(y) * (p - v * mean(p * v)),  p = D * gate * post_weight,  v = y * rs(y)
+ *                (D * gate without post_weight)
+ *   dgate        D * u: [rows] FP32 summed over the row, [hidden] FP32 summed over rows, or [rows][hidden] of dtype
+ *   dpost_weight, dpre_weight  [hidden] FP32: sums over rows of D * gate * v and of dn * x
+ * Sums are in FP32 and in an order that depends on rows, hidden and the GPU's number of SMs alone.  The workspace holds
+ * ep_rms_norm_join_workspace_bytes() at least, 16-byte aligned (0 for no rows and for invalid shapes).
+ */
+size_t ep_rms_norm_join_workspace_bytes(int64_t rows, int hidden);
+int ep_rms_norm_join_backward(const ep_join* join, const void* h, const float* post_rstd, const float* pre_rstd,
+                              const void* dh, int64_t dh_stride, const void* dn, int64_t dn_stride, void* dy,
+                              void* dresidual, float* dpost_weight, void* dgate, float* dpre_weight, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * SwiGLU for training, between ep_matmul_fp8's 16-bit output and the next ep_matmul_fp8, with its input kept in 8 bits.
+ *   gate_up      [rows][2*inner] of dtype (EP_BF16 or EP_FP16), gate then up; rows `stride` elements apart (a multiple of
+ *                8), 16-byte aligned
+ *   inner        a multiple of 16 in 16..2^20;  rows * blocks of 128 columns below 2^31
+ *   rows_end     one int32 on the device, or NULL: rows at or past it are neither read nor written (the last of a sort's
+ *                offsets)
+ *   q, scales    z = gate * sigmoid(gate) * up in FP32 as e4m3 codes [rows][inner], [rows][ceil(inner/128)]
+ *   saved, saved_scales  gate_up as codes [rows][2*inner], [rows][ceil(2*inner/128)]
+ * Both are quantised as by ep_rms_norm_fp8, by the scale's reciprocal.  A sigmoid below FP32's smallest normal number,
+ * 2^-126, counts as 0.
+ *
+ * ep_swiglu_saved_backward takes the gradient at the saved values and lets it pass the quantiser of z unchanged:
+ *   dz           [rows][inner] of dtype, rows dz_stride elements apart
+ *   d_gate_up    [rows][2*inner] of dtype: dz * up * s * (1 + gate * (1 - s)), then dz * gate * s, s = sigmoid(gate)
+ *   q, scales    the same, unrounded, as codes [rows][2*inner], [rows][ceil(2*inner/128)]; both may be NULL
+ */
+int ep_swiglu_saved(const void* gate_up, int64_t stride, int dtype, int64_t rows, int inner, const int32_t* rows_end,
+                    void* q, float* scales, void* saved, float* saved_scales, void* stream);
+int ep_swiglu_saved_backward(const void* saved, const float* saved_scales, const void* dz, int64_t dz_stride, int dtype,
+                             int64_t rows, int inner, const int32_t* rows_end, void* d_gate_up, void* q, float* scales,
+                             void* stream);
+
 /* Static description of a status code ("unknown status" for any other value); never NULL.
  * With ep_last_error, the host side of the staging PR's caller contract ("refactor(EPv2):
  * replace per-module __device__ staging with shared buffer", section "Caller contract"): a
