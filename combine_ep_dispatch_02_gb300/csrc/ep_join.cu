@@ -44,11 +44,8 @@ struct JoinArgs {
     float residual_scale, eps;
 };
 
-constexpr int kJoinWarpsPerCta = 4;    // rows of a CTA when a row is one warp's
-constexpr int kJoinMaxThreads = 512;
+constexpr int kJoinMaxThreads = 512;   // of a wide row's CTA
 constexpr int kJoinMaxHidden = kJoinMaxThreads * 8 * 8;
-constexpr int kJoinBackMaxThreads = 1024;
-constexpr int kJoinBackMaxHidden = kJoinBackMaxThreads * 8;   // a vector of 8 columns per thread
 
 // Eight values of a vector along the channels: FP32, or of the rows' type.
 template <bool FP16>
@@ -64,34 +61,392 @@ __device__ __forceinline__ void load_channels(const void* p, int fp32, int v, fl
     }
 }
 
-// Sum over a row's threads, a warp or a CTA; `part` holds 32 floats that no earlier sum of the row uses.
-template <bool WARP>
-__device__ __forceinline__ float row_sum(float sum, float* part)
+// 16 bytes of global memory into shared memory, asynchronously; a thread's copies are grouped by copies_commit() and
+// copies_wait<N>() returns when all but the newest N groups have arrived, for the thread that made them.
+__device__ __forceinline__ void copy16(void* to, const void* from)
 {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+
+// Two sums over a row's threads, a warp or a CTA; `part` holds 32 pairs that no thread still reads.
+template <bool WARP>
+__device__ __forceinline__ float2 row_sums(float2 s, float2* part)
+{
+    auto warp_sums = [&] {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        for (int o = 16; o; o >>= 1) {
+            s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+            s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+        }
+    };
+    warp_sums();
     if constexpr (!WARP) {
         const int lane = threadIdx.x & 31;
-        if (lane == 0) part[threadIdx.x >> 5] = sum;
+        if (lane == 0) part[threadIdx.x >> 5] = s;
         __syncthreads();
-        sum = lane < (int)(blockDim.x >> 5) ? part[lane] : 0.0f;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        s = lane < (int)(blockDim.x >> 5) ? part[lane] : make_float2(0.0f, 0.0f);
+        warp_sums();
     }
-    return sum;
+    return s;
 }
 
-// A row by one warp (WARP) or by the whole CTA; VPT vectors per thread.
-template <bool FP16, bool WARP, int VPT>
-__global__ void __launch_bounds__(WARP ? 32 * kJoinWarpsPerCta : kJoinMaxThreads) ep_join_kernel(const JoinArgs a)
+__device__ __forceinline__ float sum_of(const float2 (&f)[4])
 {
-    __shared__ float part[2][32];
-    const int lane = threadIdx.x & 31;
-    const int t = WARP ? lane : threadIdx.x;
-    const int stride = WARP ? 32 : blockDim.x;
-    const int64_t row = WARP ? (int64_t)blockIdx.x * kJoinWarpsPerCta + (threadIdx.x >> 5) : blockIdx.x;
+    return ((f[0].x + f[0].y) + (f[1].x + f[1].y)) + ((f[2].x + f[2].y) + (f[3].x + f[3].y));
+}
+
+// ---- rows up to kJoinTeamHidden: one CTA of a vector of 8 columns per thread walks rows blockIdx.x, + gridDim.x, ...
+//
+// Rows are on their way through STAGES stages of shared memory, of which a thread fills and reads its own vectors only,
+// so that no barrier passes between copy and use.  The vectors along the channels (both weights and the channels' gate)
+// lie there too.  A row needs two sums over its threads, the second from the first's result, and a CTA's sum costs
+// some 500 cycles of shuffles and barrier; so the first sum of the next row is made together with the second of this one,
+// and a row meets one barrier.
+
+constexpr int kJoinTeamThreads = 1024;
+constexpr int kJoinTeamHidden = 8 * kJoinTeamThreads;
+
+// A thread's vectors along the channels in shared memory: post_weight, gate, pre_weight, 16 bytes each or 32 for FP32.
+struct Channels {
+    uint4 *post, *gate, *pre;
+};
+
+__host__ __device__ inline int channel_vectors(const JoinArgs& a)   // 16-byte vectors of all three
+{
+    return (a.post_weight ? 1 + (a.post_fp32 != 0) : 0) + (a.gate_kind == EP_GATE_CHANNEL ? 1 + (a.gate_fp32 != 0) : 0) +
+           (a.pre_weight ? 1 + (a.pre_fp32 != 0) : 0);
+}
+
+__device__ __forceinline__ Channels fetch_channels(const JoinArgs& a, uint4* to)   // part of the first group of copies
+{
+    const int t = threadIdx.x;
+    auto fetch = [&](const void* from, int fp32) {
+        uint4* at = to;
+        to += blockDim.x << (fp32 != 0);
+        if (t < a.vecs) {
+            if (fp32) {   // the second half of a thread's eight lies a row of vectors further on
+                copy16(at + t, (const uint8_t*)from + 32 * t);
+                copy16(at + blockDim.x + t, (const uint8_t*)from + 32 * t + 16);
+            } else {
+                copy16(at + t, (const uint8_t*)from + 16 * t);
+            }
+        }
+        return at + t;
+    };
+    Channels c{};
+    if (a.post_weight) c.post = fetch(a.post_weight, a.post_fp32);
+    if (a.gate_kind == EP_GATE_CHANNEL) c.gate = fetch(a.gate, a.gate_fp32);
+    if (a.pre_weight) c.pre = fetch(a.pre_weight, a.pre_fp32);
+    return c;
+}
+
+template <bool FP16>
+__device__ __forceinline__ void read_channels(const uint4* p, int fp32, float2 (&w)[4])
+{
+    if (fp32) {
+        const float4 lo = *reinterpret_cast<const float4*>(p), hi = *reinterpret_cast<const float4*>(p + blockDim.x);
+        w[0] = make_float2(lo.x, lo.y);
+        w[1] = make_float2(lo.z, lo.w);
+        w[2] = make_float2(hi.x, hi.y);
+        w[3] = make_float2(hi.z, hi.w);
+    } else {
+        unpack4x2<FP16>(*p, w);
+    }
+}
+
+template <bool FP16, bool WARP, int STAGES>
+__global__ void __launch_bounds__(WARP ? 32 : kJoinTeamThreads) ep_join_team_kernel(const JoinArgs a)
+{
+    extern __shared__ uint4 staged[];
+    __shared__ float2 part[2][32];
+    const int t = threadIdx.x;
+    const bool in = t < a.vecs;
+    const int64_t at = 16 * (int64_t)t, pitch = 16 * (int64_t)a.vecs;
+    const bool element = a.gate_kind == EP_GATE_ELEMENT;
+    const int slots = element ? 3 : 2;   // y, residual, the elements' gate
+    const float inv_hidden = __frcp_rn((float)a.hidden);
     follow_predecessor();
-    if (WARP && row >= a.rows) return;
+    const Channels ch = fetch_channels(a, staged + STAGES * slots * blockDim.x);
+    auto stage_of = [&](int stage) { return staged + stage * slots * blockDim.x + t; };
+    auto fetch = [&](int64_t row, int stage) {
+        if (in && row < a.rows) {
+            uint4* to = stage_of(stage);
+            copy16(to, a.y + row * a.y_pitch + at);
+            copy16(to + blockDim.x, a.residual + row * a.r_pitch + at);
+            if (element) copy16(to + 2 * blockDim.x, a.gate + row * a.g_pitch + at);
+        }
+        copies_commit();
+    };
+    auto squares = [&](int stage) {   // of a row's y
+        float2 y[4], s = both(0.0f);
+        unpack4x2<FP16>(*stage_of(stage), y);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s = fused2(y[j], y[j], s);
+        return s.x + s.y;
+    };
+    auto root = [&](float sum) { return __frsqrt_rn(fmaf(sum, inv_hidden, a.eps)); };
+    auto gate_of = [&](int64_t row) {
+        return a.gate_kind == EP_GATE_ROW && row < a.rows ? reinterpret_cast<const float*>(a.gate)[row] : 1.0f;
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
+    float row_gate = gate_of(blockIdx.x), post = 1.0f;
+    copies_wait<STAGES - 1>();
+    if (a.post_weight) {
+        post = root(row_sums<WARP>(make_float2(in ? squares(0) : 0.0f, 0.0f), part[1]).x);
+        if (t == 0) a.post_rstd[blockIdx.x] = post;
+    }
+    int parity = 0, stage = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
+        const int64_t next = row + gridDim.x;
+        const float next_gate = gate_of(next);
+        float2 h[4], sums = both(0.0f);
+        if (in) {
+            float2 r[4], w[4];
+            unpack4x2<FP16>(*stage_of(stage), h);
+            unpack4x2<FP16>(stage_of(stage)[blockDim.x], r);
+            const float2 scale = both(row_gate * post), along = both(a.residual_scale);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = mul2(h[j], scale);
+            if (a.post_weight) {
+                read_channels<FP16>(ch.post, a.post_fp32, w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) h[j] = mul2(h[j], w[j]);
+            }
+            if (element || a.gate_kind == EP_GATE_CHANNEL) {
+                if (element) unpack4x2<FP16>(stage_of(stage)[2 * blockDim.x], w);
+                else read_channels<FP16>(ch.gate, a.gate_fp32, w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) h[j] = mul2(h[j], w[j]);
+            }
+            float2 s = both(0.0f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[j] = fused2(along, r[j], h[j]);
+                s = fused2(h[j], h[j], s);
+            }
+            st_v4(a.h + row * pitch + at, pack4x2<FP16>(h));
+            sums.y = s.x + s.y;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = both(0.0f);
+        }
+        const int after = stage + 1 == STAGES ? 0 : stage + 1;
+        copies_wait<STAGES - 2>();
+        if (a.post_weight && in && next < a.rows) sums.x = squares(after);
+        fetch(row + (int64_t)STAGES * gridDim.x, stage);
+        stage = after;
+        if (a.post_weight || a.pre_weight) sums = row_sums<WARP>(sums, part[parity]);
+        if (a.post_weight) {
+            post = root(sums.x);
+            if (t == 0 && next < a.rows) a.post_rstd[next] = post;
+        }
+        row_gate = next_gate;
+        if (!a.pre_weight) continue;
+        const float pre = root(sums.y);
+        if (t == 0) a.pre_rstd[row] = pre;
+        float m = 0.0f;
+        if (in) {
+            float2 w[4];
+            read_channels<FP16>(ch.pre, a.pre_fp32, w);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[j] = mul2(mul2(h[j], both(pre)), w[j]);
+                m = fmaxf(m, fmaxf(fabsf(h[j].x), fabsf(h[j].y)));
+            }
+            if (a.n) st_v4(a.n + row * pitch + at, pack4x2<FP16>(h));
+        }
+        if (!a.q) continue;
+#pragma unroll
+        for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float scale = e4m3_block_scale(m);
+        const float inv = __frcp_rn(scale);
+        if (in) {
+            *reinterpret_cast<uint2*>(a.q + row * a.hidden + 8 * t) =
+                make_uint2(e4m3x4_near(h[0].x, h[0].y, h[1].x, h[1].y, scale, inv),
+                           e4m3x4_near(h[2].x, h[2].y, h[3].x, h[3].y, scale, inv));
+            if ((t & 15) == 0) a.scales[row * a.blocks + (t >> 4)] = scale;
+        }
+    }
+}
+
+// The gradient.  Registers hold the three sums over rows, which leave once per CTA, and one gradient; what a later pass
+// over the row needs is read from its stage again.
+enum { kSlotH, kSlotDn, kSlotDh, kSlotY, kSlotGate };   // a stage's vectors of a thread; the last for a gate per element
+
+template <bool FP16, bool WARP, int STAGES>
+__global__ void __launch_bounds__(WARP ? 32 : kJoinTeamThreads) ep_join_backward_kernel(const JoinArgs a)
+{
+    extern __shared__ uint4 staged[];
+    __shared__ float2 part[2][32];
+    const int t = threadIdx.x;
+    const bool in = t < a.vecs;
+    const int64_t at = 16 * (int64_t)t, pitch = 16 * (int64_t)a.vecs;
+    const bool element = a.gate_kind == EP_GATE_ELEMENT;
+    const int slots = element ? 5 : 4;
+    const float inv_hidden = __frcp_rn((float)a.hidden);
+    follow_predecessor();
+    const Channels ch = fetch_channels(a, staged + STAGES * slots * blockDim.x);
+    auto vector = [&](int stage, int slot) { return staged + (stage * slots + slot) * blockDim.x + t; };
+    auto fetch = [&](int64_t row, int stage) {
+        if (in && row < a.rows) {
+            if (a.pre_weight) {
+                copy16(vector(stage, kSlotH), a.h_in + row * pitch + at);
+                copy16(vector(stage, kSlotDn), a.dn + row * a.dn_pitch + at);
+            }
+            if (a.dh) copy16(vector(stage, kSlotDh), a.dh + row * a.dh_pitch + at);
+            copy16(vector(stage, kSlotY), a.y + row * a.y_pitch + at);
+            if (element) copy16(vector(stage, kSlotGate), a.gate + row * a.g_pitch + at);
+        }
+        copies_commit();
+    };
+    float2 dpost[4], dgate[4], dpre[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dpost[j] = dgate[j] = dpre[j] = both(0.0f);
+    // a row's sum of dn * pre_weight * h, and its part of pre_weight's gradient
+    auto along_pre = [&](int stage, float pre) {
+        float2 h[4], g[4], w[4], s = both(0.0f);
+        unpack4x2<FP16>(*vector(stage, kSlotH), h);
+        unpack4x2<FP16>(*vector(stage, kSlotDn), g);
+        read_channels<FP16>(ch.pre, a.pre_fp32, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            g[j] = mul2(g[j], h[j]);
+            dpre[j] = fused2(g[j], both(pre), dpre[j]);
+            s = fused2(g[j], w[j], s);
+        }
+        return s.x + s.y;
+    };
+    struct Row { float pre, post, gate; };
+    auto scalars = [&](int64_t row) {
+        Row r{0.0f, 1.0f, 1.0f};
+        if (row < a.rows) {
+            if (a.pre_weight) r.pre = a.pre_rstd_in[row];
+            if (a.post_weight) r.post = a.post_rstd_in[row];
+            if (a.gate_kind == EP_GATE_ROW) r.gate = reinterpret_cast<const float*>(a.gate)[row];
+        }
+        return r;
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
+    Row now = scalars(blockIdx.x);
+    copies_wait<STAGES - 1>();
+    float2 sums = both(0.0f);
+    if (a.pre_weight) sums = row_sums<WARP>(make_float2(in ? along_pre(0, now.pre) : 0.0f, 0.0f), part[1]);
+    int parity = 0, stage = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
+        const int64_t next = row + gridDim.x;
+        const Row then = scalars(next);
+        float2 d[4];
+        float sum = 0.0f;
+        if (in) {
+            if (a.dh) {
+                unpack4x2<FP16>(*vector(stage, kSlotDh), d);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d[j] = both(0.0f);
+            }
+            if (a.pre_weight) {
+                float2 x[4], w[4];
+                const float2 c = both(-sums.x * inv_hidden * now.pre * now.pre);
+                unpack4x2<FP16>(*vector(stage, kSlotH), x);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d[j] = fused2(mul2(x[j], both(now.pre)), c, d[j]);
+                unpack4x2<FP16>(*vector(stage, kSlotDn), x);
+                read_channels<FP16>(ch.pre, a.pre_fp32, w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d[j] = fused2(mul2(x[j], w[j]), both(now.pre), d[j]);
+            }
+            if (a.dresidual) {
+                float2 r[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) r[j] = mul2(both(a.residual_scale), d[j]);
+                st_v4(a.dresidual + row * pitch + at, pack4x2<FP16>(r));
+            }
+            float2 v[4], e[4], s = both(0.0f);
+            unpack4x2<FP16>(*vector(stage, kSlotY), v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], both(now.post));
+            // e: gradient for the gate; d: from here on that for y's norm
+            if (a.gate_kind != EP_GATE_NONE) {
+                float2 w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) e[j] = mul2(d[j], v[j]);
+                if (a.post_weight) {
+                    read_channels<FP16>(ch.post, a.post_fp32, w);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) e[j] = mul2(e[j], w[j]);
+                }
+                if (a.gate_kind == EP_GATE_CHANNEL) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) dgate[j] = fused2(e[j], both(1.0f), dgate[j]);
+                    read_channels<FP16>(ch.gate, a.gate_fp32, w);
+                } else if (element) {
+                    st_v4(a.dgate_element + row * pitch + at, pack4x2<FP16>(e));
+                    unpack4x2<FP16>(*vector(stage, kSlotGate), w);
+                } else {
+                    sum = sum_of(e);   // over the row, before its gate
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = both(now.gate);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d[j] = mul2(d[j], w[j]);
+            }
+            if (a.post_weight) {
+                float2 w[4];
+                read_channels<FP16>(ch.post, a.post_fp32, w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    dpost[j] = fused2(d[j], v[j], dpost[j]);
+                    d[j] = mul2(d[j], w[j]);
+                    s = fused2(d[j], v[j], s);
+                }
+                if (a.gate_kind != EP_GATE_ROW) sum = s.x + s.y;
+            }
+        }
+        const int after = stage + 1 == STAGES ? 0 : stage + 1;
+        copies_wait<STAGES - 2>();
+        sums = make_float2(a.pre_weight && in && next < a.rows ? along_pre(after, then.pre) : 0.0f, sum);
+        if (a.pre_weight || a.post_weight || a.gate_kind == EP_GATE_ROW) sums = row_sums<WARP>(sums, part[parity]);
+        if (a.gate_kind == EP_GATE_ROW && t == 0) a.dgate_row[row] = sums.y;
+        if (in) {
+            if (a.post_weight) {
+                const float mean = (a.gate_kind == EP_GATE_ROW ? sums.y * now.gate : sums.y) * inv_hidden;
+                float2 v[4];
+                unpack4x2<FP16>(*vector(stage, kSlotY), v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    d[j] = mul2(fused2(mul2(v[j], both(now.post)), both(-mean), d[j]), both(now.post));
+            }
+            st_v4(a.dy + row * pitch + at, pack4x2<FP16>(d));
+        }
+        fetch(row + (int64_t)STAGES * gridDim.x, stage);
+        stage = after;
+        now = then;
+    }
+    if (!in) return;
+    float* out = a.partial + (int64_t)blockIdx.x * 3 * a.hidden + 8 * t;
+    auto leave = [&](const float2 (&s)[4], int which) {
+        float4* p = reinterpret_cast<float4*>(out + (int64_t)which * a.hidden);
+        p[0] = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
+        p[1] = make_float4(s[2].x, s[2].y, s[3].x, s[3].y);
+    };
+    if (a.post_weight) leave(dpost, 0);
+    if (a.gate_kind == EP_GATE_CHANNEL) leave(dgate, 1);
+    if (a.pre_weight) leave(dpre, 2);
+}
+
+// ---- wider rows: a CTA per row, VPT vectors of 8 columns per thread
+template <bool FP16, int VPT>
+__global__ void __launch_bounds__(kJoinMaxThreads) ep_join_wide_kernel(const JoinArgs a)
+{
+    __shared__ float2 part[2][32];
+    const int t = threadIdx.x, stride = blockDim.x;
+    const int64_t row = blockIdx.x;
+    follow_predecessor();
     float f[VPT][8];
     uint4 res[VPT], el[VPT];
     {
@@ -117,7 +472,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kJoinWarpsPerCta : kJoinMaxThreads
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum = fmaf(f[i][j], f[i][j], sum);
-        sum = row_sum<WARP>(sum, part[0]);
+        sum = row_sums<false>(make_float2(sum, 0.0f), part[0]).x;
         const float rstd = __frsqrt_rn(__fdiv_rn(sum, (float)a.hidden) + a.eps);
         if (t == 0) a.post_rstd[row] = rstd;
 #pragma unroll
@@ -150,7 +505,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kJoinWarpsPerCta : kJoinMaxThreads
         if (v < a.vecs) *reinterpret_cast<uint4*>(a.h + (row * a.vecs + v) * 16) = pack8<FP16>(f[i]);
     }
     if (!a.pre_weight) return;
-    sum = row_sum<WARP>(sum, part[1]);
+    sum = row_sums<false>(make_float2(sum, 0.0f), part[1]).x;
     const float rstd = __frsqrt_rn(__fdiv_rn(sum, (float)a.hidden) + a.eps);
     if (t == 0) a.pre_rstd[row] = rstd;
 #pragma unroll
@@ -178,160 +533,6 @@ __global__ void __launch_bounds__(WARP ? 32 * kJoinWarpsPerCta : kJoinMaxThreads
             if ((v & 15) == 0) a.scales[row * a.blocks + (v >> 4)] = scale;
         }
     }
-}
-
-// 16 bytes of global memory into shared memory, asynchronously; a thread's copies are grouped by copies_commit() and
-// copies_wait<N>() returns when all but the newest N groups have arrived, for the thread that made them.
-__device__ __forceinline__ void copy16(void* to, const void* from)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
-
-// Rows blockIdx.x, + gridDim.x, ... by one CTA, a vector of 8 columns per thread: the sums over rows stay in registers
-// and leave once per CTA.  Rows are on their way through STAGES stages of shared memory, of which a thread fills and
-// reads its own vectors only, so that no barrier passes between copy and use; registers hold the three sums and one
-// gradient, and what a later pass over the row needs is read from the stage again.
-enum { kSlotH, kSlotDn, kSlotDh, kSlotY, kSlotGate };   // a stage's vectors of a thread; the last for a gate per element
-
-template <bool FP16, bool WARP, int STAGES>
-__global__ void __launch_bounds__(WARP ? 32 : kJoinBackMaxThreads) ep_join_backward_kernel(const JoinArgs a)
-{
-    extern __shared__ uint4 staged[];
-    __shared__ float part[4][32];
-    const int t = threadIdx.x;
-    const bool in = t < a.vecs;
-    const int64_t at = 16 * (int64_t)t;
-    const int slots = a.gate_kind == EP_GATE_ELEMENT ? 5 : 4;
-    const float inv_hidden = __frcp_rn((float)a.hidden);
-    follow_predecessor();
-    auto fetch = [&](int64_t row, int stage) {
-        if (in && row < a.rows) {
-            uint4* to = staged + stage * slots * blockDim.x + t;
-            if (a.pre_weight) {
-                copy16(to + kSlotH * blockDim.x, a.h_in + row * 16 * a.vecs + at);
-                copy16(to + kSlotDn * blockDim.x, a.dn + row * a.dn_pitch + at);
-            }
-            if (a.dh) copy16(to + kSlotDh * blockDim.x, a.dh + row * a.dh_pitch + at);
-            copy16(to + kSlotY * blockDim.x, a.y + row * a.y_pitch + at);
-            if (a.gate_kind == EP_GATE_ELEMENT) copy16(to + kSlotGate * blockDim.x, a.gate + row * a.g_pitch + at);
-        }
-        copies_commit();
-    };
-    float dpost[8] = {}, dgate[8] = {}, dpre[8] = {};
-#pragma unroll
-    for (int i = 0; i < STAGES; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
-    int parity = 0, stage = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 2) {
-        const float pre = a.pre_weight ? a.pre_rstd_in[row] : 0.0f;
-        const float post = a.post_weight ? a.post_rstd_in[row] : 1.0f;
-        const float row_gate = a.gate_kind == EP_GATE_ROW ? reinterpret_cast<const float*>(a.gate)[row] : 1.0f;
-        const uint4* mine = staged + stage * slots * blockDim.x + t;
-        copies_wait<STAGES - 1>();
-        float mean = 0.0f;
-        if (a.pre_weight) {
-            float sum = 0.0f;
-            if (in) {
-                float x[8], g[8], w[8];
-                unpack8<FP16>(mine[kSlotH * blockDim.x], x);
-                unpack8<FP16>(mine[kSlotDn * blockDim.x], g);
-                load_channels<FP16>(a.pre_weight, a.pre_fp32, t, w);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float gx = g[j] * (x[j] * pre);
-                    dpre[j] += gx;
-                    sum = fmaf(gx, w[j], sum);
-                }
-            }
-            mean = row_sum<WARP>(sum, part[parity]) * inv_hidden;
-        }
-        float d[8], sum = 0.0f;
-        if (in) {
-            if (a.dh) {
-                unpack8<FP16>(mine[kSlotDh * blockDim.x], d);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) d[j] = 0.0f;
-            }
-            if (a.pre_weight) {
-                float x[8], g[8], w[8];
-                unpack8<FP16>(mine[kSlotH * blockDim.x], x);
-                unpack8<FP16>(mine[kSlotDn * blockDim.x], g);
-                load_channels<FP16>(a.pre_weight, a.pre_fp32, t, w);
-                const float along = -mean * pre;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) d[j] = fmaf(pre, fmaf(x[j], along, g[j] * w[j]), d[j]);
-            }
-            if (a.dresidual) {
-                float r[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) r[j] = a.residual_scale * d[j];
-                st_v4(a.dresidual + row * 16 * a.vecs + at, pack8<FP16>(r));
-            }
-            float v[8], u[8];
-            unpack8<FP16>(mine[kSlotY * blockDim.x], v);
-            if (a.post_weight) {
-                load_channels<FP16>(a.post_weight, a.post_fp32, t, u);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) u[j] = 1.0f;
-            }
-            // u: the gradient for the gate; d: that for y's norm, times the gate
-            float gate[8];
-            if (a.gate_kind == EP_GATE_ELEMENT) {
-                unpack8<FP16>(mine[kSlotGate * blockDim.x], gate);
-            } else if (a.gate_kind == EP_GATE_CHANNEL) {
-                load_channels<FP16>(a.gate, a.gate_fp32, t, gate);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) gate[j] = row_gate;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[j] *= post;
-                const float w = u[j], p = d[j] * gate[j];
-                u[j] = d[j] * (v[j] * w);
-                dgate[j] += u[j];
-                dpost[j] = fmaf(p, v[j], dpost[j]);
-                d[j] = p * w;
-                sum = a.gate_kind == EP_GATE_ROW ? sum + u[j] : fmaf(d[j], v[j], sum);
-            }
-            if (a.gate_kind == EP_GATE_ELEMENT) st_v4(a.dgate_element + row * 16 * a.vecs + at, pack8<FP16>(u));
-        }
-        mean = 0.0f;
-        if (a.post_weight || a.gate_kind == EP_GATE_ROW) {
-            sum = row_sum<WARP>(sum, part[parity + 1]);
-            if (a.gate_kind == EP_GATE_ROW) {
-                if (t == 0) a.dgate_row[row] = sum;
-                sum *= row_gate;
-            }
-            mean = sum * inv_hidden;
-        }
-        if (in) {
-            if (a.post_weight) {
-                float v[8];
-                unpack8<FP16>(mine[kSlotY * blockDim.x], v);
-                const float along = -mean * post;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) d[j] = post * fmaf(v[j], along, d[j]);
-            }
-            st_v4(a.dy + row * 16 * a.vecs + at, pack8<FP16>(d));
-        }
-        fetch(row + (int64_t)STAGES * gridDim.x, stage);
-        stage = stage + 1 == STAGES ? 0 : stage + 1;
-    }
-    if (!in) return;
-    float* out = a.partial + (int64_t)blockIdx.x * 3 * a.hidden + 8 * t;
-    auto leave = [&](const float (&s)[8], int which) {
-        float4* p = reinterpret_cast<float4*>(out + (int64_t)which * a.hidden);
-        p[0] = make_float4(s[0], s[1], s[2], s[3]);
-        p[1] = make_float4(s[4], s[5], s[6], s[7]);
-    };
-    if (a.post_weight) leave(dpost, 0);
-    if (a.gate_kind == EP_GATE_CHANNEL) leave(dgate, 1);
-    if (a.pre_weight) leave(dpre, 2);
 }
 
 // The CTAs' sums, added in their order: thread (column, part) adds a part of the CTAs, and the parts are added in
@@ -366,51 +567,73 @@ __global__ void __launch_bounds__(kSumColumns * kSumParts) ep_join_sum_kernel(co
     out[c] = s;
 }
 
-template <bool FP16, bool WARP>
-cudaError_t launch_join(const JoinArgs& a, int vpt, int threads, cudaStream_t s)
+// Shared memory of a CTA of the team kernels, and how many CTAs an SM holds.
+constexpr size_t kJoinShared = 227 * 1024 - 1024;   // less the static part
+
+size_t team_shared(const JoinArgs& a, int threads, int stages, int slots)
 {
-    const unsigned grid = (unsigned)(WARP ? (a.rows + kJoinWarpsPerCta - 1) / kJoinWarpsPerCta : a.rows);
-    const dim3 block(threads);
-    if constexpr (WARP) {
-        if (vpt == 1) return launch_dependent(ep_join_kernel<FP16, true, 1>, dim3(grid), block, 0, s, a);
-        if (vpt == 2) return launch_dependent(ep_join_kernel<FP16, true, 2>, dim3(grid), block, 0, s, a);
-        return launch_dependent(ep_join_kernel<FP16, true, 4>, dim3(grid), block, 0, s, a);
-    } else {
-        if (vpt == 4) return launch_dependent(ep_join_kernel<FP16, false, 4>, dim3(grid), block, 0, s, a);
-        return launch_dependent(ep_join_kernel<FP16, false, 8>, dim3(grid), block, 0, s, a);
-    }
+    return (size_t)(stages * slots + channel_vectors(a)) * threads * 16;
 }
 
-// CTAs of the gradient's kernel: as many as the SMs hold at once, but no fewer than kRowsPerCta rows to each, because
-// every CTA leaves three rows of sums.
+int team_threads(int hidden) { return (hidden / 8 + 31) / 32 * 32; }
+
+int team_ctas_per_sm(int threads, size_t shared)
+{
+    const int by_threads = kJoinTeamThreads / threads, by_shared = (int)(228 * 1024 / (shared + 2048));
+    const int n = by_threads < by_shared ? by_threads : by_shared;
+    return n < 1 ? 1 : n > 32 ? 32 : n;
+}
+
+template <auto* K>
+cudaError_t launch_team(const JoinArgs& a, int64_t ctas, int threads, size_t shared, cudaStream_t s)
+{
+    const cudaError_t e = allow_all_shared<K>();
+    return e != cudaSuccess ? e : launch_dependent(K, dim3((unsigned)ctas), dim3(threads), shared, s, a);
+}
+
+template <bool FP16>
+cudaError_t launch_join(const JoinArgs& a, int sms, cudaStream_t s)
+{
+    if (a.hidden > kJoinTeamHidden) {
+        const int vpt = a.vecs <= 4 * kJoinMaxThreads ? 4 : 8;
+        const dim3 grid((unsigned)a.rows), block(((a.vecs + vpt - 1) / vpt + 31) / 32 * 32);
+        if (vpt == 4) return launch_dependent(ep_join_wide_kernel<FP16, 4>, grid, block, 0, s, a);
+        return launch_dependent(ep_join_wide_kernel<FP16, 8>, grid, block, 0, s, a);
+    }
+    const int threads = team_threads(a.hidden), slots = a.gate_kind == EP_GATE_ELEMENT ? 3 : 2;
+    size_t shared = team_shared(a, threads, 4, slots);
+    const bool four = shared <= kJoinShared;   // else FP32 weights of the widest rows take their place
+    if (!four) shared = team_shared(a, threads, 2, slots);
+    const int64_t fit = (int64_t)sms * team_ctas_per_sm(threads, shared), ctas = a.rows < fit ? a.rows : fit;
+    if (threads == 32) return launch_team<ep_join_team_kernel<FP16, true, 4>>(a, ctas, threads, shared, s);
+    if (four) return launch_team<ep_join_team_kernel<FP16, false, 4>>(a, ctas, threads, shared, s);
+    return launch_team<ep_join_team_kernel<FP16, false, 2>>(a, ctas, threads, shared, s);
+}
+
+// CTAs of the gradient's kernel, by the shape alone, because they fix the order of the sums: as many as the SMs hold with
+// the most shared memory that a CTA of this width may take, but no fewer than kRowsPerCta rows to each while that leaves
+// every SM one, because every CTA leaves three rows of sums.
 constexpr int kRowsPerCta = 4;
 
 int join_backward_ctas(int64_t rows, int hidden, int sms)
 {
-    const int threads = (hidden / 8 + 31) / 32 * 32;
-    const int64_t fit = (int64_t)sms * (threads > 512 ? 1 : threads > 256 ? 2 : threads > 128 ? 4 : 8);
+    const int threads = team_threads(hidden);
+    const int64_t fit = (int64_t)sms * team_ctas_per_sm(threads, (size_t)(3 * 5 + 4) * threads * 16);
     const int64_t want = (rows + kRowsPerCta - 1) / kRowsPerCta;
     const int64_t least = rows < sms ? rows : sms;
     return (int)(want < least ? least : want < fit ? want : fit);
 }
 
-template <bool FP16, bool WARP, int STAGES>
-cudaError_t launch_join_backward(const JoinArgs& a, int ctas, int threads, cudaStream_t s)
-{
-    const cudaError_t e = allow_all_shared<ep_join_backward_kernel<FP16, WARP, STAGES>>();
-    if (e != cudaSuccess) return e;
-    const size_t smem = (size_t)STAGES * (a.gate_kind == EP_GATE_ELEMENT ? 5 : 4) * threads * 16;
-    return launch_dependent(ep_join_backward_kernel<FP16, WARP, STAGES>, dim3(ctas), dim3(threads), smem, s, a);
-}
-
 template <bool FP16>
 cudaError_t launch_join_backward(const JoinArgs& a, int ctas, cudaStream_t s)
 {
-    const int threads = (a.vecs + 31) / 32 * 32;
-    if (threads == 32) return launch_join_backward<FP16, true, 3>(a, ctas, threads, s);
-    // a third stage of five vectors to a thread would pass a CTA's shared memory
-    if (threads > 896) return launch_join_backward<FP16, false, 2>(a, ctas, threads, s);
-    return launch_join_backward<FP16, false, 3>(a, ctas, threads, s);
+    const int threads = team_threads(a.hidden), slots = a.gate_kind == EP_GATE_ELEMENT ? 5 : 4;
+    size_t shared = team_shared(a, threads, 3, slots);
+    const bool three = shared <= kJoinShared;   // else a gate per element or FP32 weights of wide rows take their place
+    if (!three) shared = team_shared(a, threads, 2, slots);
+    if (threads == 32) return launch_team<ep_join_backward_kernel<FP16, true, 3>>(a, ctas, threads, shared, s);
+    if (three) return launch_team<ep_join_backward_kernel<FP16, false, 3>>(a, ctas, threads, shared, s);
+    return launch_team<ep_join_backward_kernel<FP16, false, 2>>(a, ctas, threads, shared, s);
 }
 
 bool row_ok(const void* p, int64_t stride, int hidden)
@@ -478,23 +701,16 @@ extern "C" int ep_rms_norm_join(const ep_join* join, const void* residual, int64
     a.post_rstd = post_rstd; a.pre_rstd = pre_rstd;
     const bool fp16 = join->dtype == EP_FP16;
     cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t e;
-    if (a.vecs <= 128) {   // a row per warp
-        const int vpt = a.vecs <= 32 ? 1 : a.vecs <= 64 ? 2 : 4;
-        e = fp16 ? launch_join<true, true>(a, vpt, 32 * kJoinWarpsPerCta, s)
-                 : launch_join<false, true>(a, vpt, 32 * kJoinWarpsPerCta, s);
-    } else {
-        const int vpt = a.vecs <= 4 * kJoinMaxThreads ? 4 : 8;
-        const int threads = ((a.vecs + vpt - 1) / vpt + 31) / 32 * 32;
-        e = fp16 ? launch_join<true, false>(a, vpt, threads, s) : launch_join<false, false>(a, vpt, threads, s);
-    }
+    const int sms = layer_num_sms();
+    if (sms == 0) return layer_fail(EP_ERR_CUDA, "%s: cannot tell the current device's multiprocessors", who);
+    const cudaError_t e = fp16 ? launch_join<true>(a, sms, s) : launch_join<false>(a, sms, s);
     return layer_cuda(e, "ep_rms_norm_join: launch");
 }
 
 extern "C" size_t ep_rms_norm_join_workspace_bytes(int64_t rows, int hidden)
 {
     using namespace ep;
-    if (rows <= 0 || rows >= (int64_t)1 << 31 || hidden < 16 || hidden > kJoinBackMaxHidden || hidden % 16 != 0) return 0;
+    if (rows <= 0 || rows >= (int64_t)1 << 31 || hidden < 16 || hidden > kJoinTeamHidden || hidden % 16 != 0) return 0;
     return (size_t)join_backward_ctas(rows, hidden, layer_num_sms()) * 3 * hidden * sizeof(float);
 }
 
@@ -506,7 +722,7 @@ extern "C" int ep_rms_norm_join_backward(const ep_join* join, const void* h, con
     using namespace ep;
     const char* who = "ep_rms_norm_join_backward";
     JoinArgs a{};
-    if (int rc = check_join(who, join, kJoinBackMaxHidden, a)) return rc;
+    if (int rc = check_join(who, join, kJoinTeamHidden, a)) return rc;
     if ((dn != nullptr) != (a.pre_weight != nullptr) && a.rows > 0)
         return layer_fail(EP_ERR_ARG, "%s: dn and pre_weight are not both given, nor both NULL", who);
     if (!dh && !dn && a.rows > 0) return layer_fail(EP_ERR_ARG, "%s: neither dh nor dn is given", who);

@@ -101,6 +101,36 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8])
     }
 }
 
+// Two floats at once, one instruction each, rounded as two operations.
+__device__ __forceinline__ float2 mul2(const float2& a, const float2& b)
+{
+    float2 d;
+    asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 fused2(const float2& a, const float2& b, const float2& c)   // a * b + c
+{
+    float2 d;
+    asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7}; fma.rn.f32x2 z, x, y, z;\n\t"
+        "mov.b64 {%0, %1}, z; }"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Eight 16-bit values of a 16-byte vector as four pairs of floats.
+template <bool FP16>
+__device__ __forceinline__ void unpack4x2(const uint4& v, float2 (&f)[4])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f[i] = FP16 ? __half22float2(*reinterpret_cast<const __half2*>(&w[i])) : make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
+}
+
 template <bool FP16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
@@ -118,6 +148,13 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
 {
     return make_uint4(pack2<FP16>(f[0], f[1]), pack2<FP16>(f[2], f[3]), pack2<FP16>(f[4], f[5]),
                       pack2<FP16>(f[6], f[7]));
+}
+
+template <bool FP16>
+__device__ __forceinline__ uint4 pack4x2(const float2 (&f)[4])
+{
+    return make_uint4(pack2<FP16>(f[0].x, f[0].y), pack2<FP16>(f[1].x, f[1].y), pack2<FP16>(f[2].x, f[2].y),
+                      pack2<FP16>(f[3].x, f[3].y));
 }
 
 // FP32 scale of a 128-element block with largest magnitude m, as the quantising dispatch defines

@@ -93,7 +93,7 @@ def test_binding_takes_cuda_tensors_only(lib):  # noqa: F811
         ep.rms_norm_join([1.0], x)
 
 
-@pytest.mark.parametrize("name,kernels", [("ep_join.cu", 3), ("ep_swiglu.cu", 2)])
+@pytest.mark.parametrize("name,kernels", [("ep_join.cu", 4), ("ep_swiglu.cu", 2)])
 def test_kernels_read_no_memory_before_their_own_wait(name, kernels):
     """As in test_experts.py: before follow_predecessor() no kernel names an array of its arguments."""
     import re
