@@ -34,6 +34,8 @@ decltype(&ep_rms_norm_join_workspace_bytes) g_join_bytes;
 decltype(&ep_rms_norm_join_backward) g_join_back;
 decltype(&ep_swiglu_saved) g_swiglu;
 decltype(&ep_swiglu_saved_backward) g_swiglu_back;
+decltype(&ep_moe_few_workspace_bytes) g_few_bytes;
+decltype(&ep_moe_few_rows) g_few;
 decltype(&ep_strerror) g_strerror;
 decltype(&ep_last_error) g_last_error;
 PyObject* g_error;         // the package's EpError
@@ -559,6 +561,42 @@ PyObject* swiglu_saved_backward(PyObject* const* v)
     return pack({d, q, s});
 }
 
+// (x, x_scales, indices, weights, up, up_scales, down, down_scales, first_expert, out type)
+PyObject* moe_few_rows(PyObject* const* v)
+{
+    const at::Tensor& x = lead_tensor(v[0], "x");
+    if (x.dim() != 2) refuse("x has %lld dimensions, the call takes [rows][hidden]", (long long)x.dim());
+    const bool fp8 = x.scalar_type() == at::kFloat8_e4m3fn;
+    const int code = fp8 ? (int)EP_FP8_E4M3 : half_code(x, "x (float8_e4m3fn or)");
+    const at::Device dev = x.device();
+    const int64_t rows = x.size(0), hidden = x.size(1), hb = (hidden + 127) / 128;
+    const void* xp = data(x, "x", x.scalar_type(), x.sizes(), dev);
+    if (fp8 != (v[1] != Py_None)) refuse("x_scales goes with float8_e4m3fn rows, and with them alone");
+    const void* xs = data_or_null(v[1], "x_scales", at::kFloat, {rows, hb}, dev);
+    const at::Tensor& idx = tensor(v[2], "indices");
+    if (idx.dim() != 2) refuse("indices has %lld dimensions, the call takes [rows][k]", (long long)idx.dim());
+    const int64_t k = idx.size(1);
+    const void* ip = data(idx, "indices", at::kInt, {rows, k}, dev);
+    const void* wp = data(tensor(v[3], "weights"), "weights", at::kFloat, {rows, k}, dev);
+    const at::Tensor& down = tensor(v[6], "down");
+    if (down.dim() != 3 || down.size(1) != hidden)
+        refuse("down has shape %s, the call takes [experts][%lld][inner]", shape_text(down.sizes()).c_str(), (long long)hidden);
+    const int64_t experts = down.size(0), inner = down.size(2), ib = (inner + 127) / 128, ub = (2 * inner + 127) / 128;
+    const void* dp = data(down, "down", at::kFloat8_e4m3fn, down.sizes(), dev);
+    const void* ds = data(tensor(v[7], "down_scales"), "down_scales", at::kFloat, {experts, hb, ib}, dev);
+    const void* up = data(tensor(v[4], "up"), "up", at::kFloat8_e4m3fn, {experts, 2 * inner, hidden}, dev);
+    const void* us = data(tensor(v[5], "up_scales"), "up_scales", at::kFloat, {experts, ub, hb}, dev);
+    const int first = small(v[8], "first_expert"), type = small(v[9], "the output's type");
+    const c10::cuda::CUDAGuard guard(dev);
+    const size_t need = g_few_bytes(rows, clamp_int(k), clamp_int(inner));
+    at::Tensor out = empty(x.sizes(), type == EP_FP16 ? at::kHalf : at::kBFloat16, dev), work;
+    if (need) work = empty({(int64_t)need}, at::kByte, dev);
+    check(g_few(xp, (const float*)xs, code, (const int32_t*)ip, (const float*)wp, rows, clamp_int(k), first, clamp_int(experts),
+                clamp_int(hidden), clamp_int(inner), up, (const float*)us, dp, (const float*)ds, type, out.data_ptr(),
+                get(work), need, stream(dev)));
+    return wrap(out);
+}
+
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n)
 {
@@ -583,7 +621,8 @@ struct Bound {
 #define EP_BOUND(variable) {#variable, &variable}
 const Bound g_bound[] = {EP_BOUND(g_norm), EP_BOUND(g_sort_bytes), EP_BOUND(g_sort), EP_BOUND(g_rows), EP_BOUND(g_return),
                          EP_BOUND(g_back), EP_BOUND(g_matmul), EP_BOUND(g_join), EP_BOUND(g_join_bytes), EP_BOUND(g_join_back),
-                         EP_BOUND(g_swiglu), EP_BOUND(g_swiglu_back), EP_BOUND(g_strerror), EP_BOUND(g_last_error)};
+                         EP_BOUND(g_swiglu), EP_BOUND(g_swiglu_back), EP_BOUND(g_few_bytes),
+                         EP_BOUND(g_few), EP_BOUND(g_strerror), EP_BOUND(g_last_error)};
 constexpr int kBound = sizeof g_bound / sizeof g_bound[0];
 
 // bind(EpError, make_status, addresses of the C ABI functions in the order above)
@@ -622,6 +661,7 @@ PyMethodDef g_methods[] = {
     {"rms_norm_join_backward", (PyCFunction)(void (*)())entry<join_backward, 10>, METH_FASTCALL, nullptr},
     {"swiglu_saved", (PyCFunction)(void (*)())entry<swiglu_saved, 2>, METH_FASTCALL, nullptr},
     {"swiglu_saved_backward", (PyCFunction)(void (*)())entry<swiglu_saved_backward, 5>, METH_FASTCALL, nullptr},
+    {"moe_few_rows", (PyCFunction)(void (*)())entry<moe_few_rows, 10>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ep_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

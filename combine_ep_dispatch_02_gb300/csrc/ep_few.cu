@@ -1,0 +1,682 @@
+// ep_few.cu -- a whole mixture-of-experts layer for a few rows, in two kernels.
+//
+//   [gate; up] = up[e] x,  z = gate * sigmoid(gate) * up,  out[row] = sum over the row's experts e, ascending, of
+//   weight * down[e] z
+//
+// with e4m3 weights and one FP32 scale per 128 x 128 block.  The time is that of reading the weights of the experts
+// that any row names, once: 3 * inner * hidden bytes each.  So no weight passes through shared memory: a warp reads 16
+// of its rows, 128 columns a step, straight into the registers that feed the matrix units, kept several steps ahead of
+// them; it meets no barrier on the way, and 16 rows are few enough to spread any layer over the SMs.
+//
+// A lane's 16 bytes are 16 columns of one row.  Which of the K columns share a matrix instruction is free, as long as
+// both operands agree; so a lane takes its own 16 for four instructions and reads the same 16 of the other operand's
+// row.  Codes become FP16 on the way, which is exact; the sums of a block of 128 are FP32 and enter the row's, times
+// the scales, in FP32.
+//
+// Each CTA finds by itself what it has to do: it sorts the rows by expert, in shared memory, by a bit for each row and
+// expert.  A row that names an expert in several slots counts once, with the sum of those slots' weights.
+//
+// The first kernel leaves z as FP16 with a power of two for every 8 columns, so that the second's operand keeps 11 bits
+// whatever z's range; the e4m3 that a chain of products would leave has 4.  The second kernel's CTA owns 16 output
+// columns, over every expert: each output is summed in one place, in a fixed order.  It is a programmatic dependent
+// that reads weights before it waits: the first kernel lets it start only after its own wait, when all that precedes the
+// call has completed, and the weights are nothing that the first writes.
+#include "ep_layer.cuh"
+
+namespace ep {
+namespace {
+
+constexpr int kFewRows = 128;          // rows of a call
+constexpr int kFewPairs = 4096;        // (row, slot) pairs of a call
+constexpr int kFewExperts = 1024;
+constexpr int kUpWarps = 4;            // of a CTA of the first kernel
+constexpr int kDownMaxWarps = 16;
+constexpr int kWarpsPerSm = 16;        // at 128 registers a thread
+constexpr uint16_t kNone = 0xFFFF;
+
+enum { kFromE4m3 = 0, kFromFp16 = 1, kFromBf16 = 2, kFromZ = 3 };   // what the rows are held as
+
+struct FewArgs {
+    const uint8_t* x;
+    const float* x_scales;
+    const int32_t* indices;
+    const float* weights;
+    const uint8_t* up;
+    const float* up_scales;
+    const uint8_t* down;
+    const float* down_scales;
+    uint8_t* z;          // [pairs][inner] FP16
+    uint8_t* z_exp;      // [pairs][inner / 8]: 128 + the power of two of 8 columns, 0 where all are 0
+    void* out;
+    int rows, k, pairs, first, experts, H, I;
+    int hb, ib, ub;      // 128-blocks of hidden, inner and 2 * inner
+    int split;           // warps that share a unit's K in the first kernel: 1, 2 or 4
+    int out_fp16;
+};
+
+// The rows by expert, in shared memory: entry i holds up to 8 * NT rows of expert[i], list[start[i]] .. list[start[i + 1]
+// - 1].  Every CTA makes the same: z lies by place in the list, and a unit's rows are the same whichever CTA works on it.
+struct Entries {
+    uint16_t *local, *list, *expert, *start;   // [pairs] each, start one more; local: a pair's expert, kNone for none here
+    int* cursor;                               // [experts]: place of an expert's first row
+    uint32_t* named;                           // [experts][words]: the rows that name an expert, a bit each
+    int* count;
+};
+
+__host__ __device__ inline int row_words(int rows) { return (rows + 31) / 32; }
+
+__host__ __device__ inline size_t entries_bytes(int pairs, int experts, int rows)
+{
+    return (size_t)((4 * pairs + 1) * 2 + 15) / 16 * 16 + ((size_t)experts * (1 + row_words(rows)) + 4) / 4 * 16;
+}
+
+__device__ __forceinline__ Entries entries_at(uint8_t* p, const FewArgs& a)
+{
+    Entries s;
+    s.local = reinterpret_cast<uint16_t*>(p);
+    s.list = s.local + a.pairs;
+    s.expert = s.list + a.pairs;
+    s.start = s.expert + a.pairs;
+    s.cursor = reinterpret_cast<int*>(p + ((4 * a.pairs + 1) * 2 + 15) / 16 * 16);
+    s.count = s.cursor + a.experts;
+    s.named = reinterpret_cast<uint32_t*>(s.count + 1);
+    return s;
+}
+
+// 32 bits from where all SMs see the same, not from this SM's cache.
+__device__ __forceinline__ int32_t load_shared_view(const int32_t* p)
+{
+    int32_t v;
+    asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+// Place in the list of a row that names expert e.
+__device__ __forceinline__ int place_of(const Entries& s, int words, int e, int row)
+{
+    int at = s.cursor[e] + __popc(s.named[e * words + row / 32] & ((1u << (row & 31)) - 1));
+    for (int w = 0; w < row / 32; ++w) at += __popc(s.named[e * words + w]);
+    return at;
+}
+
+// Sorts the rows into entries of up to `per` rows; returns their number.  All threads of the CTA.
+__device__ __forceinline__ int make_entries(const FewArgs& a, const Entries& s, int per)
+{
+    const int words = row_words(a.rows);
+    for (int p = threadIdx.x; p < a.pairs; p += blockDim.x) {
+        const int64_t e = (int64_t)load_shared_view(a.indices + p) - a.first;
+        s.local[p] = e >= 0 && e < a.experts ? (uint16_t)e : kNone;
+    }
+    for (int i = threadIdx.x; i < a.experts * words; i += blockDim.x) s.named[i] = 0;
+    __syncthreads();
+    for (int p = threadIdx.x; p < a.pairs; p += blockDim.x) {
+        const int e = s.local[p], row = p / a.k;
+        if (e != kNone) atomicOr(&s.named[e * words + row / 32], 1u << (row & 31));
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {   // exclusive sums of rows (low half) and entries (high half)
+        const int lane = threadIdx.x;
+        int carry = 0;
+        for (int b = 0; b < a.experts; b += 32) {
+            const int e = b + lane;
+            int rows = 0;
+            if (e < a.experts)
+                for (int w = 0; w < words; ++w) rows += __popc(s.named[e * words + w]);
+            const int n = (rows + per - 1) / per, v = n << 16 | rows;
+            int sum = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += u;
+            }
+            const int at = carry + sum - v, row0 = at & 0xFFFF, entry0 = at >> 16;
+            for (int i = 0; i < n; ++i) {
+                s.expert[entry0 + i] = (uint16_t)e;
+                s.start[entry0 + i] = (uint16_t)(row0 + i * per);
+            }
+            if (e < a.experts) s.cursor[e] = row0;
+            carry += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        if (lane == 0) {
+            s.start[carry >> 16] = (uint16_t)(carry & 0xFFFF);
+            *s.count = carry >> 16;
+        }
+    }
+    __syncthreads();
+    for (int p = threadIdx.x; p < a.pairs; p += blockDim.x) {
+        const int e = s.local[p], row = p / a.k;
+        if (e == kNone) continue;
+        s.list[place_of(s, words, e, row)] = (uint16_t)row;   // slots of a row that name one expert write the same
+    }
+    __syncthreads();
+    return *s.count;
+}
+
+// 16 bytes of weights, in the order that the code has them: they are read once, well ahead of their use.
+__device__ __forceinline__ uint4 weights16(const uint8_t* p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// Two e4m3 codes to two FP16 values, exactly; the low or the high half of w.
+__device__ __forceinline__ uint32_t half_codes(uint32_t w, bool high)
+{
+    uint32_t r;
+    if (high) asm("{ .reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(r) : "r"(w));
+    else asm("{ .reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l; }" : "=r"(r) : "r"(w));
+    return r;
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 2^n for n in -126..127.
+__device__ __forceinline__ float power2(int n) { return __int_as_float((n + 127) << 23); }
+
+// 2^n as FP16, both halves, n <= 0; 0 below its smallest number.
+__device__ __forceinline__ uint32_t half_power2(int n)
+{
+    const uint32_t h = n >= -14 ? (uint32_t)(n + 15) << 10 : n >= -24 ? 1u << (n + 24) : 0u;
+    return h | h << 16;
+}
+
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b)
+{
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// A lane's part of the other operand over a block of 128 columns: columns 16 q .. + 15 of both 64-column chunks of row
+// `row` (< 0: zeros), as FP16; returns the factor that the block's sums take for that row.
+template <int FROM>
+__device__ __forceinline__ float rows16(const FewArgs& a, int row, int kb, int q, uint32_t (&b)[16])
+{
+    const int width = FROM == kFromZ ? a.I : a.H;
+    const int c0 = 128 * kb + 16 * q;
+    const bool in0 = row >= 0 && c0 < width, in1 = row >= 0 && c0 + 64 < width;
+    const int64_t at = (int64_t)row * width + c0;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    if constexpr (FROM == kFromE4m3) {
+        const uint4 lo = in0 ? __ldg(reinterpret_cast<const uint4*>(a.x + at)) : zero;
+        const uint4 hi = in1 ? __ldg(reinterpret_cast<const uint4*>(a.x + at + 64)) : zero;
+        const float scale = row >= 0 ? __ldg(a.x_scales + (int64_t)row * a.hb + kb) : 0.0f;
+        const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            b[2 * i] = half_codes(w[i], false);
+            b[2 * i + 1] = half_codes(w[i], true);
+        }
+        return scale;
+    } else {
+        const uint4* p = reinterpret_cast<const uint4*>((FROM == kFromZ ? a.z : a.x) + 2 * at);
+        uint4 v[4];
+        if constexpr (FROM == kFromZ) {   // written by the kernel before this one
+            v[0] = in0 ? p[0] : zero;
+            v[1] = in0 ? p[1] : zero;
+            v[2] = in1 ? p[8] : zero;
+            v[3] = in1 ? p[9] : zero;
+        } else {
+            v[0] = in0 ? __ldg(p) : zero;
+            v[1] = in0 ? __ldg(p + 1) : zero;
+            v[2] = in1 ? __ldg(p + 8) : zero;
+            v[3] = in1 ? __ldg(p + 9) : zero;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            b[4 * i] = v[i].x;
+            b[4 * i + 1] = v[i].y;
+            b[4 * i + 2] = v[i].z;
+            b[4 * i + 3] = v[i].w;
+        }
+        if constexpr (FROM == kFromFp16) return 1.0f;
+        if constexpr (FROM == kFromZ) {
+            // each 8 columns to the largest power of two of the block's: exact but for what falls below 2^-38 of the
+            // block's largest value
+            const uint16_t* ep = reinterpret_cast<const uint16_t*>(a.z_exp + (int64_t)row * (a.I / 8) + c0 / 8);
+            const uint32_t e0 = in0 ? ep[0] : 0, e1 = in1 ? ep[4] : 0;
+            const int e[4] = {(int)(e0 & 0xFF), (int)(e0 >> 8), (int)(e1 & 0xFF), (int)(e1 >> 8)};
+            int top = max(max(e[0], e[1]), max(e[2], e[3]));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t f = half_power2(e[i] - top);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) b[4 * i + j] = mul_half2(b[4 * i + j], f);
+            }
+            return power2(max(top, 18) - 142);
+        }
+        if constexpr (FROM == kFromBf16) {
+            // BF16's 8 bits fit FP16's 11; its range does not, so the block's largest value is brought to 2^14 .. 2^15
+            uint32_t top = 0;   // of the magnitudes' bits, two at a time
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = __vmaxu2(top, b[i] & 0x7FFF7FFFu);
+            top = max(top & 0xFFFFu, top >> 16);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = min(max((int)(top >> 7) - 127, -110), 126);
+            const float f = power2(14 - e);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) b[i] = pack2<true>(bf16_lo(b[i]) * f, bf16_hi(b[i]) * f);
+            return power2(e - 14);
+        }
+    }
+    return 0.0f;
+}
+
+// Eight columns' sums of a block of 128, times their scales, into tot: w holds the block's 16 rows of weights (row g,
+// row g + 8; then the second 64 columns), f the lane's row's factor, s0 and s1 the scales of rows g and g + 8.
+__device__ __forceinline__ void add_block(float (&tot)[4], const uint4 (&w)[4], const uint32_t (&b)[16], float f, float s0,
+                                          float s1)
+{
+    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const uint32_t lo[4] = {w[2 * c].x, w[2 * c].y, w[2 * c].z, w[2 * c].w};
+        const uint32_t hi[4] = {w[2 * c + 1].x, w[2 * c + 1].y, w[2 * c + 1].z, w[2 * c + 1].w};
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const uint32_t x[4] = {half_codes(lo[m], false), half_codes(hi[m], false), half_codes(lo[m], true),
+                                   half_codes(hi[m], true)};
+            mma_f16(d, x, b[8 * c + 2 * m], b[8 * c + 2 * m + 1]);
+        }
+    }
+    const int q = threadIdx.x & 3;
+    const float f0 = __shfl_sync(0xffffffffu, f, 8 * q), f1 = __shfl_sync(0xffffffffu, f, 8 * q + 4);
+    tot[0] = fmaf(d[0], s0 * f0, tot[0]);
+    tot[1] = fmaf(d[1], s0 * f1, tot[1]);
+    tot[2] = fmaf(d[2], s1 * f0, tot[2]);
+    tot[3] = fmaf(d[3], s1 * f1, tot[3]);
+}
+
+// Steps that a warp's weights are read ahead: as many as 128 registers a thread leave room for.
+template <int NT>
+constexpr int kAhead = NT > 2 ? 3 : 4;
+
+// Up projection and SwiGLU.  A unit is 8 columns of z, its 8 gate rows and 8 up rows, for one entry; `split` warps share
+// its K.
+template <int FROM, int NT>
+__global__ void __launch_bounds__(32 * kUpWarps, kWarpsPerSm / kUpWarps) ep_few_up_kernel(const FewArgs a)
+{
+    extern __shared__ __align__(16) uint8_t shared[];
+    __shared__ float4 parts[2][kUpWarps][NT][32];   // [round's parity]: sums of a unit's K
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const Entries s = entries_at(shared, a);
+    follow_predecessor();
+    const int entries = make_entries(a, s, 8 * NT);
+    const int teams = kUpWarps / a.split, team = warp / a.split, member = warp % a.split;
+    const int slices = a.I / 8, units = entries * slices;
+    const int k_lo = a.hb * member / a.split, k_hi = a.hb * (member + 1) / a.split, nb = k_hi - k_lo;
+    const int u0 = blockIdx.x * teams + team, stride = gridDim.x * teams;
+    const int mine = u0 < units ? (units - 1 - u0) / stride + 1 : 0;
+    const int steps = mine * nb;
+
+    constexpr int D = kAhead<NT>;
+    uint4 ring[D][4];
+    int lu = u0, lk = k_lo, ls = 0;
+    const uint8_t* lp = nullptr;
+    const int64_t up_rows = (int64_t)a.I * a.H;
+    auto point = [&] {
+        const int entry = lu / slices;
+        lp = a.up + ((int64_t)s.expert[entry] * 2 * a.I + 8 * (lu - entry * slices) + g) * a.H + 16 * q;
+    };
+    if (steps > 0) point();
+    auto load = [&](uint4 (&w)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = make_uint4(0, 0, 0, 0);
+        if (ls >= steps) return;
+        const uint8_t* p = lp + 128 * lk;
+        const int c = 128 * lk + 16 * q;
+        if (c < a.H) {
+            w[0] = weights16(p);
+            w[1] = weights16(p + up_rows);
+        }
+        if (c + 64 < a.H) {
+            w[2] = weights16(p + 64);
+            w[3] = weights16(p + up_rows + 64);
+        }
+        ++ls;
+        if (++lk == k_hi) {
+            lk = k_lo;
+            lu += stride;
+            if (ls < steps) point();
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(ring[d]);
+
+    float tot[NT][4];
+    int row[NT], k = k_lo, u = u0, first = 0, n = 0, slice = 0;
+    const float *gs = nullptr, *us = nullptr;   // the unit's scales
+    auto begin = [&] {
+        const int entry = u / slices;
+        slice = u - entry * slices;
+        first = s.start[entry];
+        n = s.start[entry + 1] - first;
+        const float* es = a.up_scales + (int64_t)s.expert[entry] * a.ub * a.hb;
+        gs = es + (int64_t)(8 * slice / 128) * a.hb;
+        us = es + (int64_t)((a.I + 8 * slice) / 128) * a.hb;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            row[t] = 8 * t + g < n ? s.list[first + 8 * t + g] : -1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tot[t][i] = 0.0f;
+        }
+    };
+    // z of the unit from its whole sums, and its power of two
+    auto finish = [&] {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            if (8 * t >= n) break;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float z = tot[t][c] * sigmoid_and_rest(tot[t][c]).x * tot[t][2 + c];
+                float m = fmaxf(fabsf(z), 0.0f);   // NaN counts as 0
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                // the largest of the 8 to 2^14 .. 2^15; an infinity stays one
+                const int e = min(max((int)(__float_as_uint(m) >> 23) - 127, -110), 127);
+                const int column = 8 * t + 2 * q + c;
+                if (column >= n) continue;
+                const int64_t place = first + column;
+                reinterpret_cast<__half*>(a.z)[place * a.I + 8 * slice + g] = __float2half_rn(z * power2(14 - e));
+                if (g == 0) a.z_exp[place * slices + slice] = m > 0.0f ? (uint8_t)(e + 128) : 0;
+            }
+        }
+    };
+    if (a.split == 1) {
+        if (steps > 0) begin();
+        for (int i0 = 0; i0 < steps; i0 += D) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                if (i0 + d >= steps) break;
+                const float s0 = __ldg(gs + k), s1 = __ldg(us + k);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if (8 * t >= n) break;
+                    uint32_t b[16];
+                    const float f = rows16<FROM>(a, row[t], k, q, b);
+                    add_block(tot[t], ring[d], b, f, s0, s1);
+                }
+                load(ring[d]);
+                if (++k == k_hi) {
+                    finish();
+                    k = k_lo;
+                    u += stride;
+                    if (i0 + d + 1 < steps) begin();
+                }
+            }
+        }
+        return;
+    }
+    // a unit's K is shared: its warps meet once per round, and every team of the CTA makes as many rounds
+    const int first_unit = blockIdx.x * teams;
+    const int rounds = first_unit < units ? (units - 1 - first_unit) / stride + 1 : 0;
+    int i = 0;   // steps done, modulo D in the ring's index: a round's steps are walked with the ring unrolled
+    for (int round = 0; round < rounds; ++round, u += stride) {
+        const bool has = u < units;
+        n = 0;
+        if (has) begin();
+        for (int left = has ? nb : 0; left > 0;) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                if (left == 0 || i != d) continue;
+                const float s0 = __ldg(gs + k), s1 = __ldg(us + k);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if (8 * t >= n) break;
+                    uint32_t b[16];
+                    const float f = rows16<FROM>(a, row[t], k, q, b);
+                    add_block(tot[t], ring[d], b, f, s0, s1);
+                }
+                load(ring[d]);
+                ++k;
+                --left;
+                i = d + 1 == D ? 0 : d + 1;
+            }
+        }
+        k = k_lo;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            if (8 * t < n) parts[round & 1][warp][t][lane] = make_float4(tot[t][0], tot[t][1], tot[t][2], tot[t][3]);
+        __syncthreads();
+        if (member == 0 && has) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (8 * t >= n) break;
+                for (int m = 1; m < a.split; ++m) {
+                    const float4 v = parts[round & 1][warp + m][t][lane];
+                    tot[t][0] += v.x;
+                    tot[t][1] += v.y;
+                    tot[t][2] += v.z;
+                    tot[t][3] += v.w;
+                }
+            }
+            finish();
+        }
+    }
+}
+
+// Down projection and the weighted sum.  A CTA owns 16 output columns; its warps share the blocks of all entries' K
+// evenly, and each keeps the rows' sums of its own part in shared memory.
+template <int NT>
+__global__ void __launch_bounds__(32 * kDownMaxWarps) ep_few_down_kernel(const FewArgs a)
+{
+    extern __shared__ __align__(16) uint8_t shared[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int warps = blockDim.x >> 5, h0 = 16 * blockIdx.x;
+    const Entries s = entries_at(shared, a);
+    float* share = reinterpret_cast<float*>(shared + entries_bytes(a.pairs, a.experts, a.rows));   // [pairs]: weights by list place
+    float* sums = share + (a.pairs + 3) / 4 * 4;                                           // [warps][rows][16]
+    // Before its wait this kernel reads what the one before it does not write, and that has let it start only after its
+    // own wait, when all that precedes the call had reached L2: ids and their weights past this SM's cache, which may hold
+    // what was there before, and the experts' weights.
+    const int entries = make_entries(a, s, 8 * NT);
+    const int total = entries * a.ib;
+    const int lo = (int)((int64_t)total * warp / warps), hi = (int)((int64_t)total * (warp + 1) / warps);
+
+    constexpr int D = kAhead<NT>;
+    uint4 ring[D][4];
+    int lb = lo, le = lo / a.ib, lk = lo - le * a.ib;
+    const uint8_t* lp = nullptr;
+    auto point = [&] { lp = a.down + ((int64_t)s.expert[le] * a.H + h0 + g) * a.I + 16 * q; };
+    if (lb < hi) point();
+    auto load = [&](uint4 (&w)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = make_uint4(0, 0, 0, 0);
+        if (lb >= hi) return;
+        const uint8_t* p = lp + 128 * lk;
+        const int c = 128 * lk + 16 * q;
+        if (c < a.I) {
+            w[0] = weights16(p);
+            w[1] = weights16(p + 8 * (int64_t)a.I);
+        }
+        if (c + 64 < a.I) {
+            w[2] = weights16(p + 64);
+            w[3] = weights16(p + 8 * (int64_t)a.I + 64);
+        }
+        ++lb;
+        if (++lk == a.ib) {
+            lk = 0;
+            ++le;
+            if (lb < hi) point();
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(ring[d]);
+    for (int i = threadIdx.x; i < warps * a.rows * 16; i += blockDim.x) sums[i] = 0.0f;
+    for (int p = threadIdx.x; p < a.pairs; p += blockDim.x) {
+        const int e = s.local[p], row = p / a.k;
+        if (e == kNone) continue;
+        float w = 0.0f;
+        for (int j = row * a.k; j < (row + 1) * a.k; ++j)
+            if (s.local[j] == e) w += __int_as_float(load_shared_view(reinterpret_cast<const int32_t*>(a.weights) + j));
+        share[place_of(s, row_words(a.rows), e, row)] = w;
+    }
+    __syncthreads();
+    follow_predecessor();
+
+    float* own = sums + warp * a.rows * 16;
+    float tot[NT][4];
+    int place[NT], e = lo / a.ib, k = lo - e * a.ib, first = 0, n = 0;
+    const float* ds = nullptr;
+    auto begin = [&] {
+        first = s.start[e];
+        n = s.start[e + 1] - first;
+        ds = a.down_scales + ((int64_t)s.expert[e] * a.hb + h0 / 128) * a.ib;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            place[t] = 8 * t + g < n ? first + 8 * t + g : -1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tot[t][i] = 0.0f;
+        }
+    };
+    // an entry's rows are distinct, so that no two lanes add to one place
+    auto finish = [&] {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            if (8 * t >= n) break;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int column = 8 * t + 2 * q + c;
+                if (column >= n) continue;
+                const float w = share[first + column];
+                float* to = own + s.list[first + column] * 16 + g;
+                to[0] = fmaf(w, tot[t][c], to[0]);
+                to[8] = fmaf(w, tot[t][2 + c], to[8]);
+            }
+        }
+        __syncwarp();
+    };
+    if (lo < hi) begin();
+    for (int i0 = lo; i0 < hi; i0 += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (i0 + d >= hi) break;
+            const float sc = __ldg(ds + k);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (8 * t >= n) break;
+                uint32_t b[16];
+                const float f = rows16<kFromZ>(a, place[t], k, q, b);
+                add_block(tot[t], ring[d], b, f, sc, sc);
+            }
+            load(ring[d]);
+            if (++k == a.ib || i0 + d + 1 == hi) {
+                finish();
+                k = 0;
+                ++e;
+                if (i0 + d + 1 < hi) begin();
+            }
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.rows * 16; i += blockDim.x) {
+        float v = 0.0f;
+        for (int w = 0; w < warps; ++w) v += sums[w * a.rows * 16 + i];
+        const int64_t at = (int64_t)(i / 16) * a.H + h0 + (i & 15);
+        if (a.out_fp16) reinterpret_cast<__half*>(a.out)[at] = __float2half_rn(v);
+        else reinterpret_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+    }
+}
+
+template <int FROM, int NT>
+cudaError_t launch_up(const FewArgs& a, int sms, cudaStream_t s)
+{
+    const size_t shared = entries_bytes(a.pairs, a.experts, a.rows);
+    const cudaError_t e = allow_all_shared<ep_few_up_kernel<FROM, NT>>();
+    if (e != cudaSuccess) return e;
+    const int64_t entries = a.pairs < a.experts ? a.pairs : (int64_t)a.experts + a.pairs / (8 * NT);   // at most
+    const int64_t teams = kUpWarps / a.split, ctas = (entries * (a.I / 8) + teams - 1) / teams;
+    const int64_t fit = (int64_t)sms * (kWarpsPerSm / kUpWarps);
+    return launch_dependent(ep_few_up_kernel<FROM, NT>, dim3((unsigned)(ctas < fit ? ctas : fit)), dim3(32 * kUpWarps), shared, s, a);
+}
+
+template <int NT>
+cudaError_t launch_few(FewArgs a, int from, int sms, cudaStream_t s)
+{
+    // experts that rows name, at most: with fewer units than half of the warps that run at once, more warps share one
+    const int64_t units = (int64_t)(a.pairs < a.experts ? a.pairs : a.experts) * (a.I / 8);
+    a.split = 1;
+    while (a.split < kUpWarps && units * a.split * 2 <= (int64_t)sms * kWarpsPerSm) a.split *= 2;
+    cudaError_t e = from == kFromE4m3 ? launch_up<kFromE4m3, NT>(a, sms, s)
+                    : from == kFromFp16 ? launch_up<kFromFp16, NT>(a, sms, s) : launch_up<kFromBf16, NT>(a, sms, s);
+    if (e != cudaSuccess) return e;
+    e = allow_all_shared<ep_few_down_kernel<NT>>();
+    if (e != cudaSuccess) return e;
+    const int ctas = a.H / 16;
+    int warps = kDownMaxWarps;
+    while (warps > 4 && (int64_t)ctas * warps > (int64_t)sms * kWarpsPerSm) warps /= 2;
+    const size_t shared = entries_bytes(a.pairs, a.experts, a.rows) + ((size_t)(a.pairs + 3) / 4 * 4 + (size_t)warps * a.rows * 16) * 4;
+    return launch_dependent(ep_few_down_kernel<NT>, dim3(ctas), dim3(32 * warps), shared, s, a);
+}
+
+size_t few_z_bytes(int64_t pairs, int inner) { return ((size_t)pairs * inner * 2 + 255) / 256 * 256; }
+
+}  // namespace
+}  // namespace ep
+
+extern "C" size_t ep_moe_few_workspace_bytes(int64_t rows, int topk, int inner)
+{
+    using namespace ep;
+    if (rows <= 0 || rows > kFewRows || topk < 1 || rows * topk > kFewPairs || inner < 16 || inner % 16 != 0 || inner > 1 << 20)
+        return 0;
+    return few_z_bytes(rows * topk, inner) + (size_t)rows * topk * (inner / 8);
+}
+
+extern "C" int ep_moe_few_rows(const void* x, const float* x_scales, int x_dtype, const int32_t* indices,
+                               const float* weights, int64_t rows, int topk, int first_expert, int experts, int hidden,
+                               int inner, const void* up, const float* up_scales, const void* down,
+                               const float* down_scales, int out_dtype, void* out, void* workspace,
+                               size_t workspace_bytes, void* stream)
+{
+    using namespace ep;
+    const char* who = "ep_moe_few_rows";
+    if (rows < 0 || rows > kFewRows)
+        return layer_fail(EP_ERR_ARG, "%s: rows=%lld outside 0..%d: more rows are sorted by expert", who, (long long)rows, kFewRows);
+    if (topk < 1 || rows * topk > kFewPairs)
+        return layer_fail(EP_ERR_ARG, "%s: topk=%d is below 1, or rows*topk passes %d", who, topk, kFewPairs);
+    if (experts < 1 || experts > kFewExperts)
+        return layer_fail(EP_ERR_ARG, "%s: experts=%d outside 1..%d", who, experts, kFewExperts);
+    if (hidden < 16 || hidden % 16 != 0 || hidden > 1 << 20)
+        return layer_fail(EP_ERR_ARG, "%s: hidden=%d is not a multiple of 16 in 16..2^20", who, hidden);
+    if (inner < 16 || inner % 16 != 0 || inner > 1 << 19)
+        return layer_fail(EP_ERR_ARG, "%s: inner=%d is not a multiple of 16 in 16..2^19", who, inner);
+    if (x_dtype != EP_FP8_E4M3 && x_dtype != EP_FP16 && x_dtype != EP_BF16)
+        return layer_fail(EP_ERR_ARG, "%s: x_dtype=%d is not EP_FP8_E4M3, EP_FP16 or EP_BF16", who, x_dtype);
+    if (out_dtype != EP_BF16 && out_dtype != EP_FP16)
+        return layer_fail(EP_ERR_ARG, "%s: out_dtype=%d is neither EP_BF16 nor EP_FP16", who, out_dtype);
+    if (rows == 0) return EP_OK;
+    if (!layer_aligned(x, 16) || (x_dtype == EP_FP8_E4M3) != (x_scales != nullptr) || (x_scales && !layer_aligned(x_scales, 4)))
+        return layer_fail(EP_ERR_ARG, "%s: x is NULL or not 16-byte aligned, or x_scales is not given with e4m3 rows alone", who);
+    if (!layer_aligned(indices, 4) || !layer_aligned(weights, 4))
+        return layer_fail(EP_ERR_ARG, "%s: indices or weights is NULL or misaligned", who);
+    if (!layer_aligned(up, 16) || !layer_aligned(down, 16) || !layer_aligned(up_scales, 4) || !layer_aligned(down_scales, 4))
+        return layer_fail(EP_ERR_ARG, "%s: up, down or a scale array is NULL or misaligned", who);
+    if (!layer_aligned(out, 16)) return layer_fail(EP_ERR_ARG, "%s: out is NULL or not 16-byte aligned", who);
+    const size_t need = ep_moe_few_workspace_bytes(rows, topk, inner);
+    if (!layer_aligned(workspace, 16) || workspace_bytes < need)
+        return layer_fail(EP_ERR_ARG, "%s: workspace of %zu bytes, %zu needed, 16-byte aligned", who, workspace_bytes, need);
+    FewArgs a{};
+    a.x = (const uint8_t*)x; a.x_scales = x_scales; a.indices = indices; a.weights = weights;
+    a.up = (const uint8_t*)up; a.up_scales = up_scales; a.down = (const uint8_t*)down; a.down_scales = down_scales;
+    a.rows = (int)rows; a.k = topk; a.pairs = (int)rows * topk; a.first = first_expert; a.experts = experts;
+    a.H = hidden; a.I = inner; a.hb = (hidden + 127) / 128; a.ib = (inner + 127) / 128; a.ub = (2 * inner + 127) / 128;
+    a.z = (uint8_t*)workspace; a.z_exp = a.z + few_z_bytes(a.pairs, inner);
+    a.out = out; a.out_fp16 = out_dtype == EP_FP16;
+    const int sms = layer_num_sms();
+    if (sms == 0) return layer_fail(EP_ERR_CUDA, "%s: cannot tell the current device's multiprocessors", who);
+    const int from = x_dtype == EP_FP8_E4M3 ? kFromE4m3 : x_dtype == EP_FP16 ? kFromFp16 : kFromBf16;
+    cudaStream_t s = (cudaStream_t)stream;
+    // an expert's rows, at most all of them, in entries of 8, 16 or 32
+    const cudaError_t e = rows <= 8 ? launch_few<1>(a, from, sms, s) : rows <= 16 ? launch_few<2>(a, from, sms, s)
+                                                                                  : launch_few<4>(a, from, sms, s);
+    return layer_cuda(e, "ep_moe_few_rows: launch");
+}

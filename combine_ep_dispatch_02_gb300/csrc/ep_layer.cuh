@@ -157,6 +157,18 @@ __device__ __forceinline__ uint4 pack4x2(const float2 (&f)[4])
                       pack2<FP16>(f[3].x, f[3].y));
 }
 
+// sigmoid(g) and 1 - sigmoid(g).  The exponential's argument is rounded to FP32, which puts the exponential off by
+// up to 1.0e-7 of |g|, and each approximate instruction by two units: under 2^-16 at the |g| of 88 where the
+// sigmoid leaves FP32's normal numbers, and 2^-19 at 10, both far inside a 16-bit value's half step, 2^-11 at the
+// finest.  From there on the exponential is held at 2^127, whose reciprocal is 0: such a sigmoid counts as 0.
+__device__ __forceinline__ float2 sigmoid_and_rest(float g)
+{
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fminf(-1.4426950408889634f * g, 127.0f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return make_float2(r, e * r);
+}
+
 // FP32 scale of a 128-element block with largest magnitude m, as the quantising dispatch defines
 // it: m / 448, and 1 for a block of zeros (fmaxf drops NaN, so a block of NaN also gets 1).
 __device__ __forceinline__ float e4m3_block_scale(float m) { return m > 0.0f ? __fdiv_rn(m, 448.0f) : 1.0f; }

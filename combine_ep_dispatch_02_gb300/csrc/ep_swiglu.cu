@@ -34,18 +34,6 @@ struct SwigluArgs {
     int z_blocks, row_blocks;   // 128-column blocks of z, and of gate | up
 };
 
-// sigmoid(g) and 1 - sigmoid(g).  The exponential's argument is rounded to FP32, which puts the exponential off by
-// up to 1.0e-7 of |g|, and each approximate instruction by two units: under 2^-17 at the |g| of 88 where the
-// sigmoid leaves FP32's normal numbers, and 2^-20 at 10, both far inside the outputs' half steps of 2^-12 at the finest.
-// From there on the exponential is held at 2^127, whose reciprocal is 0: such a sigmoid counts as 0.
-__device__ __forceinline__ float2 sigmoid_and_rest(float g)
-{
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fminf(-1.4426950408889634f * g, 127.0f)));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return make_float2(r, e * r);
-}
-
 // Largest magnitude over the sixteen lanes of a half warp; NaN counts as 0.
 __device__ __forceinline__ float block_top(const float (&f)[8])
 {

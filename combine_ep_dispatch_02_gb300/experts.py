@@ -5,6 +5,7 @@
 * ``sort_by_expert``, ``sorted_rows``, ``return_rows`` and the gradients ``sorted_rows_backward`` and
   ``return_rows_backward``: received rows in compact expert order, and back with routing weights;
 * ``matmul_fp8`` and ``matmul_fp8_swiglu``: the block-scaled e4m3 product, dense or by expert;
+* ``moe_few_rows``: the whole layer for a few rows, without a sort;
 * ``rms_norm_join`` and its gradient: the norm after a block, its gate, the scaled residual and the norm before the
   next block;
 * ``swiglu_saved`` and its gradient: SwiGLU between two products for training, its input kept as e4m3.
@@ -41,7 +42,8 @@ _OUT_CODES = {"bf16": EP_BF16, "fp16": EP_FP16}
 # the C ABI functions the binding calls, in the order of its bind()
 _BOUND = ("ep_rms_norm_fp8", "ep_sort_workspace_bytes", "ep_sort_by_expert", "ep_sorted_rows", "ep_return_rows",
           "ep_return_rows_backward", "ep_matmul_fp8", "ep_rms_norm_join", "ep_rms_norm_join_workspace_bytes",
-          "ep_rms_norm_join_backward", "ep_swiglu_saved", "ep_swiglu_saved_backward", "ep_strerror", "ep_last_error")
+          "ep_rms_norm_join_backward", "ep_swiglu_saved", "ep_swiglu_saved_backward", "ep_moe_few_workspace_bytes",
+          "ep_moe_few_rows", "ep_strerror", "ep_last_error")
 _status_words = {}
 _binding = None
 _bound_to = None
@@ -189,6 +191,24 @@ def matmul_fp8_swiglu(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, 
     scales [rows][ceil(columns/256)]), the a and a_scales of a following matmul_fp8.  Arguments as
     matmul_fp8; columns must be a multiple of 32."""
     return _on(stream, _native().matmul_fp8, a, a_scales, b, b_scales, offsets, EP_FP8_E4M3)
+
+
+def moe_few_rows(x: torch.Tensor, x_scales: Optional[torch.Tensor], indices: torch.Tensor, weights: torch.Tensor,
+                 up: torch.Tensor, up_scales: torch.Tensor, down: torch.Tensor, down_scales: torch.Tensor,
+                 first_expert: int = 0, out_dtype: str = "bf16", stream=None) -> torch.Tensor:
+    """A whole expert layer for a few rows (up to 128): out[row] = sum over the experts that the row names, ascending, of
+    weight * down[e] @ (gate * sigmoid(gate) * up), [gate; up] = up[e] @ x[row], in FP32, rounded once.  x [rows][hidden]
+    float8_e4m3fn with x_scales [rows][ceil(hidden/128)] FP32, or BF16 or FP16 with x_scales None; indices and weights
+    [rows][k] int32 and FP32; up [experts][2 * inner][hidden] (gate rows, then up rows) and down [experts][hidden][inner]
+    float8_e4m3fn with scales as ``matmul_fp8`` takes them; hidden and inner multiples of 16.  Ids outside first_expert ..
+    first_expert + experts - 1 are left out; one that a row names several times counts once, with the sum of its weights.
+    The time is that of reading the named experts' weights; from a few tokens per expert on, sorted rows and
+    ``matmul_fp8_swiglu`` are faster."""
+    code = _OUT_CODES.get(out_dtype)
+    if code is None:
+        raise EpError(EP_ERR_ARG, f"out_dtype={out_dtype!r} is neither 'bf16' nor 'fp16'")
+    return _on(stream, _native().moe_few_rows, x, x_scales, indices, weights, up, up_scales, down, down_scales,
+               first_expert, code)
 
 
 @dataclasses.dataclass

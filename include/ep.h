@@ -526,6 +526,29 @@ int ep_swiglu_saved_backward(const void* saved, const float* saved_scales, const
                              int64_t rows, int inner, const int32_t* rows_end, void* d_gate_up, void* q, float* scales,
                              void* stream);
 
+/*
+ * A whole expert layer for a few rows, in two kernels: for each row the sum, over the experts that it names, of
+ * weight * down[e] (gate * sigmoid(gate) * up), [gate; up] = up[e] x.
+ *   x            [rows][hidden], 16-byte aligned: e4m3 codes (x_dtype EP_FP8_E4M3) with x_scales [rows][ceil(hidden/128)], or
+ *                EP_FP16 or EP_BF16 with x_scales NULL
+ *   indices, weights  [rows][topk] int32 expert ids and FP32 weights.  Ids outside first_expert .. first_expert+experts-1, -1
+ *                among them, are left out; an id that a row names several times counts once, with the sum of its weights
+ *   up, up_scales      [experts][2*inner][hidden] e4m3 codes, gate rows then up rows, and FP32 scales
+ *                      [experts][ceil(2*inner/128)][ceil(hidden/128)]; 16-byte aligned
+ *   down, down_scales  [experts][hidden][inner] codes, [experts][ceil(hidden/128)][ceil(inner/128)]
+ *   out          [rows][hidden] of out_dtype (EP_BF16 or EP_FP16), 16-byte aligned; zeros for a row without an expert
+ * Sums are in FP32, over the experts in ascending order; what SwiGLU yields is held as FP16 with a power of two for every
+ * 8 columns, and each output is rounded once.  BF16 rows are brought to FP16, exactly but for what is 2^-28 of their
+ * block's largest value or less.  Limits: rows up to 128, rows*topk up to 4096, experts up to 1024, hidden up to 2^20 and
+ * inner up to 2^19, both multiples of 16.  The workspace holds ep_moe_few_workspace_bytes() at least, 16-byte aligned
+ * (0 for no rows and for invalid shapes).  More rows are better sorted by expert (ep_sort_by_expert, ep_matmul_fp8).
+ */
+size_t ep_moe_few_workspace_bytes(int64_t rows, int topk, int inner);
+int ep_moe_few_rows(const void* x, const float* x_scales, int x_dtype, const int32_t* indices, const float* weights,
+                    int64_t rows, int topk, int first_expert, int experts, int hidden, int inner, const void* up,
+                    const float* up_scales, const void* down, const float* down_scales, int out_dtype, void* out,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code ("unknown status" for any other value); never NULL.
  * With ep_last_error, the host side of the staging PR's caller contract ("refactor(EPv2):
  * replace per-module __device__ staging with shared buffer", section "Caller contract"): a

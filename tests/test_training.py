@@ -18,6 +18,9 @@ BWD = dict(h=P, post=P, pre=P, dh=P, dhs=256, dn=P, dns=256, dy=P, dres=P, dpost
 SAVE = dict(x=P, stride=512, dtype=ep.EP_BF16, rows=4, inner=256, end=None, q=P, s=P, saved=P, ss=P, stream=None)
 BACK = dict(saved=P, ss=P, dz=P, stride=256, dtype=ep.EP_BF16, rows=4, inner=256, end=None, d=P, q=None, s=None, stream=None)
 
+FEW = dict(x=P, xs=P, xd=ep.EP_FP8_E4M3, idx=P, w=P, rows=4, k=2, first=0, experts=8, hidden=256, inner=128, up=P, ups=P, down=P,
+           downs=P, od=ep.EP_BF16, out=P, ws=P, wsb=1 << 40, stream=None)
+
 
 def _join(lib, change, call, rest):
     j = ep.JoinArgs(**{**JOIN, **{k: v for k, v in change.items() if k in JOIN}})
@@ -77,6 +80,27 @@ def test_swiglu_backward_refusals(lib, change, word):  # noqa: F811
     _refused(lib, lib.ep_swiglu_saved_backward(*{**BACK, **change}.values()), "ep_swiglu_saved_backward", word)
 
 
+@pytest.mark.parametrize("change,word", [
+    (dict(rows=-1), "rows"), (dict(rows=129), "rows"), (dict(k=0), "topk"), (dict(rows=128, k=33), "topk"),
+    (dict(k=2 ** 31 - 1), "topk"), (dict(experts=0), "experts"), (dict(experts=1025), "experts"), (dict(hidden=0), "hidden"),
+    (dict(hidden=24), "hidden"), (dict(hidden=(1 << 20) + 16), "hidden"), (dict(inner=0), "inner"), (dict(inner=40), "inner"),
+    (dict(inner=(1 << 19) + 16), "inner"), (dict(xd=3), "x_dtype"), (dict(od=2), "out_dtype"), (dict(x=None), "x is"),
+    (dict(x=P + 8), "x is"), (dict(xs=None), "x_scales"), (dict(xd=0), "x_scales"), (dict(xs=P + 2), "x_scales"),
+    (dict(idx=None), "indices"), (dict(w=P + 2), "weights"), (dict(up=P + 8), "up, down"), (dict(down=None), "up, down"),
+    (dict(ups=P + 1), "scale"), (dict(downs=None), "scale"), (dict(out=P + 8), "out"), (dict(ws=None), "workspace"),
+    (dict(wsb=100), "workspace")])
+def test_few_rows_refusals(lib, change, word):  # noqa: F811
+    _refused(lib, lib.ep_moe_few_rows(*{**FEW, **change}.values()), "ep_moe_few_rows", word)
+
+
+def test_few_rows_workspace(lib):  # noqa: F811
+    assert lib.ep_moe_few_workspace_bytes(1, 8, 2048) == 8 * 2048 * 2 + 8 * 256
+    assert lib.ep_moe_few_workspace_bytes(3, 1, 16) == 256 + 3 * 2      # 96 bytes of z, rounded up
+    for bad in ((0, 8, 16), (129, 1, 16), (128, 33, 16), (1, 0, 16), (1, 1, 24), (1, 1, 0)):
+        assert lib.ep_moe_few_workspace_bytes(*bad) == 0
+    assert lib.ep_moe_few_rows(*{**FEW, "rows": 0, "x": None, "ws": None}.values()) == ep.EP_OK
+
+
 def test_empty_calls_succeed_without_a_gpu(lib):  # noqa: F811
     assert lib.ep_swiglu_saved(*{**SAVE, "rows": 0, "x": None, "q": None}.values()) == ep.EP_OK
     assert lib.ep_swiglu_saved_backward(*{**BACK, "rows": 0, "dz": None, "saved": None}.values()) == ep.EP_OK
@@ -85,7 +109,8 @@ def test_empty_calls_succeed_without_a_gpu(lib):  # noqa: F811
 def test_binding_takes_cuda_tensors_only(lib):  # noqa: F811
     x = torch.zeros(4, 256, dtype=torch.bfloat16)
     for call in (lambda: ep.rms_norm_join(x, x), lambda: ep.rms_norm_join_backward(ep.Joined(x), x, dh=x),
-                 lambda: ep.swiglu_saved(x), lambda: ep.swiglu_saved_backward(x, x, x)):
+                 lambda: ep.swiglu_saved(x), lambda: ep.swiglu_saved_backward(x, x, x),
+                 lambda: ep.moe_few_rows(x, None, x, x, x, x, x, x)):
         with pytest.raises(ep.EpError) as e:
             call()
         assert e.value.code == ep.EP_ERR_ARG and "not a CUDA device" in str(e.value)
