@@ -39,7 +39,8 @@ EXPORTS = ("ep_plan_create", "ep_plan_destroy", "ep_plan_set_variant", "ep_plan_
            "ep_rms_norm_fp8", "ep_sort_workspace_bytes", "ep_sort_by_expert", "ep_sorted_rows",
            "ep_return_rows", "ep_return_rows_backward", "ep_matmul_fp8", "ep_take_status",
            "ep_rms_norm_join", "ep_rms_norm_join_workspace_bytes", "ep_rms_norm_join_backward", "ep_swiglu_saved",
-           "ep_swiglu_saved_backward", "ep_moe_few_workspace_bytes", "ep_moe_few_rows")
+           "ep_swiglu_saved_backward", "ep_moe_few_workspace_bytes", "ep_moe_few_rows",
+           "ep_matmul_fp8_weight_gradient")
 GATE_KINDS = {"none": 0, "row": 1, "channel": 2, "element": 3}
 
 
@@ -118,6 +119,7 @@ def load_library(path: Optional[str] = None):
         "ep_swiglu_saved_backward": (I, [V, V, V, L, I, L, I, V, V, V, V, V]),
         "ep_moe_few_workspace_bytes": (SZ, [L, I, I]),
         "ep_moe_few_rows": (I, [V, V, I, V, V, L, I, I, I, I, I, V, V, V, V, I, V, V, SZ, V]),
+        "ep_matmul_fp8_weight_gradient": (I, [V, I, V, V, V, L, I, I, I, I, V, V, V]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -483,6 +485,7 @@ class Plan:
         return v.value
 
 
-from .experts import (ExpertOrder, Joined, JoinGradients, matmul_fp8, matmul_fp8_swiglu, moe_few_rows, op_status,  # noqa: E402
-                      return_rows, return_rows_backward, rms_norm_fp8, rms_norm_join, rms_norm_join_backward,
-                      sort_by_expert, sorted_rows, sorted_rows_backward, swiglu_saved, swiglu_saved_backward)
+from .experts import (ExpertOrder, Joined, JoinGradients, matmul_fp8, matmul_fp8_swiglu,  # noqa: E402
+                      matmul_fp8_weight_gradient, moe_few_rows, op_status, return_rows, return_rows_backward,
+                      rms_norm_fp8, rms_norm_join, rms_norm_join_backward, sort_by_expert, sorted_rows,
+                      sorted_rows_backward, swiglu_saved, swiglu_saved_backward)

@@ -20,7 +20,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libep.so")
 SOURCES = ("ep_api.cu", "ep_route.cu", "ep_scatter.cu", "ep_combine.cu", "ep_noalloc.cu",
            "ep_fp8wire.cu", "ep_grouped.cu", "ep_norm.cu", "ep_sort.cu", "ep_matmul.cu",
-           "ep_join.cu", "ep_swiglu.cu", "ep_few.cu")
+           "ep_join.cu", "ep_swiglu.cu", "ep_few.cu", "ep_wgrad.cu")
 BINDING = os.path.join(PKG, "_ep_binding.so")
 BINDING_STAMP = os.path.join(BUILD_DIR, "_ep_binding.stamp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -36,6 +36,7 @@ decltype(&ep_swiglu_saved) g_swiglu;
 decltype(&ep_swiglu_saved_backward) g_swiglu_back;
 decltype(&ep_moe_few_workspace_bytes) g_few_bytes;
 decltype(&ep_moe_few_rows) g_few;
+decltype(&ep_matmul_fp8_weight_gradient) g_gradient;
 decltype(&ep_strerror) g_strerror;
 decltype(&ep_last_error) g_last_error;
 PyObject* g_error;         // the package's EpError
@@ -561,6 +562,43 @@ PyObject* swiglu_saved_backward(PyObject* const* v)
     return pack({d, q, s});
 }
 
+// (dy, a, a_scales, offsets, type of the output or -1 for dy's, whether it is FP32)
+PyObject* weight_gradient(PyObject* const* v)
+{
+    const at::Tensor& dy = lead_tensor(v[0], "dy");
+    const int code = half_code(dy, "dy");
+    if (dy.dim() != 2) refuse("dy has %lld dimensions, the call takes [rows][columns]", (long long)dy.dim());
+    const at::Device dev = dy.device();
+    const int64_t rows = dy.size(0), columns = dy.size(1);
+    const at::Tensor& a = tensor(v[1], "a");
+    if (a.dim() != 2) refuse("a has %lld dimensions, the call takes [rows][inner]", (long long)a.dim());
+    const int64_t inner = a.size(1);
+    const int type = small(v[4], "the output's type");
+    const bool fp32 = truth(v[5]);
+    if (!fp32 && type >= 0 && type != code) refuse("out_dtype is neither dy's type nor 'fp32'");
+    const void* yp = data(dy, "dy", dy.scalar_type(), dy.sizes(), dev);
+    const void* ap = data(a, "a", at::kFloat8_e4m3fn, {rows, inner}, dev);
+    const void* sp = data(tensor(v[2], "a_scales"), "a_scales", at::kFloat, {rows, (inner + 127) / 128}, dev);
+    const bool grouped = v[3] != Py_None;
+    int64_t groups = 1;
+    const void* op = nullptr;
+    if (grouped) {
+        const at::Tensor& o = tensor(v[3], "offsets");
+        if (o.dim() != 1 || o.size(0) < 2) refuse("offsets has shape %s, the call takes [groups + 1]", shape_text(o.sizes()).c_str());
+        groups = o.size(0) - 1;
+        op = data(o, "offsets", at::kInt, o.sizes(), dev);
+    }
+    const int64_t shape[3] = {groups, columns, inner};
+    const c10::cuda::CUDAGuard guard(dev);
+    // a shape that the C ABI refuses gets no storage
+    const bool small_enough = columns <= 1 << 20 && inner <= 1 << 20 && groups <= 4096;
+    at::Tensor out = empty(!small_enough ? at::IntArrayRef{0} : grouped ? at::IntArrayRef(shape, 3) : at::IntArrayRef(shape + 1, 2),
+                           fp32 ? at::kFloat : dy.scalar_type(), dev);
+    check(g_gradient(yp, code, ap, (const float*)sp, (const int32_t*)op, rows, clamp_int(groups), clamp_int(columns),
+                     clamp_int(inner), fp32, out.data_ptr(), status(dev), stream(dev)));
+    return wrap(out);
+}
+
 // (x, x_scales, indices, weights, up, up_scales, down, down_scales, first_expert, out type)
 PyObject* moe_few_rows(PyObject* const* v)
 {
@@ -622,7 +660,7 @@ struct Bound {
 const Bound g_bound[] = {EP_BOUND(g_norm), EP_BOUND(g_sort_bytes), EP_BOUND(g_sort), EP_BOUND(g_rows), EP_BOUND(g_return),
                          EP_BOUND(g_back), EP_BOUND(g_matmul), EP_BOUND(g_join), EP_BOUND(g_join_bytes), EP_BOUND(g_join_back),
                          EP_BOUND(g_swiglu), EP_BOUND(g_swiglu_back), EP_BOUND(g_few_bytes),
-                         EP_BOUND(g_few), EP_BOUND(g_strerror), EP_BOUND(g_last_error)};
+                         EP_BOUND(g_few), EP_BOUND(g_gradient), EP_BOUND(g_strerror), EP_BOUND(g_last_error)};
 constexpr int kBound = sizeof g_bound / sizeof g_bound[0];
 
 // bind(EpError, make_status, addresses of the C ABI functions in the order above)
@@ -661,6 +699,7 @@ PyMethodDef g_methods[] = {
     {"rms_norm_join_backward", (PyCFunction)(void (*)())entry<join_backward, 10>, METH_FASTCALL, nullptr},
     {"swiglu_saved", (PyCFunction)(void (*)())entry<swiglu_saved, 2>, METH_FASTCALL, nullptr},
     {"swiglu_saved_backward", (PyCFunction)(void (*)())entry<swiglu_saved_backward, 5>, METH_FASTCALL, nullptr},
+    {"matmul_fp8_weight_gradient", (PyCFunction)(void (*)())entry<weight_gradient, 6>, METH_FASTCALL, nullptr},
     {"moe_few_rows", (PyCFunction)(void (*)())entry<moe_few_rows, 10>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -204,9 +204,9 @@ __device__ __forceinline__ float rows16(const FewArgs& a, int row, int kb, int q
     const int64_t at = (int64_t)row * width + c0;
     const uint4 zero = make_uint4(0, 0, 0, 0);
     if constexpr (FROM == kFromE4m3) {
-        const uint4 lo = in0 ? __ldg(reinterpret_cast<const uint4*>(a.x + at)) : zero;
-        const uint4 hi = in1 ? __ldg(reinterpret_cast<const uint4*>(a.x + at + 64)) : zero;
-        const float scale = row >= 0 ? __ldg(a.x_scales + (int64_t)row * a.hb + kb) : 0.0f;
+        const uint4 lo = in0 ? *reinterpret_cast<const uint4*>(a.x + at) : zero;
+        const uint4 hi = in1 ? *reinterpret_cast<const uint4*>(a.x + at + 64) : zero;
+        const float scale = row >= 0 ? a.x_scales[(int64_t)row * a.hb + kb] : 0.0f;
         const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -217,17 +217,10 @@ __device__ __forceinline__ float rows16(const FewArgs& a, int row, int kb, int q
     } else {
         const uint4* p = reinterpret_cast<const uint4*>((FROM == kFromZ ? a.z : a.x) + 2 * at);
         uint4 v[4];
-        if constexpr (FROM == kFromZ) {   // written by the kernel before this one
-            v[0] = in0 ? p[0] : zero;
-            v[1] = in0 ? p[1] : zero;
-            v[2] = in1 ? p[8] : zero;
-            v[3] = in1 ? p[9] : zero;
-        } else {
-            v[0] = in0 ? __ldg(p) : zero;
-            v[1] = in0 ? __ldg(p + 1) : zero;
-            v[2] = in1 ? __ldg(p + 8) : zero;
-            v[3] = in1 ? __ldg(p + 9) : zero;
-        }
+        v[0] = in0 ? p[0] : zero;
+        v[1] = in0 ? p[1] : zero;
+        v[2] = in1 ? p[8] : zero;
+        v[3] = in1 ? p[9] : zero;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             b[4 * i] = v[i].x;

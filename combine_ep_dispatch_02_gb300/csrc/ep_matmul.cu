@@ -165,59 +165,6 @@ __device__ __forceinline__ void add_scaled(float2* acc, const uint32_t (&r)[32],
     }
 }
 
-// 2 * PAIRS consecutive columns, n of which exist, of a warp's 32 rows, m of which exist (row by lane, rows `pitch`
-// bytes apart), 16-bit.  A store of 32 bytes by every lane to a row of its own visits 32 lines, two
-// cycles each, 4000 for a tile.  So four lanes first trade 32-byte pieces, two exchanges of half of
-// them, until lane q of the four holds piece q (then q + 4) of all four rows: a store then writes 128
-// bytes each of 8 rows.
-template <bool FP16, int PAIRS>
-__device__ __forceinline__ void store_rows(uint8_t* out, int64_t pitch, const float2 (&acc)[PAIRS], int m, int n, int vec)
-{
-    const int lane = threadIdx.x & 31, q = lane & 3;
-#pragma unroll
-    for (int h = 0; h < PAIRS / 32; ++h) {
-        uint32_t w[4][8];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 v = acc[32 * h + 8 * c + i];
-                w[c][i] = pack2<FP16>(v.x, v.y);
-            }
-#pragma unroll
-        for (int bit = 1; bit <= 2; bit *= 2) {
-            const bool upper = q & bit;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (c & bit) continue;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? w[c][i] : w[c | bit][i], bit);
-                    if (upper) w[c][i] = got;
-                    else w[c | bit][i] = got;
-                }
-            }
-        }
-        const int left = n - (64 * h + 16 * q);   // columns of this lane's pieces that exist
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = (lane & ~3) + r;
-            if (row >= m) break;
-            uint8_t* to = out + row * pitch + 128 * h + 32 * q;
-            if (vec == 2 && left >= 16) {
-                st_v8(to, make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]), make_uint4(w[r][4], w[r][5], w[r][6], w[r][7]));
-            } else if (vec == 1 && left >= 16) {
-                st_v4(to, make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]));
-                st_v4(to + 16, make_uint4(w[r][4], w[r][5], w[r][6], w[r][7]));
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (i < left) reinterpret_cast<uint16_t*>(to)[i] = (uint16_t)(w[r][i / 2] >> (16 * (i & 1)));
-            }
-        }
-    }
-}
-
 // gate * sigmoid(gate) * up, in this order: gate * up could pass FP32's range where the result is far inside.
 // The exponential's argument is split, so that its rounding does not enter (the product with log2 e alone would
 // be off by |gate| units in the exponential's last place).  What stays is that of log2 e to FP32, 1.9e-8 of the
@@ -940,68 +887,13 @@ ep_product_few_kernel(const MatmulArgs p, const __grid_constant__ CUtensorMap ma
     }
 }
 
-// ---- tensor maps
-
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled()
-{
-    static const EncodeTiled fn = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return (EncodeTiled)f;
-    }();
-    return fn;
-}
+// ---- launches
 
 // Map of [rows][K] codes with boxes of box_rows x 128 bytes, swizzled by 128 bytes; elements past either
 // end read as zero codes.
 int make_map(CUtensorMap* m, const char* what, const void* base, int64_t rows, int K, int box_rows)
 {
-    const EncodeTiled encode = encode_tiled();
-    if (!encode) return layer_fail(EP_ERR_CUDA, "ep_matmul_fp8: the driver has no cuTensorMapEncodeTiled");
-    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, pitch[1] = {(cuuint64_t)K};
-    const cuuint32_t box[2] = {kBlockK, (cuuint32_t)box_rows}, step[2] = {1, 1};
-    auto make = [&] {
-        return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, pitch, box, step,
-                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    };
-    CUresult r = make();
-    if (r == CUDA_ERROR_INVALID_CONTEXT) {   // a host thread's first call, which nothing has bound to the device yet
-        int dev = -1;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e == cudaSuccess) e = cudaSetDevice(dev);
-        if (e != cudaSuccess) return layer_cuda(e, "ep_matmul_fp8: binding the host thread to its device");
-        r = make();
-    }
-    if (r != CUDA_SUCCESS) return layer_fail(EP_ERR_CUDA, "ep_matmul_fp8: tensor map of %s: CUresult %d", what, (int)r);
-    return EP_OK;
-}
-
-template <typename... Params, typename... Args>
-cudaError_t launch_cluster(void (*k)(Params...), unsigned grid, int threads, size_t smem, int ctas, cudaStream_t s,
-                           const Args&... args)   // launch_dependent with clusters of `ctas`
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = ctas > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, k, args...);
+    return make_tile_map(m, "ep_matmul_fp8", what, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, K, box_rows, kBlockK, true);
 }
 
 // Tiles, at most, of `rows` rows in groups: every group that holds a row can end inside a tile.

@@ -303,6 +303,199 @@ __device__ __forceinline__ void mma_commit(uint32_t bar)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
 }
 
+// ---- the same by a pair of CTAs (a cluster of two), each holding half of the rows of A and of D and half of B's columns
+//
+// Both CTAs allocate and free; the products are issued by one thread of the first, with the addresses that the operands
+// have in its own shared memory, which are those in the second's too.
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t slot, uint32_t columns)   // one warp of each CTA
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(slot), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+
+__device__ __forceinline__ void tmem_free_pair(uint32_t base, uint32_t columns)    // the same warps
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(base), "r"(columns));
+}
+
+// Shared-memory descriptor of a 16-bit operand that lies along its rows or columns rather than along K: K lines of 64
+// elements, 128 bytes each, swizzled by 128 bytes; groups of 8 lines 1024 bytes apart, the next 64 elements `next` bytes
+// further on.  Stepping 16 along K adds 2048 to the address.
+__device__ __forceinline__ uint64_t mma_descriptor_across(uint32_t addr, uint32_t next)
+{
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(next >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
+}
+
+// Instruction descriptor: FP32 accumulator, BF16 or FP16 A and B, both across K, M x N.
+__host__ __device__ constexpr uint32_t mma_instruction_across(bool fp16, int m, int n)
+{
+    return 1u << 4 | (fp16 ? 0u : 1u << 7 | 1u << 10) | 1u << 15 | 1u << 16 | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
+}
+
+// D = A B over 16 elements of K, plus D unless first.  One thread of the first CTA.
+__device__ __forceinline__ void mma_half_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t instruction, bool first)
+{
+    asm volatile("{ .reg .pred p; setp.eq.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }"
+                 :: "r"(d), "l"(a), "l"(b), "r"(instruction), "r"((uint32_t)first) : "memory");
+}
+
+// Arrive on both CTAs' barriers at this address when every product issued so far by this thread has finished.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 :: "r"(bar), "h"((uint16_t)3) : "memory");
+}
+
+// This thread's writes to shared memory become visible to the asynchronous units.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// Four bytes of global memory into shared memory, asynchronously, and this thread's arrival on a barrier when its copies
+// so far have landed (the barrier counts that arrival).
+__device__ __forceinline__ void copy4(uint32_t to, const void* from)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" :: "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ uint4 smem_load4(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void smem_store4(uint32_t addr, const uint4& v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// 2 * PAIRS consecutive columns, n of which exist, of a warp's 32 rows, m of which exist (row by lane, rows `pitch`
+// bytes apart), 16-bit.  A store of 32 bytes by every lane to a row of its own visits 32 lines, two
+// cycles each, 4000 for a tile.  So four lanes first trade 32-byte pieces, two exchanges of half of
+// them, until lane q of the four holds piece q (then q + 4) of all four rows: a store then writes 128
+// bytes each of 8 rows.
+template <bool FP16, int PAIRS>
+__device__ __forceinline__ void store_rows(uint8_t* out, int64_t pitch, const float2 (&acc)[PAIRS], int m, int n, int vec)
+{
+    const int lane = threadIdx.x & 31, q = lane & 3;
+#pragma unroll
+    for (int h = 0; h < PAIRS / 32; ++h) {
+        uint32_t w[4][8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 v = acc[32 * h + 8 * c + i];
+                w[c][i] = pack2<FP16>(v.x, v.y);
+            }
+#pragma unroll
+        for (int bit = 1; bit <= 2; bit *= 2) {
+            const bool upper = q & bit;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (c & bit) continue;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? w[c][i] : w[c | bit][i], bit);
+                    if (upper) w[c][i] = got;
+                    else w[c | bit][i] = got;
+                }
+            }
+        }
+        const int left = n - (64 * h + 16 * q);   // columns of this lane's pieces that exist
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = (lane & ~3) + r;
+            if (row >= m) break;
+            uint8_t* to = out + row * pitch + 128 * h + 32 * q;
+            if (vec == 2 && left >= 16) {
+                st_v8(to, make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]), make_uint4(w[r][4], w[r][5], w[r][6], w[r][7]));
+            } else if (vec == 1 && left >= 16) {
+                st_v4(to, make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]));
+                st_v4(to + 16, make_uint4(w[r][4], w[r][5], w[r][6], w[r][7]));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (i < left) reinterpret_cast<uint16_t*>(to)[i] = (uint16_t)(w[r][i / 2] >> (16 * (i & 1)));
+            }
+        }
+    }
+}
+
+// ---- host side: tensor maps and cluster launches
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiled encode_tiled()
+{
+    static const EncodeTiled fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return (EncodeTiled)f;
+    }();
+    return fn;
+}
+
+// Map of a dense [rows][columns] array, elements of `size` bytes, with boxes of box_rows x box_columns, swizzled by 128 bytes
+// or not at all; elements past either end read as zeros.
+inline int make_tile_map(CUtensorMap* m, const char* who, const char* what, const void* base, CUtensorMapDataType type, int size,
+                         int64_t rows, int64_t columns, int box_rows, int box_columns, bool swizzled)
+{
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return layer_fail(EP_ERR_CUDA, "%s: the driver has no cuTensorMapEncodeTiled", who);
+    const cuuint64_t dims[2] = {(cuuint64_t)columns, (cuuint64_t)rows}, pitch[1] = {(cuuint64_t)columns * size};
+    const cuuint32_t box[2] = {(cuuint32_t)box_columns, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    auto make = [&] {
+        return encode(m, type, 2, const_cast<void*>(base), dims, pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = make();
+    if (r == CUDA_ERROR_INVALID_CONTEXT) {   // a host thread's first call, which nothing has bound to the device yet
+        int dev = -1;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaSetDevice(dev);
+        if (e != cudaSuccess) {
+            layer_cuda(e, who);
+            return layer_fail(EP_ERR_CUDA, "%s: binding the host thread to its device: %s", who, cudaGetErrorString(e));
+        }
+        r = make();
+    }
+    if (r != CUDA_SUCCESS) return layer_fail(EP_ERR_CUDA, "%s: tensor map of %s: CUresult %d", who, what, (int)r);
+    return EP_OK;
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_cluster(void (*k)(Params...), unsigned grid, int threads, size_t smem, int ctas, cudaStream_t s,
+                           const Args&... args)   // launch_dependent with clusters of `ctas`
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
 #endif  // __CUDACC__
 
 }  // namespace ep

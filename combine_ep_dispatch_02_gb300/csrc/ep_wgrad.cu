@@ -1,0 +1,343 @@
+// ep_wgrad.cu -- gradient of the block-scaled product for its weights, from rows kept as e4m3 codes.
+//
+//   dw[g][n][k] = sum over the rows i of group g of  dy[i][n] * (a[i][k] * a_scales[i][k / 128])
+//
+// on the 16-bit tensor cores: dy as it is, a's values rounded once to dy's type on their way (half a unit of 8 bits, or of
+// 11 with FP16, in each term of a sum in FP32), the result rounded once.  The scales differ from row to row, that is along
+// the sum, so they cannot enter after the product.
+//
+// Both operands lie in memory as rows, and the sum runs over rows: each is read as it lies, lines of 64 columns with K
+// from line to line.  A pair of CTAs makes tiles of 256 columns of dy by 256 of a; each holds 128 columns of either
+// operand and 128 x 256 sums in tensor memory, twice, so that a tile's sums leave while the next is multiplied.  Per CTA:
+// warp 0 loads 64 rows of dy and of codes by TMA, and the rows' scales, into one of kGradStages stages; eight warps make
+// 16-bit values of the codes, in the order that the tensor cores read; warp 1 of the first CTA multiplies for both; four
+// warps write the sums out.
+#include "ep_tcgen05.cuh"
+
+namespace ep {
+namespace {
+
+constexpr int kGradRows = 64;                      // of a stage
+constexpr int kGradHalf = 128;                     // columns of either operand in a CTA
+constexpr int kGradTile = 2 * kGradHalf;
+constexpr int kLineBytes = 8192;                   // 64 columns x 64 rows of 16 bits
+constexpr int kDyBytes = 2 * kLineBytes, kValueBytes = 2 * kLineBytes, kCodeBytes = kGradRows * kGradHalf;
+constexpr int kGradStageBytes = kDyBytes + kValueBytes + kCodeBytes;
+constexpr int kGradStages = 5;
+constexpr int kGradThreads = 512;                  // load, multiply, two idle; four writing, eight converting warps
+constexpr int kWriteWarps = 4, kConvertWarps = 8;
+constexpr int kMaxGradGroups = 4096;
+constexpr size_t kGradShared = 1024 + kGradStages * (kGradStageBytes + kGradRows * 4);
+
+struct GradArgs {
+    const float* a_scales;
+    const int32_t* offsets;   // [groups + 1], or NULL: one group of all rows
+    void* out;
+    int* status;
+    int64_t rows;
+    int groups, columns, inner, kb;
+    int n_tiles, k_tiles;
+    int64_t tiles;
+    int type, vec;            // of out: EP_BF16, EP_FP16 or kFp32; vec as for store_rows
+};
+
+constexpr int kFp32 = -1;
+
+struct GradTile {
+    int g, n0, k0, r0, r1;
+};
+
+__device__ __forceinline__ GradTile grad_tile(const GradArgs& p, int64_t t)
+{
+    GradTile x;
+    const int per = p.n_tiles * p.k_tiles;
+    x.g = (int)(t / per);
+    const int in = (int)(t - (int64_t)x.g * per);
+    x.k0 = in / p.n_tiles * kGradTile;
+    x.n0 = in % p.n_tiles * kGradTile;
+    x.r0 = 0;
+    x.r1 = (int)p.rows;
+    if (p.offsets) {
+        x.r0 = max(0, min(p.offsets[x.g], (int)p.rows));
+        x.r1 = max(x.r0, min(p.offsets[x.g + 1], (int)p.rows));
+    }
+    return x;
+}
+
+__device__ __forceinline__ int grad_steps(const GradTile& x) { return (x.r1 - x.r0 + kGradRows - 1) / kGradRows; }
+
+// 64 columns of a warp's 32 rows of a tile to memory: `m` rows and `n` columns of them exist.
+__device__ __forceinline__ void write_sums(const GradArgs& p, int64_t at, const float2 (&v)[32], int m, int n)
+{
+    if (p.type == kFp32) {
+        float* out = (float*)p.out + at + (int64_t)(threadIdx.x & 31) * p.inner;
+        if ((int)(threadIdx.x & 31) >= m) return;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)   // n is a multiple of 16
+            if (4 * j < n) reinterpret_cast<float4*>(out)[j] = make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
+    } else {
+        uint8_t* out = (uint8_t*)p.out + 2 * at;
+        if (p.type == EP_FP16) store_rows<true, 32>(out, 2 * (int64_t)p.inner, v, m, n, p.vec);
+        else store_rows<false, 32>(out, 2 * (int64_t)p.inner, v, m, n, p.vec);
+    }
+}
+
+template <bool FP16>
+__global__ void __launch_bounds__(kGradThreads, 1)
+ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_a)
+{
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t bars[3 * kGradStages + 5];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int gave_up;
+    const uint32_t stages = (smem_u32(raw) + 1023u) & ~1023u, scales = stages + kGradStages * kGradStageBytes;
+    // loaded: a stage's rows are here; ready (the first CTA's): both CTAs' values are; done: its products are
+    const uint32_t loaded = smem_u32(bars), ready = loaded + 8 * kGradStages, done = ready + 8 * kGradStages,
+                   summed = done + 8 * kGradStages, written = summed + 16, drained = written + 16;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const Giveup giveup{&gave_up, p.status};
+    const int rank = (int)cluster_rank();
+    const int64_t t_first = blockIdx.x / 2, t_step = gridDim.x / 2;
+
+    if (threadIdx.x == 0) {
+        gave_up = 0;
+        for (int i = 0; i < kGradStages; ++i) {
+            bar_init(loaded + 8 * i, 1 + 32);
+            bar_init(ready + 8 * i, 2 * kConvertWarps);
+            bar_init(done + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(summed + 8 * i, 1);
+            bar_init(written + 8 * i, 2 * kWriteWarps);
+        }
+        bar_init(drained, 1);
+        fence_barrier_init();
+        prefetch_map(&map_dy);
+        prefetch_map(&map_a);
+    }
+    if (warp == 1) tmem_alloc_pair(smem_u32(&tmem_slot), 512);
+    follow_predecessor();
+    tmem_fence_before();
+    __syncthreads();
+    cluster_sync();   // the other CTA's barriers exist
+    tmem_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp == 0) {
+        uint32_t n = 0;   // stages filled
+        const bool leader = elect_one();
+        bool ok = true;
+        for (int64_t t = t_first; t < p.tiles && ok; t += t_step) {
+            const GradTile x = grad_tile(p, t);
+            const int n0 = x.n0 + kGradHalf * rank, k0 = x.k0 + kGradHalf * rank;
+            const float* s = p.a_scales + min(k0 / 128, p.kb - 1);
+            const int steps = grad_steps(x);
+            for (int i = 0; i < steps; ++i, ++n) {
+                const uint32_t slot = n % kGradStages, use = n / kGradStages;
+                if (use > 0) ok = __all_sync(0xffffffffu, bar_wait(done + 8 * slot, (use - 1) & 1, giveup));
+                if (n == kWithheldBlock || !ok) { ok = false; break; }
+                const uint32_t dst = stages + slot * kGradStageBytes, bar = loaded + 8 * slot;
+                const int r = x.r0 + kGradRows * i;
+                if (leader) {
+                    bar_expect(bar, kDyBytes + kCodeBytes);
+                    tma_load(dst, &map_dy, n0, r, bar);
+                    tma_load(dst + kLineBytes, &map_dy, n0 + 64, r, bar);
+                    tma_load(dst + kDyBytes + kValueBytes, &map_a, k0, r, bar);
+                }
+                __syncwarp();
+                const uint32_t to = scales + 4 * (slot * kGradRows + lane);
+                if (r + lane < x.r1) copy4(to, s + (int64_t)(r + lane) * p.kb);
+                if (r + lane + 32 < x.r1) copy4(to + 128, s + (int64_t)(r + lane + 32) * p.kb);
+                copies_arrive(bar);
+            }
+        }
+        if (!ok) {   // its loads in flight
+            const long long t0 = clock64();
+            for (uint32_t j = n < kGradStages ? 0 : n - kGradStages; j < n; ++j)
+                bar_drain(loaded + 8 * (j % kGradStages), (j / kGradStages) & 1, t0);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0) {
+            constexpr uint32_t instruction = mma_instruction_across(FP16, kGradTile, kGradTile);
+            const uint64_t a0 = mma_descriptor_across(stages, kLineBytes), b0 = mma_descriptor_across(stages + kDyBytes, kLineBytes);
+            const bool leader = elect_one();
+            uint32_t n = 0, tile = 0;   // stages and tiles with rows
+            bool ok = true;
+            for (int64_t t = t_first; t < p.tiles && ok; t += t_step) {
+                const GradTile x = grad_tile(p, t);
+                const int steps = uniform(grad_steps(x));
+                if (steps == 0) continue;
+                const uint32_t u = tile & 1, d = tmem + u * kGradTile;
+                if (tile >= 2) ok = __all_sync(0xffffffffu, peer_wait(written + 8 * u, (tile / 2 - 1) & 1, giveup));
+                for (int i = 0; i < steps && ok; ++i, ++n) {
+                    const uint32_t slot = n % kGradStages;
+                    ok = __all_sync(0xffffffffu, peer_wait(ready + 8 * slot, (n / kGradStages) & 1, giveup));
+                    if (!ok) break;
+                    if (leader) {
+                        tmem_fence_after();
+                        const int k_steps = min(kGradRows, x.r1 - x.r0 - kGradRows * i + 15) / 16;
+                        const uint32_t at = slot * (kGradStageBytes >> 4);
+#pragma unroll
+                        for (int j = 0; j < kGradRows / 16; ++j)
+                            if (j < k_steps) mma_half_pair(d, a0 + at + 128 * j, b0 + at + 128 * j, instruction, i == 0 && j == 0);
+                        mma_commit_pair(done + 8 * slot);
+                        if (i + 1 == steps) mma_commit_pair(summed + 8 * u);
+                    }
+                    __syncwarp();
+                }
+                ++tile;
+            }
+            if (leader) mma_commit_pair(drained);
+        }
+        // tensor memory is freed, and the second CTA's barriers go, only after the last product has told both
+        if (elect_one()) bar_drain(drained, 0, clock64());
+        __syncwarp();
+    } else if (warp >= 4 && warp < 4 + kWriteWarps) {
+        uint32_t tile = 0;
+        bool ok = true;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        for (int64_t t = t_first; t < p.tiles && ok; t += t_step) {
+            const GradTile x = grad_tile(p, t);
+            const bool some = x.r1 > x.r0;
+            const uint32_t u = tile & 1;
+            if (some) {
+                ok = __all_sync(0xffffffffu, bar_wait(summed + 8 * u, (tile / 2) & 1, giveup));
+                if (!ok) break;
+                tmem_fence_after();
+            }
+            const int row = x.n0 + kGradHalf * rank + (warp & 3) * 32;
+            const int64_t at = ((int64_t)x.g * p.columns + row) * p.inner + x.k0;
+#pragma unroll 1
+            for (int c = 0; c < kGradTile; c += 64) {
+                float2 v[32];
+                if (some) {
+                    uint32_t r[32];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        tmem_load32(r, tmem + lanes + u * kGradTile + c + 32 * h);
+                        tmem_wait(r);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[16 * h + j] = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = make_float2(0.0f, 0.0f);
+                }
+                if (x.k0 + c < p.inner && row < p.columns) write_sums(p, at + c, v, p.columns - row, p.inner - x.k0 - c);
+            }
+            if (some) {
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) peer_arrive(peer_smem(written + 8 * u, 0));
+                ++tile;
+            }
+        }
+    } else if (warp >= 8) {
+        const int w = warp - 8, row = 4 * w + lane / 8, piece = lane & 7;   // 16 codes of rows `row` and `row` + 32
+        const uint32_t to0 = (uint32_t)(kDyBytes + piece / 4 * kLineBytes);
+        const uint32_t arrive = peer_smem(ready, 0);
+        uint32_t n = 0;
+        bool ok = true;
+        for (int64_t t = t_first; t < p.tiles && ok; t += t_step) {
+            const GradTile x = grad_tile(p, t);
+            const int steps = grad_steps(x);
+            for (int i = 0; i < steps; ++i, ++n) {
+                const uint32_t slot = n % kGradStages, stage = stages + slot * kGradStageBytes;
+                ok = __all_sync(0xffffffffu, bar_wait(loaded + 8 * slot, (n / kGradStages) & 1, giveup));
+                if (!ok) break;
+                const int left = x.r1 - x.r0 - kGradRows * i;   // rows of this stage that are the group's
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = row + 32 * h;
+                    const uint4 c = smem_load4(stage + kDyBytes + kValueBytes + r * kGradHalf + 16 * piece);
+                    const float s = smem_load(scales + 4 * (slot * kGradRows + r));
+                    const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+                    uint32_t v[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 lo = mul2(e4m3x2_to_float2(word[j] & 0xFFFFu), both(s));
+                        const float2 hi = mul2(e4m3x2_to_float2(word[j] >> 16), both(s));
+                        v[2 * j] = r < left ? pack2<FP16>(lo.x, lo.y) : 0u;
+                        v[2 * j + 1] = r < left ? pack2<FP16>(hi.x, hi.y) : 0u;
+                    }
+                    const uint32_t to = stage + to0 + r * 128, at = 2 * (piece & 3), swap = r & 7;
+                    smem_store4(to + ((at ^ swap) << 4), make_uint4(v[0], v[1], v[2], v[3]));
+                    smem_store4(to + (((at + 1) ^ swap) << 4), make_uint4(v[4], v[5], v[6], v[7]));
+                }
+                // the rest of the last 16 rows that are multiplied: dy's rows there are another group's
+                if (left < kGradRows) {
+                    const int r = left + (int)(threadIdx.x - 256) / 16, q = threadIdx.x & 15;
+                    if (r < (left + 15) / 16 * 16) smem_store4(stage + q / 8 * kLineBytes + r * 128 + 16 * (q & 7), make_uint4(0, 0, 0, 0));
+                }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) peer_arrive(arrive + 8 * slot);
+            }
+        }
+    }
+    tmem_fence_before();
+    __syncthreads();
+    cluster_sync();   // no product, arrival or read of the pair's memory is under way
+    if (warp == 1) {
+        tmem_fence_after();
+        tmem_free_pair(tmem, 512);
+    }
+}
+
+template <bool FP16>
+cudaError_t launch_gradient(const GradArgs& p, const CUtensorMap& dy, const CUtensorMap& a, int sms, cudaStream_t s)
+{
+    const cudaError_t e = allow_all_shared<ep_weight_gradient_kernel<FP16>>();
+    if (e != cudaSuccess) return e;
+    const int64_t pairs = p.tiles < sms / 2 ? p.tiles : sms / 2;
+    return launch_cluster(ep_weight_gradient_kernel<FP16>, (unsigned)(2 * pairs), kGradThreads, kGradShared, 2, s, p, dy, a);
+}
+
+}  // namespace
+}  // namespace ep
+
+extern "C" int ep_matmul_fp8_weight_gradient(const void* dy, int dtype, const void* a, const float* a_scales,
+                                             const int32_t* offsets, int64_t rows, int groups, int columns, int inner,
+                                             int out_fp32, void* dw, int32_t* device_status, void* stream)
+{
+    using namespace ep;
+    const char* who = "ep_matmul_fp8_weight_gradient";
+    if (rows < 0 || rows > INT32_MAX - kGradRows)
+        return layer_fail(EP_ERR_ARG, "%s: rows=%lld outside 0..2^31-1-%d", who, (long long)rows, kGradRows);
+    if (groups < 1 || groups > kMaxGradGroups || (!offsets && groups != 1))
+        return layer_fail(EP_ERR_ARG, "%s: groups=%d outside 1..%d, or several without offsets", who, groups, kMaxGradGroups);
+    if (inner < 16 || inner % 16 != 0 || inner > 1 << 20)
+        return layer_fail(EP_ERR_ARG, "%s: inner=%d is not a multiple of 16 in 16..2^20", who, inner);
+    if (columns < 8 || columns % 8 != 0 || columns > 1 << 20)
+        return layer_fail(EP_ERR_ARG, "%s: columns=%d is not a multiple of 8 in 8..2^20", who, columns);
+    if (dtype != EP_BF16 && dtype != EP_FP16)
+        return layer_fail(EP_ERR_ARG, "%s: dtype=%d is neither EP_BF16 nor EP_FP16", who, dtype);
+    if (!layer_aligned(device_status, 4))
+        return layer_fail(EP_ERR_ARG, "%s: device_status is NULL or not 4-byte aligned", who);
+    if (!layer_aligned(dw, 16)) return layer_fail(EP_ERR_ARG, "%s: dw is NULL or not 16-byte aligned", who);
+    if (offsets && !layer_aligned(offsets, 4)) return layer_fail(EP_ERR_ARG, "%s: offsets is not 4-byte aligned", who);
+    cudaStream_t s = (cudaStream_t)stream;
+    if (rows == 0)   // no row in any group
+        return layer_cuda(cudaMemsetAsync(dw, 0, (size_t)groups * columns * inner * (out_fp32 ? 4 : 2), s), who);
+    if (!layer_aligned(dy, 16) || !layer_aligned(a, 16) || !layer_aligned(a_scales, 4))
+        return layer_fail(EP_ERR_ARG, "%s: dy, a or a_scales is NULL or misaligned", who);
+    GradArgs p{};
+    p.a_scales = a_scales; p.offsets = offsets; p.out = dw; p.status = device_status; p.rows = rows; p.groups = groups;
+    p.columns = columns; p.inner = inner; p.kb = (inner + 127) / 128;
+    p.n_tiles = (columns + kGradTile - 1) / kGradTile; p.k_tiles = (inner + kGradTile - 1) / kGradTile;
+    p.tiles = (int64_t)groups * p.n_tiles * p.k_tiles;
+    p.type = out_fp32 ? kFp32 : dtype;
+    p.vec = layer_aligned(dw, 32) ? 2 : 1;
+    const int sms = layer_num_sms();
+    if (sms < 2) return layer_fail(EP_ERR_CUDA, "%s: cannot tell the current device's multiprocessors", who);
+    CUtensorMap m_dy, m_a;
+    const bool fp16 = dtype == EP_FP16;
+    if (int rc = make_tile_map(&m_dy, who, "dy", dy, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                               rows, columns, kGradRows, 64, true))
+        return rc;
+    if (int rc = make_tile_map(&m_a, who, "a", a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, inner, kGradRows, kGradHalf, false))
+        return rc;
+    const cudaError_t e = fp16 ? launch_gradient<true>(p, m_dy, m_a, sms, s) : launch_gradient<false>(p, m_dy, m_a, sms, s);
+    return layer_cuda(e, "ep_matmul_fp8_weight_gradient: launch");
+}

@@ -5,6 +5,7 @@
 * ``sort_by_expert``, ``sorted_rows``, ``return_rows`` and the gradients ``sorted_rows_backward`` and
   ``return_rows_backward``: received rows in compact expert order, and back with routing weights;
 * ``matmul_fp8`` and ``matmul_fp8_swiglu``: the block-scaled e4m3 product, dense or by expert;
+* ``matmul_fp8_weight_gradient``: the product's gradient for its weights, from rows kept as e4m3;
 * ``moe_few_rows``: the whole layer for a few rows, without a sort;
 * ``rms_norm_join`` and its gradient: the norm after a block, its gate, the scaled residual and the norm before the
   next block;
@@ -43,7 +44,7 @@ _OUT_CODES = {"bf16": EP_BF16, "fp16": EP_FP16}
 _BOUND = ("ep_rms_norm_fp8", "ep_sort_workspace_bytes", "ep_sort_by_expert", "ep_sorted_rows", "ep_return_rows",
           "ep_return_rows_backward", "ep_matmul_fp8", "ep_rms_norm_join", "ep_rms_norm_join_workspace_bytes",
           "ep_rms_norm_join_backward", "ep_swiglu_saved", "ep_swiglu_saved_backward", "ep_moe_few_workspace_bytes",
-          "ep_moe_few_rows", "ep_strerror", "ep_last_error")
+          "ep_moe_few_rows", "ep_matmul_fp8_weight_gradient", "ep_strerror", "ep_last_error")
 _status_words = {}
 _binding = None
 _bound_to = None
@@ -191,6 +192,20 @@ def matmul_fp8_swiglu(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, 
     scales [rows][ceil(columns/256)]), the a and a_scales of a following matmul_fp8.  Arguments as
     matmul_fp8; columns must be a multiple of 32."""
     return _on(stream, _native().matmul_fp8, a, a_scales, b, b_scales, offsets, EP_FP8_E4M3)
+
+
+def matmul_fp8_weight_gradient(dy: torch.Tensor, a: torch.Tensor, a_scales: torch.Tensor,
+                               offsets: Optional[torch.Tensor] = None, out_dtype: Optional[str] = None,
+                               stream=None) -> torch.Tensor:
+    """Gradient of matmul_fp8 for b: dy^T @ (a * a_scales), by group if offsets are given.  dy [rows][columns] BF16 or FP16,
+    columns a multiple of 8; a, a_scales and offsets as there.  Returns [columns][inner], or [groups][columns][inner] with
+    zeros for a group without rows, of dy's type or, with out_dtype "fp32", FP32.  a's values are rounded once to dy's
+    type; products and sums are FP32.  The gradient for a is a ``matmul_fp8`` of dy's codes with the transposed weights,
+    whose 128 x 128 blocks keep their scales."""
+    if out_dtype is not None and out_dtype != "fp32" and out_dtype not in _OUT_CODES:
+        raise EpError(EP_ERR_ARG, f"out_dtype={out_dtype!r} is none of 'bf16', 'fp16' and 'fp32'")
+    return _on(stream, _native().matmul_fp8_weight_gradient, dy, a, a_scales, offsets, _OUT_CODES.get(out_dtype, -1),
+               out_dtype == "fp32")
 
 
 def moe_few_rows(x: torch.Tensor, x_scales: Optional[torch.Tensor], indices: torch.Tensor, weights: torch.Tensor,

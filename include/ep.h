@@ -527,6 +527,22 @@ int ep_swiglu_saved_backward(const void* saved, const float* saved_scales, const
                              void* stream);
 
 /*
+ * Gradient of ep_matmul_fp8 for b, from its rows kept as e4m3 codes:
+ *   dw[g][n][k] = sum over the rows i of group g of dy[i][n] * (a[i][k] * a_scales[i][k/128])
+ *   dy           [rows][columns] of dtype (EP_BF16 or EP_FP16), dense, 16-byte aligned; columns a multiple of 8
+ *   a, a_scales, offsets, rows, groups, inner  as ep_matmul_fp8 takes them
+ *   dw           [groups][columns][inner] of dtype, or FP32 if out_fp32 is not 0; 16-byte aligned; zeros for a group without
+ *                rows
+ * The values a * a_scale are rounded once to dtype (with EP_FP16 those past 65504 become infinite), products and sums are
+ * FP32, in an order that the shapes and offsets fix, and dw is rounded once.  A bounded wait that runs out on the GPU is
+ * recorded as EP_ERR_DEVICE_TIMEOUT; dw is then not valid.  The first call on a device looks up a driver entry point and
+ * should come before any stream capture.
+ */
+int ep_matmul_fp8_weight_gradient(const void* dy, int dtype, const void* a, const float* a_scales, const int32_t* offsets,
+                                  int64_t rows, int groups, int columns, int inner, int out_fp32, void* dw,
+                                  int32_t* device_status, void* stream);
+
+/*
  * A whole expert layer for a few rows, in two kernels: for each row the sum, over the experts that it names, of
  * weight * down[e] (gate * sigmoid(gate) * up), [gate; up] = up[e] x.
  *   x            [rows][hidden], 16-byte aligned: e4m3 codes (x_dtype EP_FP8_E4M3) with x_scales [rows][ceil(hidden/128)], or

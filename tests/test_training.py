@@ -18,6 +18,8 @@ BWD = dict(h=P, post=P, pre=P, dh=P, dhs=256, dn=P, dns=256, dy=P, dres=P, dpost
 SAVE = dict(x=P, stride=512, dtype=ep.EP_BF16, rows=4, inner=256, end=None, q=P, s=P, saved=P, ss=P, stream=None)
 BACK = dict(saved=P, ss=P, dz=P, stride=256, dtype=ep.EP_BF16, rows=4, inner=256, end=None, d=P, q=None, s=None, stream=None)
 
+GRAD = dict(dy=P, dtype=ep.EP_BF16, a=P, s=P, offsets=None, rows=64, groups=1, columns=128, inner=256, fp32=0, dw=P, status=P,
+            stream=None)
 FEW = dict(x=P, xs=P, xd=ep.EP_FP8_E4M3, idx=P, w=P, rows=4, k=2, first=0, experts=8, hidden=256, inner=128, up=P, ups=P, down=P,
            downs=P, od=ep.EP_BF16, out=P, ws=P, wsb=1 << 40, stream=None)
 
@@ -81,6 +83,17 @@ def test_swiglu_backward_refusals(lib, change, word):  # noqa: F811
 
 
 @pytest.mark.parametrize("change,word", [
+    (dict(rows=-1), "rows"), (dict(rows=(1 << 31) - 64), "rows"), (dict(groups=0), "groups"), (dict(groups=2), "groups"),
+    (dict(groups=4097, offsets=P), "groups"), (dict(inner=0), "inner"), (dict(inner=24), "inner"),
+    (dict(inner=(1 << 20) + 16), "inner"), (dict(columns=0), "columns"), (dict(columns=12), "columns"),
+    (dict(columns=(1 << 20) + 8), "columns"), (dict(dtype=2), "dtype"), (dict(status=None), "device_status"),
+    (dict(dw=None), "dw"), (dict(dw=P + 8), "dw"), (dict(offsets=P + 2), "offsets"), (dict(dy=P + 8), "dy, a"),
+    (dict(a=None), "dy, a"), (dict(s=P + 2), "a_scales")])
+def test_weight_gradient_refusals(lib, change, word):  # noqa: F811
+    _refused(lib, lib.ep_matmul_fp8_weight_gradient(*{**GRAD, **change}.values()), "ep_matmul_fp8_weight_gradient", word)
+
+
+@pytest.mark.parametrize("change,word", [
     (dict(rows=-1), "rows"), (dict(rows=129), "rows"), (dict(k=0), "topk"), (dict(rows=128, k=33), "topk"),
     (dict(k=2 ** 31 - 1), "topk"), (dict(experts=0), "experts"), (dict(experts=1025), "experts"), (dict(hidden=0), "hidden"),
     (dict(hidden=24), "hidden"), (dict(hidden=(1 << 20) + 16), "hidden"), (dict(inner=0), "inner"), (dict(inner=40), "inner"),
@@ -110,7 +123,7 @@ def test_binding_takes_cuda_tensors_only(lib):  # noqa: F811
     x = torch.zeros(4, 256, dtype=torch.bfloat16)
     for call in (lambda: ep.rms_norm_join(x, x), lambda: ep.rms_norm_join_backward(ep.Joined(x), x, dh=x),
                  lambda: ep.swiglu_saved(x), lambda: ep.swiglu_saved_backward(x, x, x),
-                 lambda: ep.moe_few_rows(x, None, x, x, x, x, x, x)):
+                 lambda: ep.moe_few_rows(x, None, x, x, x, x, x, x), lambda: ep.matmul_fp8_weight_gradient(x, x, x)):
         with pytest.raises(ep.EpError) as e:
             call()
         assert e.value.code == ep.EP_ERR_ARG and "not a CUDA device" in str(e.value)
@@ -118,7 +131,15 @@ def test_binding_takes_cuda_tensors_only(lib):  # noqa: F811
         ep.rms_norm_join([1.0], x)
 
 
-@pytest.mark.parametrize("name,kernels", [("ep_join.cu", 4), ("ep_swiglu.cu", 2)])
+def test_out_types_are_named(lib):  # noqa: F811
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    with pytest.raises(ep.EpError, match="out_dtype"):
+        ep.matmul_fp8_weight_gradient(x, x, x, out_dtype="fp64")
+    with pytest.raises(ep.EpError, match="out_dtype"):
+        ep.moe_few_rows(x, None, x, x, x, x, x, x, out_dtype="fp32")
+
+
+@pytest.mark.parametrize("name,kernels", [("ep_join.cu", 4), ("ep_swiglu.cu", 2), ("ep_wgrad.cu", 1)])
 def test_kernels_read_no_memory_before_their_own_wait(name, kernels):
     """As in test_experts.py: before follow_predecessor() no kernel names an array of its arguments."""
     import re
@@ -134,4 +155,4 @@ def test_kernels_read_no_memory_before_their_own_wait(name, kernels):
     for body in bodies:
         before, wait, _ = body.partition("follow_predecessor();")
         assert wait
-        assert not set(re.findall(r"\ba\.(\w+)", before)) & arrays, (name, before[-300:])
+        assert not set(re.findall(r"\b[ap]\.(\w+)", before)) & (arrays - {"status"}), (name, before[-300:])

@@ -335,3 +335,108 @@ def test_swiglu_strides_extremes_and_no_rows():
     lost = torch.zeros(256, dtype=torch.bool, device=DEV)
     lost[5] = lost[133] = True                # both gradients at a gate that is not a number have it as a factor
     assert torch.isfinite(d[0]).all() and torch.equal(torch.isnan(d[1]), lost)
+
+
+# ------------------------------------------------------------------------------------------- weights
+
+def _gradient_inputs(g, rows, columns, inner, t):
+    a, s, _, _ = ep.rms_norm_fp8(_randn(g, rows, inner).to(torch.bfloat16), 1 + 0.2 * _randn(g, inner))
+    return _randn(g, rows, columns).to(t), a, s * torch.rand(s.shape, generator=g, device=DEV)
+
+
+def _check_gradient(dy, a, s, offsets=None, out_dtype=None):
+    t, rows = dy.dtype, dy.shape[0]
+    got = ep.matmul_fp8_weight_gradient(dy, a, s, offsets=offsets, out_dtype=out_dtype)
+    edges = [0, rows] if offsets is None else offsets.tolist()
+    assert got.shape == ((len(edges) - 1,) if offsets is not None else ()) + (dy.shape[1], a.shape[1])
+    for i, (lo, hi) in enumerate(zip(edges[:-1], edges[1:])):
+        out = got if offsets is None else got[i]
+        if hi <= lo:
+            assert not out.any()
+            continue
+        d, v = dy[lo:hi].double(), _values(a[lo:hi], s[lo:hi])
+        want = d.T @ v
+        # each value's rounding to dy's type (FP16's smallest step is 2^-24), and the sum in FP32
+        per = v.abs() * (2.0 ** -8 if t == torch.bfloat16 else 2.0 ** -11) + (2.0 ** -25 if t == torch.float16 else 0.0)
+        bound = d.abs().T @ (per * (1 + 2.0 ** -10) + 2 * U * (hi - lo + 8) * v.abs())
+        half = _half_bound(out.dtype, want) if out.dtype != torch.float32 else U * want.abs()
+        _within(out, want, half + bound * 1.01, f"group {i}")
+    return got
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows,columns,inner", [(64, 256, 256), (128, 128, 128), (1, 8, 16), (16, 256, 256), (63, 264, 272),
+                                                (65, 8, 1040), (300, 520, 144), (1000, 1024, 512), (777, 2056, 16),
+                                                (4099, 136, 2064)])
+def test_weight_gradient(rows, columns, inner, dtype):
+    g = _gen(rows + columns + inner)
+    dy, a, s = _gradient_inputs(g, rows, columns, inner, HALF[dtype])
+    _check_gradient(dy, a, s)
+    _check_gradient(dy, a, s, out_dtype="fp32")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("columns,inner,edges", [
+    (264, 272, [0, 1, 1, 65, 128, 128, 400, 419]), (512, 256, [0, 0, 0, 33]), (128, 1040, [5, 64, 200, 200]),
+    (1024, 2048, [0, 64, 192, 448, 449, 1000]), (8, 16, list(range(0, 260, 4)))])
+def test_weight_gradient_by_group(columns, inner, edges, dtype):
+    g, rows = _gen(columns + inner), edges[-1] + 7
+    dy, a, s = _gradient_inputs(g, rows, columns, inner, HALF[dtype])
+    # rows outside every group, and what is not a number next to a group's rows, do not enter
+    dy[edges[-1]:] = float("nan")
+    a.view(torch.uint8)[edges[-1]:] = 0x7F
+    dy[:edges[0]] = float("inf")
+    offsets = torch.tensor(edges, dtype=torch.int32, device=DEV)
+    got = _check_gradient(dy, a, s, offsets)
+    for _ in range(3):
+        assert torch.equal(ep.matmul_fp8_weight_gradient(dy, a, s, offsets=offsets), got)
+    poisoned, last = dy.clone(), len(edges) - 2
+    if edges[-1] > edges[-2]:
+        poisoned[edges[-2]:] = float("nan")
+        other = ep.matmul_fp8_weight_gradient(poisoned, a, s, offsets=offsets)
+        assert torch.equal(other[:last], got[:last]) and torch.isnan(other[last]).all()
+
+
+def test_weight_gradient_of_no_rows_and_of_offsets_outside_the_buffer():
+    g = _gen(12)
+    dy, a, s = _gradient_inputs(g, 40, 64, 128, torch.bfloat16)
+    offsets = torch.zeros(4, dtype=torch.int32, device=DEV)
+    assert ep.matmul_fp8_weight_gradient(dy[:0], a[:0], s[:0], offsets=offsets).shape == (3, 64, 128)
+    assert not ep.matmul_fp8_weight_gradient(dy, a, s, offsets=offsets).any()
+    assert not ep.matmul_fp8_weight_gradient(dy[:0], a[:0], s[:0]).any()
+    wide = torch.tensor([-9, 20, 10, 99], dtype=torch.int32, device=DEV)     # held inside; a group that ends before it starts
+    got = ep.matmul_fp8_weight_gradient(dy, a, s, offsets=wide)
+    held = torch.tensor([0, 20, 20, 40], dtype=torch.int32, device=DEV)
+    want = ep.matmul_fp8_weight_gradient(dy, a, s, offsets=held)
+    assert torch.equal(got[:2], want[:2])
+    assert torch.equal(got[2], ep.matmul_fp8_weight_gradient(dy[10:].contiguous(), a[10:].contiguous(), s[10:].contiguous()))
+
+
+def test_weight_gradient_with_many_tiles_to_a_pair():
+    """More tiles than pairs of CTAs, groups of no and of few rows among them: both accumulators are used again."""
+    g = _gen(13)
+    counts = torch.randint(0, 150, (64,), generator=g, device=DEV)
+    counts[::7] = 0
+    offsets = torch.cat([counts.new_zeros(1), counts.cumsum(0)]).int()
+    dy, a, s = _gradient_inputs(g, int(offsets[-1]), 640, 528, torch.bfloat16)
+    _check_gradient(dy, a, s, offsets)
+
+
+def test_weight_gradient_on_a_stream_and_in_a_graph():
+    g = _gen(14)
+    dy, a, s = _gradient_inputs(g, 200, 256, 384, torch.bfloat16)
+    offsets = torch.tensor([0, 77, 200], dtype=torch.int32, device=DEV)
+    want = ep.matmul_fp8_weight_gradient(dy, a, s, offsets=offsets)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = ep.matmul_fp8_weight_gradient(dy, a, s, offsets=offsets, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = ep.matmul_fp8_weight_gradient(dy, a, s, offsets=offsets)
+    graph.replay()
+    assert torch.equal(out, want)
+    dy.mul_(2)
+    graph.replay()
+    assert torch.equal(out, 2 * want)
