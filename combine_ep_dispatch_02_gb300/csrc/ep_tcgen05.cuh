@@ -349,8 +349,16 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar)
                  :: "r"(bar), "h"((uint16_t)3) : "memory");
 }
 
+// Arrive on a barrier of the pair's first CTA.  Ordered within this CTA alone, a thousand cycles cheaper than for the
+// cluster: what it announces is this CTA's shared or tensor memory, written before fence_async() or read before
+// tmem_fence_before(), which the tensor cores use where it lies.
+__device__ __forceinline__ void pair_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+
 // This thread's writes to shared memory become visible to the asynchronous units.
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Four bytes of global memory into shared memory, asynchronously, and this thread's arrival on a barrier when its copies
 // so far have landed (the barrier counts that arrival).

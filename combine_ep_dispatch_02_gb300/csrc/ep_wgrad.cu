@@ -24,8 +24,11 @@ constexpr int kLineBytes = 8192;                   // 64 columns x 64 rows of 16
 constexpr int kDyBytes = 2 * kLineBytes, kValueBytes = 2 * kLineBytes, kCodeBytes = kGradRows * kGradHalf;
 constexpr int kGradStageBytes = kDyBytes + kValueBytes + kCodeBytes;
 constexpr int kGradStages = 5;
-constexpr int kGradThreads = 512;                  // load, multiply, two idle; four writing, eight converting warps
-constexpr int kWriteWarps = 4, kConvertWarps = 8;
+constexpr int kWriteWarps = 4;
+// Warps that convert a stage.  Each stage has a team of its own: a barrier's parity tells one phase from the next alone, so
+// whoever waits for a stage's phase has to have seen the one before.
+constexpr int kConvertTeam = 4;
+constexpr int kGradThreads = 32 * (4 + kWriteWarps + kGradStages * kConvertTeam);   // load, multiply, two idle, write, convert
 constexpr int kMaxGradGroups = 4096;
 constexpr size_t kGradShared = 1024 + kGradStages * (kGradStageBytes + kGradRows * 4);
 
@@ -103,7 +106,7 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
         gave_up = 0;
         for (int i = 0; i < kGradStages; ++i) {
             bar_init(loaded + 8 * i, 1 + 32);
-            bar_init(ready + 8 * i, 2 * kConvertWarps);
+            bar_init(ready + 8 * i, 2 * kConvertTeam);
             bar_init(done + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -169,10 +172,10 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
                 const int steps = uniform(grad_steps(x));
                 if (steps == 0) continue;
                 const uint32_t u = tile & 1, d = tmem + u * kGradTile;
-                if (tile >= 2) ok = __all_sync(0xffffffffu, peer_wait(written + 8 * u, (tile / 2 - 1) & 1, giveup));
+                if (tile >= 2) ok = __all_sync(0xffffffffu, bar_wait(written + 8 * u, (tile / 2 - 1) & 1, giveup));
                 for (int i = 0; i < steps && ok; ++i, ++n) {
                     const uint32_t slot = n % kGradStages;
-                    ok = __all_sync(0xffffffffu, peer_wait(ready + 8 * slot, (n / kGradStages) & 1, giveup));
+                    ok = __all_sync(0xffffffffu, bar_wait(ready + 8 * slot, (n / kGradStages) & 1, giveup));
                     if (!ok) break;
                     if (leader) {
                         tmem_fence_after();
@@ -229,12 +232,13 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
             if (some) {
                 tmem_fence_before();
                 __syncwarp();
-                if (lane == 0) peer_arrive(peer_smem(written + 8 * u, 0));
+                if (lane == 0) pair_arrive(peer_smem(written + 8 * u, 0));
                 ++tile;
             }
         }
     } else if (warp >= 8) {
-        const int w = warp - 8, row = 4 * w + lane / 8, piece = lane & 7;   // 16 codes of rows `row` and `row` + 32
+        const int team = (warp - 8) / kConvertTeam, thread = (int)(threadIdx.x - 256) % (32 * kConvertTeam);
+        const int row = thread / 8, piece = lane & 7;   // 16 codes of every (4 * kConvertTeam)th row from `row` on
         const uint32_t to0 = (uint32_t)(kDyBytes + piece / 4 * kLineBytes);
         const uint32_t arrive = peer_smem(ready, 0);
         uint32_t n = 0;
@@ -243,21 +247,29 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
             const GradTile x = grad_tile(p, t);
             const int steps = grad_steps(x);
             for (int i = 0; i < steps; ++i, ++n) {
-                const uint32_t slot = n % kGradStages, stage = stages + slot * kGradStageBytes;
+                const uint32_t slot = n % kGradStages;
+                if (slot != (uint32_t)team) continue;
+                const uint32_t stage = stages + slot * kGradStageBytes;
                 ok = __all_sync(0xffffffffu, bar_wait(loaded + 8 * slot, (n / kGradStages) & 1, giveup));
                 if (!ok) break;
                 const int left = x.r1 - x.r0 - kGradRows * i;   // rows of this stage that are the group's
+                constexpr int kTimes = kGradRows / (4 * kConvertTeam);
+                uint4 c[kTimes];
+                float s[kTimes];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = row + 32 * h;
-                    const uint4 c = smem_load4(stage + kDyBytes + kValueBytes + r * kGradHalf + 16 * piece);
-                    const float s = smem_load(scales + 4 * (slot * kGradRows + r));
-                    const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+                for (int h = 0; h < kTimes; ++h) {
+                    c[h] = smem_load4(stage + kDyBytes + kValueBytes + (row + 4 * kConvertTeam * h) * kGradHalf + 16 * piece);
+                    s[h] = smem_load(scales + 4 * (slot * kGradRows + row + 4 * kConvertTeam * h));
+                }
+#pragma unroll
+                for (int h = 0; h < kTimes; ++h) {
+                    const int r = row + 4 * kConvertTeam * h;
+                    const uint32_t word[4] = {c[h].x, c[h].y, c[h].z, c[h].w};
                     uint32_t v[8];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float2 lo = mul2(e4m3x2_to_float2(word[j] & 0xFFFFu), both(s));
-                        const float2 hi = mul2(e4m3x2_to_float2(word[j] >> 16), both(s));
+                        const float2 lo = mul2(e4m3x2_to_float2(word[j] & 0xFFFFu), both(s[h]));
+                        const float2 hi = mul2(e4m3x2_to_float2(word[j] >> 16), both(s[h]));
                         v[2 * j] = r < left ? pack2<FP16>(lo.x, lo.y) : 0u;
                         v[2 * j + 1] = r < left ? pack2<FP16>(hi.x, hi.y) : 0u;
                     }
@@ -267,12 +279,13 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
                 }
                 // the rest of the last 16 rows that are multiplied: dy's rows there are another group's
                 if (left < kGradRows) {
-                    const int r = left + (int)(threadIdx.x - 256) / 16, q = threadIdx.x & 15;
-                    if (r < (left + 15) / 16 * 16) smem_store4(stage + q / 8 * kLineBytes + r * 128 + 16 * (q & 7), make_uint4(0, 0, 0, 0));
+                    const int q = thread & 15, end = (left + 15) / 16 * 16;
+                    for (int r = left + thread / 16; r < end; r += 2 * kConvertTeam)
+                        smem_store4(stage + q / 8 * kLineBytes + r * 128 + 16 * (q & 7), make_uint4(0, 0, 0, 0));
                 }
                 fence_async();
                 __syncwarp();
-                if (lane == 0) peer_arrive(arrive + 8 * slot);
+                if (lane == 0) pair_arrive(arrive + 8 * slot);
             }
         }
     }
