@@ -383,15 +383,50 @@ __device__ __forceinline__ void smem_store4(uint32_t addr, const uint4& v)
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// 2 * PAIRS consecutive columns, n of which exist, of a warp's 32 rows, m of which exist (row by lane, rows `pitch`
-// bytes apart), 16-bit.  A store of 32 bytes by every lane to a row of its own visits 32 lines, two
-// cycles each, 4000 for a tile.  So four lanes first trade 32-byte pieces, two exchanges of half of
-// them, until lane q of the four holds piece q (then q + 4) of all four rows: a store then writes 128
-// bytes each of 8 rows.
+// 64 consecutive columns, n of which exist, of a warp's 32 rows, m of which exist (row by lane, rows `pitch` bytes
+// apart), 16-bit: w holds a lane's row in 32-byte pieces.  A store of 32 bytes by every lane to a row of its own visits 32
+// lines, two cycles each, 4000 for a tile.  So four lanes first trade the pieces, two exchanges of half of
+// them, until lane q of the four holds piece q of all four rows: a store then writes 128 bytes each of 8 rows.
+__device__ __forceinline__ void store_lines(uint8_t* out, int64_t pitch, uint32_t (&w)[4][8], int m, int n, int vec)
+{
+    const int lane = threadIdx.x & 31, q = lane & 3;
+#pragma unroll
+    for (int bit = 1; bit <= 2; bit *= 2) {
+        const bool upper = q & bit;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (c & bit) continue;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? w[c][i] : w[c | bit][i], bit);
+                if (upper) w[c][i] = got;
+                else w[c | bit][i] = got;
+            }
+        }
+    }
+    const int left = n - 16 * q;   // columns of this lane's pieces that exist
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int row = (lane & ~3) + r;
+        if (row >= m) break;
+        uint8_t* to = out + row * pitch + 32 * q;
+        if (vec == 2 && left >= 16) {
+            st_v8(to, make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]), make_uint4(w[r][4], w[r][5], w[r][6], w[r][7]));
+        } else if (vec == 1 && left >= 16) {
+            st_v4(to, make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]));
+            st_v4(to + 16, make_uint4(w[r][4], w[r][5], w[r][6], w[r][7]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (i < left) reinterpret_cast<uint16_t*>(to)[i] = (uint16_t)(w[r][i / 2] >> (16 * (i & 1)));
+        }
+    }
+}
+
+// The same for 2 * PAIRS columns that are still FP32.
 template <bool FP16, int PAIRS>
 __device__ __forceinline__ void store_rows(uint8_t* out, int64_t pitch, const float2 (&acc)[PAIRS], int m, int n, int vec)
 {
-    const int lane = threadIdx.x & 31, q = lane & 3;
 #pragma unroll
     for (int h = 0; h < PAIRS / 32; ++h) {
         uint32_t w[4][8];
@@ -402,37 +437,7 @@ __device__ __forceinline__ void store_rows(uint8_t* out, int64_t pitch, const fl
                 const float2 v = acc[32 * h + 8 * c + i];
                 w[c][i] = pack2<FP16>(v.x, v.y);
             }
-#pragma unroll
-        for (int bit = 1; bit <= 2; bit *= 2) {
-            const bool upper = q & bit;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (c & bit) continue;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? w[c][i] : w[c | bit][i], bit);
-                    if (upper) w[c][i] = got;
-                    else w[c | bit][i] = got;
-                }
-            }
-        }
-        const int left = n - (64 * h + 16 * q);   // columns of this lane's pieces that exist
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = (lane & ~3) + r;
-            if (row >= m) break;
-            uint8_t* to = out + row * pitch + 128 * h + 32 * q;
-            if (vec == 2 && left >= 16) {
-                st_v8(to, make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]), make_uint4(w[r][4], w[r][5], w[r][6], w[r][7]));
-            } else if (vec == 1 && left >= 16) {
-                st_v4(to, make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]));
-                st_v4(to + 16, make_uint4(w[r][4], w[r][5], w[r][6], w[r][7]));
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (i < left) reinterpret_cast<uint16_t*>(to)[i] = (uint16_t)(w[r][i / 2] >> (16 * (i & 1)));
-            }
-        }
+        store_lines(out + 128 * h, pitch, w, m, n - 64 * h, vec);
     }
 }
 

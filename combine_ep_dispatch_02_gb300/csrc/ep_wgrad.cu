@@ -9,9 +9,9 @@
 // Both operands lie in memory as rows, and the sum runs over rows: each is read as it lies, lines of 64 columns with K
 // from line to line.  A pair of CTAs makes tiles of 256 columns of dy by 256 of a; each holds 128 columns of either
 // operand and 128 x 256 sums in tensor memory, twice, so that a tile's sums leave while the next is multiplied.  Per CTA:
-// warp 0 loads 64 rows of dy and of codes by TMA, and the rows' scales, into one of kGradStages stages; eight warps make
-// 16-bit values of the codes, in the order that the tensor cores read; warp 1 of the first CTA multiplies for both; four
-// warps write the sums out.
+// warp 0 loads 64 rows of dy and of codes by TMA, and the rows' scales, into one of kGradStages stages; two warps to a
+// stage make 16-bit values of the codes, in the order that the tensor cores read; warp 1 of the first CTA multiplies for
+// both; eight warps write the sums out.
 #include "ep_tcgen05.cuh"
 
 namespace ep {
@@ -24,11 +24,14 @@ constexpr int kLineBytes = 8192;                   // 64 columns x 64 rows of 16
 constexpr int kDyBytes = 2 * kLineBytes, kValueBytes = 2 * kLineBytes, kCodeBytes = kGradRows * kGradHalf;
 constexpr int kGradStageBytes = kDyBytes + kValueBytes + kCodeBytes;
 constexpr int kGradStages = 5;
-constexpr int kWriteWarps = 4;
+// Two to a quarter of the lanes, 128 columns each.  With four, 340 and 245 us.
+constexpr int kWriteWarps = 8;
+constexpr int kFirstWriter = 2, kFirstConverter = kFirstWriter + kWriteWarps;
 // Warps that convert a stage.  Each stage has a team of its own: a barrier's parity tells one phase from the next alone, so
-// whoever waits for a stage's phase has to have seen the one before.
-constexpr int kConvertTeam = 4;
-constexpr int kGradThreads = 32 * (4 + kWriteWarps + kGradStages * kConvertTeam);   // load, multiply, two idle, write, convert
+// whoever waits for a stage's phase has to have seen the one before.  Teams of 1, 2 and 4 warps: 8192 rows in 8 groups
+// of 4096 x 7168 401, 352 and 345 us, 2048 rows in 16 groups 223, 217 and 293 us (the writing warps then lack registers).
+constexpr int kConvertTeam = 2;
+constexpr int kGradThreads = 32 * (kFirstConverter + kGradStages * kConvertTeam);   // load, multiply, write, convert
 constexpr int kMaxGradGroups = 4096;
 constexpr size_t kGradShared = 1024 + kGradStages * (kGradStageBytes + kGradRows * 4);
 
@@ -41,10 +44,8 @@ struct GradArgs {
     int groups, columns, inner, kb;
     int n_tiles, k_tiles;
     int64_t tiles;
-    int type, vec;            // of out: EP_BF16, EP_FP16 or kFp32; vec as for store_rows
+    int out_fp32, vec;        // vec: as for store_lines
 };
-
-constexpr int kFp32 = -1;
 
 struct GradTile {
     int g, n0, k0, r0, r1;
@@ -56,8 +57,8 @@ __device__ __forceinline__ GradTile grad_tile(const GradArgs& p, int64_t t)
     const int per = p.n_tiles * p.k_tiles;
     x.g = (int)(t / per);
     const int in = (int)(t - (int64_t)x.g * per);
-    x.k0 = in / p.n_tiles * kGradTile;
-    x.n0 = in % p.n_tiles * kGradTile;
+    x.n0 = in / p.k_tiles * kGradTile;
+    x.k0 = in % p.k_tiles * kGradTile;
     x.r0 = 0;
     x.r1 = (int)p.rows;
     if (p.offsets) {
@@ -69,20 +70,34 @@ __device__ __forceinline__ GradTile grad_tile(const GradArgs& p, int64_t t)
 
 __device__ __forceinline__ int grad_steps(const GradTile& x) { return (x.r1 - x.r0 + kGradRows - 1) / kGradRows; }
 
-// 64 columns of a warp's 32 rows of a tile to memory: `m` rows and `n` columns of them exist.
-__device__ __forceinline__ void write_sums(const GradArgs& p, int64_t at, const float2 (&v)[32], int m, int n)
+// 64 columns of a warp's 32 rows of a tile to memory, from tensor memory (zeros where there is none): `m` rows and `n`
+// columns of them exist.
+template <bool FP16>
+__device__ __forceinline__ void write_sums(const GradArgs& p, int64_t at, uint32_t from, bool some, int m, int n)
 {
-    if (p.type == kFp32) {
-        float* out = (float*)p.out + at + (int64_t)(threadIdx.x & 31) * p.inner;
-        if ((int)(threadIdx.x & 31) >= m) return;
+    uint32_t w[4][8];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)   // n is a multiple of 16
-            if (4 * j < n) reinterpret_cast<float4*>(out)[j] = make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
-    } else {
-        uint8_t* out = (uint8_t*)p.out + 2 * at;
-        if (p.type == EP_FP16) store_rows<true, 32>(out, 2 * (int64_t)p.inner, v, m, n, p.vec);
-        else store_rows<false, 32>(out, 2 * (int64_t)p.inner, v, m, n, p.vec);
+    for (int h = 0; h < 2; ++h) {
+        uint32_t r[32];
+        if (some) {
+            tmem_load32(r, from + 32 * h);
+            tmem_wait(r);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = 0;
+        }
+        if (p.out_fp32) {
+            uint4* out = reinterpret_cast<uint4*>((float*)p.out + at + (int64_t)(threadIdx.x & 31) * p.inner + 32 * h);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)   // n is a multiple of 16
+                if ((int)(threadIdx.x & 31) < m && 32 * h + 4 * j < n)
+                    out[j] = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            w[2 * h + j / 8][j & 7] = pack2<FP16>(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
     }
+    if (!p.out_fp32) store_lines((uint8_t*)p.out + 2 * at, 2 * (int64_t)p.inner, w, m, n, p.vec);
 }
 
 template <bool FP16>
@@ -196,10 +211,11 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
         // tensor memory is freed, and the second CTA's barriers go, only after the last product has told both
         if (elect_one()) bar_drain(drained, 0, clock64());
         __syncwarp();
-    } else if (warp >= 4 && warp < 4 + kWriteWarps) {
+    } else if (warp < kFirstConverter) {
         uint32_t tile = 0;
         bool ok = true;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const int part = (warp - kFirstWriter) / 4 * kGradHalf;
         for (int64_t t = t_first; t < p.tiles && ok; t += t_step) {
             const GradTile x = grad_tile(p, t);
             const bool some = x.r1 > x.r0;
@@ -212,23 +228,9 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
             const int row = x.n0 + kGradHalf * rank + (warp & 3) * 32;
             const int64_t at = ((int64_t)x.g * p.columns + row) * p.inner + x.k0;
 #pragma unroll 1
-            for (int c = 0; c < kGradTile; c += 64) {
-                float2 v[32];
-                if (some) {
-                    uint32_t r[32];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        tmem_load32(r, tmem + lanes + u * kGradTile + c + 32 * h);
-                        tmem_wait(r);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) v[16 * h + j] = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = make_float2(0.0f, 0.0f);
-                }
-                if (x.k0 + c < p.inner && row < p.columns) write_sums(p, at + c, v, p.columns - row, p.inner - x.k0 - c);
-            }
+            for (int c = part; c < part + kGradHalf; c += 64)
+                if (x.k0 + c < p.inner && row < p.columns)
+                    write_sums<FP16>(p, at + c, tmem + lanes + u * kGradTile + c, some, p.columns - row, p.inner - x.k0 - c);
             if (some) {
                 tmem_fence_before();
                 __syncwarp();
@@ -236,8 +238,8 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
                 ++tile;
             }
         }
-    } else if (warp >= 8) {
-        const int team = (warp - 8) / kConvertTeam, thread = (int)(threadIdx.x - 256) % (32 * kConvertTeam);
+    } else {
+        const int team = (warp - kFirstConverter) / kConvertTeam, thread = (int)(threadIdx.x - 32 * kFirstConverter) % (32 * kConvertTeam);
         const int row = thread / 8, piece = lane & 7;   // 16 codes of every (4 * kConvertTeam)th row from `row` on
         const uint32_t to0 = (uint32_t)(kDyBytes + piece / 4 * kLineBytes);
         const uint32_t arrive = peer_smem(ready, 0);
@@ -340,7 +342,7 @@ extern "C" int ep_matmul_fp8_weight_gradient(const void* dy, int dtype, const vo
     p.columns = columns; p.inner = inner; p.kb = (inner + 127) / 128;
     p.n_tiles = (columns + kGradTile - 1) / kGradTile; p.k_tiles = (inner + kGradTile - 1) / kGradTile;
     p.tiles = (int64_t)groups * p.n_tiles * p.k_tiles;
-    p.type = out_fp32 ? kFp32 : dtype;
+    p.out_fp32 = out_fp32 != 0;
     p.vec = layer_aligned(dw, 32) ? 2 : 1;
     const int sms = layer_num_sms();
     if (sms < 2) return layer_fail(EP_ERR_CUDA, "%s: cannot tell the current device's multiprocessors", who);
