@@ -21,6 +21,8 @@
 // columns, over every expert: each output is summed in one place, in a fixed order.  It is a programmatic dependent
 // that reads weights before it waits: the first kernel lets it start only after its own wait, when all that precedes the
 // call has completed, and the weights are nothing that the first writes.
+#include <type_traits>
+
 #include "ep_layer.cuh"
 
 namespace ep {
@@ -30,8 +32,6 @@ constexpr int kFewRows = 128;          // rows of a call
 constexpr int kFewPairs = 4096;        // (row, slot) pairs of a call
 constexpr int kFewExperts = 1024;
 constexpr int kUpWarps = 4;            // of a CTA of the first kernel
-constexpr int kDownMaxWarps = 16;
-constexpr int kWarpsPerSm = 16;        // at 128 registers a thread
 constexpr uint16_t kNone = 0xFFFF;
 
 enum { kFromE4m3 = 0, kFromFp16 = 1, kFromBf16 = 2, kFromZ = 3 };   // what the rows are held as
@@ -152,13 +152,19 @@ __device__ __forceinline__ int make_entries(const FewArgs& a, const Entries& s, 
     return *s.count;
 }
 
-// 16 bytes of weights, in the order that the code has them: they are read once, well ahead of their use.
-__device__ __forceinline__ uint4 weights16(const uint8_t* p)
+// 16 bytes of weights on their way into shared memory, past this SM's cache; zeros if not `in`.
+__device__ __forceinline__ void copy_weights(uint32_t to, const uint8_t* from, bool in)
 {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" :: "r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
+}
+
+// A step's 16 rows of weights, a lane's 16 bytes of four: rows g and g + 8, then the second 64 columns of both.
+__device__ __forceinline__ void read_weights(uint32_t from, uint4 (&w)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w) : "r"(from + 512 * i) : "memory");
 }
 
 // Two e4m3 codes to two FP16 values, exactly; the low or the high half of w.
@@ -193,48 +199,64 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b)
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// A lane's part of the other operand over a block of 128 columns: columns 16 q .. + 15 of both 64-column chunks of row
-// `row` (< 0: zeros), as FP16; returns the factor that the block's sums take for that row.
+// A lane's part of the other operand over a block of 128 columns, as it lies in memory: columns 16 q .. + 15 of both
+// 64-column chunks of a row, and what it takes to make FP16 values of them.
 template <int FROM>
-__device__ __forceinline__ float rows16(const FewArgs& a, int row, int kb, int q, uint32_t (&b)[16])
+struct Rows16 {
+    uint4 v[FROM == kFromE4m3 ? 2 : 4];
+    uint32_t e0, e1;   // kFromZ: the powers of two of either chunk's 8 + 8 columns
+    float f;           // kFromE4m3: the block's scale
+};
+
+// at: bytes from x (or z) to the lane's columns; scale: elements from x_scales (bytes from z_exp) to the block's.  Of a short
+// last block, whose weights read as zeros, only the columns that exist (in0, in1) are read.
+template <int FROM>
+__device__ __forceinline__ void fetch_rows(const FewArgs& a, uint32_t at, uint32_t scale, bool in0, bool in1, Rows16<FROM>& r)
 {
-    const int width = FROM == kFromZ ? a.I : a.H;
-    const int c0 = 128 * kb + 16 * q;
-    const bool in0 = row >= 0 && c0 < width, in1 = row >= 0 && c0 + 64 < width;
-    const int64_t at = (int64_t)row * width + c0;
+    const uint4* p = reinterpret_cast<const uint4*>((FROM == kFromZ ? a.z : a.x) + at);
     const uint4 zero = make_uint4(0, 0, 0, 0);
     if constexpr (FROM == kFromE4m3) {
-        const uint4 lo = in0 ? *reinterpret_cast<const uint4*>(a.x + at) : zero;
-        const uint4 hi = in1 ? *reinterpret_cast<const uint4*>(a.x + at + 64) : zero;
-        const float scale = row >= 0 ? a.x_scales[(int64_t)row * a.hb + kb] : 0.0f;
-        const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        r.v[0] = in0 ? p[0] : zero;
+        r.v[1] = in1 ? p[4] : zero;
+        r.f = a.x_scales[scale];
+    } else {
+        r.v[0] = in0 ? p[0] : zero;
+        r.v[1] = in0 ? p[1] : zero;
+        r.v[2] = in1 ? p[8] : zero;
+        r.v[3] = in1 ? p[9] : zero;
+        if constexpr (FROM == kFromZ) {
+            const uint16_t* e = reinterpret_cast<const uint16_t*>(a.z_exp + scale);
+            r.e0 = in0 ? e[0] : 0;
+            r.e1 = in1 ? e[4] : 0;
+        }
+    }
+}
+
+// The same as FP16; returns the factor that the block's sums take for that row.
+template <int FROM>
+__device__ __forceinline__ float half_rows(const Rows16<FROM>& r, uint32_t (&b)[16])
+{
+    if constexpr (FROM == kFromE4m3) {
+        const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             b[2 * i] = half_codes(w[i], false);
             b[2 * i + 1] = half_codes(w[i], true);
         }
-        return scale;
+        return r.f;
     } else {
-        const uint4* p = reinterpret_cast<const uint4*>((FROM == kFromZ ? a.z : a.x) + 2 * at);
-        uint4 v[4];
-        v[0] = in0 ? p[0] : zero;
-        v[1] = in0 ? p[1] : zero;
-        v[2] = in1 ? p[8] : zero;
-        v[3] = in1 ? p[9] : zero;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            b[4 * i] = v[i].x;
-            b[4 * i + 1] = v[i].y;
-            b[4 * i + 2] = v[i].z;
-            b[4 * i + 3] = v[i].w;
+            b[4 * i] = r.v[i].x;
+            b[4 * i + 1] = r.v[i].y;
+            b[4 * i + 2] = r.v[i].z;
+            b[4 * i + 3] = r.v[i].w;
         }
         if constexpr (FROM == kFromFp16) return 1.0f;
         if constexpr (FROM == kFromZ) {
             // each 8 columns to the largest power of two of the block's: exact but for what falls below 2^-38 of the
             // block's largest value
-            const uint16_t* ep = reinterpret_cast<const uint16_t*>(a.z_exp + (int64_t)row * (a.I / 8) + c0 / 8);
-            const uint32_t e0 = in0 ? ep[0] : 0, e1 = in1 ? ep[4] : 0;
-            const int e[4] = {(int)(e0 & 0xFF), (int)(e0 >> 8), (int)(e1 & 0xFF), (int)(e1 >> 8)};
+            const int e[4] = {(int)(r.e0 & 0xFF), (int)(r.e0 >> 8), (int)(r.e1 & 0xFF), (int)(r.e1 >> 8)};
             int top = max(max(e[0], e[1]), max(e[2], e[3]));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -265,88 +287,106 @@ __device__ __forceinline__ float rows16(const FewArgs& a, int row, int kb, int q
 }
 
 // Eight columns' sums of a block of 128, times their scales, into tot: w holds the block's 16 rows of weights (row g,
-// row g + 8; then the second 64 columns), f the lane's row's factor, s0 and s1 the scales of rows g and g + 8.
+// row g + 8; then the second 64 columns), f the lane's row's factor (1 unless FACTOR), s0 and s1 the scales of rows g and
+// g + 8.
+template <bool FACTOR>
 __device__ __forceinline__ void add_block(float (&tot)[4], const uint4 (&w)[4], const uint32_t (&b)[16], float f, float s0,
                                           float s1)
 {
-    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float d[2][4] = {};   // two sums, so that only four products wait for one another
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const uint32_t lo[4] = {w[2 * c].x, w[2 * c].y, w[2 * c].z, w[2 * c].w};
-        const uint32_t hi[4] = {w[2 * c + 1].x, w[2 * c + 1].y, w[2 * c + 1].z, w[2 * c + 1].w};
+    for (int m = 0; m < 4; ++m) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const uint32_t x[4] = {half_codes(lo[m], false), half_codes(hi[m], false), half_codes(lo[m], true),
-                                   half_codes(hi[m], true)};
-            mma_f16(d, x, b[8 * c + 2 * m], b[8 * c + 2 * m + 1]);
+        for (int c = 0; c < 2; ++c) {
+            const uint32_t lo = m == 0 ? w[2 * c].x : m == 1 ? w[2 * c].y : m == 2 ? w[2 * c].z : w[2 * c].w;
+            const uint32_t hi = m == 0 ? w[2 * c + 1].x : m == 1 ? w[2 * c + 1].y : m == 2 ? w[2 * c + 1].z : w[2 * c + 1].w;
+            const uint32_t x[4] = {half_codes(lo, false), half_codes(hi, false), half_codes(lo, true), half_codes(hi, true)};
+            mma_f16(d[c], x, b[8 * c + 2 * m], b[8 * c + 2 * m + 1]);
         }
     }
-    const int q = threadIdx.x & 3;
-    const float f0 = __shfl_sync(0xffffffffu, f, 8 * q), f1 = __shfl_sync(0xffffffffu, f, 8 * q + 4);
-    tot[0] = fmaf(d[0], s0 * f0, tot[0]);
-    tot[1] = fmaf(d[1], s0 * f1, tot[1]);
-    tot[2] = fmaf(d[2], s1 * f0, tot[2]);
-    tot[3] = fmaf(d[3], s1 * f1, tot[3]);
+    float f0 = 1.0f, f1 = 1.0f;
+    if constexpr (FACTOR) {
+        const int q = threadIdx.x & 3;
+        f0 = __shfl_sync(0xffffffffu, f, 8 * q);
+        f1 = __shfl_sync(0xffffffffu, f, 8 * q + 4);
+    }
+    tot[0] = fmaf(d[0][0] + d[1][0], s0 * f0, tot[0]);
+    tot[1] = fmaf(d[0][1] + d[1][1], s0 * f1, tot[1]);
+    tot[2] = fmaf(d[0][2] + d[1][2], s1 * f0, tot[2]);
+    tot[3] = fmaf(d[0][3] + d[1][3], s1 * f1, tot[3]);
 }
 
-// Steps that a warp's weights are read ahead: as many as 128 registers a thread leave room for.
+// Steps of 2 KB that a warp's weights are read ahead, and warps of an SM; the other operand and the scales are read one
+// step ahead.
+constexpr int kStepBytes = 2048;
 template <int NT>
-constexpr int kAhead = NT > 2 ? 3 : 4;
+constexpr int kAhead = NT < 4 ? 6 : 4;
+template <int NT>
+constexpr int kWarpsPerSm = NT == 1 ? 16 : 12;
+// Eights of rows that are fetched ahead: a whole step's, or with more than two, one eight ahead of the one in hand.
+template <int NT>
+constexpr int kFetched = NT <= 2 ? NT : 1;
 
-// Up projection and SwiGLU.  A unit is 8 columns of z, its 8 gate rows and 8 up rows, for one entry; `split` warps share
-// its K.
-template <int FROM, int NT>
-__global__ void __launch_bounds__(32 * kUpWarps, kWarpsPerSm / kUpWarps) ep_few_up_kernel(const FewArgs a)
+// Up projection and SwiGLU.  A unit is 8 columns of z, its 8 gate rows and 8 up rows, for one entry, and a warp's, or with
+// SPLIT `split` warps', which share its K.
+template <int FROM, int NT, bool SPLIT>
+__global__ void __launch_bounds__(32 * kUpWarps, kWarpsPerSm<NT> / kUpWarps) ep_few_up_kernel(const FewArgs a)
 {
     extern __shared__ __align__(16) uint8_t shared[];
-    __shared__ float4 parts[2][kUpWarps][NT][32];   // [round's parity]: sums of a unit's K
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const Entries s = entries_at(shared, a);
     follow_predecessor();
     const int entries = make_entries(a, s, 8 * NT);
-    const int teams = kUpWarps / a.split, team = warp / a.split, member = warp % a.split;
+    const int split = SPLIT ? a.split : 1, teams = kUpWarps / split, team = warp / split, member = warp % split;
     const int slices = a.I / 8, units = entries * slices;
-    const int k_lo = a.hb * member / a.split, k_hi = a.hb * (member + 1) / a.split, nb = k_hi - k_lo;
+    const int k_lo = a.hb * member / split, k_hi = a.hb * (member + 1) / split, nb = k_hi - k_lo;
     const int u0 = blockIdx.x * teams + team, stride = gridDim.x * teams;
     const int mine = u0 < units ? (units - 1 - u0) / stride + 1 : 0;
     const int steps = mine * nb;
 
-    constexpr int D = kAhead<NT>;
-    uint4 ring[D][4];
-    int lu = u0, lk = k_lo, ls = 0;
-    const uint8_t* lp = nullptr;
+    constexpr int D = kAhead<NT>, kElement = FROM == kFromE4m3 ? 1 : 2;
+    constexpr bool kFactor = FROM != kFromFp16;
+    // a lane fills and reads its own bytes of the warp's ring, so that nothing passes between lanes
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(shared + entries_bytes(a.pairs, a.experts, a.rows)) +
+                          warp * D * kStepBytes + 16 * lane;
+    const uint32_t ring_end = ring + D * kStepBytes;
+    // Of K's last block a lane's columns of either chunk may not exist.
+    const bool tail = a.H % 128 != 0 && k_hi == a.hb, tail0 = !tail || 128 * (a.hb - 1) + 16 * q < a.H,
+               tail1 = !tail || 128 * (a.hb - 1) + 16 * q + 64 < a.H;
     const int64_t up_rows = (int64_t)a.I * a.H;
+    int lu = u0, left = steps > 0 ? nb : 0;   // of the loads: unit, and its blocks not yet under way
+    const uint8_t *lp = nullptr, *lq = nullptr;
     auto point = [&] {
         const int entry = lu / slices;
-        lp = a.up + ((int64_t)s.expert[entry] * 2 * a.I + 8 * (lu - entry * slices) + g) * a.H + 16 * q;
+        lp = a.up + ((int64_t)s.expert[entry] * 2 * a.I + 8 * (lu - entry * slices) + g) * a.H + 128 * k_lo + 16 * q;
+        lq = lp + up_rows;
     };
-    if (steps > 0) point();
-    auto load = [&](uint4 (&w)[4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = make_uint4(0, 0, 0, 0);
-        if (ls >= steps) return;
-        const uint8_t* p = lp + 128 * lk;
-        const int c = 128 * lk + 16 * q;
-        if (c < a.H) {
-            w[0] = weights16(p);
-            w[1] = weights16(p + up_rows);
+    if (left > 0) point();
+    auto load = [&](uint32_t to) {
+        if (left > 0) {
+            const bool in0 = left > 1 || tail0, in1 = left > 1 || tail1;
+            copy_weights(to, lp, in0);
+            copy_weights(to + 512, lq, in0);
+            copy_weights(to + 1024, lp + 64, in1);
+            copy_weights(to + 1536, lq + 64, in1);
+            lp += 128;
+            lq += 128;
+            if (--left == 0) {
+                lu += stride;
+                if (lu < units) {
+                    left = nb;
+                    point();
+                }
+            }
         }
-        if (c + 64 < a.H) {
-            w[2] = weights16(p + 64);
-            w[3] = weights16(p + up_rows + 64);
-        }
-        ++ls;
-        if (++lk == k_hi) {
-            lk = k_lo;
-            lu += stride;
-            if (ls < steps) point();
-        }
+        copies_commit();
     };
-#pragma unroll
-    for (int d = 0; d < D; ++d) load(ring[d]);
+    for (uint32_t to = ring; to != ring_end; to += kStepBytes) load(to);
 
-    float tot[NT][4];
-    int row[NT], k = k_lo, u = u0, first = 0, n = 0, slice = 0;
+    // the unit whose operand is fetched, and the block of K.  Columns past an entry's rows repeat one of its rows: what
+    // they sum up is not used.
+    int u = u0, k = k_lo, first = 0, n = 0, slice = 0;
+    uint32_t row_at[NT], row_scale[NT];
     const float *gs = nullptr, *us = nullptr;   // the unit's scales
     auto begin = [&] {
         const int entry = u / slices;
@@ -356,15 +396,40 @@ __global__ void __launch_bounds__(32 * kUpWarps, kWarpsPerSm / kUpWarps) ep_few_
         const float* es = a.up_scales + (int64_t)s.expert[entry] * a.ub * a.hb;
         gs = es + (int64_t)(8 * slice / 128) * a.hb;
         us = es + (int64_t)((a.I + 8 * slice) / 128) * a.hb;
+        k = k_lo;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            row[t] = 8 * t + g < n ? s.list[first + 8 * t + g] : -1;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tot[t][i] = 0.0f;
+            const uint32_t row = s.list[first + (8 * t + g < n ? 8 * t + g : 0)];
+            row_at[t] = (row * a.H + 16 * q) * kElement;
+            row_scale[t] = row * a.hb;
         }
     };
-    // z of the unit from its whole sums, and its power of two
-    auto finish = [&] {
+    Rows16<FROM> x[kFetched<NT>];
+    float s0 = 0.0f, s1 = 0.0f, tot[NT][4];
+    auto fetch = [&](int t, Rows16<FROM>& r) {
+        const bool whole = k + 1 < a.hb;
+        fetch_rows<FROM>(a, row_at[t] + 128 * kElement * k, row_scale[t] + k, whole || tail0, whole || tail1, r);
+    };
+    auto scales = [&] {
+        s0 = gs[k];
+        s1 = us[k];
+    };
+    auto clear = [&] {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tot[t][i] = 0.0f;
+    };
+    clear();
+    if (steps > 0) {
+        begin();
+        scales();
+#pragma unroll
+        for (int t = 0; t < kFetched<NT>; ++t)
+            if (8 * t < n) fetch(t, x[t]);
+    }
+    // z of a unit from its whole sums, and its power of two
+    auto finish = [&](int first, int n, int slice) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             if (8 * t >= n) break;
@@ -384,67 +449,84 @@ __global__ void __launch_bounds__(32 * kUpWarps, kWarpsPerSm / kUpWarps) ep_few_
             }
         }
     };
-    if (a.split == 1) {
-        if (steps > 0) begin();
-        for (int i0 = 0; i0 < steps; i0 += D) {
-#pragma unroll
-            for (int d = 0; d < D; ++d) {
-                if (i0 + d >= steps) break;
-                const float s0 = __ldg(gs + k), s1 = __ldg(us + k);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    if (8 * t >= n) break;
-                    uint32_t b[16];
-                    const float f = rows16<FROM>(a, row[t], k, q, b);
-                    add_block(tot[t], ring[d], b, f, s0, s1);
-                }
-                load(ring[d]);
-                if (++k == k_hi) {
-                    finish();
-                    k = k_lo;
-                    u += stride;
-                    if (i0 + d + 1 < steps) begin();
-                }
+    uint32_t at = ring;
+    // One step of a unit of `rows` rows, whose operand is here, or its first 8 rows'.  The next step's is fetched: that of
+    // the same unit's next block, or, once `next` has begun another unit, of its first.  MORE: there is a next step.
+    auto step = [&](auto more, int rows, auto next) {
+        constexpr bool MORE = decltype(more)::value;
+        uint4 w[4];
+        copies_wait<D - 1>();
+        read_weights(at, w);
+        const float s0_now = s0, s1_now = s1;
+        if constexpr (kFetched<NT> == NT) {
+            if constexpr (MORE) {
+                next();
+                scales();
             }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (8 * t >= rows && (!MORE || 8 * t >= n)) break;
+                uint32_t b[16];
+                const float f = half_rows<FROM>(x[t], b);   // of nothing, past `rows`: not used
+                if (MORE && 8 * t < n) fetch(t, x[t]);
+                if (8 * t < rows) add_block<kFactor>(tot[t], w, b, f, s0_now, s1_now);
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (8 * t >= rows) break;
+                uint32_t b[16];
+                const float f = half_rows<FROM>(x[0], b);
+                if (t + 1 < NT && 8 * (t + 1) < rows) {
+                    fetch(t + 1 < NT ? t + 1 : 0, x[0]);
+                } else if constexpr (MORE) {
+                    next();
+                    scales();
+                    fetch(0, x[0]);
+                }
+                add_block<kFactor>(tot[t], w, b, f, s0_now, s1_now);
+            }
+        }
+        load(at);   // its bytes are in registers, and used
+        at = at + kStepBytes == ring_end ? ring : at + kStepBytes;
+    };
+    constexpr std::true_type kMore{};
+    constexpr std::false_type kLast{};
+    // a unit from its first step to its last, during which the next unit's first operand is fetched
+    auto unit_steps = [&](bool another) {
+        const int rows = n;
+        for (int i = 1; i < nb; ++i) step(kMore, rows, [&] { ++k; });
+        if (another) step(kMore, rows, [&] { u += stride; begin(); });
+        else step(kLast, rows, [] {});
+    };
+    if constexpr (!SPLIT) {
+        for (int i = 1; i <= mine; ++i) {
+            const int first_now = first, n_now = n, slice_now = slice;
+            unit_steps(i < mine);
+            finish(first_now, n_now, slice_now);
+            clear();
         }
         return;
     }
-    // a unit's K is shared: its warps meet once per round, and every team of the CTA makes as many rounds
+    // a unit's warps meet once per round, and every team of the CTA makes as many rounds
+    __shared__ float4 parts[2][kUpWarps][NT][32];   // [round's parity]: sums of a unit's K
     const int first_unit = blockIdx.x * teams;
     const int rounds = first_unit < units ? (units - 1 - first_unit) / stride + 1 : 0;
-    int i = 0;   // steps done, modulo D in the ring's index: a round's steps are walked with the ring unrolled
-    for (int round = 0; round < rounds; ++round, u += stride) {
-        const bool has = u < units;
-        n = 0;
-        if (has) begin();
-        for (int left = has ? nb : 0; left > 0;) {
-#pragma unroll
-            for (int d = 0; d < D; ++d) {
-                if (left == 0 || i != d) continue;
-                const float s0 = __ldg(gs + k), s1 = __ldg(us + k);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    if (8 * t >= n) break;
-                    uint32_t b[16];
-                    const float f = rows16<FROM>(a, row[t], k, q, b);
-                    add_block(tot[t], ring[d], b, f, s0, s1);
-                }
-                load(ring[d]);
-                ++k;
-                --left;
-                i = d + 1 == D ? 0 : d + 1;
-            }
-        }
-        k = k_lo;
+    for (int round = 0; round < rounds; ++round) {
+        const int unit = u0 + round * stride;
+        const bool has = unit < units;
+        const int entry = has ? unit / slices : 0, slice_now = unit - entry * slices;
+        const int first_now = has ? s.start[entry] : 0, n_now = has ? s.start[entry + 1] - first_now : 0;
+        if (has && nb > 0) unit_steps(round + 1 < mine);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-            if (8 * t < n) parts[round & 1][warp][t][lane] = make_float4(tot[t][0], tot[t][1], tot[t][2], tot[t][3]);
+            if (8 * t < n_now) parts[round & 1][warp][t][lane] = make_float4(tot[t][0], tot[t][1], tot[t][2], tot[t][3]);
         __syncthreads();
         if (member == 0 && has) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                if (8 * t >= n) break;
-                for (int m = 1; m < a.split; ++m) {
+                if (8 * t >= n_now) break;
+                for (int m = 1; m < split; ++m) {
                     const float4 v = parts[round & 1][warp + m][t][lane];
                     tot[t][0] += v.x;
                     tot[t][1] += v.y;
@@ -452,15 +534,16 @@ __global__ void __launch_bounds__(32 * kUpWarps, kWarpsPerSm / kUpWarps) ep_few_
                     tot[t][3] += v.w;
                 }
             }
-            finish();
+            finish(first_now, n_now, slice_now);
         }
+        clear();
     }
 }
 
 // Down projection and the weighted sum.  A CTA owns 16 output columns; its warps share the blocks of all entries' K
 // evenly, and each keeps the rows' sums of its own part in shared memory.
 template <int NT>
-__global__ void __launch_bounds__(32 * kDownMaxWarps) ep_few_down_kernel(const FewArgs a)
+__global__ void __launch_bounds__(32 * kWarpsPerSm<NT>) ep_few_down_kernel(const FewArgs a)
 {
     extern __shared__ __align__(16) uint8_t shared[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
@@ -476,34 +559,33 @@ __global__ void __launch_bounds__(32 * kDownMaxWarps) ep_few_down_kernel(const F
     const int lo = (int)((int64_t)total * warp / warps), hi = (int)((int64_t)total * (warp + 1) / warps);
 
     constexpr int D = kAhead<NT>;
-    uint4 ring[D][4];
-    int lb = lo, le = lo / a.ib, lk = lo - le * a.ib;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sums + (size_t)warps * a.rows * 16) + warp * D * kStepBytes + 16 * lane;
+    const uint32_t ring_end = ring + D * kStepBytes;
+    // Of K's last block a lane's columns of either chunk may not exist.
+    const bool tail0 = 128 * (a.ib - 1) + 16 * q < a.I, tail1 = 128 * (a.ib - 1) + 16 * q + 64 < a.I;
+    const int64_t eight_rows = 8 * (int64_t)a.I;
+    int lb = lo, le = lo / a.ib, left = a.ib - (lo - le * a.ib);   // of the loads: block, its entry, the entry's blocks left
     const uint8_t* lp = nullptr;
-    auto point = [&] { lp = a.down + ((int64_t)s.expert[le] * a.H + h0 + g) * a.I + 16 * q; };
+    auto point = [&] { lp = a.down + ((int64_t)s.expert[le] * a.H + h0 + g) * a.I + 128 * (a.ib - left) + 16 * q; };
     if (lb < hi) point();
-    auto load = [&](uint4 (&w)[4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = make_uint4(0, 0, 0, 0);
-        if (lb >= hi) return;
-        const uint8_t* p = lp + 128 * lk;
-        const int c = 128 * lk + 16 * q;
-        if (c < a.I) {
-            w[0] = weights16(p);
-            w[1] = weights16(p + 8 * (int64_t)a.I);
+    auto load = [&](uint32_t to) {
+        if (lb < hi) {
+            const bool in0 = left > 1 || tail0, in1 = left > 1 || tail1;
+            copy_weights(to, lp, in0);
+            copy_weights(to + 512, lp + eight_rows, in0);
+            copy_weights(to + 1024, lp + 64, in1);
+            copy_weights(to + 1536, lp + eight_rows + 64, in1);
+            ++lb;
+            lp += 128;
+            if (--left == 0) {
+                left = a.ib;
+                ++le;
+                if (lb < hi) point();
+            }
         }
-        if (c + 64 < a.I) {
-            w[2] = weights16(p + 64);
-            w[3] = weights16(p + 8 * (int64_t)a.I + 64);
-        }
-        ++lb;
-        if (++lk == a.ib) {
-            lk = 0;
-            ++le;
-            if (lb < hi) point();
-        }
+        copies_commit();
     };
-#pragma unroll
-    for (int d = 0; d < D; ++d) load(ring[d]);
+    for (uint32_t to = ring; to != ring_end; to += kStepBytes) load(to);
     for (int i = threadIdx.x; i < warps * a.rows * 16; i += blockDim.x) sums[i] = 0.0f;
     for (int p = threadIdx.x; p < a.pairs; p += blockDim.x) {
         const int e = s.local[p], row = p / a.k;
@@ -517,8 +599,9 @@ __global__ void __launch_bounds__(32 * kDownMaxWarps) ep_few_down_kernel(const F
     follow_predecessor();
 
     float* own = sums + warp * a.rows * 16;
-    float tot[NT][4];
-    int place[NT], e = lo / a.ib, k = lo - e * a.ib, first = 0, n = 0;
+    // the entry whose operand is fetched, and the block of K; columns past an entry's rows as in the first kernel
+    int e = lo / a.ib, k = lo - e * a.ib, first = 0, n = 0;
+    uint32_t row_at[NT], row_exp[NT];
     const float* ds = nullptr;
     auto begin = [&] {
         first = s.start[e];
@@ -526,13 +609,33 @@ __global__ void __launch_bounds__(32 * kDownMaxWarps) ep_few_down_kernel(const F
         ds = a.down_scales + ((int64_t)s.expert[e] * a.hb + h0 / 128) * a.ib;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            place[t] = 8 * t + g < n ? first + 8 * t + g : -1;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tot[t][i] = 0.0f;
+            const uint32_t place = first + (8 * t + g < n ? 8 * t + g : 0);
+            row_at[t] = (place * a.I + 16 * q) * 2;
+            row_exp[t] = place * (a.I / 8) + 2 * q;
         }
     };
+    Rows16<kFromZ> x[kFetched<NT>];
+    float sc = 0.0f, tot[NT][4];
+    auto fetch = [&](int t, Rows16<kFromZ>& r) {
+        const bool whole = k + 1 < a.ib;
+        fetch_rows<kFromZ>(a, row_at[t] + 256 * k, row_exp[t] + 16 * k, whole || tail0, whole || tail1, r);
+    };
+    auto clear = [&] {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tot[t][i] = 0.0f;
+    };
+    clear();
+    if (lo < hi) {
+        begin();
+        sc = ds[k];
+#pragma unroll
+        for (int t = 0; t < kFetched<NT>; ++t)
+            if (8 * t < n) fetch(t, x[t]);
+    }
     // an entry's rows are distinct, so that no two lanes add to one place
-    auto finish = [&] {
+    auto finish = [&](int first, int n) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             if (8 * t >= n) break;
@@ -548,27 +651,55 @@ __global__ void __launch_bounds__(32 * kDownMaxWarps) ep_few_down_kernel(const F
         }
         __syncwarp();
     };
-    if (lo < hi) begin();
-    for (int i0 = lo; i0 < hi; i0 += D) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            if (i0 + d >= hi) break;
-            const float sc = __ldg(ds + k);
+    uint32_t at = ring;
+    auto step = [&](auto more, int rows, auto next) {   // as in the first kernel
+        constexpr bool MORE = decltype(more)::value;
+        uint4 w[4];
+        copies_wait<D - 1>();
+        read_weights(at, w);
+        const float sc_now = sc;
+        if constexpr (kFetched<NT> == NT) {
+            if constexpr (MORE) {
+                next();
+                sc = ds[k];
+            }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                if (8 * t >= n) break;
+                if (8 * t >= rows && (!MORE || 8 * t >= n)) break;
                 uint32_t b[16];
-                const float f = rows16<kFromZ>(a, place[t], k, q, b);
-                add_block(tot[t], ring[d], b, f, sc, sc);
+                const float f = half_rows<kFromZ>(x[t], b);   // of nothing, past `rows`: not used
+                if (MORE && 8 * t < n) fetch(t, x[t]);
+                if (8 * t < rows) add_block<true>(tot[t], w, b, f, sc_now, sc_now);
             }
-            load(ring[d]);
-            if (++k == a.ib || i0 + d + 1 == hi) {
-                finish();
-                k = 0;
-                ++e;
-                if (i0 + d + 1 < hi) begin();
+        } else {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (8 * t >= rows) break;
+                uint32_t b[16];
+                const float f = half_rows<kFromZ>(x[0], b);
+                if (t + 1 < NT && 8 * (t + 1) < rows) {
+                    fetch(t + 1 < NT ? t + 1 : 0, x[0]);
+                } else if constexpr (MORE) {
+                    next();
+                    sc = ds[k];
+                    fetch(0, x[0]);
+                }
+                add_block<true>(tot[t], w, b, f, sc_now, sc_now);
             }
         }
+        load(at);   // its bytes are in registers, and used
+        at = at + kStepBytes == ring_end ? ring : at + kStepBytes;
+    };
+    constexpr std::true_type kMore{};
+    constexpr std::false_type kLast{};
+    for (int i = lo; i < hi;) {   // an entry, or what of its K is this warp's
+        const int first_now = first, n_now = n, blocks = min(a.ib - k, hi - i);
+        for (int j = 1; j < blocks; ++j) step(kMore, n_now, [&] { ++k; });
+        i += blocks;
+        if (i < hi) step(kMore, n_now, [&] { ++e; k = 0; begin(); });
+        else step(kLast, n_now, [] {});
+        finish(first_now, n_now);
+        clear();
     }
     __syncthreads();
     for (int i = threadIdx.x; i < a.rows * 16; i += blockDim.x) {
@@ -583,13 +714,17 @@ __global__ void __launch_bounds__(32 * kDownMaxWarps) ep_few_down_kernel(const F
 template <int FROM, int NT>
 cudaError_t launch_up(const FewArgs& a, int sms, cudaStream_t s)
 {
-    const size_t shared = entries_bytes(a.pairs, a.experts, a.rows);
-    const cudaError_t e = allow_all_shared<ep_few_up_kernel<FROM, NT>>();
-    if (e != cudaSuccess) return e;
+    const size_t shared = entries_bytes(a.pairs, a.experts, a.rows) + (size_t)kUpWarps * kAhead<NT> * kStepBytes;
     const int64_t entries = a.pairs < a.experts ? a.pairs : (int64_t)a.experts + a.pairs / (8 * NT);   // at most
     const int64_t teams = kUpWarps / a.split, ctas = (entries * (a.I / 8) + teams - 1) / teams;
-    const int64_t fit = (int64_t)sms * (kWarpsPerSm / kUpWarps);
-    return launch_dependent(ep_few_up_kernel<FROM, NT>, dim3((unsigned)(ctas < fit ? ctas : fit)), dim3(32 * kUpWarps), shared, s, a);
+    const int64_t fit = (int64_t)sms * (kWarpsPerSm<NT> / kUpWarps);
+    const dim3 grid((unsigned)(ctas < fit ? ctas : fit)), block(32 * kUpWarps);
+    if (a.split > 1) {
+        const cudaError_t e = allow_all_shared<ep_few_up_kernel<FROM, NT, true>>();
+        return e != cudaSuccess ? e : launch_dependent(ep_few_up_kernel<FROM, NT, true>, grid, block, shared, s, a);
+    }
+    const cudaError_t e = allow_all_shared<ep_few_up_kernel<FROM, NT, false>>();
+    return e != cudaSuccess ? e : launch_dependent(ep_few_up_kernel<FROM, NT, false>, grid, block, shared, s, a);
 }
 
 template <int NT>
@@ -598,17 +733,21 @@ cudaError_t launch_few(FewArgs a, int from, int sms, cudaStream_t s)
     // experts that rows name, at most: with fewer units than half of the warps that run at once, more warps share one
     const int64_t units = (int64_t)(a.pairs < a.experts ? a.pairs : a.experts) * (a.I / 8);
     a.split = 1;
-    while (a.split < kUpWarps && units * a.split * 2 <= (int64_t)sms * kWarpsPerSm) a.split *= 2;
+    while (a.split < kUpWarps && units * a.split * 2 <= (int64_t)sms * kWarpsPerSm<NT>) a.split *= 2;
     cudaError_t e = from == kFromE4m3 ? launch_up<kFromE4m3, NT>(a, sms, s)
                     : from == kFromFp16 ? launch_up<kFromFp16, NT>(a, sms, s) : launch_up<kFromBf16, NT>(a, sms, s);
     if (e != cudaSuccess) return e;
     e = allow_all_shared<ep_few_down_kernel<NT>>();
     if (e != cudaSuccess) return e;
     const int ctas = a.H / 16;
-    int warps = kDownMaxWarps;
-    while (warps > 4 && (int64_t)ctas * warps > (int64_t)sms * kWarpsPerSm) warps /= 2;
-    const size_t shared = entries_bytes(a.pairs, a.experts, a.rows) + ((size_t)(a.pairs + 3) / 4 * 4 + (size_t)warps * a.rows * 16) * 4;
-    return launch_dependent(ep_few_down_kernel<NT>, dim3(ctas), dim3(32 * warps), shared, s, a);
+    int warps = kWarpsPerSm<NT>;
+    auto shared = [&] {
+        return entries_bytes(a.pairs, a.experts, a.rows) + (size_t)(a.pairs + 3) / 4 * 16 + (size_t)warps * a.rows * 64 +
+               (size_t)warps * kAhead<NT> * kStepBytes;
+    };
+    while (warps > 4 && (int64_t)ctas * warps > (int64_t)sms * kWarpsPerSm<NT>) warps /= 2;
+    while (shared() > 226 * 1024) warps /= 2;   // ends: one warp of 4096 pairs and 1024 experts takes 84 KB
+    return launch_dependent(ep_few_down_kernel<NT>, dim3(ctas), dim3(32 * warps), shared(), s, a);
 }
 
 size_t few_z_bytes(int64_t pairs, int inner) { return ((size_t)pairs * inner * 2 + 255) / 256 * 256; }
@@ -619,7 +758,8 @@ size_t few_z_bytes(int64_t pairs, int inner) { return ((size_t)pairs * inner * 2
 extern "C" size_t ep_moe_few_workspace_bytes(int64_t rows, int topk, int inner)
 {
     using namespace ep;
-    if (rows <= 0 || rows > kFewRows || topk < 1 || rows * topk > kFewPairs || inner < 16 || inner % 16 != 0 || inner > 1 << 20)
+    if (rows <= 0 || rows > kFewRows || topk < 1 || rows * topk > kFewPairs || inner < 16 || inner % 16 != 0 || inner > 1 << 19 ||
+        rows * topk * inner >= (int64_t)1 << 31)
         return 0;
     return few_z_bytes(rows * topk, inner) + (size_t)rows * topk * (inner / 8);
 }
@@ -642,6 +782,8 @@ extern "C" int ep_moe_few_rows(const void* x, const float* x_scales, int x_dtype
         return layer_fail(EP_ERR_ARG, "%s: hidden=%d is not a multiple of 16 in 16..2^20", who, hidden);
     if (inner < 16 || inner % 16 != 0 || inner > 1 << 19)
         return layer_fail(EP_ERR_ARG, "%s: inner=%d is not a multiple of 16 in 16..2^19", who, inner);
+    if (rows * topk * inner >= (int64_t)1 << 31)   // bytes of z are counted in 32 bits
+        return layer_fail(EP_ERR_ARG, "%s: rows*topk*inner=%lld reaches 2^31", who, (long long)(rows * topk * inner));
     if (x_dtype != EP_FP8_E4M3 && x_dtype != EP_FP16 && x_dtype != EP_BF16)
         return layer_fail(EP_ERR_ARG, "%s: x_dtype=%d is not EP_FP8_E4M3, EP_FP16 or EP_BF16", who, x_dtype);
     if (out_dtype != EP_BF16 && out_dtype != EP_FP16)

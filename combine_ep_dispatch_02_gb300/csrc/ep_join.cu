@@ -61,16 +61,6 @@ __device__ __forceinline__ void load_channels(const void* p, int fp32, int v, fl
     }
 }
 
-// 16 bytes of global memory into shared memory, asynchronously; a thread's copies are grouped by copies_commit() and
-// copies_wait<N>() returns when all but the newest N groups have arrived, for the thread that made them.
-__device__ __forceinline__ void copy16(void* to, const void* from)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
-
 // Two sums over a row's threads, a warp or a CTA; `part` holds 32 pairs that no thread still reads.
 template <bool WARP>
 __device__ __forceinline__ float2 row_sums(float2 s, float2* part)

@@ -83,6 +83,16 @@ __device__ __forceinline__ void follow_predecessor()
     allow_dependents();
 }
 
+// 16 bytes of global memory into shared memory, asynchronously; a thread's copies are grouped by copies_commit() and
+// copies_wait<N>() returns when all but the newest N groups have arrived, for the thread that made them.
+__device__ __forceinline__ void copy16(void* to, const void* from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+
 // Eight 16-bit values of a 16-byte vector as floats, and back (rounded to nearest even once).
 template <bool FP16>
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8])
