@@ -186,11 +186,10 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
 // 2^n for n in -126..127.
 __device__ __forceinline__ float power2(int n) { return __int_as_float((n + 127) << 23); }
 
-// 2^n as FP16, both halves, n <= 0; 0 below its smallest number.
-__device__ __forceinline__ uint32_t half_power2(int n)
+// 2^-m and 2^-n as FP16 in the low and the high half, m, n >= 0; 0 below its smallest number.
+__device__ __forceinline__ uint32_t half_power2(int m, int n)
 {
-    const uint32_t h = n >= -14 ? (uint32_t)(n + 15) << 10 : n >= -24 ? 1u << (n + 24) : 0u;
-    return h | h << 16;
+    return pack2<true>(power2(-min(m, 126)), power2(-min(n, 126)));
 }
 
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b)
@@ -208,26 +207,26 @@ struct Rows16 {
     float f;           // kFromE4m3: the block's scale
 };
 
-// at: bytes from x (or z) to the lane's columns; scale: elements from x_scales (bytes from z_exp) to the block's.  Of a short
-// last block, whose weights read as zeros, only the columns that exist (in0, in1) are read.
-template <int FROM>
+// at: bytes from x (or z) to the lane's columns; scale: elements from x_scales (bytes from z_exp) to the block's.  WHOLE: all
+// columns exist; otherwise, of a short last block, whose weights read as zeros, those of in0 and in1.
+template <int FROM, bool WHOLE>
 __device__ __forceinline__ void fetch_rows(const FewArgs& a, uint32_t at, uint32_t scale, bool in0, bool in1, Rows16<FROM>& r)
 {
     const uint4* p = reinterpret_cast<const uint4*>((FROM == kFromZ ? a.z : a.x) + at);
     const uint4 zero = make_uint4(0, 0, 0, 0);
     if constexpr (FROM == kFromE4m3) {
-        r.v[0] = in0 ? p[0] : zero;
-        r.v[1] = in1 ? p[4] : zero;
+        r.v[0] = WHOLE || in0 ? p[0] : zero;
+        r.v[1] = WHOLE || in1 ? p[4] : zero;
         r.f = a.x_scales[scale];
     } else {
-        r.v[0] = in0 ? p[0] : zero;
-        r.v[1] = in0 ? p[1] : zero;
-        r.v[2] = in1 ? p[8] : zero;
-        r.v[3] = in1 ? p[9] : zero;
+        r.v[0] = WHOLE || in0 ? p[0] : zero;
+        r.v[1] = WHOLE || in0 ? p[1] : zero;
+        r.v[2] = WHOLE || in1 ? p[8] : zero;
+        r.v[3] = WHOLE || in1 ? p[9] : zero;
         if constexpr (FROM == kFromZ) {
             const uint16_t* e = reinterpret_cast<const uint16_t*>(a.z_exp + scale);
-            r.e0 = in0 ? e[0] : 0;
-            r.e1 = in1 ? e[4] : 0;
+            r.e0 = WHOLE || in0 ? e[0] : 0;
+            r.e1 = WHOLE || in1 ? e[4] : 0;
         }
     }
 }
@@ -261,10 +260,14 @@ __device__ __forceinline__ float half_rows(const Rows16<FROM>& r, uint32_t (&b)[
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t f = half_power2(e[i] - top);
+            for (int i = 0; i < 4; i += 2) {
+                const uint32_t f = half_power2(top - e[i], top - e[i + 1]);
+                const uint32_t lo = __byte_perm(f, 0, 0x1010), hi = __byte_perm(f, 0, 0x3232);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) b[4 * i + j] = mul_half2(b[4 * i + j], f);
+                for (int j = 0; j < 4; ++j) {
+                    b[4 * i + j] = mul_half2(b[4 * i + j], lo);
+                    b[4 * i + 4 + j] = mul_half2(b[4 * i + 4 + j], hi);
+                }
             }
             return power2(max(top, 18) - 142);
         }
@@ -319,10 +322,19 @@ __device__ __forceinline__ void add_block(float (&tot)[4], const uint4 (&w)[4], 
 // Steps of 2 KB that a warp's weights are read ahead, and warps of an SM; the other operand and the scales are read one
 // step ahead.
 constexpr int kStepBytes = 2048;
+#ifndef V_D1
+#define V_D1 6
+#endif
+#ifndef V_DN
+#define V_DN 4
+#endif
+#ifndef V_WN
+#define V_WN 16
+#endif
 template <int NT>
-constexpr int kAhead = NT < 4 ? 6 : 4;
+constexpr int kAhead = NT == 1 ? V_D1 : V_DN;
 template <int NT>
-constexpr int kWarpsPerSm = NT == 1 ? 16 : 12;
+constexpr int kWarpsPerSm = NT == 1 ? 16 : V_WN;
 // Eights of rows that are fetched ahead: a whole step's, or with more than two, one eight ahead of the one in hand.
 template <int NT>
 constexpr int kFetched = NT <= 2 ? NT : 1;
@@ -353,6 +365,7 @@ __global__ void __launch_bounds__(32 * kUpWarps, kWarpsPerSm<NT> / kUpWarps) ep_
     // Of K's last block a lane's columns of either chunk may not exist.
     const bool tail = a.H % 128 != 0 && k_hi == a.hb, tail0 = !tail || 128 * (a.hb - 1) + 16 * q < a.H,
                tail1 = !tail || 128 * (a.hb - 1) + 16 * q + 64 < a.H;
+    const int whole = a.H / 128;   // blocks without such columns
     const int64_t up_rows = (int64_t)a.I * a.H;
     int lu = u0, left = steps > 0 ? nb : 0;   // of the loads: unit, and its blocks not yet under way
     const uint8_t *lp = nullptr, *lq = nullptr;
@@ -407,8 +420,9 @@ __global__ void __launch_bounds__(32 * kUpWarps, kWarpsPerSm<NT> / kUpWarps) ep_
     Rows16<FROM> x[kFetched<NT>];
     float s0 = 0.0f, s1 = 0.0f, tot[NT][4];
     auto fetch = [&](int t, Rows16<FROM>& r) {
-        const bool whole = k + 1 < a.hb;
-        fetch_rows<FROM>(a, row_at[t] + 128 * kElement * k, row_scale[t] + k, whole || tail0, whole || tail1, r);
+        const uint32_t at = row_at[t] + 128 * kElement * k, scale = row_scale[t] + k;
+        if (k < whole) fetch_rows<FROM, true>(a, at, scale, true, true, r);
+        else fetch_rows<FROM, false>(a, at, scale, tail0, tail1, r);
     };
     auto scales = [&] {
         s0 = gs[k];
@@ -563,6 +577,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerSm<NT>) ep_few_down_kernel(const
     const uint32_t ring_end = ring + D * kStepBytes;
     // Of K's last block a lane's columns of either chunk may not exist.
     const bool tail0 = 128 * (a.ib - 1) + 16 * q < a.I, tail1 = 128 * (a.ib - 1) + 16 * q + 64 < a.I;
+    const int whole = a.I / 128;   // blocks without such columns
     const int64_t eight_rows = 8 * (int64_t)a.I;
     int lb = lo, le = lo / a.ib, left = a.ib - (lo - le * a.ib);   // of the loads: block, its entry, the entry's blocks left
     const uint8_t* lp = nullptr;
@@ -617,8 +632,9 @@ __global__ void __launch_bounds__(32 * kWarpsPerSm<NT>) ep_few_down_kernel(const
     Rows16<kFromZ> x[kFetched<NT>];
     float sc = 0.0f, tot[NT][4];
     auto fetch = [&](int t, Rows16<kFromZ>& r) {
-        const bool whole = k + 1 < a.ib;
-        fetch_rows<kFromZ>(a, row_at[t] + 256 * k, row_exp[t] + 16 * k, whole || tail0, whole || tail1, r);
+        const uint32_t at = row_at[t] + 256 * k, exp = row_exp[t] + 16 * k;
+        if (k < whole) fetch_rows<kFromZ, true>(a, at, exp, true, true, r);
+        else fetch_rows<kFromZ, false>(a, at, exp, tail0, tail1, r);
     };
     auto clear = [&] {
 #pragma unroll
@@ -739,14 +755,14 @@ cudaError_t launch_few(FewArgs a, int from, int sms, cudaStream_t s)
     if (e != cudaSuccess) return e;
     e = allow_all_shared<ep_few_down_kernel<NT>>();
     if (e != cudaSuccess) return e;
-    const int ctas = a.H / 16;
-    int warps = kWarpsPerSm<NT>;
+    // as many warps to a CTA as let all CTAs run at once; fewer where rows' sums would leave no room for the weights
+    const int ctas = a.H / 16, per_sm = (ctas + sms - 1) / sms;
+    int warps = per_sm < kWarpsPerSm<NT> ? kWarpsPerSm<NT> / per_sm : 1;
     auto shared = [&] {
         return entries_bytes(a.pairs, a.experts, a.rows) + (size_t)(a.pairs + 3) / 4 * 16 + (size_t)warps * a.rows * 64 +
                (size_t)warps * kAhead<NT> * kStepBytes;
     };
-    while (warps > 4 && (int64_t)ctas * warps > (int64_t)sms * kWarpsPerSm<NT>) warps /= 2;
-    while (shared() > 226 * 1024) warps /= 2;   // ends: one warp of 4096 pairs and 1024 experts takes 84 KB
+    while (shared() > 226 * 1024) --warps;   // ends: one warp of 4096 pairs and 1024 experts takes 84 KB
     return launch_dependent(ep_few_down_kernel<NT>, dim3(ctas), dim3(32 * warps), shared(), s, a);
 }
 
