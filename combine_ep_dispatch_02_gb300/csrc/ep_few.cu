@@ -289,6 +289,8 @@ __device__ __forceinline__ float half_rows(const Rows16<FROM>& r, uint32_t (&b)[
     return 0.0f;
 }
 
+constexpr int kStepBytes = 2048;   // 16 rows of a block of 128 columns
+
 // Eight columns' sums of a block of 128, times their scales, into tot: w holds the block's 16 rows of weights (row g,
 // row g + 8; then the second 64 columns), f the lane's row's factor (1 unless FACTOR), s0 and s1 the scales of rows g and
 // g + 8.
@@ -319,30 +321,54 @@ __device__ __forceinline__ void add_block(float (&tot)[4], const uint4 (&w)[4], 
     tot[3] = fmaf(d[0][3] + d[1][3], s1 * f1, tot[3]);
 }
 
-// Steps of 2 KB that a warp's weights are read ahead, and warps of an SM; the other operand and the scales are read one
-// step ahead.
-constexpr int kStepBytes = 2048;
-#ifndef V_D1
-#define V_D1 6
-#endif
-#ifndef V_DN
-#define V_DN 4
-#endif
-#ifndef V_WN
-#define V_WN 16
-#endif
-template <int NT>
-constexpr int kAhead = NT == 1 ? V_D1 : V_DN;
-template <int NT>
-constexpr int kWarpsPerSm = NT == 1 ? 16 : V_WN;
-// Eights of rows that are fetched ahead: a whole step's, or with more than two, one eight ahead of the one in hand.
-template <int NT>
-constexpr int kFetched = NT <= 2 ? NT : 1;
+// Two matrices' sums of a block at once; their weights, from `from` in shared memory on, are read one after the other.
+template <bool FACTOR>
+__device__ __forceinline__ void add_two_blocks(float (&tot)[2][4], uint32_t from, const uint32_t (&b)[16], float f, float s0,
+                                               float s1)
+{
+    float f0 = 1.0f, f1 = 1.0f;
+    if constexpr (FACTOR) {
+        const int q = threadIdx.x & 3;
+        f0 = __shfl_sync(0xffffffffu, f, 8 * q);
+        f1 = __shfl_sync(0xffffffffu, f, 8 * q + 4);
+    }
+    const float scale[4] = {s0 * f0, s0 * f1, s1 * f0, s1 * f1};
+    uint4 w[2][4];
+    read_weights(from, w[0]);
+    read_weights(from + kStepBytes, w[1]);
+    float d[2][4] = {};
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const uint4 &l = w[m][2 * c], &h = w[m][2 * c + 1];
+                const uint32_t lo = i == 0 ? l.x : i == 1 ? l.y : i == 2 ? l.z : l.w, hi = i == 0 ? h.x : i == 1 ? h.y : i == 2 ? h.z : h.w;
+                const uint32_t x[4] = {half_codes(lo, false), half_codes(hi, false), half_codes(lo, true), half_codes(hi, true)};
+                mma_f16(d[m], x, b[8 * c + 2 * i], b[8 * c + 2 * i + 1]);
+            }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tot[m][i] = fmaf(d[m][i], scale[i], tot[m][i]);
+}
 
-// Up projection and SwiGLU.  A unit is 8 columns of z, its 8 gate rows and 8 up rows, for one entry, and a warp's, or with
-// SPLIT `split` warps', which share its K.
+// Steps that a warp's weights are read ahead, of 4 KB in the first kernel and 2 KB in the second; the other operand and the
+// scales are read one step ahead.  More of them took longer: 7 rows of 8 experts of 7168 x 2048 194 us, with 3 and 6 steps
+// 261 us, because what shared memory takes the other operand lacks in the SM's cache.
+constexpr int kUpStepBytes = 2 * kStepBytes, kUpAhead = 2, kDownAhead = 3;
+
+// Warps of an SM, by the registers that they take.
+template <int NT>
+constexpr int kUpWarpsPerSm = NT == 1 ? 16 : 12;
+template <int NT>
+constexpr int kDownWarpsPerSm = NT == 1 ? 20 : 16;
+
+// Up projection and SwiGLU.  A unit is 16 columns of z for one entry, two matrices of 8 gate rows and 8 up rows, so that what
+// it takes to make the other operand is shared by two; a unit is a warp's, or with SPLIT `split` warps', which share its K.
 template <int FROM, int NT, bool SPLIT>
-__global__ void __launch_bounds__(32 * kUpWarps, kWarpsPerSm<NT> / kUpWarps) ep_few_up_kernel(const FewArgs a)
+__global__ void __launch_bounds__(32 * kUpWarps, kUpWarpsPerSm<NT> / kUpWarps) ep_few_up_kernel(const FewArgs a)
 {
     extern __shared__ __align__(16) uint8_t shared[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
@@ -350,38 +376,42 @@ __global__ void __launch_bounds__(32 * kUpWarps, kWarpsPerSm<NT> / kUpWarps) ep_
     follow_predecessor();
     const int entries = make_entries(a, s, 8 * NT);
     const int split = SPLIT ? a.split : 1, teams = kUpWarps / split, team = warp / split, member = warp % split;
-    const int slices = a.I / 8, units = entries * slices;
+    const int slices = a.I / 16, units = entries * slices;
     const int k_lo = a.hb * member / split, k_hi = a.hb * (member + 1) / split, nb = k_hi - k_lo;
     const int u0 = blockIdx.x * teams + team, stride = gridDim.x * teams;
     const int mine = u0 < units ? (units - 1 - u0) / stride + 1 : 0;
     const int steps = mine * nb;
 
-    constexpr int D = kAhead<NT>, kElement = FROM == kFromE4m3 ? 1 : 2;
+    constexpr int D = kUpAhead, kElement = FROM == kFromE4m3 ? 1 : 2;
     constexpr bool kFactor = FROM != kFromFp16;
     // a lane fills and reads its own bytes of the warp's ring, so that nothing passes between lanes
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(shared + entries_bytes(a.pairs, a.experts, a.rows)) +
-                          warp * D * kStepBytes + 16 * lane;
-    const uint32_t ring_end = ring + D * kStepBytes;
+                          warp * D * kUpStepBytes + 16 * lane;
+    const uint32_t ring_end = ring + D * kUpStepBytes;
     // Of K's last block a lane's columns of either chunk may not exist.
     const bool tail = a.H % 128 != 0 && k_hi == a.hb, tail0 = !tail || 128 * (a.hb - 1) + 16 * q < a.H,
                tail1 = !tail || 128 * (a.hb - 1) + 16 * q + 64 < a.H;
     const int whole = a.H / 128;   // blocks without such columns
-    const int64_t up_rows = (int64_t)a.I * a.H;
+    const int64_t up_rows = (int64_t)a.I * a.H, eight_rows = 8 * (int64_t)a.H;
     int lu = u0, left = steps > 0 ? nb : 0;   // of the loads: unit, and its blocks not yet under way
     const uint8_t *lp = nullptr, *lq = nullptr;
     auto point = [&] {
         const int entry = lu / slices;
-        lp = a.up + ((int64_t)s.expert[entry] * 2 * a.I + 8 * (lu - entry * slices) + g) * a.H + 128 * k_lo + 16 * q;
+        lp = a.up + ((int64_t)s.expert[entry] * 2 * a.I + 16 * (lu - entry * slices) + g) * a.H + 128 * k_lo + 16 * q;
         lq = lp + up_rows;
     };
     if (left > 0) point();
     auto load = [&](uint32_t to) {
         if (left > 0) {
             const bool in0 = left > 1 || tail0, in1 = left > 1 || tail1;
-            copy_weights(to, lp, in0);
-            copy_weights(to + 512, lq, in0);
-            copy_weights(to + 1024, lp + 64, in1);
-            copy_weights(to + 1536, lq + 64, in1);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const uint8_t *p = lp + m * eight_rows, *r = lq + m * eight_rows;
+                copy_weights(to + kStepBytes * m, p, in0);
+                copy_weights(to + kStepBytes * m + 512, r, in0);
+                copy_weights(to + kStepBytes * m + 1024, p + 64, in1);
+                copy_weights(to + kStepBytes * m + 1536, r + 64, in1);
+            }
             lp += 128;
             lq += 128;
             if (--left == 0) {
@@ -394,7 +424,7 @@ __global__ void __launch_bounds__(32 * kUpWarps, kWarpsPerSm<NT> / kUpWarps) ep_
         }
         copies_commit();
     };
-    for (uint32_t to = ring; to != ring_end; to += kStepBytes) load(to);
+    for (uint32_t to = ring; to != ring_end; to += kUpStepBytes) load(to);
 
     // the unit whose operand is fetched, and the block of K.  Columns past an entry's rows repeat one of its rows: what
     // they sum up is not used.
@@ -407,8 +437,8 @@ __global__ void __launch_bounds__(32 * kUpWarps, kWarpsPerSm<NT> / kUpWarps) ep_
         first = s.start[entry];
         n = s.start[entry + 1] - first;
         const float* es = a.up_scales + (int64_t)s.expert[entry] * a.ub * a.hb;
-        gs = es + (int64_t)(8 * slice / 128) * a.hb;
-        us = es + (int64_t)((a.I + 8 * slice) / 128) * a.hb;
+        gs = es + (int64_t)(16 * slice / 128) * a.hb;
+        us = es + (int64_t)((a.I + 16 * slice) / 128) * a.hb;
         k = k_lo;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -417,8 +447,8 @@ __global__ void __launch_bounds__(32 * kUpWarps, kWarpsPerSm<NT> / kUpWarps) ep_
             row_scale[t] = row * a.hb;
         }
     };
-    Rows16<FROM> x[kFetched<NT>];
-    float s0 = 0.0f, s1 = 0.0f, tot[NT][4];
+    Rows16<FROM> x[NT];
+    float s0 = 0.0f, s1 = 0.0f, tot[NT][2][4];
     auto fetch = [&](int t, Rows16<FROM>& r) {
         const uint32_t at = row_at[t] + 128 * kElement * k, scale = row_scale[t] + k;
         if (k < whole) fetch_rows<FROM, true>(a, at, scale, true, true, r);
@@ -432,14 +462,14 @@ __global__ void __launch_bounds__(32 * kUpWarps, kWarpsPerSm<NT> / kUpWarps) ep_
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) tot[t][i] = 0.0f;
+            for (int i = 0; i < 8; ++i) tot[t][i / 4][i & 3] = 0.0f;
     };
     clear();
     if (steps > 0) {
         begin();
         scales();
 #pragma unroll
-        for (int t = 0; t < kFetched<NT>; ++t)
+        for (int t = 0; t < NT; ++t)
             if (8 * t < n) fetch(t, x[t]);
     }
     // z of a unit from its whole sums, and its power of two
@@ -448,61 +478,43 @@ __global__ void __launch_bounds__(32 * kUpWarps, kWarpsPerSm<NT> / kUpWarps) ep_
         for (int t = 0; t < NT; ++t) {
             if (8 * t >= n) break;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const float z = tot[t][c] * sigmoid_and_rest(tot[t][c]).x * tot[t][2 + c];
-                float m = fmaxf(fabsf(z), 0.0f);   // NaN counts as 0
+            for (int i = 0; i < 4; ++i) {
+                const int m = i / 2, c = i & 1;
+                const float z = tot[t][m][c] * sigmoid_and_rest(tot[t][m][c]).x * tot[t][m][2 + c];
+                float top = fmaxf(fabsf(z), 0.0f);   // NaN counts as 0
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 // the largest of the 8 to 2^14 .. 2^15; an infinity stays one
-                const int e = min(max((int)(__float_as_uint(m) >> 23) - 127, -110), 127);
+                const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -110), 127);
                 const int column = 8 * t + 2 * q + c;
                 if (column >= n) continue;
                 const int64_t place = first + column;
-                reinterpret_cast<__half*>(a.z)[place * a.I + 8 * slice + g] = __float2half_rn(z * power2(14 - e));
-                if (g == 0) a.z_exp[place * slices + slice] = m > 0.0f ? (uint8_t)(e + 128) : 0;
+                reinterpret_cast<__half*>(a.z)[place * a.I + 16 * slice + 8 * m + g] = __float2half_rn(z * power2(14 - e));
+                if (g == 0) a.z_exp[place * 2 * slices + 2 * slice + m] = top > 0.0f ? (uint8_t)(e + 128) : 0;
             }
         }
     };
     uint32_t at = ring;
-    // One step of a unit of `rows` rows, whose operand is here, or its first 8 rows'.  The next step's is fetched: that of
+    // One step of a unit of `rows` rows, whose operand is here.  The next step's is fetched: that of
     // the same unit's next block, or, once `next` has begun another unit, of its first.  MORE: there is a next step.
     auto step = [&](auto more, int rows, auto next) {
         constexpr bool MORE = decltype(more)::value;
-        uint4 w[4];
         copies_wait<D - 1>();
-        read_weights(at, w);
         const float s0_now = s0, s1_now = s1;
-        if constexpr (kFetched<NT> == NT) {
-            if constexpr (MORE) {
-                next();
-                scales();
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if (8 * t >= rows && (!MORE || 8 * t >= n)) break;
-                uint32_t b[16];
-                const float f = half_rows<FROM>(x[t], b);   // of nothing, past `rows`: not used
-                if (MORE && 8 * t < n) fetch(t, x[t]);
-                if (8 * t < rows) add_block<kFactor>(tot[t], w, b, f, s0_now, s1_now);
-            }
-        } else {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if (8 * t >= rows) break;
-                uint32_t b[16];
-                const float f = half_rows<FROM>(x[0], b);
-                if (t + 1 < NT && 8 * (t + 1) < rows) {
-                    fetch(t + 1 < NT ? t + 1 : 0, x[0]);
-                } else if constexpr (MORE) {
-                    next();
-                    scales();
-                    fetch(0, x[0]);
-                }
-                add_block<kFactor>(tot[t], w, b, f, s0_now, s1_now);
-            }
+        if constexpr (MORE) {
+            next();
+            scales();
         }
-        load(at);   // its bytes are in registers, and used
-        at = at + kStepBytes == ring_end ? ring : at + kStepBytes;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            if (8 * t >= rows && (!MORE || 8 * t >= n)) break;
+            uint32_t b[16];
+            const float f = half_rows<FROM>(x[t], b);   // of nothing, past `rows`: not used
+            if (MORE && 8 * t < n) fetch(t, x[t]);
+            if (8 * t < rows) add_two_blocks<kFactor>(tot[t], at, b, f, s0_now, s1_now);
+        }
+        load(at);   // its bytes have been read, and used
+        at = at + kUpStepBytes == ring_end ? ring : at + kUpStepBytes;
     };
     constexpr std::true_type kMore{};
     constexpr std::false_type kLast{};
@@ -523,7 +535,7 @@ __global__ void __launch_bounds__(32 * kUpWarps, kWarpsPerSm<NT> / kUpWarps) ep_
         return;
     }
     // a unit's warps meet once per round, and every team of the CTA makes as many rounds
-    __shared__ float4 parts[2][kUpWarps][NT][32];   // [round's parity]: sums of a unit's K
+    __shared__ float4 parts[kUpWarps][NT][2][32];   // sums of a unit's K
     const int first_unit = blockIdx.x * teams;
     const int rounds = first_unit < units ? (units - 1 - first_unit) / stride + 1 : 0;
     for (int round = 0; round < rounds; ++round) {
@@ -532,24 +544,32 @@ __global__ void __launch_bounds__(32 * kUpWarps, kWarpsPerSm<NT> / kUpWarps) ep_
         const int entry = has ? unit / slices : 0, slice_now = unit - entry * slices;
         const int first_now = has ? s.start[entry] : 0, n_now = has ? s.start[entry + 1] - first_now : 0;
         if (has && nb > 0) unit_steps(round + 1 < mine);
+        if (member > 0) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-            if (8 * t < n_now) parts[round & 1][warp][t][lane] = make_float4(tot[t][0], tot[t][1], tot[t][2], tot[t][3]);
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+                    if (8 * t < n_now)
+                        parts[warp][t][m][lane] = make_float4(tot[t][m][0], tot[t][m][1], tot[t][m][2], tot[t][m][3]);
+        }
         __syncthreads();
         if (member == 0 && has) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 if (8 * t >= n_now) break;
-                for (int m = 1; m < split; ++m) {
-                    const float4 v = parts[round & 1][warp + m][t][lane];
-                    tot[t][0] += v.x;
-                    tot[t][1] += v.y;
-                    tot[t][2] += v.z;
-                    tot[t][3] += v.w;
-                }
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+                    for (int w = 1; w < split; ++w) {
+                        const float4 v = parts[warp + w][t][m][lane];
+                        tot[t][m][0] += v.x;
+                        tot[t][m][1] += v.y;
+                        tot[t][m][2] += v.z;
+                        tot[t][m][3] += v.w;
+                    }
             }
             finish(first_now, n_now, slice_now);
         }
+        __syncthreads();   // the sums have been taken
         clear();
     }
 }
@@ -557,7 +577,7 @@ __global__ void __launch_bounds__(32 * kUpWarps, kWarpsPerSm<NT> / kUpWarps) ep_
 // Down projection and the weighted sum.  A CTA owns 16 output columns; its warps share the blocks of all entries' K
 // evenly, and each keeps the rows' sums of its own part in shared memory.
 template <int NT>
-__global__ void __launch_bounds__(32 * kWarpsPerSm<NT>) ep_few_down_kernel(const FewArgs a)
+__global__ void __launch_bounds__(32 * kDownWarpsPerSm<NT>) ep_few_down_kernel(const FewArgs a)
 {
     extern __shared__ __align__(16) uint8_t shared[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
@@ -572,7 +592,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerSm<NT>) ep_few_down_kernel(const
     const int total = entries * a.ib;
     const int lo = (int)((int64_t)total * warp / warps), hi = (int)((int64_t)total * (warp + 1) / warps);
 
-    constexpr int D = kAhead<NT>;
+    constexpr int D = kDownAhead;
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sums + (size_t)warps * a.rows * 16) + warp * D * kStepBytes + 16 * lane;
     const uint32_t ring_end = ring + D * kStepBytes;
     // Of K's last block a lane's columns of either chunk may not exist.
@@ -629,7 +649,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerSm<NT>) ep_few_down_kernel(const
             row_exp[t] = place * (a.I / 8) + 2 * q;
         }
     };
-    Rows16<kFromZ> x[kFetched<NT>];
+    Rows16<kFromZ> x[NT];
     float sc = 0.0f, tot[NT][4];
     auto fetch = [&](int t, Rows16<kFromZ>& r) {
         const uint32_t at = row_at[t] + 256 * k, exp = row_exp[t] + 16 * k;
@@ -647,7 +667,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerSm<NT>) ep_few_down_kernel(const
         begin();
         sc = ds[k];
 #pragma unroll
-        for (int t = 0; t < kFetched<NT>; ++t)
+        for (int t = 0; t < NT; ++t)
             if (8 * t < n) fetch(t, x[t]);
     }
     // an entry's rows are distinct, so that no two lanes add to one place
@@ -674,34 +694,17 @@ __global__ void __launch_bounds__(32 * kWarpsPerSm<NT>) ep_few_down_kernel(const
         copies_wait<D - 1>();
         read_weights(at, w);
         const float sc_now = sc;
-        if constexpr (kFetched<NT> == NT) {
-            if constexpr (MORE) {
-                next();
-                sc = ds[k];
-            }
+        if constexpr (MORE) {
+            next();
+            sc = ds[k];
+        }
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if (8 * t >= rows && (!MORE || 8 * t >= n)) break;
-                uint32_t b[16];
-                const float f = half_rows<kFromZ>(x[t], b);   // of nothing, past `rows`: not used
-                if (MORE && 8 * t < n) fetch(t, x[t]);
-                if (8 * t < rows) add_block<true>(tot[t], w, b, f, sc_now, sc_now);
-            }
-        } else {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if (8 * t >= rows) break;
-                uint32_t b[16];
-                const float f = half_rows<kFromZ>(x[0], b);
-                if (t + 1 < NT && 8 * (t + 1) < rows) {
-                    fetch(t + 1 < NT ? t + 1 : 0, x[0]);
-                } else if constexpr (MORE) {
-                    next();
-                    sc = ds[k];
-                    fetch(0, x[0]);
-                }
-                add_block<true>(tot[t], w, b, f, sc_now, sc_now);
-            }
+        for (int t = 0; t < NT; ++t) {
+            if (8 * t >= rows && (!MORE || 8 * t >= n)) break;
+            uint32_t b[16];
+            const float f = half_rows<kFromZ>(x[t], b);   // of nothing, past `rows`: not used
+            if (MORE && 8 * t < n) fetch(t, x[t]);
+            if (8 * t < rows) add_block<true>(tot[t], w, b, f, sc_now, sc_now);
         }
         load(at);   // its bytes are in registers, and used
         at = at + kStepBytes == ring_end ? ring : at + kStepBytes;
@@ -730,10 +733,10 @@ __global__ void __launch_bounds__(32 * kWarpsPerSm<NT>) ep_few_down_kernel(const
 template <int FROM, int NT>
 cudaError_t launch_up(const FewArgs& a, int sms, cudaStream_t s)
 {
-    const size_t shared = entries_bytes(a.pairs, a.experts, a.rows) + (size_t)kUpWarps * kAhead<NT> * kStepBytes;
+    const size_t shared = entries_bytes(a.pairs, a.experts, a.rows) + (size_t)kUpWarps * kUpAhead * kUpStepBytes;
     const int64_t entries = a.pairs < a.experts ? a.pairs : (int64_t)a.experts + a.pairs / (8 * NT);   // at most
-    const int64_t teams = kUpWarps / a.split, ctas = (entries * (a.I / 8) + teams - 1) / teams;
-    const int64_t fit = (int64_t)sms * (kWarpsPerSm<NT> / kUpWarps);
+    const int64_t teams = kUpWarps / a.split, ctas = (entries * (a.I / 16) + teams - 1) / teams;
+    const int64_t fit = (int64_t)sms * (kUpWarpsPerSm<NT> / kUpWarps);
     const dim3 grid((unsigned)(ctas < fit ? ctas : fit)), block(32 * kUpWarps);
     if (a.split > 1) {
         const cudaError_t e = allow_all_shared<ep_few_up_kernel<FROM, NT, true>>();
@@ -746,10 +749,15 @@ cudaError_t launch_up(const FewArgs& a, int sms, cudaStream_t s)
 template <int NT>
 cudaError_t launch_few(FewArgs a, int from, int sms, cudaStream_t s)
 {
-    // experts that rows name, at most: with fewer units than half of the warps that run at once, more warps share one
-    const int64_t units = (int64_t)(a.pairs < a.experts ? a.pairs : a.experts) * (a.I / 8);
+    // Warps to a unit: such that the last round of units, of the experts that rows name at most, leaves few warps idle; each
+    // doubling costs some 5 %.
+    const int64_t units = (int64_t)(a.pairs < a.experts ? a.pairs : a.experts) * (a.I / 16), at_once = (int64_t)sms * kUpWarpsPerSm<NT>;
+    auto cost = [&](int split) {   // in units of one warp, times 1.05 per doubling
+        return (double)((units * split + at_once - 1) / at_once) / split * (split == 1 ? 1.0 : split == 2 ? 1.05 : 1.1);
+    };
     a.split = 1;
-    while (a.split < kUpWarps && units * a.split * 2 <= (int64_t)sms * kWarpsPerSm<NT>) a.split *= 2;
+    for (int split = 2; split <= kUpWarps; split *= 2)
+        if (cost(split) < cost(a.split)) a.split = split;
     cudaError_t e = from == kFromE4m3 ? launch_up<kFromE4m3, NT>(a, sms, s)
                     : from == kFromFp16 ? launch_up<kFromFp16, NT>(a, sms, s) : launch_up<kFromBf16, NT>(a, sms, s);
     if (e != cudaSuccess) return e;
@@ -757,10 +765,10 @@ cudaError_t launch_few(FewArgs a, int from, int sms, cudaStream_t s)
     if (e != cudaSuccess) return e;
     // as many warps to a CTA as let all CTAs run at once; fewer where rows' sums would leave no room for the weights
     const int ctas = a.H / 16, per_sm = (ctas + sms - 1) / sms;
-    int warps = per_sm < kWarpsPerSm<NT> ? kWarpsPerSm<NT> / per_sm : 1;
+    int warps = per_sm < kDownWarpsPerSm<NT> ? kDownWarpsPerSm<NT> / per_sm : 1;
     auto shared = [&] {
         return entries_bytes(a.pairs, a.experts, a.rows) + (size_t)(a.pairs + 3) / 4 * 16 + (size_t)warps * a.rows * 64 +
-               (size_t)warps * kAhead<NT> * kStepBytes;
+               (size_t)warps * kDownAhead * kStepBytes;
     };
     while (shared() > 226 * 1024) --warps;   // ends: one warp of 4096 pairs and 1024 experts takes 84 KB
     return launch_dependent(ep_few_down_kernel<NT>, dim3(ctas), dim3(32 * warps), shared(), s, a);
@@ -826,8 +834,8 @@ extern "C" int ep_moe_few_rows(const void* x, const float* x_scales, int x_dtype
     if (sms == 0) return layer_fail(EP_ERR_CUDA, "%s: cannot tell the current device's multiprocessors", who);
     const int from = x_dtype == EP_FP8_E4M3 ? kFromE4m3 : x_dtype == EP_FP16 ? kFromFp16 : kFromBf16;
     cudaStream_t s = (cudaStream_t)stream;
-    // an expert's rows, at most all of them, in entries of 8, 16 or 32
-    const cudaError_t e = rows <= 8 ? launch_few<1>(a, from, sms, s) : rows <= 16 ? launch_few<2>(a, from, sms, s)
-                                                                                  : launch_few<4>(a, from, sms, s);
+    // An expert's rows, at most all of them, in entries of 8 or 16.  Entries of 32 took longer even for 63 rows to each of 8
+    // experts (221 against 212 us), because the sums leave fewer registers for warps.
+    const cudaError_t e = rows <= 8 ? launch_few<1>(a, from, sms, s) : launch_few<2>(a, from, sms, s);
     return layer_cuda(e, "ep_moe_few_rows: launch");
 }
