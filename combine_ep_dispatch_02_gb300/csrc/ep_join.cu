@@ -61,67 +61,76 @@ __device__ __forceinline__ void load_channels(const void* p, int fp32, int v, fl
     }
 }
 
-// Two sums over a row's threads, a warp or a CTA; `part` holds 32 pairs that no thread still reads.
+// Two sums over a row's threads, a warp or a CTA of up to 16; `part` holds 16 pairs that no thread still reads.  Half of a
+// warp adds up one of them, the other half the other.
 template <bool WARP>
-__device__ __forceinline__ float2 row_sums(float2 s, float2* part)
+__device__ __forceinline__ float2 row_sums(float2 s, float* part)
 {
-    auto warp_sums = [&] {
+    const int lane = threadIdx.x & 31;
+    const bool upper = lane & 16;
+    float v = upper ? s.y : s.x;
+    v += __shfl_xor_sync(0xffffffffu, upper ? s.x : s.y, 16);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
-            s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
-        }
-    };
-    warp_sums();
+    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if constexpr (!WARP) {
-        const int lane = threadIdx.x & 31;
-        if (lane == 0) part[threadIdx.x >> 5] = s;
+        if ((lane & 15) == 0) part[(lane & 16) + (threadIdx.x >> 5)] = v;
         __syncthreads();
-        s = lane < (int)(blockDim.x >> 5) ? part[lane] : make_float2(0.0f, 0.0f);
-        warp_sums();
+        v = (lane & 15) < (int)(blockDim.x >> 5) ? part[lane] : 0.0f;
+#pragma unroll
+        for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     }
-    return s;
+    const float other = __shfl_xor_sync(0xffffffffu, v, 16);
+    return upper ? make_float2(other, v) : make_float2(v, other);
 }
 
-__device__ __forceinline__ float sum_of(const float2 (&f)[4])
+// 1 / sqrt(v): the approximation, off by two units, and one step of Newton's method.
+__device__ __forceinline__ float root_of(float v)
 {
-    return ((f[0].x + f[0].y) + (f[1].x + f[1].y)) + ((f[2].x + f[2].y) + (f[3].x + f[3].y));
+    float r;
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    const float e = fmaf(-v * r, r, 1.0f);   // not a number where v is 0 or infinite, whose roots are exact
+    return fabsf(e) < 1.0f ? fmaf(0.5f * r, e, r) : r;
 }
 
-// ---- rows up to kJoinTeamHidden: one CTA of a vector of 8 columns per thread walks rows blockIdx.x, + gridDim.x, ...
+// ---- rows up to kJoinTeamHidden: one CTA of VPT vectors of 8 columns per thread walks rows blockIdx.x, + gridDim.x, ...
 //
 // Rows are on their way through STAGES stages of shared memory, of which a thread fills and reads its own vectors only,
 // so that no barrier passes between copy and use.  The vectors along the channels (both weights and the channels' gate)
 // lie there too.  A row needs two sums over its threads, the second from the first's result, and a CTA's sum costs
-// some 500 cycles of shuffles and barrier; so the first sum of the next row is made together with the second of this one,
-// and a row meets one barrier.
+// some 400 cycles of shuffles and barrier; so the first sum of the next row is made together with the second of this one,
+// and a row meets one barrier.  What bounds it is the instructions as much as the bytes: two vectors per thread halve what
+// sums, roots and addresses cost an element, and FP32 arithmetic is done in pairs.
 
-constexpr int kJoinTeamThreads = 1024;
-constexpr int kJoinTeamHidden = 8 * kJoinTeamThreads;
+constexpr int kJoinTeamThreads = 512;
+constexpr int kJoinTeamHidden = 16 * kJoinTeamThreads;
 
 // A thread's vectors along the channels in shared memory: post_weight, gate, pre_weight, 16 bytes each or 32 for FP32.
 struct Channels {
     uint4 *post, *gate, *pre;
 };
 
-__host__ __device__ inline int channel_vectors(const JoinArgs& a)   // 16-byte vectors of all three
+__host__ __device__ inline int channel_vectors(const JoinArgs& a)   // 16-byte vectors of all three, per vector of a row
 {
     return (a.post_weight ? 1 + (a.post_fp32 != 0) : 0) + (a.gate_kind == EP_GATE_CHANNEL ? 1 + (a.gate_fp32 != 0) : 0) +
            (a.pre_weight ? 1 + (a.pre_fp32 != 0) : 0);
 }
 
+template <int VPT>
 __device__ __forceinline__ Channels fetch_channels(const JoinArgs& a, uint4* to)   // part of the first group of copies
 {
-    const int t = threadIdx.x;
+    const int t = threadIdx.x, width = VPT * blockDim.x;
     auto fetch = [&](const void* from, int fp32) {
         uint4* at = to;
-        to += blockDim.x << (fp32 != 0);
-        if (t < a.vecs) {
-            if (fp32) {   // the second half of a thread's eight lies a row of vectors further on
-                copy16(at + t, (const uint8_t*)from + 32 * t);
-                copy16(at + blockDim.x + t, (const uint8_t*)from + 32 * t + 16);
+        to += width << (fp32 != 0);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = i * blockDim.x + t;
+            if (v >= a.vecs) continue;
+            if (fp32) {   // the second half of a vector's eight lies a row of vectors further on
+                copy16(at + v, (const uint8_t*)from + 32 * v);
+                copy16(at + width + v, (const uint8_t*)from + 32 * v + 16);
             } else {
-                copy16(at + t, (const uint8_t*)from + 16 * t);
+                copy16(at + v, (const uint8_t*)from + 16 * v);
             }
         }
         return at + t;
@@ -133,11 +142,12 @@ __device__ __forceinline__ Channels fetch_channels(const JoinArgs& a, uint4* to)
     return c;
 }
 
-template <bool FP16>
-__device__ __forceinline__ void read_channels(const uint4* p, int fp32, float2 (&w)[4])
+template <bool FP16, int VPT>
+__device__ __forceinline__ void read_channels(const uint4* p, int fp32, int i, float2 (&w)[4])   // the thread's vector i
 {
+    p += i * blockDim.x;
     if (fp32) {
-        const float4 lo = *reinterpret_cast<const float4*>(p), hi = *reinterpret_cast<const float4*>(p + blockDim.x);
+        const float4 lo = *reinterpret_cast<const float4*>(p), hi = *reinterpret_cast<const float4*>(p + VPT * blockDim.x);
         w[0] = make_float2(lo.x, lo.y);
         w[1] = make_float2(lo.z, lo.w);
         w[2] = make_float2(hi.x, hi.y);
@@ -147,118 +157,141 @@ __device__ __forceinline__ void read_channels(const uint4* p, int fp32, float2 (
     }
 }
 
-template <bool FP16, bool WARP, int STAGES>
-__global__ void __launch_bounds__(WARP ? 32 : kJoinTeamThreads) ep_join_team_kernel(const JoinArgs a)
+template <bool FP16, bool WARP, int VPT, int STAGES>
+__global__ void __launch_bounds__(WARP ? 32 : kJoinTeamThreads, WARP ? 24 : 2) ep_join_team_kernel(const JoinArgs a)
 {
     extern __shared__ uint4 staged[];
-    __shared__ float2 part[2][32];
-    const int t = threadIdx.x;
-    const bool in = t < a.vecs;
-    const int64_t at = 16 * (int64_t)t, pitch = 16 * (int64_t)a.vecs;
+    __shared__ float part[2][32];
+    const int t = threadIdx.x, threads = blockDim.x;
+    const bool all = (VPT - 1) * threads + t < a.vecs;   // the thread's last vector exists; with two, the first always does
+    const int64_t at = 16 * (int64_t)t, pitch = 16 * (int64_t)a.vecs, next_vector = 16 * (int64_t)threads;
     const bool element = a.gate_kind == EP_GATE_ELEMENT;
-    const int slots = element ? 3 : 2;   // y, residual, the elements' gate
+    const int slots = element ? 3 : 2, slot = VPT * threads;   // y, residual, the elements' gate
     const float inv_hidden = __frcp_rn((float)a.hidden);
     follow_predecessor();
-    const Channels ch = fetch_channels(a, staged + STAGES * slots * blockDim.x);
-    auto stage_of = [&](int stage) { return staged + stage * slots * blockDim.x + t; };
-    auto fetch = [&](int64_t row, int stage) {
-        if (in && row < a.rows) {
-            uint4* to = stage_of(stage);
-            copy16(to, a.y + row * a.y_pitch + at);
-            copy16(to + blockDim.x, a.residual + row * a.r_pitch + at);
-            if (element) copy16(to + 2 * blockDim.x, a.gate + row * a.g_pitch + at);
+    const Channels ch = fetch_channels<VPT>(a, staged + STAGES * slots * slot);
+    uint4* const mine = staged + t;
+    int64_t ahead = blockIdx.x;   // the next row to fetch
+    const uint8_t *yp = a.y + ahead * a.y_pitch + at, *rp = a.residual + ahead * a.r_pitch + at;
+    const uint8_t* gp = a.gate + (element ? ahead * a.g_pitch + at : 0);
+    auto fetch = [&](int stage) {
+        if (ahead < a.rows) {
+            uint4* to = mine + stage * slots * slot;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                if (i + 1 == VPT && !all) break;
+                copy16(to + i * threads, yp + i * next_vector);
+                copy16(to + slot + i * threads, rp + i * next_vector);
+                if (element) copy16(to + 2 * slot + i * threads, gp + i * next_vector);
+            }
+            ahead += gridDim.x;
+            yp += gridDim.x * a.y_pitch;
+            rp += gridDim.x * a.r_pitch;
+            if (element) gp += gridDim.x * a.g_pitch;
         }
         copies_commit();
     };
     auto squares = [&](int stage) {   // of a row's y
-        float2 y[4], s = both(0.0f);
-        unpack4x2<FP16>(*stage_of(stage), y);
+        float2 s = both(0.0f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s = fused2(y[j], y[j], s);
+        for (int i = 0; i < VPT; ++i) {
+            if (i + 1 == VPT && !all) break;
+            float2 y[4];
+            unpack4x2<FP16>(mine[stage * slots * slot + i * threads], y);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s = fused2(y[j], y[j], s);
+        }
         return s.x + s.y;
     };
-    auto root = [&](float sum) { return __frsqrt_rn(fmaf(sum, inv_hidden, a.eps)); };
     auto gate_of = [&](int64_t row) {
         return a.gate_kind == EP_GATE_ROW && row < a.rows ? reinterpret_cast<const float*>(a.gate)[row] : 1.0f;
     };
 #pragma unroll
-    for (int i = 0; i < STAGES; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
+    for (int i = 0; i < STAGES; ++i) fetch(i);
     float row_gate = gate_of(blockIdx.x), post = 1.0f;
     copies_wait<STAGES - 1>();
     if (a.post_weight) {
-        post = root(row_sums<WARP>(make_float2(in ? squares(0) : 0.0f, 0.0f), part[1]).x);
+        post = root_of(fmaf(row_sums<WARP>(make_float2(squares(0), 0.0f), part[1]).x, inv_hidden, a.eps));
         if (t == 0) a.post_rstd[blockIdx.x] = post;
     }
     int parity = 0, stage = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
-        const int64_t next = row + gridDim.x;
-        const float next_gate = gate_of(next);
-        float2 h[4], sums = both(0.0f);
-        if (in) {
+    int64_t out = blockIdx.x * pitch + at;   // bytes into h and n
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1, out += gridDim.x * pitch) {
+        const float next_gate = gate_of(row + gridDim.x);
+        float2 h[VPT][4], s = both(0.0f), sums = both(0.0f);
+        const float2 scale = both(row_gate * post), along = both(a.residual_scale);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            if (i + 1 == VPT && !all) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) h[i][j] = both(0.0f);
+                break;
+            }
+            const uint4* from = mine + stage * slots * slot + i * threads;
             float2 r[4], w[4];
-            unpack4x2<FP16>(*stage_of(stage), h);
-            unpack4x2<FP16>(stage_of(stage)[blockDim.x], r);
-            const float2 scale = both(row_gate * post), along = both(a.residual_scale);
+            unpack4x2<FP16>(from[0], h[i]);
+            unpack4x2<FP16>(from[slot], r);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) h[j] = mul2(h[j], scale);
+            for (int j = 0; j < 4; ++j) h[i][j] = mul2(h[i][j], scale);
             if (a.post_weight) {
-                read_channels<FP16>(ch.post, a.post_fp32, w);
+                read_channels<FP16, VPT>(ch.post, a.post_fp32, i, w);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) h[j] = mul2(h[j], w[j]);
+                for (int j = 0; j < 4; ++j) h[i][j] = mul2(h[i][j], w[j]);
             }
             if (element || a.gate_kind == EP_GATE_CHANNEL) {
-                if (element) unpack4x2<FP16>(stage_of(stage)[2 * blockDim.x], w);
-                else read_channels<FP16>(ch.gate, a.gate_fp32, w);
+                if (element) unpack4x2<FP16>(from[2 * slot], w);
+                else read_channels<FP16, VPT>(ch.gate, a.gate_fp32, i, w);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) h[j] = mul2(h[j], w[j]);
+                for (int j = 0; j < 4; ++j) h[i][j] = mul2(h[i][j], w[j]);
             }
-            float2 s = both(0.0f);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                h[j] = fused2(along, r[j], h[j]);
-                s = fused2(h[j], h[j], s);
+                h[i][j] = fused2(along, r[j], h[i][j]);
+                s = fused2(h[i][j], h[i][j], s);
             }
-            st_v4(a.h + row * pitch + at, pack4x2<FP16>(h));
-            sums.y = s.x + s.y;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) h[j] = both(0.0f);
+            st_v4(a.h + out + i * next_vector, pack4x2<FP16>(h[i]));
         }
+        sums.y = s.x + s.y;
         const int after = stage + 1 == STAGES ? 0 : stage + 1;
         copies_wait<STAGES - 2>();
-        if (a.post_weight && in && next < a.rows) sums.x = squares(after);
-        fetch(row + (int64_t)STAGES * gridDim.x, stage);
+        const bool another = row + gridDim.x < a.rows;
+        if (a.post_weight && another) sums.x = squares(after);
+        fetch(stage);
         stage = after;
         if (a.post_weight || a.pre_weight) sums = row_sums<WARP>(sums, part[parity]);
         if (a.post_weight) {
-            post = root(sums.x);
-            if (t == 0 && next < a.rows) a.post_rstd[next] = post;
+            post = root_of(fmaf(sums.x, inv_hidden, a.eps));
+            if (t == 0 && another) a.post_rstd[row + gridDim.x] = post;
         }
         row_gate = next_gate;
         if (!a.pre_weight) continue;
-        const float pre = root(sums.y);
+        const float pre = root_of(fmaf(sums.y, inv_hidden, a.eps));
         if (t == 0) a.pre_rstd[row] = pre;
-        float m = 0.0f;
-        if (in) {
-            float2 w[4];
-            read_channels<FP16>(ch.pre, a.pre_fp32, w);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                h[j] = mul2(mul2(h[j], both(pre)), w[j]);
-                m = fmaxf(m, fmaxf(fabsf(h[j].x), fabsf(h[j].y)));
+        for (int i = 0; i < VPT; ++i) {
+            const bool in = i + 1 < VPT || all;
+            float m = 0.0f;
+            if (in) {
+                float2 w[4];
+                read_channels<FP16, VPT>(ch.pre, a.pre_fp32, i, w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    h[i][j] = mul2(mul2(h[i][j], both(pre)), w[j]);
+                    m = fmaxf(m, fmaxf(fabsf(h[i][j].x), fabsf(h[i][j].y)));
+                }
+                if (a.n) st_v4(a.n + out + i * next_vector, pack4x2<FP16>(h[i]));
             }
-            if (a.n) st_v4(a.n + row * pitch + at, pack4x2<FP16>(h));
-        }
-        if (!a.q) continue;
+            if (!a.q) continue;
 #pragma unroll
-        for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float scale = e4m3_block_scale(m);
-        const float inv = __frcp_rn(scale);
-        if (in) {
-            *reinterpret_cast<uint2*>(a.q + row * a.hidden + 8 * t) =
-                make_uint2(e4m3x4_near(h[0].x, h[0].y, h[1].x, h[1].y, scale, inv),
-                           e4m3x4_near(h[2].x, h[2].y, h[3].x, h[3].y, scale, inv));
-            if ((t & 15) == 0) a.scales[row * a.blocks + (t >> 4)] = scale;
+            for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float block = quick_block_scale(m), inv = quick_reciprocal(block);
+            if (in) {
+                const int v = i * threads + t;
+                *reinterpret_cast<uint2*>(a.q + ((out - at) >> 1) + 8 * v) =
+                    make_uint2(e4m3x4_near(h[i][0].x, h[i][0].y, h[i][1].x, h[i][1].y, block, inv),
+                               e4m3x4_near(h[i][2].x, h[i][2].y, h[i][3].x, h[i][3].y, block, inv));
+                if ((t & 15) == 0) a.scales[row * a.blocks + (v >> 4)] = block;
+            }
         }
     }
 }
@@ -267,46 +300,67 @@ __global__ void __launch_bounds__(WARP ? 32 : kJoinTeamThreads) ep_join_team_ker
 // over the row needs is read from its stage again.
 enum { kSlotH, kSlotDn, kSlotDh, kSlotY, kSlotGate };   // a stage's vectors of a thread; the last for a gate per element
 
-template <bool FP16, bool WARP, int STAGES>
-__global__ void __launch_bounds__(WARP ? 32 : kJoinTeamThreads) ep_join_backward_kernel(const JoinArgs a)
+template <bool FP16, bool WARP, int VPT, int STAGES>
+__global__ void __launch_bounds__(WARP ? 32 : kJoinTeamThreads, 1) ep_join_backward_kernel(const JoinArgs a)
 {
     extern __shared__ uint4 staged[];
-    __shared__ float2 part[2][32];
-    const int t = threadIdx.x;
-    const bool in = t < a.vecs;
-    const int64_t at = 16 * (int64_t)t, pitch = 16 * (int64_t)a.vecs;
+    __shared__ float part[2][32];
+    const int t = threadIdx.x, threads = blockDim.x;
+    const bool all = (VPT - 1) * threads + t < a.vecs;   // as above
+    const int64_t at = 16 * (int64_t)t, pitch = 16 * (int64_t)a.vecs, next_vector = 16 * (int64_t)threads;
     const bool element = a.gate_kind == EP_GATE_ELEMENT;
-    const int slots = element ? 5 : 4;
+    const int slots = element ? 5 : 4, slot = VPT * threads;
     const float inv_hidden = __frcp_rn((float)a.hidden);
     follow_predecessor();
-    const Channels ch = fetch_channels(a, staged + STAGES * slots * blockDim.x);
-    auto vector = [&](int stage, int slot) { return staged + (stage * slots + slot) * blockDim.x + t; };
-    auto fetch = [&](int64_t row, int stage) {
-        if (in && row < a.rows) {
-            if (a.pre_weight) {
-                copy16(vector(stage, kSlotH), a.h_in + row * pitch + at);
-                copy16(vector(stage, kSlotDn), a.dn + row * a.dn_pitch + at);
+    const Channels ch = fetch_channels<VPT>(a, staged + STAGES * slots * slot);
+    uint4* const mine = staged + t;
+    auto vector = [&](int stage, int which, int i) { return mine + (stage * slots + which) * slot + i * threads; };
+    int64_t ahead = blockIdx.x;   // the next row to fetch
+    const uint8_t *hp = a.h_in + ahead * pitch + at, *np = a.dn + ahead * a.dn_pitch + at, *dp = a.dh + ahead * a.dh_pitch + at,
+                  *yp = a.y + ahead * a.y_pitch + at, *gp = a.gate + (element ? ahead * a.g_pitch + at : 0);
+    auto fetch = [&](int stage) {
+        if (ahead < a.rows) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                if (i + 1 == VPT && !all) break;
+                if (a.pre_weight) {
+                    copy16(vector(stage, kSlotH, i), hp + i * next_vector);
+                    copy16(vector(stage, kSlotDn, i), np + i * next_vector);
+                }
+                if (a.dh) copy16(vector(stage, kSlotDh, i), dp + i * next_vector);
+                copy16(vector(stage, kSlotY, i), yp + i * next_vector);
+                if (element) copy16(vector(stage, kSlotGate, i), gp + i * next_vector);
             }
-            if (a.dh) copy16(vector(stage, kSlotDh), a.dh + row * a.dh_pitch + at);
-            copy16(vector(stage, kSlotY), a.y + row * a.y_pitch + at);
-            if (element) copy16(vector(stage, kSlotGate), a.gate + row * a.g_pitch + at);
+            ahead += gridDim.x;
+            hp += gridDim.x * pitch;
+            np += gridDim.x * a.dn_pitch;
+            dp += gridDim.x * a.dh_pitch;
+            yp += gridDim.x * a.y_pitch;
+            if (element) gp += gridDim.x * a.g_pitch;
         }
         copies_commit();
     };
-    float2 dpost[4], dgate[4], dpre[4];
+    float2 dpost[VPT][4], dgate[VPT][4], dpre[VPT][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) dpost[j] = dgate[j] = dpre[j] = both(0.0f);
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dpost[i][j] = dgate[i][j] = dpre[i][j] = both(0.0f);
     // a row's sum of dn * pre_weight * h, and its part of pre_weight's gradient
     auto along_pre = [&](int stage, float pre) {
-        float2 h[4], g[4], w[4], s = both(0.0f);
-        unpack4x2<FP16>(*vector(stage, kSlotH), h);
-        unpack4x2<FP16>(*vector(stage, kSlotDn), g);
-        read_channels<FP16>(ch.pre, a.pre_fp32, w);
+        float2 s = both(0.0f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            g[j] = mul2(g[j], h[j]);
-            dpre[j] = fused2(g[j], both(pre), dpre[j]);
-            s = fused2(g[j], w[j], s);
+        for (int i = 0; i < VPT; ++i) {
+            if (i + 1 == VPT && !all) break;
+            float2 h[4], g[4], w[4];
+            unpack4x2<FP16>(*vector(stage, kSlotH, i), h);
+            unpack4x2<FP16>(*vector(stage, kSlotDn, i), g);
+            read_channels<FP16, VPT>(ch.pre, a.pre_fp32, i, w);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                g[j] = mul2(g[j], h[j]);
+                dpre[i][j] = fused2(g[j], both(pre), dpre[i][j]);
+                s = fused2(g[j], w[j], s);
+            }
         }
         return s.x + s.y;
     };
@@ -321,108 +375,115 @@ __global__ void __launch_bounds__(WARP ? 32 : kJoinTeamThreads) ep_join_backward
         return r;
     };
 #pragma unroll
-    for (int i = 0; i < STAGES; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
+    for (int i = 0; i < STAGES; ++i) fetch(i);
     Row now = scalars(blockIdx.x);
     copies_wait<STAGES - 1>();
     float2 sums = both(0.0f);
-    if (a.pre_weight) sums = row_sums<WARP>(make_float2(in ? along_pre(0, now.pre) : 0.0f, 0.0f), part[1]);
+    if (a.pre_weight) sums = row_sums<WARP>(make_float2(along_pre(0, now.pre), 0.0f), part[1]);
     int parity = 0, stage = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
-        const int64_t next = row + gridDim.x;
-        const Row then = scalars(next);
-        float2 d[4];
-        float sum = 0.0f;
-        if (in) {
+    int64_t out = blockIdx.x * pitch + at;   // bytes into the gradients
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1, out += gridDim.x * pitch) {
+        const Row then = scalars(row + gridDim.x);
+        float2 d[VPT][4], s = both(0.0f), row_sum = both(0.0f);
+        const float2 pre = both(now.pre), post = both(now.post), c = both(-sums.x * inv_hidden * now.pre * now.pre);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            if (i + 1 == VPT && !all) break;
+            float2 w[4];
             if (a.dh) {
-                unpack4x2<FP16>(*vector(stage, kSlotDh), d);
+                unpack4x2<FP16>(*vector(stage, kSlotDh, i), d[i]);
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) d[j] = both(0.0f);
+                for (int j = 0; j < 4; ++j) d[i][j] = both(0.0f);
             }
             if (a.pre_weight) {
-                float2 x[4], w[4];
-                const float2 c = both(-sums.x * inv_hidden * now.pre * now.pre);
-                unpack4x2<FP16>(*vector(stage, kSlotH), x);
+                float2 x[4];
+                unpack4x2<FP16>(*vector(stage, kSlotH, i), x);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) d[j] = fused2(mul2(x[j], both(now.pre)), c, d[j]);
-                unpack4x2<FP16>(*vector(stage, kSlotDn), x);
-                read_channels<FP16>(ch.pre, a.pre_fp32, w);
+                for (int j = 0; j < 4; ++j) d[i][j] = fused2(mul2(x[j], pre), c, d[i][j]);
+                unpack4x2<FP16>(*vector(stage, kSlotDn, i), x);
+                read_channels<FP16, VPT>(ch.pre, a.pre_fp32, i, w);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) d[j] = fused2(mul2(x[j], w[j]), both(now.pre), d[j]);
+                for (int j = 0; j < 4; ++j) d[i][j] = fused2(mul2(x[j], w[j]), pre, d[i][j]);
             }
             if (a.dresidual) {
                 float2 r[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) r[j] = mul2(both(a.residual_scale), d[j]);
-                st_v4(a.dresidual + row * pitch + at, pack4x2<FP16>(r));
+                for (int j = 0; j < 4; ++j) r[j] = mul2(both(a.residual_scale), d[i][j]);
+                st_v4(a.dresidual + out + i * next_vector, pack4x2<FP16>(r));
             }
-            float2 v[4], e[4], s = both(0.0f);
-            unpack4x2<FP16>(*vector(stage, kSlotY), v);
+            float2 v[4];
+            unpack4x2<FP16>(*vector(stage, kSlotY, i), v);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], both(now.post));
+            for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], post);
             // e: gradient for the gate; d: from here on that for y's norm
             if (a.gate_kind != EP_GATE_NONE) {
-                float2 w[4];
+                float2 e[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) e[j] = mul2(d[j], v[j]);
+                for (int j = 0; j < 4; ++j) e[j] = mul2(d[i][j], v[j]);
                 if (a.post_weight) {
-                    read_channels<FP16>(ch.post, a.post_fp32, w);
+                    read_channels<FP16, VPT>(ch.post, a.post_fp32, i, w);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) e[j] = mul2(e[j], w[j]);
                 }
                 if (a.gate_kind == EP_GATE_CHANNEL) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) dgate[j] = fused2(e[j], both(1.0f), dgate[j]);
-                    read_channels<FP16>(ch.gate, a.gate_fp32, w);
+                    for (int j = 0; j < 4; ++j) dgate[i][j] = fused2(e[j], both(1.0f), dgate[i][j]);
+                    read_channels<FP16, VPT>(ch.gate, a.gate_fp32, i, w);
                 } else if (element) {
-                    st_v4(a.dgate_element + row * pitch + at, pack4x2<FP16>(e));
-                    unpack4x2<FP16>(*vector(stage, kSlotGate), w);
-                } else {
-                    sum = sum_of(e);   // over the row, before its gate
+                    st_v4(a.dgate_element + out + i * next_vector, pack4x2<FP16>(e));
+                    unpack4x2<FP16>(*vector(stage, kSlotGate, i), w);
+                } else {   // over the row, before its gate
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) w[j] = both(now.gate);
+                    for (int j = 0; j < 4; ++j) {
+                        row_sum = fused2(e[j], both(1.0f), row_sum);
+                        w[j] = both(now.gate);
+                    }
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) d[j] = mul2(d[j], w[j]);
+                for (int j = 0; j < 4; ++j) d[i][j] = mul2(d[i][j], w[j]);
             }
             if (a.post_weight) {
-                float2 w[4];
-                read_channels<FP16>(ch.post, a.post_fp32, w);
+                read_channels<FP16, VPT>(ch.post, a.post_fp32, i, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    dpost[j] = fused2(d[j], v[j], dpost[j]);
-                    d[j] = mul2(d[j], w[j]);
-                    s = fused2(d[j], v[j], s);
+                    dpost[i][j] = fused2(d[i][j], v[j], dpost[i][j]);
+                    d[i][j] = mul2(d[i][j], w[j]);
+                    s = fused2(d[i][j], v[j], s);
                 }
-                if (a.gate_kind != EP_GATE_ROW) sum = s.x + s.y;
             }
         }
+        if (a.gate_kind == EP_GATE_ROW) s = row_sum;
         const int after = stage + 1 == STAGES ? 0 : stage + 1;
         copies_wait<STAGES - 2>();
-        sums = make_float2(a.pre_weight && in && next < a.rows ? along_pre(after, then.pre) : 0.0f, sum);
+        sums = make_float2(a.pre_weight && row + gridDim.x < a.rows ? along_pre(after, then.pre) : 0.0f, s.x + s.y);
         if (a.pre_weight || a.post_weight || a.gate_kind == EP_GATE_ROW) sums = row_sums<WARP>(sums, part[parity]);
         if (a.gate_kind == EP_GATE_ROW && t == 0) a.dgate_row[row] = sums.y;
-        if (in) {
-            if (a.post_weight) {
-                const float mean = (a.gate_kind == EP_GATE_ROW ? sums.y * now.gate : sums.y) * inv_hidden;
-                float2 v[4];
-                unpack4x2<FP16>(*vector(stage, kSlotY), v);
+        const float2 mean = both(-(a.gate_kind == EP_GATE_ROW ? sums.y * now.gate : sums.y) * inv_hidden);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    d[j] = mul2(fused2(mul2(v[j], both(now.post)), both(-mean), d[j]), both(now.post));
+        for (int i = 0; i < VPT; ++i) {
+            if (i + 1 == VPT && !all) break;
+            if (a.post_weight) {
+                float2 v[4];
+                unpack4x2<FP16>(*vector(stage, kSlotY, i), v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d[i][j] = mul2(fused2(mul2(v[j], post), mean, d[i][j]), post);
             }
-            st_v4(a.dy + row * pitch + at, pack4x2<FP16>(d));
+            st_v4(a.dy + out + i * next_vector, pack4x2<FP16>(d[i]));
         }
-        fetch(row + (int64_t)STAGES * gridDim.x, stage);
+        fetch(stage);
         stage = after;
         now = then;
     }
-    if (!in) return;
-    float* out = a.partial + (int64_t)blockIdx.x * 3 * a.hidden + 8 * t;
-    auto leave = [&](const float2 (&s)[4], int which) {
-        float4* p = reinterpret_cast<float4*>(out + (int64_t)which * a.hidden);
-        p[0] = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
-        p[1] = make_float4(s[2].x, s[2].y, s[3].x, s[3].y);
+    auto leave = [&](const float2 (&s)[VPT][4], int which) {
+        float* to = a.partial + ((int64_t)blockIdx.x * 3 + which) * a.hidden;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            if (i + 1 == VPT && !all) break;
+            float4* p = reinterpret_cast<float4*>(to + 8 * (i * threads + t));
+            p[0] = make_float4(s[i][0].x, s[i][0].y, s[i][1].x, s[i][1].y);
+            p[1] = make_float4(s[i][2].x, s[i][2].y, s[i][3].x, s[i][3].y);
+        }
     };
     if (a.post_weight) leave(dpost, 0);
     if (a.gate_kind == EP_GATE_CHANNEL) leave(dgate, 1);
@@ -433,7 +494,7 @@ __global__ void __launch_bounds__(WARP ? 32 : kJoinTeamThreads) ep_join_backward
 template <bool FP16, int VPT>
 __global__ void __launch_bounds__(kJoinMaxThreads) ep_join_wide_kernel(const JoinArgs a)
 {
-    __shared__ float2 part[2][32];
+    __shared__ float part[2][32];
     const int t = threadIdx.x, stride = blockDim.x;
     const int64_t row = blockIdx.x;
     follow_predecessor();
@@ -463,7 +524,7 @@ __global__ void __launch_bounds__(kJoinMaxThreads) ep_join_wide_kernel(const Joi
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum = fmaf(f[i][j], f[i][j], sum);
         sum = row_sums<false>(make_float2(sum, 0.0f), part[0]).x;
-        const float rstd = __frsqrt_rn(__fdiv_rn(sum, (float)a.hidden) + a.eps);
+        const float rstd = root_of(sum / (float)a.hidden + a.eps);
         if (t == 0) a.post_rstd[row] = rstd;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -496,7 +557,7 @@ __global__ void __launch_bounds__(kJoinMaxThreads) ep_join_wide_kernel(const Joi
     }
     if (!a.pre_weight) return;
     sum = row_sums<false>(make_float2(sum, 0.0f), part[1]).x;
-    const float rstd = __frsqrt_rn(__fdiv_rn(sum, (float)a.hidden) + a.eps);
+    const float rstd = root_of(sum / (float)a.hidden + a.eps);
     if (t == 0) a.pre_rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -558,27 +619,33 @@ __global__ void __launch_bounds__(kSumColumns * kSumParts) ep_join_sum_kernel(co
 }
 
 // Shared memory of a CTA of the team kernels, and how many CTAs an SM holds.
-constexpr size_t kJoinShared = 227 * 1024 - 1024;   // less the static part
+constexpr size_t kJoinShared = 227 * 1024 - 1024;   // less the static part, 256 bytes
 
-size_t team_shared(const JoinArgs& a, int threads, int stages, int slots)
+int team_vectors(int hidden) { return hidden <= 256 ? 1 : 2; }   // of a thread
+
+int team_threads(int hidden)
 {
-    return (size_t)(stages * slots + channel_vectors(a)) * threads * 16;
+    const int columns = 8 * team_vectors(hidden);
+    return (hidden / columns + (hidden % columns != 0) + 31) / 32 * 32;
 }
 
-int team_threads(int hidden) { return (hidden / 8 + 31) / 32 * 32; }
-
-int team_ctas_per_sm(int threads, size_t shared)
+size_t team_shared(const JoinArgs& a, int stages, int slots)
 {
-    const int by_threads = kJoinTeamThreads / threads, by_shared = (int)(228 * 1024 / (shared + 2048));
+    return (size_t)(stages * slots + channel_vectors(a)) * team_vectors(a.hidden) * team_threads(a.hidden) * 16;
+}
+
+int team_ctas_per_sm(int most_threads, int threads, size_t shared)
+{
+    const int by_threads = most_threads / threads, by_shared = (int)(228 * 1024 / (shared + 2048));
     const int n = by_threads < by_shared ? by_threads : by_shared;
-    return n < 1 ? 1 : n > 32 ? 32 : n;
+    return n < 1 ? 1 : n > 24 ? 24 : n;
 }
 
 template <auto* K>
-cudaError_t launch_team(const JoinArgs& a, int64_t ctas, int threads, size_t shared, cudaStream_t s)
+cudaError_t launch_team(const JoinArgs& a, int64_t ctas, size_t shared, cudaStream_t s)
 {
     const cudaError_t e = allow_all_shared<K>();
-    return e != cudaSuccess ? e : launch_dependent(K, dim3((unsigned)ctas), dim3(threads), shared, s, a);
+    return e != cudaSuccess ? e : launch_dependent(K, dim3((unsigned)ctas), dim3(team_threads(a.hidden)), shared, s, a);
 }
 
 template <bool FP16>
@@ -590,14 +657,22 @@ cudaError_t launch_join(const JoinArgs& a, int sms, cudaStream_t s)
         if (vpt == 4) return launch_dependent(ep_join_wide_kernel<FP16, 4>, grid, block, 0, s, a);
         return launch_dependent(ep_join_wide_kernel<FP16, 8>, grid, block, 0, s, a);
     }
+    // Four stages where they leave an SM as many CTAs as its registers do, else two: two CTAs on an SM hide each other's
+    // barriers.
     const int threads = team_threads(a.hidden), slots = a.gate_kind == EP_GATE_ELEMENT ? 3 : 2;
-    size_t shared = team_shared(a, threads, 4, slots);
-    const bool four = shared <= kJoinShared;   // else FP32 weights of the widest rows take their place
-    if (!four) shared = team_shared(a, threads, 2, slots);
-    const int64_t fit = (int64_t)sms * team_ctas_per_sm(threads, shared), ctas = a.rows < fit ? a.rows : fit;
-    if (threads == 32) return launch_team<ep_join_team_kernel<FP16, true, 4>>(a, ctas, threads, shared, s);
-    if (four) return launch_team<ep_join_team_kernel<FP16, false, 4>>(a, ctas, threads, shared, s);
-    return launch_team<ep_join_team_kernel<FP16, false, 2>>(a, ctas, threads, shared, s);
+    constexpr int kThreads = 2 * kJoinTeamThreads;
+    // one launch for each number of stages, so that the shared memory is that of the kernel's own
+    auto launch = [&](auto* kernel_of, int stages) {
+        const size_t shared = team_shared(a, stages, slots);
+        const int64_t fit = (int64_t)sms * team_ctas_per_sm(kThreads, threads, shared);
+        return kernel_of(a, a.rows < fit ? a.rows : fit, shared, s);
+    };
+    if (a.hidden <= 256) return launch(&launch_team<ep_join_team_kernel<FP16, true, 1, 4>>, 4);
+    if (threads == 32) return launch(&launch_team<ep_join_team_kernel<FP16, true, 2, 4>>, 4);
+    const size_t shared = team_shared(a, 4, slots);
+    if (shared <= kJoinShared && team_ctas_per_sm(kThreads, threads, shared) == team_ctas_per_sm(kThreads, threads, 0))
+        return launch(&launch_team<ep_join_team_kernel<FP16, false, 2, 4>>, 4);
+    return launch(&launch_team<ep_join_team_kernel<FP16, false, 2, 2>>, 2);
 }
 
 // CTAs of the gradient's kernel, by the shape alone, because they fix the order of the sums: as many as the SMs hold with
@@ -608,7 +683,7 @@ constexpr int kRowsPerCta = 4;
 int join_backward_ctas(int64_t rows, int hidden, int sms)
 {
     const int threads = team_threads(hidden);
-    const int64_t fit = (int64_t)sms * team_ctas_per_sm(threads, (size_t)(3 * 5 + 4) * threads * 16);
+    const int64_t fit = (int64_t)sms * team_ctas_per_sm(kJoinTeamThreads, threads, (size_t)(3 * 5 + 4) * team_vectors(hidden) * threads * 16);
     const int64_t want = (rows + kRowsPerCta - 1) / kRowsPerCta;
     const int64_t least = rows < sms ? rows : sms;
     return (int)(want < least ? least : want < fit ? want : fit);
@@ -617,13 +692,13 @@ int join_backward_ctas(int64_t rows, int hidden, int sms)
 template <bool FP16>
 cudaError_t launch_join_backward(const JoinArgs& a, int ctas, cudaStream_t s)
 {
-    const int threads = team_threads(a.hidden), slots = a.gate_kind == EP_GATE_ELEMENT ? 5 : 4;
-    size_t shared = team_shared(a, threads, 3, slots);
-    const bool three = shared <= kJoinShared;   // else a gate per element or FP32 weights of wide rows take their place
-    if (!three) shared = team_shared(a, threads, 2, slots);
-    if (threads == 32) return launch_team<ep_join_backward_kernel<FP16, true, 3>>(a, ctas, threads, shared, s);
-    if (three) return launch_team<ep_join_backward_kernel<FP16, false, 3>>(a, ctas, threads, shared, s);
-    return launch_team<ep_join_backward_kernel<FP16, false, 2>>(a, ctas, threads, shared, s);
+    const int slots = a.gate_kind == EP_GATE_ELEMENT ? 5 : 4;
+    const size_t shared = team_shared(a, 3, slots);
+    if (a.hidden <= 256) return launch_team<ep_join_backward_kernel<FP16, true, 1, 3>>(a, ctas, shared, s);
+    if (team_threads(a.hidden) == 32) return launch_team<ep_join_backward_kernel<FP16, true, 2, 3>>(a, ctas, shared, s);
+    if (shared <= kJoinShared) return launch_team<ep_join_backward_kernel<FP16, false, 2, 3>>(a, ctas, shared, s);
+    // a gate per element or FP32 weights of wide rows take the third stage's place
+    return launch_team<ep_join_backward_kernel<FP16, false, 2, 2>>(a, ctas, team_shared(a, 2, slots), s);
 }
 
 bool row_ok(const void* p, int64_t stride, int hidden)

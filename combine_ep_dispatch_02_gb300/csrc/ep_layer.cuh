@@ -183,6 +183,23 @@ __device__ __forceinline__ float2 sigmoid_and_rest(float g)
 // it: m / 448, and 1 for a block of zeros (fmaxf drops NaN, so a block of NaN also gets 1).
 __device__ __forceinline__ float e4m3_block_scale(float m) { return m > 0.0f ? __fdiv_rn(m, 448.0f) : 1.0f; }
 
+// The same in three operations, from the product with 1 / 448 and its residual, which an m above 2^-100 leaves exact.
+__device__ __forceinline__ float quick_block_scale(float m)
+{
+    constexpr float kInv = 1.0f / 448.0f;
+    if (!(m >= 0x1p-100f && m <= 0x1p120f)) return e4m3_block_scale(m);
+    const float q = m * kInv;
+    return fmaf(fmaf(-q, 448.0f, m), kInv, q);
+}
+
+// 1 / v for codes by e4m3x4_near, off by two units at most; infinite, and not used there, for v below 2^-126.
+__device__ __forceinline__ float quick_reciprocal(float v)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // Four e4m3 codes of v / scale; inv = RN(1 / scale).  The correctly rounded quotient comes from
 // the reciprocal and one residual step where no intermediate underflows or overflows (see
 // div_by_scale), from an IEEE division elsewhere; the branch is uniform over a block's lanes.

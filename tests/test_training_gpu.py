@@ -69,7 +69,7 @@ def _check_join(m, alpha, eps, fp8):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("gate,post,pre", FORMS)
-@pytest.mark.parametrize("rows,hidden", SHAPES + [(2, 16400), (1, 32768)])
+@pytest.mark.parametrize("rows,hidden", SHAPES + [(2, 16400), (1, 32768), (3000, 272), (3000, 256), (2000, 512), (999, 528)])
 def test_join(rows, hidden, gate, post, pre, dtype):
     m = _inputs(rows, hidden, HALF[dtype], gate, post, pre, rows * 1009 + hidden)
     _check_join(m, 0.75, 1e-6, fp8=pre is not None and hidden % 32 == 0)
@@ -139,7 +139,7 @@ def _check_backward(m, j, dh, dn, alpha):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("gate,post,pre", FORMS)
-@pytest.mark.parametrize("rows,hidden", SHAPES + [(1500, 272), (641, 7168)])
+@pytest.mark.parametrize("rows,hidden", SHAPES + [(1500, 272), (1500, 256), (900, 512), (641, 7168)])
 def test_join_backward(rows, hidden, gate, post, pre, dtype):
     t = HALF[dtype]
     m = _inputs(rows, hidden, t, gate, post, pre, rows * 1013 + hidden)
