@@ -46,15 +46,26 @@ __device__ __forceinline__ float block_top(const float (&f)[8])
 }
 
 // Eight codes of a block's lane and, by its first lane, the block's scale.  A lane that is not `in` takes part with
-// zeros in the maximum.  The codes are those of the product with the scale's reciprocal, within an FP32 unit of
+// zeros in the maximum.  The codes are those of the product with the scale's reciprocal, within three FP32 units of
 // the quotient that they round.
 __device__ __forceinline__ void write_codes(const float (&f)[8], bool in, uint8_t* q, float* scale_out)
 {
-    const float scale = e4m3_block_scale(block_top(f));
-    const float inv = __frcp_rn(scale);
+    const float scale = quick_block_scale(block_top(f));
     if (!in) return;
-    *reinterpret_cast<uint2*>(q) = make_uint2(e4m3x4_near(f[0], f[1], f[2], f[3], scale, inv),
-                                              e4m3x4_near(f[4], f[5], f[6], f[7], scale, inv));
+    uint2 codes;
+    if (scale >= 0x1p-100f) {
+        const float2 inv = both(quick_reciprocal(scale));
+        uint32_t c[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 v = mul2(make_float2(f[2 * j], f[2 * j + 1]), inv);
+            c[j] = e4m3x2(v.x, v.y);
+        }
+        codes = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+    } else {
+        codes = make_uint2(e4m3x4_near(f[0], f[1], f[2], f[3], scale, 0.0f), e4m3x4_near(f[4], f[5], f[6], f[7], scale, 0.0f));
+    }
+    *reinterpret_cast<uint2*>(q) = codes;
     if ((threadIdx.x & 15) == 0) *scale_out = scale;
 }
 
@@ -91,7 +102,7 @@ __global__ void __launch_bounds__(kSwigluThreads) ep_swiglu_saved_kernel(const S
     for (int i = 0; i < kSwigluUnits; ++i) {
         const uint32_t u = (blockIdx.x * kSwigluUnits + i) * kSwigluTeams + (threadIdx.x >> 4);
         row[i] = u < units ? (int)(u / per_row) : -1;
-        block[i] = (int)(u % per_row);
+        block[i] = (int)(u - (u / per_row) * per_row);
         v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
         if (row[i] < 0) continue;
         const uint8_t* x = a.x + row[i] * a.pitch;
