@@ -32,7 +32,22 @@ struct SwigluArgs {
     int64_t pitch;              // bytes between rows of x
     int rows, inner;
     int z_blocks, row_blocks;   // 128-column blocks of z, and of gate | up
+    uint32_t per_row, divide;   // blocks that the kernel works on in a row; the multiplier and shift of a division by them
+    int shift;
 };
+
+// Whole-number division of u < 2^31 by d: u * ceil(2^(31 + l) / d) / 2^(31 + l) with d <= 2^l is exact (T. Granlund,
+// P. L. Montgomery, "Division by invariant integers using multiplication", PLDI 1994).
+void set_per_row(SwigluArgs& a, int d)
+{
+    int l = 0;
+    while (((int64_t)1 << l) < d) ++l;
+    a.per_row = (uint32_t)d;
+    a.divide = (uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d);
+    a.shift = 31 + l;
+}
+
+__device__ __forceinline__ uint32_t row_of(const SwigluArgs& a, uint32_t u) { return (uint32_t)(((uint64_t)u * a.divide) >> a.shift); }
 
 // Largest magnitude over the sixteen lanes of a half warp; NaN counts as 0.
 __device__ __forceinline__ float block_top(const float (&f)[8])
@@ -45,13 +60,35 @@ __device__ __forceinline__ float block_top(const float (&f)[8])
     return m;
 }
 
-// Eight codes of a block's lane and, by its first lane, the block's scale.  A lane that is not `in` takes part with
-// zeros in the maximum.  The codes are those of the product with the scale's reciprocal, within three FP32 units of
-// the quotient that they round.
-__device__ __forceinline__ void write_codes(const float (&f)[8], bool in, uint8_t* q, float* scale_out)
+// The same for two vectors of eight 16-bit values at once, in packed arithmetic.
+template <bool FP16>
+__device__ __forceinline__ float2 block_tops(const uint4& a, const uint4& b)
 {
-    const float scale = quick_block_scale(block_top(f));
+    auto larger = [](uint32_t x, uint32_t y) {
+        if constexpr (FP16) {
+            const __half2 m = __hmax2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+            return *reinterpret_cast<const uint32_t*>(&m);
+        } else {
+            const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+            return *reinterpret_cast<const uint32_t*>(&m);
+        }
+    };
+    constexpr uint32_t kMagnitude = 0x7FFF7FFFu;
+    const uint32_t p = larger(larger(a.x & kMagnitude, a.y & kMagnitude), larger(a.z & kMagnitude, a.w & kMagnitude));
+    const uint32_t q = larger(larger(b.x & kMagnitude, b.y & kMagnitude), larger(b.z & kMagnitude, b.w & kMagnitude));
+    uint32_t m = larger(__byte_perm(p, q, 0x5410), __byte_perm(p, q, 0x7632));   // a's in the low half, b's in the high
+#pragma unroll
+    for (int o = 8; o; o >>= 1) m = larger(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float2 top = FP16 ? __half22float2(*reinterpret_cast<const __half2*>(&m)) : make_float2(bf16_lo(m), bf16_hi(m));
+    return make_float2(fmaxf(top.x, 0.0f), fmaxf(top.y, 0.0f));   // a block of what is not a number alone: 0
+}
+
+// Eight codes of a lane of a block whose largest magnitude is `top` and, by the block's first lane, its scale.  The codes are those of the product with the scale's reciprocal, within three FP32 units of
+// the quotient that they round.
+__device__ __forceinline__ void write_codes(const float (&f)[8], float top, bool in, uint8_t* q, float* scale_out)
+{
     if (!in) return;
+    const float scale = quick_block_scale(top);
     uint2 codes;
     if (scale >= 0x1p-100f) {
         const float2 inv = both(quick_reciprocal(scale));
@@ -92,17 +129,17 @@ template <bool FP16, bool STRADDLE>
 __global__ void __launch_bounds__(kSwigluThreads) ep_swiglu_saved_kernel(const SwigluArgs a)
 {
     const int lane = threadIdx.x & 15;
-    const uint32_t per_row = STRADDLE ? a.z_blocks + a.row_blocks : a.z_blocks;
     follow_predecessor();
     const int rows = rows_in_use(a);
-    const uint32_t units = (uint32_t)rows * per_row;
+    const uint32_t units = (uint32_t)rows * a.per_row;
     uint4 v[kSwigluUnits][2];
     int row[kSwigluUnits], block[kSwigluUnits];
 #pragma unroll
     for (int i = 0; i < kSwigluUnits; ++i) {
         const uint32_t u = (blockIdx.x * kSwigluUnits + i) * kSwigluTeams + (threadIdx.x >> 4);
-        row[i] = u < units ? (int)(u / per_row) : -1;
-        block[i] = (int)(u - (u / per_row) * per_row);
+        const uint32_t r = row_of(a, u);
+        row[i] = u < units ? (int)r : -1;
+        block[i] = (int)(u - r * a.per_row);
         v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
         if (row[i] < 0) continue;
         const uint8_t* x = a.x + row[i] * a.pitch;
@@ -129,12 +166,13 @@ __global__ void __launch_bounds__(kSwigluThreads) ep_swiglu_saved_kernel(const S
         uint8_t* saved = a.saved + r * 2 * a.inner + c;
         float* saved_scales = a.saved_scales + r * a.row_blocks + b;
         if constexpr (!STRADDLE) {
-            write_codes(gate, live && c < a.inner, saved, saved_scales);
-            write_codes(up, live && c < a.inner, saved + a.inner, saved_scales + a.z_blocks);
+            const float2 top = block_tops<FP16>(v[i][0], v[i][1]);
+            write_codes(gate, top.x, live && c < a.inner, saved, saved_scales);
+            write_codes(up, top.y, live && c < a.inner, saved + a.inner, saved_scales + a.z_blocks);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) z[j] = own ? gate[j] : gate[j] * sigmoid_and_rest(gate[j]).x * up[j];
-        write_codes(z, live && c < (own ? 2 : 1) * a.inner, own ? saved : a.q + r * a.inner + c,
+        write_codes(z, block_top(z), live && c < (own ? 2 : 1) * a.inner, own ? saved : a.q + r * a.inner + c,
                     own ? saved_scales : a.scales + r * a.z_blocks + b);
     }
 }
@@ -145,10 +183,9 @@ template <bool FP16, bool QUANTISE, bool STRADDLE>
 __global__ void __launch_bounds__(kSwigluThreads) ep_swiglu_backward_kernel(const SwigluArgs a)
 {
     const int lane = threadIdx.x & 15;
-    const uint32_t per_row = STRADDLE ? a.row_blocks : a.z_blocks;
     follow_predecessor();
     const int rows = rows_in_use(a);
-    const uint32_t units = (uint32_t)rows * per_row;
+    const uint32_t units = (uint32_t)rows * a.per_row;
     uint2 g[kSwigluUnits], p[kSwigluUnits];
     uint4 dz[kSwigluUnits];
     float gs[kSwigluUnits], ps[kSwigluUnits];
@@ -156,8 +193,8 @@ __global__ void __launch_bounds__(kSwigluThreads) ep_swiglu_backward_kernel(cons
 #pragma unroll
     for (int i = 0; i < kSwigluUnits; ++i) {
         const uint32_t u = (blockIdx.x * kSwigluUnits + i) * kSwigluTeams + (threadIdx.x >> 4);
-        const int r = (int)(u / per_row);
-        at[i] = 128 * (int)(u % per_row) + 8 * lane;
+        const int r = (int)row_of(a, u);
+        at[i] = 128 * (int)(u - r * a.per_row) + 8 * lane;
         row[i] = u < units && at[i] < (STRADDLE ? 2 : 1) * a.inner ? r : -1;
         col[i] = STRADDLE && at[i] >= a.inner ? at[i] - a.inner : at[i];
         g[i] = p[i] = make_uint2(0, 0);
@@ -193,7 +230,7 @@ __global__ void __launch_bounds__(kSwigluThreads) ep_swiglu_backward_kernel(cons
 #pragma unroll
             for (int j = 0; j < 8; ++j) gate[j] = second ? up[j] : gate[j];
             if (in) st_v4(out + 2 * (int64_t)at[i], pack8<FP16>(gate));
-            write_codes(gate, in, a.q + r * 2 * a.inner + at[i], a.scales + r * a.row_blocks + at[i] / 128);
+            write_codes(gate, block_top(gate), in, a.q + r * 2 * a.inner + at[i], a.scales + r * a.row_blocks + at[i] / 128);
         } else {
             if (in) {
                 st_v4(out + 2 * (int64_t)col[i], pack8<FP16>(gate));
@@ -202,17 +239,17 @@ __global__ void __launch_bounds__(kSwigluThreads) ep_swiglu_backward_kernel(cons
             if constexpr (QUANTISE) {
                 uint8_t* q = a.q + r * 2 * a.inner;
                 float* scales = a.scales + r * a.row_blocks;
-                write_codes(gate, in, q + col[i], scales + col[i] / 128);
-                write_codes(up, in, q + a.inner + col[i], scales + (a.inner + col[i]) / 128);
+                write_codes(gate, block_top(gate), in, q + col[i], scales + col[i] / 128);
+                write_codes(up, block_top(up), in, q + a.inner + col[i], scales + (a.inner + col[i]) / 128);
             }
         }
     }
 }
 
-unsigned swiglu_grid(const SwigluArgs& a, int per_row)
+unsigned swiglu_grid(const SwigluArgs& a)
 {
     const int64_t per_cta = kSwigluTeams * kSwigluUnits;
-    return (unsigned)(((int64_t)a.rows * per_row + per_cta - 1) / per_cta);
+    return (unsigned)(((int64_t)a.rows * a.per_row + per_cta - 1) / per_cta);
 }
 
 // What forward and backward check alike; `x` names the 16-bit input, of `width` columns.
@@ -252,7 +289,8 @@ extern "C" int ep_swiglu_saved(const void* gate_up, int64_t stride, int dtype, i
     a.q = (uint8_t*)q; a.scales = scales; a.saved = (uint8_t*)saved; a.saved_scales = saved_scales;
     a.pitch = 2 * stride; a.rows = (int)rows;
     const bool straddle = inner % 128 != 0, fp16 = dtype == EP_FP16;
-    const dim3 grid(swiglu_grid(a, straddle ? a.z_blocks + a.row_blocks : a.z_blocks)), threads(kSwigluThreads);
+    set_per_row(a, straddle ? a.z_blocks + a.row_blocks : a.z_blocks);
+    const dim3 grid(swiglu_grid(a)), threads(kSwigluThreads);
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
     if (straddle)
@@ -283,7 +321,8 @@ extern "C" int ep_swiglu_saved_backward(const void* saved, const float* saved_sc
     a.d = (uint8_t*)d_gate_up; a.q = (uint8_t*)q; a.scales = scales;
     a.pitch = 2 * dz_stride; a.rows = (int)rows;
     const bool straddle = q && inner % 128 != 0, fp16 = dtype == EP_FP16;
-    const dim3 grid(swiglu_grid(a, straddle ? a.row_blocks : a.z_blocks)), threads(kSwigluThreads);
+    set_per_row(a, straddle ? a.row_blocks : a.z_blocks);
+    const dim3 grid(swiglu_grid(a)), threads(kSwigluThreads);
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
     if (straddle)
