@@ -296,9 +296,12 @@ __global__ void __launch_bounds__(WARP ? 32 : kJoinTeamThreads, WARP ? 24 : 2) e
     }
 }
 
-// The gradient.  Registers hold the three sums over rows, which leave once per CTA, and one gradient; what a later pass
-// over the row needs is read from its stage again.
+// The gradient.  The vectors along the channels lie in shared memory as FP32: pre_weight, and post_weight times the
+// channels' gate.  One sum over rows, of q = D * v, gives both post_weight's gradient and the channels' gate's, each times
+// the other; a row's own gate is a factor of all that follows D, and its gradient is the sum that the norm needs.  What a
+// later pass over the row needs is read from its stage again.
 enum { kSlotH, kSlotDn, kSlotDh, kSlotY, kSlotGate };   // a stage's vectors of a thread; the last for a gate per element
+constexpr int kBackChannels = 4;                        // 16-byte vectors of both channel vectors, per vector of a row
 
 template <bool FP16, bool WARP, int VPT, int STAGES>
 __global__ void __launch_bounds__(WARP ? 32 : kJoinTeamThreads, 1) ep_join_backward_kernel(const JoinArgs a)
@@ -312,24 +315,23 @@ __global__ void __launch_bounds__(WARP ? 32 : kJoinTeamThreads, 1) ep_join_backw
     const int slots = element ? 5 : 4, slot = VPT * threads;
     const float inv_hidden = __frcp_rn((float)a.hidden);
     follow_predecessor();
-    const Channels ch = fetch_channels<VPT>(a, staged + STAGES * slots * slot);
     uint4* const mine = staged + t;
-    auto vector = [&](int stage, int which, int i) { return mine + (stage * slots + which) * slot + i * threads; };
     int64_t ahead = blockIdx.x;   // the next row to fetch
     const uint8_t *hp = a.h_in + ahead * pitch + at, *np = a.dn + ahead * a.dn_pitch + at, *dp = a.dh + ahead * a.dh_pitch + at,
                   *yp = a.y + ahead * a.y_pitch + at, *gp = a.gate + (element ? ahead * a.g_pitch + at : 0);
     auto fetch = [&](int stage) {
         if (ahead < a.rows) {
+            uint4* to = mine + stage * slots * slot;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 if (i + 1 == VPT && !all) break;
                 if (a.pre_weight) {
-                    copy16(vector(stage, kSlotH, i), hp + i * next_vector);
-                    copy16(vector(stage, kSlotDn, i), np + i * next_vector);
+                    copy16(to + kSlotH * slot + i * threads, hp + i * next_vector);
+                    copy16(to + kSlotDn * slot + i * threads, np + i * next_vector);
                 }
-                if (a.dh) copy16(vector(stage, kSlotDh, i), dp + i * next_vector);
-                copy16(vector(stage, kSlotY, i), yp + i * next_vector);
-                if (element) copy16(vector(stage, kSlotGate, i), gp + i * next_vector);
+                if (a.dh) copy16(to + kSlotDh * slot + i * threads, dp + i * next_vector);
+                copy16(to + kSlotY * slot + i * threads, yp + i * next_vector);
+                if (element) copy16(to + kSlotGate * slot + i * threads, gp + i * next_vector);
             }
             ahead += gridDim.x;
             hp += gridDim.x * pitch;
@@ -340,21 +342,47 @@ __global__ void __launch_bounds__(WARP ? 32 : kJoinTeamThreads, 1) ep_join_backw
         }
         copies_commit();
     };
-    float2 dpost[VPT][4], dgate[VPT][4], dpre[VPT][4];
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) fetch(i);
+    float4* const channels = reinterpret_cast<float4*>(mine + STAGES * slots * slot);   // pre, then post * gate; two halves each
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        if (i + 1 == VPT && !all) break;
+        const int v = i * threads + t;
+        float pre[8], post[8], gate[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) pre[j] = post[j] = gate[j] = 1.0f;
+        if (a.pre_weight) load_channels<FP16>(a.pre_weight, a.pre_fp32, v, pre);
+        if (a.post_weight) load_channels<FP16>(a.post_weight, a.post_fp32, v, post);
+        if (a.gate_kind == EP_GATE_CHANNEL) load_channels<FP16>(a.gate, a.gate_fp32, v, gate);
+        float4* to = channels + i * threads;
+        to[0] = make_float4(pre[0], pre[1], pre[2], pre[3]);
+        to[slot] = make_float4(pre[4], pre[5], pre[6], pre[7]);
+        to[2 * slot] = make_float4(post[0] * gate[0], post[1] * gate[1], post[2] * gate[2], post[3] * gate[3]);
+        to[3 * slot] = make_float4(post[4] * gate[4], post[5] * gate[5], post[6] * gate[6], post[7] * gate[7]);
+    }
+    auto read_channel = [&](int which, int i, float2 (&w)[4]) {
+        const float4 lo = channels[2 * which * slot + i * threads], hi = channels[(2 * which + 1) * slot + i * threads];
+        w[0] = make_float2(lo.x, lo.y);
+        w[1] = make_float2(lo.z, lo.w);
+        w[2] = make_float2(hi.x, hi.y);
+        w[3] = make_float2(hi.z, hi.w);
+    };
+    float2 sum_q[VPT][4], dpre[VPT][4];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) dpost[i][j] = dgate[i][j] = dpre[i][j] = both(0.0f);
+        for (int j = 0; j < 4; ++j) sum_q[i][j] = dpre[i][j] = both(0.0f);
     // a row's sum of dn * pre_weight * h, and its part of pre_weight's gradient
-    auto along_pre = [&](int stage, float pre) {
+    auto along_pre = [&](const uint4* from, float pre) {
         float2 s = both(0.0f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (i + 1 == VPT && !all) break;
             float2 h[4], g[4], w[4];
-            unpack4x2<FP16>(*vector(stage, kSlotH, i), h);
-            unpack4x2<FP16>(*vector(stage, kSlotDn, i), g);
-            read_channels<FP16, VPT>(ch.pre, a.pre_fp32, i, w);
+            unpack4x2<FP16>(from[kSlotH * slot + i * threads], h);
+            unpack4x2<FP16>(from[kSlotDn * slot + i * threads], g);
+            read_channel(0, i, w);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 g[j] = mul2(g[j], h[j]);
@@ -374,120 +402,112 @@ __global__ void __launch_bounds__(WARP ? 32 : kJoinTeamThreads, 1) ep_join_backw
         }
         return r;
     };
-#pragma unroll
-    for (int i = 0; i < STAGES; ++i) fetch(i);
     Row now = scalars(blockIdx.x);
     copies_wait<STAGES - 1>();
     float2 sums = both(0.0f);
-    if (a.pre_weight) sums = row_sums<WARP>(make_float2(along_pre(0, now.pre), 0.0f), part[1]);
+    if (a.pre_weight) sums = row_sums<WARP>(make_float2(along_pre(mine, now.pre), 0.0f), part[1]);
     int parity = 0, stage = 0;
+    const uint4* here = mine;   // this row's stage
     int64_t out = blockIdx.x * pitch + at;   // bytes into the gradients
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1, out += gridDim.x * pitch) {
         const Row then = scalars(row + gridDim.x);
-        float2 d[VPT][4], s = both(0.0f), row_sum = both(0.0f);
-        const float2 pre = both(now.pre), post = both(now.post), c = both(-sums.x * inv_hidden * now.pre * now.pre);
+        float2 d[VPT][4], s = both(0.0f);
+        const float2 pre = both(now.pre), post = both(now.post), gate = both(now.gate), c = both(-sums.x * inv_hidden * now.pre * now.pre);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (i + 1 == VPT && !all) break;
-            float2 w[4];
+            const uint4* from = here + i * threads;
+            float2 w[4], x[4];
             if (a.dh) {
-                unpack4x2<FP16>(*vector(stage, kSlotDh, i), d[i]);
+                unpack4x2<FP16>(from[kSlotDh * slot], d[i]);
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) d[i][j] = both(0.0f);
             }
             if (a.pre_weight) {
-                float2 x[4];
-                unpack4x2<FP16>(*vector(stage, kSlotH, i), x);
+                unpack4x2<FP16>(from[kSlotH * slot], x);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) d[i][j] = fused2(mul2(x[j], pre), c, d[i][j]);
-                unpack4x2<FP16>(*vector(stage, kSlotDn, i), x);
-                read_channels<FP16, VPT>(ch.pre, a.pre_fp32, i, w);
+                unpack4x2<FP16>(from[kSlotDn * slot], x);
+                read_channel(0, i, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) d[i][j] = fused2(mul2(x[j], w[j]), pre, d[i][j]);
             }
             if (a.dresidual) {
-                float2 r[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) r[j] = mul2(both(a.residual_scale), d[i][j]);
-                st_v4(a.dresidual + out + i * next_vector, pack4x2<FP16>(r));
+                for (int j = 0; j < 4; ++j) x[j] = mul2(both(a.residual_scale), d[i][j]);
+                st_v4(a.dresidual + out + i * next_vector, pack4x2<FP16>(x));
             }
             float2 v[4];
-            unpack4x2<FP16>(*vector(stage, kSlotY, i), v);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], post);
-            // e: gradient for the gate; d: from here on that for y's norm
-            if (a.gate_kind != EP_GATE_NONE) {
+            unpack4x2<FP16>(from[kSlotY * slot], v);
+            read_channel(1, i, w);
+            if (element) {
                 float2 e[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) e[j] = mul2(d[i][j], v[j]);
-                if (a.post_weight) {
-                    read_channels<FP16, VPT>(ch.post, a.post_fp32, i, w);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) e[j] = mul2(e[j], w[j]);
-                }
-                if (a.gate_kind == EP_GATE_CHANNEL) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) dgate[i][j] = fused2(e[j], both(1.0f), dgate[i][j]);
-                    read_channels<FP16, VPT>(ch.gate, a.gate_fp32, i, w);
-                } else if (element) {
-                    st_v4(a.dgate_element + out + i * next_vector, pack4x2<FP16>(e));
-                    unpack4x2<FP16>(*vector(stage, kSlotGate, i), w);
-                } else {   // over the row, before its gate
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        row_sum = fused2(e[j], both(1.0f), row_sum);
-                        w[j] = both(now.gate);
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) d[i][j] = mul2(d[i][j], w[j]);
-            }
-            if (a.post_weight) {
-                read_channels<FP16, VPT>(ch.post, a.post_fp32, i, w);
+                unpack4x2<FP16>(from[kSlotGate * slot], x);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    dpost[i][j] = fused2(d[i][j], v[j], dpost[i][j]);
+                    v[j] = mul2(v[j], post);
+                    const float2 q = mul2(d[i][j], v[j]);
+                    e[j] = mul2(q, w[j]);
+                    sum_q[i][j] = fused2(q, x[j], sum_q[i][j]);
+                    d[i][j] = mul2(mul2(d[i][j], w[j]), x[j]);
+                    s = fused2(d[i][j], v[j], s);
+                }
+                st_v4(a.dgate_element + out + i * next_vector, pack4x2<FP16>(e));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[j] = mul2(v[j], post);
+                    sum_q[i][j] = fused2(mul2(d[i][j], v[j]), gate, sum_q[i][j]);
                     d[i][j] = mul2(d[i][j], w[j]);
                     s = fused2(d[i][j], v[j], s);
                 }
             }
         }
-        if (a.gate_kind == EP_GATE_ROW) s = row_sum;
-        const int after = stage + 1 == STAGES ? 0 : stage + 1;
+        const uint4* after = stage + 1 == STAGES ? mine : here + slots * slot;
         copies_wait<STAGES - 2>();
         sums = make_float2(a.pre_weight && row + gridDim.x < a.rows ? along_pre(after, then.pre) : 0.0f, s.x + s.y);
         if (a.pre_weight || a.post_weight || a.gate_kind == EP_GATE_ROW) sums = row_sums<WARP>(sums, part[parity]);
         if (a.gate_kind == EP_GATE_ROW && t == 0) a.dgate_row[row] = sums.y;
-        const float2 mean = both(-(a.gate_kind == EP_GATE_ROW ? sums.y * now.gate : sums.y) * inv_hidden);
+        const float2 mean = both(-sums.y * inv_hidden), scale = both(now.post * now.gate);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (i + 1 == VPT && !all) break;
             if (a.post_weight) {
                 float2 v[4];
-                unpack4x2<FP16>(*vector(stage, kSlotY, i), v);
+                unpack4x2<FP16>(here[kSlotY * slot + i * threads], v);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) d[i][j] = mul2(fused2(mul2(v[j], post), mean, d[i][j]), post);
+                for (int j = 0; j < 4; ++j) d[i][j] = fused2(mul2(v[j], post), mean, d[i][j]);
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[i][j] = mul2(d[i][j], scale);
             st_v4(a.dy + out + i * next_vector, pack4x2<FP16>(d[i]));
         }
         fetch(stage);
-        stage = after;
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+        here = after;
         now = then;
     }
-    auto leave = [&](const float2 (&s)[VPT][4], int which) {
+    // each sum times what it lacks: one of the channels' two factors, or nothing
+    auto leave = [&](const float2 (&s)[VPT][4], int which, const void* factor, int fp32) {
         float* to = a.partial + ((int64_t)blockIdx.x * 3 + which) * a.hidden;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (i + 1 == VPT && !all) break;
-            float4* p = reinterpret_cast<float4*>(to + 8 * (i * threads + t));
-            p[0] = make_float4(s[i][0].x, s[i][0].y, s[i][1].x, s[i][1].y);
-            p[1] = make_float4(s[i][2].x, s[i][2].y, s[i][3].x, s[i][3].y);
+            const int v = i * threads + t;
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = 1.0f;
+            if (factor) load_channels<FP16>(factor, fp32, v, f);
+            float4* p = reinterpret_cast<float4*>(to + 8 * v);
+            p[0] = make_float4(s[i][0].x * f[0], s[i][0].y * f[1], s[i][1].x * f[2], s[i][1].y * f[3]);
+            p[1] = make_float4(s[i][2].x * f[4], s[i][2].y * f[5], s[i][3].x * f[6], s[i][3].y * f[7]);
         }
     };
-    if (a.post_weight) leave(dpost, 0);
-    if (a.gate_kind == EP_GATE_CHANNEL) leave(dgate, 1);
-    if (a.pre_weight) leave(dpre, 2);
+    const bool channel = a.gate_kind == EP_GATE_CHANNEL;
+    if (a.post_weight) leave(sum_q, 0, channel ? a.gate : nullptr, a.gate_fp32);
+    if (channel) leave(sum_q, 1, a.post_weight, a.post_fp32);
+    if (a.pre_weight) leave(dpre, 2, nullptr, 0);
 }
 
 // ---- wider rows: a CTA per row, VPT vectors of 8 columns per thread
@@ -683,7 +703,7 @@ constexpr int kRowsPerCta = 4;
 int join_backward_ctas(int64_t rows, int hidden, int sms)
 {
     const int threads = team_threads(hidden);
-    const int64_t fit = (int64_t)sms * team_ctas_per_sm(kJoinTeamThreads, threads, (size_t)(3 * 5 + 4) * team_vectors(hidden) * threads * 16);
+    const int64_t fit = (int64_t)sms * team_ctas_per_sm(kJoinTeamThreads, threads, (size_t)(3 * 5 + kBackChannels) * team_vectors(hidden) * threads * 16);
     const int64_t want = (rows + kRowsPerCta - 1) / kRowsPerCta;
     const int64_t least = rows < sms ? rows : sms;
     return (int)(want < least ? least : want < fit ? want : fit);
@@ -693,12 +713,11 @@ template <bool FP16>
 cudaError_t launch_join_backward(const JoinArgs& a, int ctas, cudaStream_t s)
 {
     const int slots = a.gate_kind == EP_GATE_ELEMENT ? 5 : 4;
-    const size_t shared = team_shared(a, 3, slots);
-    if (a.hidden <= 256) return launch_team<ep_join_backward_kernel<FP16, true, 1, 3>>(a, ctas, shared, s);
-    if (team_threads(a.hidden) == 32) return launch_team<ep_join_backward_kernel<FP16, true, 2, 3>>(a, ctas, shared, s);
-    if (shared <= kJoinShared) return launch_team<ep_join_backward_kernel<FP16, false, 2, 3>>(a, ctas, shared, s);
-    // a gate per element or FP32 weights of wide rows take the third stage's place
-    return launch_team<ep_join_backward_kernel<FP16, false, 2, 2>>(a, ctas, team_shared(a, 2, slots), s);
+    auto shared = [&](int stages) { return (size_t)(stages * slots + kBackChannels) * team_vectors(a.hidden) * team_threads(a.hidden) * 16; };
+    if (a.hidden <= 256) return launch_team<ep_join_backward_kernel<FP16, true, 1, 3>>(a, ctas, shared(3), s);
+    if (team_threads(a.hidden) == 32) return launch_team<ep_join_backward_kernel<FP16, true, 2, 3>>(a, ctas, shared(3), s);
+    if (shared(3) <= kJoinShared) return launch_team<ep_join_backward_kernel<FP16, false, 2, 3>>(a, ctas, shared(3), s);
+    return launch_team<ep_join_backward_kernel<FP16, false, 2, 2>>(a, ctas, shared(2), s);
 }
 
 bool row_ok(const void* p, int64_t stride, int hidden)
