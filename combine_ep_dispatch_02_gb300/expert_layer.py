@@ -8,7 +8,8 @@ logical ranks' hidden rows and their routing and runs
     rms_norm_fp8 -> dispatch (FP8) -> sort by expert -> product with SwiGLU -> product
                  -> weighted return -> combine
 
-with the residual kept beside it.  Nothing in it waits for the GPU.  The command builds one layer with
+with the residual kept beside it.  ``decode`` is the same layer for a few rows of one set: norm, then the whole
+of the experts in one call.  Nothing in it waits for the GPU.  The command builds one layer with
 random weights, compares it with the same layer in FP32 and prints the median time of a pass.
 """
 from __future__ import annotations
@@ -57,6 +58,14 @@ class ExpertLayer:
         out, _ = p.combine(ep.return_rows(order, out, d.recv_w), None, d.epoch)
         return out, h.view(W, M, H)
 
+    def decode(self, x: torch.Tensor, residual: torch.Tensor, route):
+        """x, residual [rows][hidden] BF16, up to 128 rows of any rank; route(y) gives the experts [rows][k] int32 and
+        weights [rows][k] FP32 of the normed rows y [rows][hidden].  Returns (the experts' output [rows][hidden], the sum
+        x + residual that the next layer adds)."""
+        q, scales, h, y = ep.rms_norm_fp8(x, self.norm_weight, residual=residual, want_y=True)
+        experts, weights = route(y)
+        return ep.moe_few_rows(q, scales, experts, weights, *self.up, *self.down), h
+
     def close(self):
         self.plan.close()
 
@@ -89,6 +98,7 @@ def main(argv=None):
     a.add_argument("--hidden", type=int, default=2048)
     a.add_argument("--inner", type=int, default=1024)
     a.add_argument("--tokens-per-rank", type=int, default=256)
+    a.add_argument("--decode-rows", type=int, default=0, help="time decode with this many rows too")
     a.add_argument("--passes", type=int, default=20)
     a = a.parse_args(argv)
     W, E, k, H, I, M = a.ranks, a.experts_per_rank, a.topk, a.hidden, a.inner, a.tokens_per_rank
@@ -114,18 +124,31 @@ def main(argv=None):
     out, h = layer.forward(x, residual, route, n_tok)
     want = reference(x, residual, chosen["experts"].long(), chosen["weights"], n_tok, up, down, norm_weight)
     rel = ((out.float() - want).norm() / want.norm()).item()
-    times = []
-    for _ in range(a.passes):
-        t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-        t0.record()
-        layer.forward(x, residual, route, n_tok)
-        t1.record()
-        torch.cuda.synchronize()
-        times.append(t0.elapsed_time(t1) * 1e3)
+
+    def median(call):
+        times = []
+        for _ in range(a.passes):
+            t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            t0.record()
+            call()
+            t1.record()
+            torch.cuda.synchronize()
+            times.append(t0.elapsed_time(t1) * 1e3)
+        return sorted(times)[len(times) // 2]
+    shape = f"{W} x {E} experts, top-{k}, hidden {H}, inner {I}"
+    us = median(lambda: layer.forward(x, residual, route, n_tok))
+    print(f"{int(n_tok.sum())} tokens, {shape}: {us:.0f} us a pass, {rel:.3f} from the layer in FP32")
+    if a.decode_rows:
+        xd, rd = randn(a.decode_rows, H).to(torch.bfloat16), randn(a.decode_rows, H).to(torch.bfloat16)
+        out, _ = layer.decode(xd, rd, route)
+        want = reference(xd[None], rd[None], chosen["experts"][None].long(), chosen["weights"][None], [a.decode_rows], up, down,
+                         norm_weight)[0]
+        off = ((out.float() - want).norm() / want.norm()).item()
+        us = median(lambda: layer.decode(xd, rd, route))
+        print(f"{a.decode_rows} rows decoded, {shape}: {us:.0f} us a pass, {off:.3f} from the layer in FP32")
+        rel = max(rel, off)
     assert layer.plan.status() == 0 and ep.op_status() == 0
     layer.close()
-    print(f"{int(n_tok.sum())} tokens, {W} x {E} experts, top-{k}, hidden {H}, inner {I}: "
-          f"{sorted(times)[len(times) // 2]:.0f} us a pass, {rel:.3f} from the layer in FP32")
     return rel
 
 

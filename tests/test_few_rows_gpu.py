@@ -243,3 +243,11 @@ def test_nothing_of_the_workspace_is_read_before_it_is_written(rows):
                                *(t.data_ptr() for t in layer), ep.EP_BF16, out.data_ptr(), ws.data_ptr(), need,
                                torch.cuda.current_stream().cuda_stream) == ep.EP_OK
     assert torch.equal(out, want) and (ws[need:] == 0xFF).all()
+
+
+def test_example_layer_decodes():
+    """The rows are quantised once; see the bound of the example layer's other tests."""
+    from combine_ep_dispatch_02_gb300 import expert_layer
+    for rows in (1, 20, 128):
+        assert expert_layer.main(["--tokens-per-rank", "20", "--hidden", "512", "--inner", "272", "--passes", "1",
+                                  "--decode-rows", str(rows)]) <= 2.0 ** -3

@@ -440,3 +440,52 @@ def test_weight_gradient_on_a_stream_and_in_a_graph():
     dy.mul_(2)
     graph.replay()
     assert torch.equal(out, 2 * want)
+
+
+# ------------------------------------------------------------------------------------------- together
+
+@pytest.mark.parametrize("args", [["--rows", "97", "--hidden", "512", "--inner", "256", "--steps", "1"],
+                                  ["--rows", "33", "--experts", "5", "--topk", "3", "--hidden", "272", "--inner", "144", "--steps", "1"]])
+def test_a_training_step_has_the_gradients_of_the_block(args):
+    """Against autograd in FP64, by norms.  Rows pass e4m3 (2^-4 of each element at most, so of any norm) three times on the
+    way forward and twice on the way back, and a gradient is a product of one of each: five of them, with what each is
+    amplified by in the next kept below 2, leave less than 5 * 2^-4 * 2."""
+    from combine_ep_dispatch_02_gb300 import expert_training
+    for name, off in expert_training.main(args).items():
+        assert off <= 5 * 2.0 ** -3, (name, off)
+
+
+def test_training_step_replays_in_a_graph_and_back_to_back():
+    """Forward and backward as one graph, and as a stream of calls whose memory is reused: as calls one by one."""
+    from combine_ep_dispatch_02_gb300.expert_training import ExpertBlock
+    g, E, H, inner, rows = _gen(15), 6, 256, 144, 50
+    block = ExpertBlock(_randn(g, E, 2 * inner, H) * H ** -0.5, _randn(g, E, H, inner) * inner ** -0.5,
+                        *(1 + 0.1 * _randn(g, H) for _ in range(4)), 0.5)
+    x, dn = _randn(g, rows, H).to(torch.bfloat16), _randn(g, rows, H).to(torch.bfloat16)
+    idx = torch.rand(rows, E, generator=g, device=DEV).topk(2, 1).indices.int()
+    w = torch.softmax(_randn(g, rows, 2), 1)
+
+    def step():
+        n, kept = block.forward(x, idx, w)
+        return {"n": n, **block.backward(kept, dn)}
+    first = step()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        again = step()
+    for k in first:
+        assert torch.equal(first[k], again[k]), k
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    graph.replay()
+    for k in first:
+        assert torch.equal(first[k], out[k]), k
+    x.copy_(_randn(g, rows, H).to(torch.bfloat16))
+    graph.replay()
+    for k, v in step().items():
+        assert torch.equal(v, out[k]), k
