@@ -202,6 +202,25 @@ def test_join_strides_and_streams():
         assert torch.equal(getattr(x, name), getattr(z, name)), name
 
 
+@pytest.mark.parametrize("over", ["y", "residual"])
+@pytest.mark.parametrize("gate,post,pre", [FORMS[2], FORMS[3], FORMS[4]])
+@pytest.mark.parametrize("rows,hidden", [(700, 256), (700, 512), (700, 2064), (320, 8192), (3, 16400)])
+def test_join_writes_h_over_its_input(rows, hidden, gate, post, pre, over):
+    lib, m = ep.load_library(), _inputs(rows, hidden, torch.bfloat16, gate, post, pre, rows + hidden)
+    want = ep.rms_norm_join(**m, residual_scale=0.5)
+    m = {k: v if v is None else v.clone() for k, v in m.items()}
+    w, v, g = m["post_weight"], m["pre_weight"], m["gate"]
+    at = [None if t is None else t.data_ptr() for t in (w, g, v)]
+    j = ep.JoinArgs(m["y"].data_ptr(), hidden, at[0], at[1], hidden, at[2], rows, hidden, ep.EP_BF16,
+                    int(w is not None and w.dtype == torch.float32), int(v is not None and v.dtype == torch.float32),
+                    ep.GATE_KINDS[gate.rstrip("32")], int(g.dtype == torch.float32), 0.5, 1e-6)
+    n, root, pre_root = torch.empty_like(want.h), torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    rc = lib.ep_rms_norm_join(j, m["residual"].data_ptr(), hidden, m[over].data_ptr(), None if v is None else n.data_ptr(), None,
+                              None, root.data_ptr(), pre_root.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert rc == ep.EP_OK and torch.equal(m[over], want.h)
+    assert v is None or torch.equal(n, want.n)
+
+
 def test_join_of_no_rows_and_of_rows_of_zeros():
     t = torch.bfloat16
     w = torch.ones(256, dtype=t, device=DEV)
