@@ -8,8 +8,8 @@ logical ranks' hidden rows and their routing and runs
     rms_norm_fp8 -> dispatch (FP8) -> sort by expert -> product with SwiGLU -> product
                  -> weighted return -> combine
 
-with the residual kept beside it.  ``decode`` is the same layer for a few rows of one set: norm, then the whole
-of the experts in one call.  Nothing in it waits for the GPU.  The command builds one layer with
+with the residual kept beside it.  ``decode`` is the same layer for a few rows of one set: norm, then the whole of the
+experts in one call, or in the calls above where experts have several rows each.  Nothing in it waits for the GPU.  The command builds one layer with
 random weights, compares it with the same layer in FP32 and prints the median time of a pass.
 """
 from __future__ import annotations
@@ -59,12 +59,21 @@ class ExpertLayer:
         return out, h.view(W, M, H)
 
     def decode(self, x: torch.Tensor, residual: torch.Tensor, route):
-        """x, residual [rows][hidden] BF16, up to 128 rows of any rank; route(y) gives the experts [rows][k] int32 and
-        weights [rows][k] FP32 of the normed rows y [rows][hidden].  Returns (the experts' output [rows][hidden], the sum
-        x + residual that the next layer adds)."""
+        """x, residual [rows][hidden] BF16 of any rank; route(y) gives the experts [rows][k] int32 and weights [rows][k]
+        FP32 of the normed rows y [rows][hidden].  Returns (the experts' output [rows][hidden], the sum x + residual that
+        the next layer adds)."""
         q, scales, h, y = ep.rms_norm_fp8(x, self.norm_weight, residual=residual, want_y=True)
         experts, weights = route(y)
-        return ep.moe_few_rows(q, scales, experts, weights, *self.up, *self.down), h
+        rows, k = experts.shape
+        # One call against the sorted calls, in us: 1, 4, 8, 16 and 32 rows with 8 of 32 experts of 7168 x 2048 63 and 69, 152
+        # and 155, 216 and 214, 251 and 222, 328 and 230; 8 and 32 rows with 2 of 8 65 and 66, 91 and 70; 1, 8 and 32 rows with
+        # 4 of 32 of 2048 x 1024 13 and 19, 35 and 38, 55 and 47.  So the one call up to two rows to an expert on average.
+        if rows <= 128 and rows * k <= 2 * self.up[0].shape[0]:
+            return ep.moe_few_rows(q, scales, experts, weights, *self.up, *self.down), h
+        order = ep.sort_by_expert(experts, self.up[0].shape[0])
+        row, row_scales = ep.sorted_rows(order, q, scales)
+        z, z_scales = ep.matmul_fp8_swiglu(row, row_scales, *self.up, offsets=order.offsets)
+        return ep.return_rows(order, ep.matmul_fp8(z, z_scales, *self.down, offsets=order.offsets), weights), h
 
     def close(self):
         self.plan.close()

@@ -217,8 +217,8 @@ def moe_few_rows(x: torch.Tensor, x_scales: Optional[torch.Tensor], indices: tor
     [rows][k] int32 and FP32; up [experts][2 * inner][hidden] (gate rows, then up rows) and down [experts][hidden][inner]
     float8_e4m3fn with scales as ``matmul_fp8`` takes them; hidden and inner multiples of 16.  Ids outside first_expert ..
     first_expert + experts - 1 are left out; one that a row names several times counts once, with the sum of its weights.
-    The time is that of reading the named experts' weights; from a few tokens per expert on, sorted rows and
-    ``matmul_fp8_swiglu`` are faster."""
+    rows * k up to 4096, rows * k * inner below 2^31.  The time is that of reading the named experts' weights; from some two
+    rows to an expert on, sorted rows with ``matmul_fp8_swiglu`` and ``matmul_fp8`` are faster."""
     code = _OUT_CODES.get(out_dtype)
     if code is None:
         raise EpError(EP_ERR_ARG, f"out_dtype={out_dtype!r} is neither 'bf16' nor 'fp16'")

@@ -555,9 +555,10 @@ int ep_matmul_fp8_weight_gradient(const void* dy, int dtype, const void* a, cons
  *   out          [rows][hidden] of out_dtype (EP_BF16 or EP_FP16), 16-byte aligned; zeros for a row without an expert
  * Sums are in FP32, over the experts in ascending order; what SwiGLU yields is held as FP16 with a power of two for every
  * 8 columns, and each output is rounded once.  BF16 rows are brought to FP16, exactly but for what is 2^-28 of their
- * block's largest value or less.  Limits: rows up to 128, rows*topk up to 4096, experts up to 1024, hidden up to 2^20 and
- * inner up to 2^19, both multiples of 16.  The workspace holds ep_moe_few_workspace_bytes() at least, 16-byte aligned
- * (0 for no rows and for invalid shapes).  More rows are better sorted by expert (ep_sort_by_expert, ep_matmul_fp8).
+ * block's largest value or less.  Limits: rows up to 128, rows*topk up to 4096, rows*topk*inner below 2^31, experts up to
+ * 1024, hidden up to 2^20 and inner up to 2^19, both multiples of 16.  The workspace holds ep_moe_few_workspace_bytes() at least, 16-byte aligned
+ * (0 for no rows and for invalid shapes).  From some two rows to an expert on, rows sorted by expert and ep_matmul_fp8 are
+ * faster: 64 rows that name 8 of 32 experts of 7168 x 2048 take 462 us here and 240 us there, 4 rows 152 and 155.
  */
 size_t ep_moe_few_workspace_bytes(int64_t rows, int topk, int inner);
 int ep_moe_few_rows(const void* x, const float* x_scales, int x_dtype, const int32_t* indices, const float* weights,
