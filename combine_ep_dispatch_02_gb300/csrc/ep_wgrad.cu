@@ -241,7 +241,7 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
     } else {
         const int team = (warp - kFirstConverter) / kConvertTeam, thread = (int)(threadIdx.x - 32 * kFirstConverter) % (32 * kConvertTeam);
         const int row = thread / 8, piece = lane & 7;   // 16 codes of every (4 * kConvertTeam)th row from `row` on
-        const uint32_t to0 = (uint32_t)(kDyBytes + piece / 4 * kLineBytes);
+        const uint32_t to0 = (uint32_t)(kDyBytes + piece / 4 * kLineBytes), other = piece / 4;
         const uint32_t arrive = peer_smem(ready, 0);
         uint32_t n = 0;
         bool ok = true;
@@ -266,7 +266,10 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
 #pragma unroll
                 for (int h = 0; h < kTimes; ++h) {
                     const int r = row + 4 * kConvertTeam * h;
-                    const uint32_t word[4] = {c[h].x, c[h].y, c[h].z, c[h].w};
+                    // the lanes of the second line begin with their other half, so that each eight lanes, which hold a row,
+                    // fill all banks with a store: both lines' rows lie on the same
+                    const uint32_t word[4] = {other ? c[h].z : c[h].x, other ? c[h].w : c[h].y, other ? c[h].x : c[h].z,
+                                              other ? c[h].y : c[h].w};
                     uint32_t v[8];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -275,9 +278,9 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
                         v[2 * j] = r < left ? pack2<FP16>(lo.x, lo.y) : 0u;
                         v[2 * j + 1] = r < left ? pack2<FP16>(hi.x, hi.y) : 0u;
                     }
-                    const uint32_t to = stage + to0 + r * 128, at = 2 * (piece & 3), swap = r & 7;
+                    const uint32_t to = stage + to0 + r * 128, at = 2 * (piece & 3) + other, swap = r & 7;
                     smem_store4(to + ((at ^ swap) << 4), make_uint4(v[0], v[1], v[2], v[3]));
-                    smem_store4(to + (((at + 1) ^ swap) << 4), make_uint4(v[4], v[5], v[6], v[7]));
+                    smem_store4(to + ((at ^ 1 ^ swap) << 4), make_uint4(v[4], v[5], v[6], v[7]));
                 }
                 // the rest of the last 16 rows that are multiplied: dy's rows there are another group's
                 if (left < kGradRows) {
