@@ -105,13 +105,15 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_a)
 {
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t bars[3 * kGradStages + 5];
+    __shared__ __align__(8) uint64_t bars[5 * kGradStages + 5];
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
     const uint32_t stages = (smem_u32(raw) + 1023u) & ~1023u, scales = stages + kGradStages * kGradStageBytes;
-    // loaded: a stage's rows are here; ready (the first CTA's): both CTAs' values are; done: its products are
-    const uint32_t loaded = smem_u32(bars), ready = loaded + 8 * kGradStages, done = ready + 8 * kGradStages,
-                   summed = done + 8 * kGradStages, written = summed + 16, drained = written + 16;
+    // coded: a stage's codes and scales are here; taken: they are in registers; loaded: its rows of dy are here; ready (the
+    // first CTA's): both CTAs' operands are; done: its products are
+    const uint32_t coded = smem_u32(bars), taken = coded + 8 * kGradStages, loaded = taken + 8 * kGradStages,
+                   ready = loaded + 8 * kGradStages, done = ready + 8 * kGradStages, summed = done + 8 * kGradStages,
+                   written = summed + 16, drained = written + 16;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const Giveup giveup{&gave_up, p.status};
     const int rank = (int)cluster_rank();
@@ -120,7 +122,9 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
     if (threadIdx.x == 0) {
         gave_up = 0;
         for (int i = 0; i < kGradStages; ++i) {
-            bar_init(loaded + 8 * i, 1 + 32);
+            bar_init(coded + 8 * i, 1 + 32);
+            bar_init(taken + 8 * i, kConvertTeam);
+            bar_init(loaded + 8 * i, 1);
             bar_init(ready + 8 * i, 2 * kConvertTeam);
             bar_init(done + 8 * i, 1);
         }
@@ -142,36 +146,55 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
     const uint32_t tmem = tmem_slot;
 
     if (warp == 0) {
-        uint32_t n = 0;   // stages filled
+        // A stage's codes come as soon as those before them are in registers, its rows of dy a stage later, when the products
+        // of what was there are done: by then its codes are being converted.
+        uint32_t n = 0, m = 0;   // stages of codes and of dy on their way
+        int dy_column = 0, dy_row = 0;   // of stage m
         const bool leader = elect_one();
         bool ok = true;
+        auto load_dy = [&] {
+            const uint32_t slot = m % kGradStages, use = m / kGradStages, dst = stages + slot * kGradStageBytes, bar = loaded + 8 * slot;
+            if (use > 0 && !__all_sync(0xffffffffu, bar_wait(done + 8 * slot, (use - 1) & 1, giveup))) return false;
+            if (leader) {
+                bar_expect(bar, kDyBytes);
+                tma_load(dst, &map_dy, dy_column, dy_row, bar);
+                tma_load(dst + kLineBytes, &map_dy, dy_column + 64, dy_row, bar);
+            }
+            __syncwarp();
+            ++m;
+            return true;
+        };
         for (int64_t t = t_first; t < p.tiles && ok; t += t_step) {
             const GradTile x = grad_tile(p, t);
             const int n0 = x.n0 + kGradHalf * rank, k0 = x.k0 + kGradHalf * rank;
             const float* s = p.a_scales + min(k0 / 128, p.kb - 1);
             const int steps = grad_steps(x);
-            for (int i = 0; i < steps; ++i, ++n) {
+            for (int i = 0; i < steps && ok; ++i) {
                 const uint32_t slot = n % kGradStages, use = n / kGradStages;
-                if (use > 0) ok = __all_sync(0xffffffffu, bar_wait(done + 8 * slot, (use - 1) & 1, giveup));
+                if (use > 0) ok = __all_sync(0xffffffffu, bar_wait(taken + 8 * slot, (use - 1) & 1, giveup));
                 if (n == kWithheldBlock || !ok) { ok = false; break; }
-                const uint32_t dst = stages + slot * kGradStageBytes, bar = loaded + 8 * slot;
+                const uint32_t bar = coded + 8 * slot;
                 const int r = x.r0 + kGradRows * i;
                 if (leader) {
-                    bar_expect(bar, kDyBytes + kCodeBytes);
-                    tma_load(dst, &map_dy, n0, r, bar);
-                    tma_load(dst + kLineBytes, &map_dy, n0 + 64, r, bar);
-                    tma_load(dst + kDyBytes + kValueBytes, &map_a, k0, r, bar);
+                    bar_expect(bar, kCodeBytes);
+                    tma_load(stages + slot * kGradStageBytes + kDyBytes + kValueBytes, &map_a, k0, r, bar);
                 }
                 __syncwarp();
                 const uint32_t to = scales + 4 * (slot * kGradRows + lane);
                 if (r + lane < x.r1) copy4(to, s + (int64_t)(r + lane) * p.kb);
                 if (r + lane + 32 < x.r1) copy4(to + 128, s + (int64_t)(r + lane + 32) * p.kb);
                 copies_arrive(bar);
+                if (n++ > 0) ok = load_dy();
+                dy_column = n0;
+                dy_row = r;
             }
         }
-        if (!ok) {   // its loads in flight
+        if (ok && n > 0) ok = load_dy();
+        if (!ok || *giveup.flag) {   // its loads in flight, for which no other role may wait
             const long long t0 = clock64();
             for (uint32_t j = n < kGradStages ? 0 : n - kGradStages; j < n; ++j)
+                bar_drain(coded + 8 * (j % kGradStages), (j / kGradStages) & 1, t0);
+            for (uint32_t j = m < kGradStages ? 0 : m - kGradStages; j < m; ++j)
                 bar_drain(loaded + 8 * (j % kGradStages), (j / kGradStages) & 1, t0);
         }
         __syncwarp();
@@ -249,10 +272,10 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
             const GradTile x = grad_tile(p, t);
             const int steps = grad_steps(x);
             for (int i = 0; i < steps; ++i, ++n) {
-                const uint32_t slot = n % kGradStages;
+                const uint32_t slot = n % kGradStages, use = n / kGradStages;
                 if (slot != (uint32_t)team) continue;
                 const uint32_t stage = stages + slot * kGradStageBytes;
-                ok = __all_sync(0xffffffffu, bar_wait(loaded + 8 * slot, (n / kGradStages) & 1, giveup));
+                ok = __all_sync(0xffffffffu, bar_wait(coded + 8 * slot, use & 1, giveup));
                 if (!ok) break;
                 const int left = x.r1 - x.r0 - kGradRows * i;   // rows of this stage that are the group's
                 constexpr int kTimes = kGradRows / (4 * kConvertTeam);
@@ -263,6 +286,10 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
                     c[h] = smem_load4(stage + kDyBytes + kValueBytes + (row + 4 * kConvertTeam * h) * kGradHalf + 16 * piece);
                     s[h] = smem_load(scales + 4 * (slot * kGradRows + row + 4 * kConvertTeam * h));
                 }
+                __syncwarp();
+                if (lane == 0) bar_arrive(taken + 8 * slot);
+                if (use > 0) ok = __all_sync(0xffffffffu, bar_wait(done + 8 * slot, (use - 1) & 1, giveup));
+                if (!ok) break;
 #pragma unroll
                 for (int h = 0; h < kTimes; ++h) {
                     const int r = row + 4 * kConvertTeam * h;
@@ -282,6 +309,8 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
                     smem_store4(to + ((at ^ swap) << 4), make_uint4(v[0], v[1], v[2], v[3]));
                     smem_store4(to + ((at ^ 1 ^ swap) << 4), make_uint4(v[4], v[5], v[6], v[7]));
                 }
+                ok = __all_sync(0xffffffffu, bar_wait(loaded + 8 * slot, use & 1, giveup));
+                if (!ok) break;
                 // the rest of the last 16 rows that are multiplied: dy's rows there are another group's
                 if (left < kGradRows) {
                     const int q = thread & 15, end = (left + 15) / 16 * 16;
