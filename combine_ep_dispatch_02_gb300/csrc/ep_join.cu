@@ -11,6 +11,11 @@
 //
 // All in FP32; each output is rounded once.  mean(p * v) is the mean of gate * D * u, so that a row's own gate and the
 // norm share one sum.
+//
+// Measured: 32768 rows of 7168, codes out, 289 us (5.7 TB/s): bytes take 244 us, and three quarters of the issue slots
+// are taken.  One row 3.4 us.  The gradient of 8192 rows of 7168 143 us (4.9 TB/s; bytes 104): the CTA's 16 warps, all
+// that its 126 registers and 200 KB of rows on their way allow, wait for one another at a sum and for their stages, and
+// 9 us go to the sums over CTAs.
 #include "ep_layer.cuh"
 
 namespace ep {

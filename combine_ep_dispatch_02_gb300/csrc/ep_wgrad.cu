@@ -12,6 +12,12 @@
 // warp 0 loads 64 rows of dy and of codes by TMA, and the rows' scales, into one of kGradStages stages; two warps to a
 // stage make 16-bit values of the codes, in the order that the tensor cores read; warp 1 of the first CTA multiplies for
 // both; eight warps write the sums out.
+//
+// Measured: 8192 rows in 8 groups of 4096 x 7168 326 us (1475 TFLOP/s), 32768 in 32 groups 1393 us (1380 TFLOP/s, for
+// which the card holds 1.75 GHz at its power limit; at 2.07 GHz a plain BF16 product reaches 1890). A stage takes 880 cycles,
+// of which its products need 512 and shared memory 640: 24 KB come in, the codes are read, the values written, and the
+// tensor cores read 32 KB. The rest is the conversion: with its work left out the same rows take 259 us, without the sums'
+// way out 291.
 #include "ep_tcgen05.cuh"
 
 namespace ep {
