@@ -371,6 +371,17 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar)
     asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" :: "r"(bar) : "memory");
 }
 
+// A box of shared memory to global memory, asynchronously, by one thread; the thread's stores are one group each, and
+// stores_wait_read() returns when their bytes have been read, stores_wait() when they have been written.
+__device__ __forceinline__ void tma_store3(const CUtensorMap* map, uint32_t from, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 :: "l"(map), "r"(from), "r"(x), "r"(y), "r"(z) : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void stores_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void stores_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 __device__ __forceinline__ uint4 smem_load4(uint32_t addr)
 {
     uint4 v;
@@ -460,19 +471,17 @@ inline EncodeTiled encode_tiled()
     return fn;
 }
 
-// Map of a dense [rows][columns] array, elements of `size` bytes, with boxes of box_rows x box_columns, swizzled by 128 bytes
-// or not at all; elements past either end read as zeros.
-inline int make_tile_map(CUtensorMap* m, const char* who, const char* what, const void* base, CUtensorMapDataType type, int size,
-                         int64_t rows, int64_t columns, int box_rows, int box_columns, bool swizzled)
+// Map of a dense array of `rank` dimensions, innermost first, with boxes of `box`; elements past an end read as zeros and are
+// not written.
+inline int make_box_map(CUtensorMap* m, const char* who, const char* what, const void* base, CUtensorMapDataType type, int rank,
+                        const cuuint64_t* dims, const cuuint64_t* pitch, const cuuint32_t* box, CUtensorMapSwizzle swizzle)
 {
     const EncodeTiled encode = encode_tiled();
     if (!encode) return layer_fail(EP_ERR_CUDA, "%s: the driver has no cuTensorMapEncodeTiled", who);
-    const cuuint64_t dims[2] = {(cuuint64_t)columns, (cuuint64_t)rows}, pitch[1] = {(cuuint64_t)columns * size};
-    const cuuint32_t box[2] = {(cuuint32_t)box_columns, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    const cuuint32_t step[3] = {1, 1, 1};
     auto make = [&] {
-        return encode(m, type, 2, const_cast<void*>(base), dims, pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                      swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        return encode(m, type, rank, const_cast<void*>(base), dims, pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     };
     CUresult r = make();
     if (r == CUDA_ERROR_INVALID_CONTEXT) {   // a host thread's first call, which nothing has bound to the device yet
@@ -487,6 +496,15 @@ inline int make_tile_map(CUtensorMap* m, const char* who, const char* what, cons
     }
     if (r != CUDA_SUCCESS) return layer_fail(EP_ERR_CUDA, "%s: tensor map of %s: CUresult %d", who, what, (int)r);
     return EP_OK;
+}
+
+// Of [rows][columns], elements of `size` bytes, with boxes of box_rows x box_columns, swizzled by 128 bytes or not at all.
+inline int make_tile_map(CUtensorMap* m, const char* who, const char* what, const void* base, CUtensorMapDataType type, int size,
+                         int64_t rows, int64_t columns, int box_rows, int box_columns, bool swizzled)
+{
+    const cuuint64_t dims[2] = {(cuuint64_t)columns, (cuuint64_t)rows}, pitch[1] = {(cuuint64_t)columns * size};
+    const cuuint32_t box[2] = {(cuuint32_t)box_columns, (cuuint32_t)box_rows};
+    return make_box_map(m, who, what, base, type, 2, dims, pitch, box, swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 template <typename... Params, typename... Args>

@@ -39,18 +39,18 @@ constexpr int kFirstWriter = 2, kFirstConverter = kFirstWriter + kWriteWarps;
 constexpr int kConvertTeam = 2;
 constexpr int kGradThreads = 32 * (kFirstConverter + kGradStages * kConvertTeam);   // load, multiply, write, convert
 constexpr int kMaxGradGroups = 4096;
-constexpr size_t kGradShared = 1024 + kGradStages * (kGradStageBytes + kGradRows * 4);
+constexpr int kOutBytes = 2048;   // of a writing warp
+constexpr size_t kGradShared = 1024 + kGradStages * (kGradStageBytes + kGradRows * 4) + kWriteWarps * kOutBytes;
 
 struct GradArgs {
     const float* a_scales;
     const int32_t* offsets;   // [groups + 1], or NULL: one group of all rows
-    void* out;
     int* status;
     int64_t rows;
     int groups, columns, inner, kb;
     int n_tiles, k_tiles;
     int64_t tiles;
-    int out_fp32, vec;        // vec: as for store_lines
+    int out_fp32;
 };
 
 struct GradTile {
@@ -76,45 +76,46 @@ __device__ __forceinline__ GradTile grad_tile(const GradArgs& p, int64_t t)
 
 __device__ __forceinline__ int grad_steps(const GradTile& x) { return (x.r1 - x.r0 + kGradRows - 1) / kGradRows; }
 
-// 64 columns of a warp's 32 rows of a tile to memory, from tensor memory (zeros where there is none): `m` rows and `n`
-// columns of them exist.
+// A warp's 32 rows of 32 sums to memory, through 2 KB of shared memory of its own and a TMA store, which writes no more
+// of them than exist: x and y are their first column and row in group g.  32-bit sums go in two halves.  The box's rows
+// of 64 bytes are swizzled, so that eight lanes' 16 bytes fill all banks.
 template <bool FP16>
-__device__ __forceinline__ void write_sums(const GradArgs& p, int64_t at, uint32_t from, bool some, int m, int n)
+__device__ __forceinline__ void write_sums(const GradArgs& p, const CUtensorMap* map, uint32_t buffer, const uint32_t (&r)[32],
+                                           int x, int y, int g)
 {
-    uint32_t w[4][8];
+    const int lane = threadIdx.x & 31;
+    auto send = [&](const uint32_t* w, int column) {
+        if (lane == 0) stores_wait_read();   // of what was in the buffer
+        __syncwarp();
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t r[32];
-        if (some) {
-            tmem_load32(r, from + 32 * h);
-            tmem_wait(r);
-        } else {
+        for (int j = 0; j < 4; ++j)
+            smem_store4(buffer + 64 * lane + ((j ^ ((lane >> 1) & 3)) << 4), make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
+        fence_async();
+        __syncwarp();
+        if (lane == 0) tma_store3(map, buffer, column, y, g);
+    };
+    if (p.out_fp32) {
+        send(r, x);
+        if (x + 16 < p.inner) send(r + 16, x + 16);
+    } else {
+        uint32_t w[16];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = 0;
-        }
-        if (p.out_fp32) {
-            uint4* out = reinterpret_cast<uint4*>((float*)p.out + at + (int64_t)(threadIdx.x & 31) * p.inner + 32 * h);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)   // n is a multiple of 16
-                if ((int)(threadIdx.x & 31) < m && 32 * h + 4 * j < n)
-                    out[j] = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            w[2 * h + j / 8][j & 7] = pack2<FP16>(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+        for (int j = 0; j < 16; ++j) w[j] = pack2<FP16>(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+        send(w, x);
     }
-    if (!p.out_fp32) store_lines((uint8_t*)p.out + 2 * at, 2 * (int64_t)p.inner, w, m, n, p.vec);
 }
 
 template <bool FP16>
 __global__ void __launch_bounds__(kGradThreads, 1)
-ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_a)
+ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_a,
+                          const __grid_constant__ CUtensorMap map_dw)
 {
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t bars[5 * kGradStages + 5];
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
-    const uint32_t stages = (smem_u32(raw) + 1023u) & ~1023u, scales = stages + kGradStages * kGradStageBytes;
+    const uint32_t stages = (smem_u32(raw) + 1023u) & ~1023u, outs = stages + kGradStages * kGradStageBytes,
+                   scales = outs + kWriteWarps * kOutBytes;
     // coded: a stage's codes and scales are here; taken: they are in registers; loaded: its rows of dy are here; ready (the
     // first CTA's): both CTAs' operands are; done: its products are
     const uint32_t coded = smem_u32(bars), taken = coded + 8 * kGradStages, loaded = taken + 8 * kGradStages,
@@ -142,6 +143,7 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
         fence_barrier_init();
         prefetch_map(&map_dy);
         prefetch_map(&map_a);
+        prefetch_map(&map_dw);
     }
     if (warp == 1) tmem_alloc_pair(smem_u32(&tmem_slot), 512);
     follow_predecessor();
@@ -245,6 +247,7 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
         bool ok = true;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const int part = (warp - kFirstWriter) / 4 * kGradHalf;
+        const uint32_t buffer = outs + (warp - kFirstWriter) * kOutBytes;
         for (int64_t t = t_first; t < p.tiles && ok; t += t_step) {
             const GradTile x = grad_tile(p, t);
             const bool some = x.r1 > x.r0;
@@ -255,11 +258,18 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
                 tmem_fence_after();
             }
             const int row = x.n0 + kGradHalf * rank + (warp & 3) * 32;
-            const int64_t at = ((int64_t)x.g * p.columns + row) * p.inner + x.k0;
 #pragma unroll 1
-            for (int c = part; c < part + kGradHalf; c += 64)
-                if (x.k0 + c < p.inner && row < p.columns)
-                    write_sums<FP16>(p, at + c, tmem + lanes + u * kGradTile + c, some, p.columns - row, p.inner - x.k0 - c);
+            for (int c = part; c < part + kGradHalf && x.k0 + c < p.inner && row < p.columns; c += 32) {
+                uint32_t r[32];
+                if (some) {
+                    tmem_load32(r, tmem + lanes + u * kGradTile + c);
+                    tmem_wait(r);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] = 0;
+                }
+                write_sums<FP16>(p, &map_dw, buffer, r, x.k0 + c, row, x.g);
+            }
             if (some) {
                 tmem_fence_before();
                 __syncwarp();
@@ -267,6 +277,8 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
                 ++tile;
             }
         }
+        if (lane == 0) stores_wait();
+        __syncwarp();
     } else {
         const int team = (warp - kFirstConverter) / kConvertTeam, thread = (int)(threadIdx.x - 32 * kFirstConverter) % (32 * kConvertTeam);
         const int row = thread / 8, piece = lane & 7;   // 16 codes of every (4 * kConvertTeam)th row from `row` on
@@ -339,12 +351,13 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
 }
 
 template <bool FP16>
-cudaError_t launch_gradient(const GradArgs& p, const CUtensorMap& dy, const CUtensorMap& a, int sms, cudaStream_t s)
+cudaError_t launch_gradient(const GradArgs& p, const CUtensorMap& dy, const CUtensorMap& a, const CUtensorMap& dw, int sms,
+                            cudaStream_t s)
 {
     const cudaError_t e = allow_all_shared<ep_weight_gradient_kernel<FP16>>();
     if (e != cudaSuccess) return e;
     const int64_t pairs = p.tiles < sms / 2 ? p.tiles : sms / 2;
-    return launch_cluster(ep_weight_gradient_kernel<FP16>, (unsigned)(2 * pairs), kGradThreads, kGradShared, 2, s, p, dy, a);
+    return launch_cluster(ep_weight_gradient_kernel<FP16>, (unsigned)(2 * pairs), kGradThreads, kGradShared, 2, s, p, dy, a, dw);
 }
 
 }  // namespace
@@ -376,21 +389,25 @@ extern "C" int ep_matmul_fp8_weight_gradient(const void* dy, int dtype, const vo
     if (!layer_aligned(dy, 16) || !layer_aligned(a, 16) || !layer_aligned(a_scales, 4))
         return layer_fail(EP_ERR_ARG, "%s: dy, a or a_scales is NULL or misaligned", who);
     GradArgs p{};
-    p.a_scales = a_scales; p.offsets = offsets; p.out = dw; p.status = device_status; p.rows = rows; p.groups = groups;
+    p.a_scales = a_scales; p.offsets = offsets; p.status = device_status; p.rows = rows; p.groups = groups;
     p.columns = columns; p.inner = inner; p.kb = (inner + 127) / 128;
     p.n_tiles = (columns + kGradTile - 1) / kGradTile; p.k_tiles = (inner + kGradTile - 1) / kGradTile;
     p.tiles = (int64_t)groups * p.n_tiles * p.k_tiles;
     p.out_fp32 = out_fp32 != 0;
-    p.vec = layer_aligned(dw, 32) ? 2 : 1;
     const int sms = layer_num_sms();
     if (sms < 2) return layer_fail(EP_ERR_CUDA, "%s: cannot tell the current device's multiprocessors", who);
-    CUtensorMap m_dy, m_a;
+    CUtensorMap m_dy, m_a, m_dw;
     const bool fp16 = dtype == EP_FP16;
-    if (int rc = make_tile_map(&m_dy, who, "dy", dy, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                               rows, columns, kGradRows, 64, true))
-        return rc;
+    const CUtensorMapDataType half = fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    if (int rc = make_tile_map(&m_dy, who, "dy", dy, half, 2, rows, columns, kGradRows, 64, true)) return rc;
     if (int rc = make_tile_map(&m_a, who, "a", a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, inner, kGradRows, kGradHalf, false))
         return rc;
-    const cudaError_t e = fp16 ? launch_gradient<true>(p, m_dy, m_a, sms, s) : launch_gradient<false>(p, m_dy, m_a, sms, s);
+    const cuuint64_t size = p.out_fp32 ? 4 : 2, row_bytes = size * inner;
+    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)columns, (cuuint64_t)groups}, pitch[2] = {row_bytes, row_bytes * columns};
+    const cuuint32_t box[3] = {p.out_fp32 ? 16u : 32u, 32, 1};
+    if (int rc = make_box_map(&m_dw, who, "dw", dw, p.out_fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : half, 3, dims, pitch, box,
+                              CU_TENSOR_MAP_SWIZZLE_64B))
+        return rc;
+    const cudaError_t e = fp16 ? launch_gradient<true>(p, m_dy, m_a, m_dw, sms, s) : launch_gradient<false>(p, m_dy, m_a, m_dw, sms, s);
     return layer_cuda(e, "ep_matmul_fp8_weight_gradient: launch");
 }
