@@ -116,7 +116,7 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
     __shared__ int gave_up;
     const uint32_t stages = (smem_u32(raw) + 1023u) & ~1023u, outs = stages + kGradStages * kGradStageBytes,
                    scales = outs + kWriteWarps * kOutBytes;
-    // coded: a stage's codes and scales are here; taken: they are in registers; loaded: its rows of dy are here; ready (the
+    // coded: a stage's codes and scales are here; taken: they have been converted; loaded: its rows of dy are here; ready (the
     // first CTA's): both CTAs' operands are; done: its products are
     const uint32_t coded = smem_u32(bars), taken = coded + 8 * kGradStages, loaded = taken + 8 * kGradStages,
                    ready = loaded + 8 * kGradStages, done = ready + 8 * kGradStages, summed = done + 8 * kGradStages,
@@ -154,8 +154,8 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
     const uint32_t tmem = tmem_slot;
 
     if (warp == 0) {
-        // A stage's codes come as soon as those before them are in registers, its rows of dy a stage later, when the products
-        // of what was there are done: by then its codes are being converted.
+        // A stage's codes come as soon as those before them have been converted, its rows of dy a stage later, when the products
+        // of what was there are done.
         uint32_t n = 0, m = 0;   // stages of codes and of dy on their way
         int dy_column = 0, dy_row = 0;   // of stage m
         const bool leader = elect_one();
@@ -304,8 +304,6 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
                     c[h] = smem_load4(stage + kDyBytes + kValueBytes + (row + 4 * kConvertTeam * h) * kGradHalf + 16 * piece);
                     s[h] = smem_load(scales + 4 * (slot * kGradRows + row + 4 * kConvertTeam * h));
                 }
-                __syncwarp();
-                if (lane == 0) bar_arrive(taken + 8 * slot);
                 if (use > 0) ok = __all_sync(0xffffffffu, bar_wait(done + 8 * slot, (use - 1) & 1, giveup));
                 if (!ok) break;
 #pragma unroll
@@ -327,6 +325,11 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
                     smem_store4(to + ((at ^ swap) << 4), make_uint4(v[0], v[1], v[2], v[3]));
                     smem_store4(to + ((at ^ 1 ^ swap) << 4), make_uint4(v[4], v[5], v[6], v[7]));
                 }
+                // Behind the fence, because the next codes come by the asynchronous unit, which no barrier alone orders after this
+                // warp's reads: handed back as soon as they were read, a stage in some million had the next one's codes.
+                fence_async();
+                __syncwarp();
+                if (lane == 0) bar_arrive(taken + 8 * slot);
                 ok = __all_sync(0xffffffffu, bar_wait(loaded + 8 * slot, use & 1, giveup));
                 if (!ok) break;
                 // the rest of the last 16 rows that are multiplied: dy's rows there are another group's
@@ -334,8 +337,8 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
                     const int q = thread & 15, end = (left + 15) / 16 * 16;
                     for (int r = left + thread / 16; r < end; r += 2 * kConvertTeam)
                         smem_store4(stage + q / 8 * kLineBytes + r * 128 + 16 * (q & 7), make_uint4(0, 0, 0, 0));
+                    fence_async();
                 }
-                fence_async();
                 __syncwarp();
                 if (lane == 0) pair_arrive(arrive + 8 * slot);
             }

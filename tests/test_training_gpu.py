@@ -441,6 +441,27 @@ def test_weight_gradient_with_many_tiles_to_a_pair():
     _check_gradient(dy, a, s, offsets)
 
 
+@pytest.mark.parametrize("rows,columns,inner,groups", [(8192, 4096, 7168, 8), (16384, 1024, 2048, 8), (6000, 2048, 2064, 7)])
+def test_weight_gradients_are_the_same_every_time(rows, columns, inner, groups):
+    """Many stages one after another, random codes: one that met another stage's rows, codes or scales would differ."""
+    g = _gen(rows)
+    dy = _randn(g, rows, columns).to(torch.bfloat16)
+    a = (100 * _randn(g, rows, inner)).clamp_(-448, 448).to(torch.float8_e4m3fn)
+    s = torch.rand(rows, _blocks(inner), generator=g, device=DEV)
+    offsets = torch.linspace(0, rows, groups + 1, device=DEV).int()
+    want = ep.matmul_fp8_weight_gradient(dy, a, s, offsets=offsets)
+    for _ in range(60):
+        assert torch.equal(ep.matmul_fp8_weight_gradient(dy, a, s, offsets=offsets), want)
+    # the first and the last group against products of the values as the kernel rounds them: see test_weight_gradient
+    for e in (0, groups - 1):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        v = (a[lo:hi].float() * s[lo:hi].repeat_interleave(128, 1)[:, :inner]).to(torch.bfloat16).float()
+        y = dy[lo:hi].float()
+        exact = y.t().double() @ v.double()
+        size = y.abs().t().double() @ v.abs().double()
+        _within(want[e], exact, _half_bound(torch.bfloat16, exact) + (hi - lo) * U * size, f"group {e}")
+
+
 def test_weight_gradient_on_a_stream_and_in_a_graph():
     g = _gen(14)
     dy, a, s = _gradient_inputs(g, 200, 256, 384, torch.bfloat16)
