@@ -11,13 +11,13 @@
 // operand and 128 x 256 sums in tensor memory, twice, so that a tile's sums leave while the next is multiplied.  Per CTA:
 // warp 0 loads 64 rows of dy and of codes by TMA, and the rows' scales, into one of kGradStages stages; two warps to a
 // stage make 16-bit values of the codes, in the order that the tensor cores read; warp 1 of the first CTA multiplies for
-// both; eight warps write the sums out.
+// both; eight warps hand the sums to TMA stores.
 //
-// Measured: 8192 rows in 8 groups of 4096 x 7168 326 us (1475 TFLOP/s), 32768 in 32 groups 1393 us (1380 TFLOP/s, for
-// which the card holds 1.75 GHz at its power limit; at 2.07 GHz a plain BF16 product reaches 1890). A stage takes 880 cycles,
-// of which its products need 512 and shared memory 640: 24 KB come in, the codes are read, the values written, and the
-// tensor cores read 32 KB. The rest is the conversion: with its work left out the same rows take 259 us, without the sums'
-// way out 291.
+// Measured: 8192 rows in 8 groups of 4096 x 7168 314 us (1530 TFLOP/s), 2048 in 16 groups 171 us (5.5 TB/s of dw), 32768 in
+// 32 groups 1365 us (1410 TFLOP/s, where the card holds 1.75 GHz at its power limit; a plain BF16 product reaches 1890 in a
+// burst and 1700 at the limit).  A stage takes 850 cycles, of which its products need 512 and shared memory 640: 24 KB
+// come in, the codes are read, the values written, and the tensor cores read 32 KB.  The rest is the conversion, a stage's
+// chain of 128 codes a lane: with it left out, and the sums' way out as it was before, 340 us became 259.
 #include "ep_tcgen05.cuh"
 
 namespace ep {
@@ -30,12 +30,13 @@ constexpr int kLineBytes = 8192;                   // 64 columns x 64 rows of 16
 constexpr int kDyBytes = 2 * kLineBytes, kValueBytes = 2 * kLineBytes, kCodeBytes = kGradRows * kGradHalf;
 constexpr int kGradStageBytes = kDyBytes + kValueBytes + kCodeBytes;
 constexpr int kGradStages = 5;
-// Two to a quarter of the lanes, 128 columns each.  With four, 340 and 245 us.
+// Two to a quarter of the lanes, 128 columns each.  8 and 4 warps: 8192 rows in 8 groups of 4096 x 7168 314 and 320 us, 2048
+// in 16 groups 171 and 226.
 constexpr int kWriteWarps = 8;
 constexpr int kFirstWriter = 2, kFirstConverter = kFirstWriter + kWriteWarps;
 // Warps that convert a stage.  Each stage has a team of its own: a barrier's parity tells one phase from the next alone, so
-// whoever waits for a stage's phase has to have seen the one before.  Teams of 1, 2 and 4 warps: 8192 rows in 8 groups
-// of 4096 x 7168 401, 352 and 345 us, 2048 rows in 16 groups 223, 217 and 293 us (the writing warps then lack registers).
+// whoever waits for a stage's phase has to have seen the one before.  Teams of 2 and 4 warps: the same rows
+// 314 and 341 us, 171 and 182 (with 62 registers a thread instead of 93); of 1 against 2, when both were slower, 401 and 352.
 constexpr int kConvertTeam = 2;
 constexpr int kGradThreads = 32 * (kFirstConverter + kGradStages * kConvertTeam);   // load, multiply, write, convert
 constexpr int kMaxGradGroups = 4096;
