@@ -8,7 +8,7 @@
 //
 // HBM-bound by its bytes (7 of a z forward, 8 or 10 backward), with arithmetic close behind: a lane owns 8
 // columns of gate and the same 8 of up, so sixteen lanes hold a block of 128, its maximum takes four shuffles and nothing
-// passes through shared memory.  32768 rows of 2048 take 88 us (5.4 TB/s), the gradient with codes 107 us (6.4 TB/s): the
+// passes through shared memory.  32768 rows of 2048 take 84 us (5.6 TB/s), the gradient with codes 103 us (6.6 TB/s): the
 // forward pass has three quantisers and a sigmoid for 7 bytes, and its instructions take as long as its bytes.  Where the row's blocks straddle gate and up (inner no multiple of 128), blocks of
 // the row are quantised by sixteen lanes of their own, which read again what their neighbours have just read.
 #include "ep_layer.cuh"
@@ -16,7 +16,9 @@
 namespace ep {
 namespace {
 
-constexpr int kSwigluThreads = 256;
+// Small CTAs, nine to an SM, whose ends lie apart: 32768 rows of 2048 84.4 us and, the gradient, 103.2; with 256 threads 88.1
+// and 108.4, with ten CTAs (51 registers) 87.5 and 102.8, with 512 threads 96 and 115.
+constexpr int kSwigluThreads = 128, kSwigluCtas = 9;
 constexpr int kSwigluTeams = kSwigluThreads / 16;   // half warps, a block of 128 columns each
 constexpr int kSwigluUnits = 2;                     // blocks of a half warp, so that both loads are on their way at once
 
@@ -127,7 +129,7 @@ __device__ __forceinline__ int rows_in_use(const SwigluArgs& a)
 // Unit u: a block of z's columns with its gate and up, all three of which are quantised; with STRADDLE z alone, and the
 // units past a row's z blocks quantise the row's own blocks.
 template <bool FP16, bool STRADDLE>
-__global__ void __launch_bounds__(kSwigluThreads) ep_swiglu_saved_kernel(const SwigluArgs a)
+__global__ void __launch_bounds__(kSwigluThreads, kSwigluCtas) ep_swiglu_saved_kernel(const SwigluArgs a)
 {
     const int lane = threadIdx.x & 15;
     follow_predecessor();
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(kSwigluThreads) ep_swiglu_saved_kernel(const S
 // Unit u: a block of z's columns, whose gradients of gate and up leave; with QUANTISE also as codes.  With STRADDLE
 // (and codes) a unit is instead a block of the row of both gradients.
 template <bool FP16, bool QUANTISE, bool STRADDLE>
-__global__ void __launch_bounds__(kSwigluThreads) ep_swiglu_backward_kernel(const SwigluArgs a)
+__global__ void __launch_bounds__(kSwigluThreads, kSwigluCtas) ep_swiglu_backward_kernel(const SwigluArgs a)
 {
     const int lane = threadIdx.x & 15;
     follow_predecessor();
