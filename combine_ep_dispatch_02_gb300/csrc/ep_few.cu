@@ -21,8 +21,9 @@
 // Each CTA finds by itself what it has to do: it sorts the rows by expert, in shared memory, by a bit for each row and
 // expert.  A row that names an expert in several slots counts once, with the sum of those slots' weights.
 //
-// The first kernel leaves z as FP16 with a power of two for every 8 columns, so that the second's operand keeps 11 bits
-// whatever z's range; the e4m3 that a chain of products would leave has 4.  The second kernel's CTA owns 16 output
+// The first kernel leaves z as FP16 with a power of two for every 8 columns.  The second brings a block of 128 columns to one
+// power of two, so that its operand keeps 11 bits down to 2^-28 of the block's largest value, and what is smaller to 2^-39 of
+// that value; the e4m3 that a chain of products would leave has 4 bits.  The second kernel's CTA owns 16 output
 // columns, over every expert: each output is summed in one place, in a fixed order.  It is a programmatic dependent
 // that reads weights before it waits: the first kernel lets it start only after its own wait, when all that precedes the
 // call has completed, and the weights are nothing that the first writes.
@@ -191,10 +192,10 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
 // 2^n for n in -126..127.
 __device__ __forceinline__ float power2(int n) { return __int_as_float((n + 127) << 23); }
 
-// 2^-m and 2^-n as FP16 in the low and the high half, m, n >= 0; 0 below its smallest number.
+// 2^-m and 2^-n as FP16 in the low and the high half, held at its smallest number, 2^-24; m, n >= 0.
 __device__ __forceinline__ uint32_t half_power2(int m, int n)
 {
-    return pack2<true>(power2(-min(m, 126)), power2(-min(n, 126)));
+    return pack2<true>(power2(-min(m, 24)), power2(-min(n, 24)));
 }
 
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b)
@@ -258,21 +259,27 @@ __device__ __forceinline__ float half_rows(const Rows16<FROM>& r, uint32_t (&b)[
         }
         if constexpr (FROM == kFromFp16) return 1.0f;
         if constexpr (FROM == kFromZ) {
-            // each 8 columns to the largest power of two of the block's: exact but for what falls below 2^-38 of the
-            // block's largest value
+            // Each 8 columns to the largest power of two of the block's, which lies in 2^14 .. 2^15.  Below FP16's normal
+            // numbers, 2^-28 of it, bits are lost: 2^-39 of it at the most, and half as much in the first of two steps.
             const int e[4] = {(int)(r.e0 & 0xFF), (int)(r.e0 >> 8), (int)(r.e1 & 0xFF), (int)(r.e1 >> 8)};
             int top = max(max(e[0], e[1]), max(e[2], e[3]));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-                const uint32_t f = half_power2(top - e[i], top - e[i + 1]);
+            auto bring = [&](int i, uint32_t f) {   // the lane's vectors i and i + 1
                 const uint32_t lo = __byte_perm(f, 0, 0x1010), hi = __byte_perm(f, 0, 0x3232);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     b[4 * i + j] = mul_half2(b[4 * i + j], lo);
                     b[4 * i + 4 + j] = mul_half2(b[4 * i + 4 + j], hi);
                 }
+            };
+            const uint32_t f0 = half_power2(top - e[0], top - e[1]), f1 = half_power2(top - e[2], top - e[3]);
+            bring(0, f0);
+            bring(2, f1);
+            // At 2^-24, of all powers the one with the lowest bit, the way may go on: rare, and nothing is left past 2^-48.
+            if ((f0 | f1) & 0x00010001u) {
+                bring(0, half_power2(max(top - e[0] - 24, 0), max(top - e[1] - 24, 0)));
+                bring(2, half_power2(max(top - e[2] - 24, 0), max(top - e[3] - 24, 0)));
             }
             return power2(max(top, 18) - 142);
         }
