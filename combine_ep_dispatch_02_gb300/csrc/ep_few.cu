@@ -110,8 +110,9 @@ __device__ __forceinline__ int make_entries(const FewArgs& a, const Entries& s, 
 {
     const int words = row_words(a.rows);
     for (int p = threadIdx.x; p < a.pairs; p += blockDim.x) {
-        const int64_t e = (int64_t)load_shared_view(a.indices + p) - a.first;
-        s.local[p] = e >= 0 && e < a.experts ? (uint16_t)e : kNone;
+        const int32_t id = load_shared_view(a.indices + p);
+        const int64_t e = (int64_t)id - a.first;
+        s.local[p] = id >= 0 && e >= 0 && e < a.experts ? (uint16_t)e : kNone;   // first may be negative, an id here not
     }
     for (int i = threadIdx.x; i < a.experts * words; i += blockDim.x) s.named[i] = 0;
     __syncthreads();

@@ -215,8 +215,9 @@ def moe_few_rows(x: torch.Tensor, x_scales: Optional[torch.Tensor], indices: tor
     weight * down[e] @ (gate * sigmoid(gate) * up), [gate; up] = up[e] @ x[row], in FP32, rounded once.  x [rows][hidden]
     float8_e4m3fn with x_scales [rows][ceil(hidden/128)] FP32, or BF16 or FP16 with x_scales None; indices and weights
     [rows][k] int32 and FP32; up [experts][2 * inner][hidden] (gate rows, then up rows) and down [experts][hidden][inner]
-    float8_e4m3fn with scales as ``matmul_fp8`` takes them; hidden and inner multiples of 16.  Ids outside first_expert ..
-    first_expert + experts - 1 are left out; one that a row names several times counts once, with the sum of its weights.
+    float8_e4m3fn with scales as ``matmul_fp8`` takes them; hidden and inner multiples of 16.  Negative ids and those
+    outside first_expert .. first_expert + experts - 1 are left out; one that a row names several times counts once, with the
+    sum of its weights.
     rows * k up to 4096, rows * k * inner below 2^31.  The time is that of reading the named experts' weights; from some two
     rows to an expert on, sorted rows with ``matmul_fp8_swiglu`` and ``matmul_fp8`` are faster."""
     code = _OUT_CODES.get(out_dtype)

@@ -547,8 +547,9 @@ int ep_matmul_fp8_weight_gradient(const void* dy, int dtype, const void* a, cons
  * weight * down[e] (gate * sigmoid(gate) * up), [gate; up] = up[e] x.
  *   x            [rows][hidden], 16-byte aligned: e4m3 codes (x_dtype EP_FP8_E4M3) with x_scales [rows][ceil(hidden/128)], or
  *                EP_FP16 or EP_BF16 with x_scales NULL
- *   indices, weights  [rows][topk] int32 expert ids and FP32 weights.  Ids outside first_expert .. first_expert+experts-1, -1
- *                among them, are left out; an id that a row names several times counts once, with the sum of its weights
+ *   indices, weights  [rows][topk] int32 expert ids and FP32 weights.  Negative ids and those outside first_expert ..
+ *                first_expert+experts-1 are left out; an id that a row names several times counts once, with the sum of
+ *                its weights
  *   up, up_scales      [experts][2*inner][hidden] e4m3 codes, gate rows then up rows, and FP32 scales
  *                      [experts][ceil(2*inner/128)][ceil(hidden/128)]; 16-byte aligned
  *   down, down_scales  [experts][hidden][inner] codes, [experts][ceil(hidden/128)][ceil(inner/128)]

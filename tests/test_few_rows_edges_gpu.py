@@ -4,6 +4,7 @@ import torch
 
 import combine_ep_dispatch_02_gb300 as ep
 from test_experts_gpu import DEV, F8, HALF, U, _built, _gen, _half_bound, _no_status, _randn, _within  # noqa: F401
+from test_few_rows_gpu import _layer, _rows
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +37,18 @@ def test_columns_far_below_their_block_keep_their_values(rows, kind):
     want, bound = d @ z, d.abs() @ (err + (inner + 8) * 2 * U * z.abs())
     # half of either output type's smallest step near 0 is within _half_bound's 2^-25 (FP16) and far below these values (BF16)
     _within(out, want.expand(rows, -1), (_half_bound(out.dtype, want) + bound * 1.01).expand(rows, -1), "out")
+
+
+@pytest.mark.parametrize("first", [-1, -3, -4, -7, -(2 ** 31)])
+def test_negative_ids_are_left_out_whatever_the_first_expert(first):
+    """-1 marks a dropped slot also where first_expert is negative, as on a rank whose range starts before the experts do."""
+    g = _gen(20)
+    layer = _layer(g, 4, 256, 128)
+    x, xs = _rows(g, 20, 256, "fp8")
+    idx = torch.randint(-5, 6, (20, 6), generator=g, device=DEV, dtype=torch.int32)
+    idx[0] = -1
+    idx[1, :] = torch.tensor([-1, 0, -2, -(2 ** 31), 1, -1], device=DEV)
+    w = torch.softmax(_randn(g, 20, 6), 1)
+    out = ep.moe_few_rows(x, xs, idx, w, *layer, first_expert=first)
+    assert torch.equal(out, ep.moe_few_rows(x, xs, torch.where(idx < 0, 1000, idx), w, *layer, first_expert=first))
+    assert not out[0].any()
