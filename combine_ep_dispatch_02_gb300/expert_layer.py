@@ -64,13 +64,14 @@ class ExpertLayer:
         the next layer adds)."""
         q, scales, h, y = ep.rms_norm_fp8(x, self.norm_weight, residual=residual, want_y=True)
         experts, weights = route(y)
-        rows, k = experts.shape
+        (rows, k), held = experts.shape, self.up[0].shape[0]
         # One call against the sorted calls, in us: 1, 4, 8, 16 and 32 rows with 8 of 32 experts of 7168 x 2048 63 and 69, 152
         # and 155, 216 and 214, 251 and 222, 328 and 230; 8 and 32 rows with 2 of 8 65 and 66, 91 and 70; 1, 8 and 32 rows with
-        # 4 of 32 of 2048 x 1024 13 and 19, 35 and 38, 55 and 47.  So the one call up to two rows to an expert on average.
-        if rows <= 128 and rows * k <= 2 * self.up[0].shape[0]:
+        # 4 of 32 of 2048 x 1024 13 and 19, 35 and 38, 55 and 47.  So the one call up to two rows to an expert on average,
+        # where it takes as many rows and experts.
+        if rows <= 128 and held <= 1024 and rows * k <= 2 * held:
             return ep.moe_few_rows(q, scales, experts, weights, *self.up, *self.down), h
-        order = ep.sort_by_expert(experts, self.up[0].shape[0])
+        order = ep.sort_by_expert(experts, held)
         row, row_scales = ep.sorted_rows(order, q, scales)
         z, z_scales = ep.matmul_fp8_swiglu(row, row_scales, *self.up, offsets=order.offsets)
         return ep.return_rows(order, ep.matmul_fp8(z, z_scales, *self.down, offsets=order.offsets), weights), h

@@ -52,3 +52,11 @@ def test_negative_ids_are_left_out_whatever_the_first_expert(first):
     out = ep.moe_few_rows(x, xs, idx, w, *layer, first_expert=first)
     assert torch.equal(out, ep.moe_few_rows(x, xs, torch.where(idx < 0, 1000, idx), w, *layer, first_expert=first))
     assert not out[0].any()
+
+
+def test_example_layer_decodes_with_more_experts_than_the_one_call_takes():
+    """1040 experts: within what the sorted calls take, above moe_few_rows's 1024.  The bound is that of the example layer's
+    other tests."""
+    from combine_ep_dispatch_02_gb300 import expert_layer
+    assert expert_layer.main(["--ranks", "4", "--experts-per-rank", "260", "--topk", "4", "--tokens-per-rank", "8", "--hidden", "128",
+                              "--inner", "32", "--passes", "1", "--decode-rows", "5"]) <= 2.0 ** -3
