@@ -1,8 +1,8 @@
 // ep_tcgen05.cuh -- the asynchronous machinery the product kernels use, as inline PTX: mbarriers with
 // bounded waits, tiled TMA loads, and the fifth-generation tensor cores with their tensor memory.
 //
-// Bounded waits.  Every wait gives up after kWaitCycles clock cycles (or as soon as another thread of
-// the CTA gave up), records EP_ERR_DEVICE_TIMEOUT and returns false.  The warps that load and those that
+// Bounded waits.  Every wait gives up after kWaitCycles clock cycles, or the longer limit that a wait for a whole tile is
+// given (or as soon as another thread of the CTA gave up), records EP_ERR_DEVICE_TIMEOUT and returns false.  The warps that load and those that
 // make factors then leave; the multiplying and the scaling warps go through all their blocks, on whatever
 // is there, because named barriers, whose waits have no limit, need every warp's arrivals in step.  What
 // is in flight is waited for (bounded again), tensor memory is freed, and the kernel returns.
@@ -14,7 +14,8 @@
 
 namespace ep {
 
-// a second and a half at 2 GHz; the longest legitimate wait is a tile's, under a millisecond
+// a second and a half at 2 GHz; the longest legitimate wait of this limit is that of a product's tile, whose K of 2^20
+// at the most is 8192 blocks of some 1000 cycles, 4 ms
 #ifndef EP_WAIT_CYCLES
 #define EP_WAIT_CYCLES (3ll << 30)
 #endif
@@ -98,13 +99,13 @@ struct Giveup {
 };
 
 // Wait until the barrier's phase of this parity has completed; false if the wait gave up.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Giveup& g)
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Giveup& g, long long limit = kWaitCycles)
 {
     if (bar_test(bar, parity)) return true;
     const long long t0 = clock64();
     while (!bar_try(bar, parity)) {
         if (*g.flag) return false;
-        if (clock64() - t0 > kWaitCycles) {
+        if (clock64() - t0 > limit) {
             *g.flag = 1;
             record_status(g.status, EP_ERR_DEVICE_TIMEOUT);
             return false;

@@ -41,6 +41,8 @@ constexpr int kConvertTeam = 2;
 constexpr int kGradThreads = 32 * (kFirstConverter + kGradStages * kConvertTeam);   // load, multiply, write, convert
 constexpr int kMaxGradGroups = 4096;
 constexpr int kOutBytes = 2048;   // of a writing warp
+// A tile's sums come after all of its stages, up to 2^25 of some 850 cycles: the wait for them is given this much for each.
+constexpr long long kStageCycles = 1 << 13;
 constexpr size_t kGradShared = 1024 + kGradStages * (kGradStageBytes + kGradRows * 4) + kWriteWarps * kOutBytes;
 
 struct GradArgs {
@@ -240,8 +242,6 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
             }
             if (leader) mma_commit_pair(drained);
         }
-        // tensor memory is freed, and the second CTA's barriers go, only after the last product has told both
-        if (elect_one()) bar_drain(drained, 0, clock64());
         __syncwarp();
     } else if (warp < kFirstConverter) {
         uint32_t tile = 0;
@@ -254,7 +254,8 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
             const bool some = x.r1 > x.r0;
             const uint32_t u = tile & 1;
             if (some) {
-                ok = __all_sync(0xffffffffu, bar_wait(summed + 8 * u, (tile / 2) & 1, giveup));
+                const long long limit = kWaitCycles + kStageCycles * grad_steps(x);
+                ok = __all_sync(0xffffffffu, bar_wait(summed + 8 * u, (tile / 2) & 1, giveup, limit));
                 if (!ok) break;
                 tmem_fence_after();
             }
@@ -347,6 +348,9 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
     }
     tmem_fence_before();
     __syncthreads();
+    // Tensor memory is freed, and the second CTA's barriers go, only after the last product has told both.  Here and not before,
+    // so that the limit counts from the end of this CTA's other roles, however long the kernel's work takes.
+    if (warp == 1 && elect_one()) bar_drain(drained, 0, clock64());
     cluster_sync();   // no product, arrival or read of the pair's memory is under way
     if (warp == 1) {
         tmem_fence_after();

@@ -1,0 +1,35 @@
+"""Calls of the training operators that the other files leave out (bounds: see test_training_gpu.py)."""
+import os
+
+import pytest
+import torch
+
+import combine_ep_dispatch_02_gb300 as ep
+from combine_ep_dispatch_02_gb300 import build
+from test_experts_gpu import DEV, F8, _built, _no_status  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------------------- weights
+
+def test_weight_gradient_of_a_tile_that_takes_longer_than_one_wait(tmp_path, monkeypatch):
+    """A tile's sums come after all of its stages.  A test build lets a wait last 4 million cycles; a million rows take some
+    14 million, of which every single wait but the sums' is a few thousand: the call is right and reports nothing.  Whole
+    numbers, so that the sum is exact."""
+    d = str(tmp_path)
+    lib = ep.load_library(build.build(force=True, defines=["EP_WAIT_CYCLES=4000000"], lib_path=os.path.join(d, "libep.so"),
+                                      build_dir=d))
+    rows, columns, inner = 1 << 20, 8, 16
+    dy = torch.ones(rows, columns, dtype=torch.bfloat16, device=DEV)
+    a = torch.full((rows, inner), 0x38, dtype=torch.uint8, device=DEV).view(F8)      # 1.0
+    s = torch.full((rows, 1), 0.5, device=DEV)
+    offsets = torch.tensor([0, 5, rows - 7, rows], dtype=torch.int32, device=DEV)
+    with monkeypatch.context() as m:
+        m.setattr(ep, "_lib", lib)
+        for _ in range(3):
+            whole = ep.matmul_fp8_weight_gradient(dy, a, s, out_dtype="fp32")
+            parts = ep.matmul_fp8_weight_gradient(dy, a, s, offsets=offsets, out_dtype="fp32")
+        assert ep.op_status(DEV) == 0
+    assert (whole == rows / 2).all()
+    assert torch.equal(parts[:, 0, 0].cpu(), torch.tensor([2.5, rows / 2 - 6, 3.5])) and (parts == parts[:, :1, :1]).all()
