@@ -600,11 +600,10 @@ __global__ void __launch_bounds__(kJoinMaxThreads) ep_join_wide_kernel(const Joi
         if (!a.q) continue;
 #pragma unroll
         for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float scale = e4m3_block_scale(m);
-        const float inv = __frcp_rn(scale);
+        const float scale = quick_block_scale(m), inv = quick_reciprocal(scale);   // as above: one rule at every width
         if (in) {
-            const uint2 q = make_uint2(e4m3x4_scaled(f[i][0], f[i][1], f[i][2], f[i][3], scale, inv),
-                                       e4m3x4_scaled(f[i][4], f[i][5], f[i][6], f[i][7], scale, inv));
+            const uint2 q = make_uint2(e4m3x4_near(f[i][0], f[i][1], f[i][2], f[i][3], scale, inv),
+                                       e4m3x4_near(f[i][4], f[i][5], f[i][6], f[i][7], scale, inv));
             *reinterpret_cast<uint2*>(a.q + (row * a.vecs + v) * 8) = q;
             if ((v & 15) == 0) a.scales[row * a.blocks + (v >> 4)] = scale;
         }

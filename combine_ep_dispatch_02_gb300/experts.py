@@ -257,7 +257,8 @@ def rms_norm_join(y: torch.Tensor, residual: torch.Tensor, post_weight: Optional
     eps) * pre_weight, only with pre_weight, from the unrounded h.  y and residual [rows][hidden] BF16 or FP16, hidden a
     multiple of 16 up to 32768, rows any multiple of 8 elements apart; weights [hidden] of y's type or FP32; gate
     [hidden] (of y's type or FP32), [rows][1] (FP32) or [rows][hidden] (of y's type).  fp8: n as e4m3 codes and block
-    scales, as ``rms_norm_fp8`` writes them.  want_n: n in 16 bits (by default where the codes are not wanted)."""
+    scales, as ``rms_norm_fp8`` writes them but by the scale's reciprocal: a value within three FP32 units of the middle of two
+    codes may take the other.  want_n: n in 16 bits (by default where the codes are not wanted)."""
     if want_n is None:
         want_n = pre_weight is not None and not fp8
     return Joined(*_on(stream, _native().rms_norm_join, y, residual, post_weight, gate, pre_weight, residual_scale, eps,

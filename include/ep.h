@@ -476,8 +476,10 @@ typedef struct ep_join {
 /*
  *   residual     [rows][hidden] of dtype, rows residual_stride elements apart
  *   h, n         [rows][hidden] of dtype, dense; n may be NULL
- *   q, scales    n as e4m3 codes [rows][hidden] and FP32 scales [rows][ceil(hidden/128)], quantised as by
- *                ep_rms_norm_fp8: the input of an EP_FP8_E4M3 dispatch or of ep_matmul_fp8; both may be NULL
+ *   q, scales    n as e4m3 codes [rows][hidden] and FP32 scales [rows][ceil(hidden/128)]: the input of an EP_FP8_E4M3
+ *                dispatch or of ep_matmul_fp8; both may be NULL.  The scales are ep_rms_norm_fp8's; the codes round the
+ *                product with the scale's reciprocal, which is within three units in the last place of FP32 of the
+ *                quotient that ep_rms_norm_fp8 rounds, so a value that close to the middle of two codes may take the other
  *   post_rstd, pre_rstd  [rows] FP32: rs(y) and rs(h), for the gradient; each is written if its weight is given
  * h may be y or residual itself, if that is dense.
  */
@@ -512,7 +514,7 @@ int ep_rms_norm_join_backward(const ep_join* join, const void* h, const float* p
  *                offsets)
  *   q, scales    z = gate * sigmoid(gate) * up in FP32 as e4m3 codes [rows][inner], [rows][ceil(inner/128)]
  *   saved, saved_scales  gate_up as codes [rows][2*inner], [rows][ceil(2*inner/128)]
- * Both are quantised as by ep_rms_norm_fp8, by the scale's reciprocal.  A sigmoid below FP32's smallest normal number,
+ * Both are quantised as by ep_rms_norm_join, by the scale's reciprocal.  A sigmoid below FP32's smallest normal number,
  * 2^-126, counts as 0.
  *
  * ep_swiglu_saved_backward takes the gradient at the saved values and lets it pass the quantiser of z unchanged:

@@ -6,9 +6,28 @@ import torch
 
 import combine_ep_dispatch_02_gb300 as ep
 from combine_ep_dispatch_02_gb300 import build
-from test_experts_gpu import DEV, F8, _built, _no_status  # noqa: F401
+from test_experts_gpu import DEV, F8, _built, _gen, _no_status, _randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------------------- join
+
+def test_join_codes_follow_one_rule_at_every_width():
+    """A row and the same row twice over have the same mean square: here exactly, because y is a small whole number of 1/8
+    and widths are powers of two, so that every sum is exact.  So the codes of both are bit for bit those of the row, though
+    another kernel makes them."""
+    g, rows, hidden = _gen(30), 1024, 8192
+    y = (torch.randint(-16, 17, (rows, hidden), generator=g, device=DEV) / 8).to(torch.bfloat16)
+    w = _randn(g, hidden)
+    zero = torch.zeros_like(y)
+    one = ep.rms_norm_join(y, zero, pre_weight=w, fp8=True, want_n=True)
+    two = ep.rms_norm_join(torch.cat([y, y], 1), torch.cat([zero, zero], 1), pre_weight=torch.cat([w, w]), fp8=True, want_n=True)
+    assert torch.equal(two.pre_rstd, one.pre_rstd)
+    for half in (0, 1):
+        assert torch.equal(two.n[:, half * hidden:(half + 1) * hidden], one.n)
+        assert torch.equal(two.scales[:, half * hidden // 128:(half + 1) * hidden // 128], one.scales)
+        assert torch.equal(two.q.view(torch.uint8)[:, half * hidden:(half + 1) * hidden], one.q.view(torch.uint8))
 
 
 # ------------------------------------------------------------------------------------------- weights
