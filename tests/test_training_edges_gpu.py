@@ -6,12 +6,22 @@ import torch
 
 import combine_ep_dispatch_02_gb300 as ep
 from combine_ep_dispatch_02_gb300 import build
-from test_experts_gpu import DEV, F8, _built, _gen, _no_status, _randn  # noqa: F401
+from test_experts_gpu import DEV, F8, HALF, _built, _gen, _no_status, _randn  # noqa: F401
+from test_training_gpu import FORMS, _check_join, _inputs
 
 pytestmark = pytest.mark.gpu
 
 
 # ------------------------------------------------------------------------------------------- join
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("gate,post,pre", [f for f in FORMS if f[2]])
+@pytest.mark.parametrize("rows,hidden", [(1, 16), (7, 144), (300, 272), (33, 1040), (4, 2064), (5, 528), (9, 7184), (3, 4112), (2, 8176),
+                                         (2, 8208), (2, 16400), (1, 32752)])
+def test_join_codes_with_a_short_last_block(rows, hidden, gate, post, pre, dtype):
+    """Widths whose last 128-block has 16 to 112 columns, in a thread's first vector and in its last."""
+    _check_join(_inputs(rows, hidden, HALF[dtype], gate, post, pre, rows * 1019 + hidden), 0.75, 1e-6, fp8=True)
+
 
 def test_join_codes_follow_one_rule_at_every_width():
     """A row and the same row twice over have the same mean square: here exactly, because y is a small whole number of 1/8
