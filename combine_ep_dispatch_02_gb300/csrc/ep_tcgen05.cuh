@@ -98,19 +98,41 @@ struct Giveup {
     int* status;
 };
 
+// Whose arrivals a barrier takes, and so what a wait for its phase orders: this CTA's threads and asynchronous units; or both
+// CTAs' of a pair (pair_arrive below), which leaves tensor memory to the caller's tmem_fence_after(), or orders what both wrote
+// to their shared memory too.
+enum Arrivals { kOwnArrivals, kPairTensor, kPairShared };
+
+template <Arrivals FROM>
+__device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity, bool wait)
+{
+    if constexpr (FROM == kOwnArrivals) return wait ? bar_try(bar, parity) : bar_test(bar, parity);
+    uint32_t ok;
+    if (wait)
+        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+                     : "=r"(ok) : "r"(bar), "r"(parity), "r"(kSuspendNs) : "memory");
+    else
+        asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                     : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+
 // Wait until the barrier's phase of this parity has completed; false if the wait gave up.
+template <Arrivals FROM = kOwnArrivals>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Giveup& g, long long limit = kWaitCycles)
 {
-    if (bar_test(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!bar_try(bar, parity)) {
-        if (*g.flag) return false;
-        if (clock64() - t0 > limit) {
-            *g.flag = 1;
-            record_status(g.status, EP_ERR_DEVICE_TIMEOUT);
-            return false;
+    if (!bar_done<FROM>(bar, parity, false)) {
+        const long long t0 = clock64();
+        while (!bar_done<FROM>(bar, parity, true)) {
+            if (*g.flag) return false;
+            if (clock64() - t0 > limit) {
+                *g.flag = 1;
+                record_status(g.status, EP_ERR_DEVICE_TIMEOUT);
+                return false;
+            }
         }
     }
+    if constexpr (FROM == kPairShared) asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
     return true;
 }
 
@@ -350,12 +372,17 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar)
                  :: "r"(bar), "h"((uint16_t)3) : "memory");
 }
 
-// Arrive on a barrier of the pair's first CTA.  Ordered within this CTA alone, a thousand cycles cheaper than for the
-// cluster: what it announces is this CTA's shared or tensor memory, written before fence_async() or read before
-// tmem_fence_before(), which the tensor cores use where it lies.
+// The second CTA's arrival on a barrier of the pair's first, whose waits are of the same kind.  kPairTensor: the thread's use of
+// tensor memory before tmem_fence_before() is over.  kPairShared: this CTA's shared memory, written before fence_async(), may be
+// multiplied.  The fence is held to shared memory: one of everything, an arrival with release semantics for the cluster, takes a
+// thousand cycles longer (8192 rows in 8 groups of 4096 x 7168 377 us; 319 so; 314 ordered within the CTA alone, which the
+// memory model does not carry to the other CTA's thread that issues the products).
+template <Arrivals TO>
 __device__ __forceinline__ void pair_arrive(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+    static_assert(TO != kOwnArrivals, "bar_arrive");
+    if constexpr (TO == kPairShared) asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
 }
 
 // This thread's writes to shared memory become visible to the asynchronous units.

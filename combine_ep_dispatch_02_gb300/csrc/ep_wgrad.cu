@@ -221,10 +221,10 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
                 const int steps = uniform(grad_steps(x));
                 if (steps == 0) continue;
                 const uint32_t u = tile & 1, d = tmem + u * kGradTile;
-                if (tile >= 2) ok = __all_sync(0xffffffffu, bar_wait(written + 8 * u, (tile / 2 - 1) & 1, giveup));
+                if (tile >= 2) ok = __all_sync(0xffffffffu, bar_wait<kPairTensor>(written + 8 * u, (tile / 2 - 1) & 1, giveup));
                 for (int i = 0; i < steps && ok; ++i, ++n) {
                     const uint32_t slot = n % kGradStages;
-                    ok = __all_sync(0xffffffffu, bar_wait(ready + 8 * slot, (n / kGradStages) & 1, giveup));
+                    ok = __all_sync(0xffffffffu, bar_wait<kPairShared>(ready + 8 * slot, (n / kGradStages) & 1, giveup));
                     if (!ok) break;
                     if (leader) {
                         tmem_fence_after();
@@ -275,7 +275,10 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
             if (some) {
                 tmem_fence_before();
                 __syncwarp();
-                if (lane == 0) pair_arrive(peer_smem(written + 8 * u, 0));
+                if (lane == 0) {
+                    if (rank == 0) bar_arrive(written + 8 * u);
+                    else pair_arrive<kPairTensor>(peer_smem(written + 8 * u, 0));
+                }
                 ++tile;
             }
         }
@@ -285,7 +288,7 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
         const int team = (warp - kFirstConverter) / kConvertTeam, thread = (int)(threadIdx.x - 32 * kFirstConverter) % (32 * kConvertTeam);
         const int row = thread / 8, piece = lane & 7;   // 16 codes of every (4 * kConvertTeam)th row from `row` on
         const uint32_t to0 = (uint32_t)(kDyBytes + piece / 4 * kLineBytes), other = piece / 4;
-        const uint32_t arrive = peer_smem(ready, 0);
+        const uint32_t first_ready = peer_smem(ready, 0);
         uint32_t n = 0;
         bool ok = true;
         for (int64_t t = t_first; t < p.tiles && ok; t += t_step) {
@@ -342,7 +345,10 @@ ep_weight_gradient_kernel(const GradArgs p, const __grid_constant__ CUtensorMap 
                     fence_async();
                 }
                 __syncwarp();
-                if (lane == 0) pair_arrive(arrive + 8 * slot);
+                if (lane == 0) {
+                    if (rank == 0) bar_arrive(ready + 8 * slot);
+                    else pair_arrive<kPairShared>(first_ready + 8 * slot);
+                }
             }
         }
     }
