@@ -1,4 +1,5 @@
 """Calls of the training operators that the other files leave out (bounds: see test_training_gpu.py)."""
+import copy
 import os
 
 import pytest
@@ -62,3 +63,50 @@ def test_weight_gradient_of_a_tile_that_takes_longer_than_one_wait(tmp_path, mon
         assert ep.op_status(DEV) == 0
     assert (whole == rows / 2).all()
     assert torch.equal(parts[:, 0, 0].cpu(), torch.tensor([2.5, rows / 2 - 6, 3.5])) and (parts == parts[:, :1, :1]).all()
+
+
+# ------------------------------------------------------------------------------------------- together
+
+@pytest.mark.parametrize("rows,E,k,H,inner", [(97, 8, 2, 512, 256), (33, 5, 3, 272, 144), (200, 4, 1, 1024, 512)])
+def test_a_training_step_against_the_block_and_blocks_that_differ(rows, E, k, H, inner):
+    """Gradients by their norms, closely enough that a forgotten factor or term shows.  A code is off by up to 2^-4, evenly
+    spread over its step of 2^-3 of the power of two below the value v: 2^-4 / sqrt(3) of that power, so, with v's place
+    between two powers evenly spread over its logarithm, (3 / 8 / ln 2)^(1/2) of 2^-4 / sqrt(3) of v, 2.7 %, in the root
+    mean square, which is what a norm of many values shows.  The rows pass five such roundings, forward and back, whose
+    errors have nothing to do with each other: the root of 5 of them, 6 %, and twice that where SwiGLU's slope or the norms
+    raise it.  16-bit roundings are 2^-8 each.  So 2^-3.
+
+    With one expert to a row the block does not depend on the row's routing weight, but for eps: y = w * out, and the norm
+    after the experts drops y's scale.  So dy is at right angles to y, and that weight's gradient, dy * out, is 0 up to eps:
+    its error is held against the two vectors' norms, not against itself."""
+    from combine_ep_dispatch_02_gb300.expert_training import ExpertBlock, reference
+    g = _gen(rows + H)
+    block = ExpertBlock(_randn(g, E, 2 * inner, H) * H ** -0.5, _randn(g, E, H, inner) * inner ** -0.5,
+                        *(1 + 0.3 * _randn(g, H) for _ in range(4)), 0.75)
+    x, dn = _randn(g, rows, H).to(torch.bfloat16), _randn(g, rows, H).to(torch.bfloat16)
+    idx = torch.rand(rows, E, generator=g, device=DEV).topk(k, 1).indices.int()
+    w = 0.25 + torch.rand(rows, k, generator=g, device=DEV)
+    n, kept = block.forward(x, idx, w)
+    got = {"n": n, **block.backward(kept, dn)}
+
+    y, joined = kept[10], kept[11]
+    dy = ep.rms_norm_join_backward(joined, y, dn=dn, post_weight=block.post, gate=block.gate, pre_weight=block.pre,
+                                   residual_scale=0.75).dy
+    sizes = {"weights": (dy.double().norm(dim=1) * y.double().norm(dim=1) / w[:, 0].double()).norm()} if k == 1 else {}
+
+    def off(weights=w, **change):
+        other = copy.copy(block)
+        for name, v in change.items():
+            setattr(other, name, v)
+        want_n, want = reference(other, x, idx.long(), weights, dn)
+        want["n"] = want_n
+        return {name: ((got[name].double() - want[name]).norm() / sizes.get(name, want[name].norm())).item() for name in got}
+    for name, v in off().items():
+        assert v <= 2.0 ** -3, (name, v)
+    # the same measure tells the block from one with another factor
+    one = torch.ones_like(block.gate)
+    for change in [dict(residual_scale=1.0), dict(gate=one), dict(post=one), dict(pre=one), dict(norm=one),
+                   dict(up=(block.up[0], 0.75 * block.up[1])),
+                   dict(down=(block.down[0].view(torch.uint8).roll(1, 0).view(F8), block.down[1].roll(1, 0)))] + \
+                  [dict(weights=torch.ones_like(w))] * (k > 1):
+        assert max(off(**change).values()) > 2.0 ** -3, list(change)
