@@ -110,3 +110,36 @@ def test_a_training_step_against_the_block_and_blocks_that_differ(rows, E, k, H,
                    dict(down=(block.down[0].view(torch.uint8).roll(1, 0).view(F8), block.down[1].roll(1, 0)))] + \
                   [dict(weights=torch.ones_like(w))] * (k > 1):
         assert max(off(**change).values()) > 2.0 ** -3, list(change)
+
+
+def test_calls_on_two_streams_at_once():
+    """Products, norms and gradients of two streams share the SMs; each result is that of the call alone."""
+    g, rows, H, inner = _gen(40), 777, 1040, 528
+    x, r = _randn(g, rows, 2 * inner).to(torch.bfloat16), _randn(g, rows, H).to(torch.bfloat16)
+    w = (1 + 0.1 * _randn(g, H)).to(torch.bfloat16)
+    offsets = torch.tensor([0, 300, 300, 777], dtype=torch.int32, device=DEV)
+    q, s, saved, saved_s = ep.swiglu_saved(x, offsets=offsets)
+    joined = ep.rms_norm_join(r, r, post_weight=w, gate=w, pre_weight=w, fp8=True, want_n=True)
+
+    def fields(o):
+        return tuple(v for v in (getattr(o, f) for f in o.__dataclass_fields__) if v is not None)
+    calls = [lambda: ep.swiglu_saved(x, offsets=offsets),
+             lambda: ep.swiglu_saved_backward(saved, saved_s, q.to(torch.bfloat16), offsets=offsets, fp8=True),
+             lambda: (ep.matmul_fp8_weight_gradient(r, q, s, offsets=offsets),),
+             lambda: fields(ep.rms_norm_join(r, r, post_weight=w, gate=w, pre_weight=w, fp8=True, want_n=True)),
+             lambda: fields(ep.rms_norm_join_backward(joined, r, dh=r, dn=r, post_weight=w, gate=w, pre_weight=w))]
+    want = [c() for c in calls]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for i in range(40):
+        outs = []
+        for k in range(len(calls)):
+            for n, st in enumerate(streams):
+                j = (k + i * n) % len(calls)
+                with torch.cuda.stream(st):
+                    outs.append((j, calls[j]()))
+        torch.cuda.synchronize()
+        for j, out in outs:
+            for a, b in zip(out, want[j]):
+                assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8)), j
+        del outs
