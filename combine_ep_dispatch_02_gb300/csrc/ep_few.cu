@@ -8,10 +8,11 @@
 // through a ring of its own in shared memory that only its own lanes' copies fill and read, a few steps ahead: it meets
 // no barrier on the way, and so few rows spread any layer over the SMs.
 //
-// Measured, with 8 experts of 32 of 7168 x 2048: one row 62 us (352 MB, 5.7 TB/s), with 20 of 32 for 4 rows 152 us (5.8
-// TB/s).  Each further expert takes 7.1 us, 0.92 of a copy's bandwidth; some 11 us are the two kernels' sorts, first trips
-// to memory and last steps.  From two rows to an expert on the matrix instructions of 16 x 8 (and what makes their second
-// operand) bound it: 16 rows of 8 experts of 32 take 251 us, 64 rows 462.
+// Measured, with 8 experts of 32 of 7168 x 2048: one row 64 us (352 MB, 5.5 TB/s; 52 by bytes), with 20 of 32 for 4 rows
+// 154 us (5.7 TB/s).  Each further expert takes 7.3 us, 0.90 of a copy's bandwidth; some 6 us are the two kernels' sorts, first
+// trips to memory and last steps.  From two rows to an expert on the matrix instructions of 16 x 8 (and what makes their
+// second operand) bound it: 16 rows of 8 experts of 32 take 252 us, 64 rows 469.  One BF16 row, whose values take a
+// multiplication and a conversion each, 2 us more than one of e4m3 or FP16; 64 of them, on 32 of 256 experts, 231 us for 222.
 //
 // A lane's 16 bytes are 16 columns of one row.  Which of the K columns share a matrix instruction is free, as long as
 // both operands agree; so a lane takes its own 16 for four instructions and reads the same 16 of the other operand's

@@ -13,11 +13,15 @@
 // stage make 16-bit values of the codes, in the order that the tensor cores read; warp 1 of the first CTA multiplies for
 // both; eight warps hand the sums to TMA stores.
 //
-// Measured: 8192 rows in 8 groups of 4096 x 7168 314 us (1530 TFLOP/s), 2048 in 16 groups 171 us (5.5 TB/s of dw), 32768 in
-// 32 groups 1365 us (1410 TFLOP/s, where the card holds 1.75 GHz at its power limit; a plain BF16 product reaches 1890 in a
-// burst and 1700 at the limit).  A stage takes 850 cycles, of which its products need 512 and shared memory 640: 24 KB
-// come in, the codes are read, the values written, and the tensor cores read 32 KB.  The rest is the conversion, a stage's
-// chain of 128 codes a lane: with it left out, and the sums' way out as it was before, 340 us became 259.
+// Measured: 8192 rows in 8 groups of 4096 x 7168 317 us in a burst (1520 TFLOP/s), 2048 in 16 groups 171 us (5.5 TB/s of
+// dw), 32768 in 32 groups 1240 us in a burst and 1397 to 1433 at the power limit (1340 to 1380 TFLOP/s at 1.75 GHz; a plain
+// BF16 product reaches 1890 in a burst and 1700 at the limit); with FP32 sums out 347, 318 and 1365 to 1531.  A stage takes 850
+// cycles, of which its products need 512 and shared memory 640: 24 KB come in, the codes are read, the values written, and the
+// tensor cores read 32 KB.  The rest is the conversion, a stage's chain of 128 codes a lane: with it left out, and the sums' way
+// out as it was before, 340 us became 259.
+//
+// A pair sums all rows of its tile, so fewer tiles than half the SMs leave SMs idle: 16384 rows into 1024 x 1024, 512 x 512 and
+// 136 x 256 take 86, 85 and 83 us, 256 stages one after another, where bytes and operations take 18, 5 and 1.
 #include "ep_tcgen05.cuh"
 
 namespace ep {
@@ -30,12 +34,13 @@ constexpr int kLineBytes = 8192;                   // 64 columns x 64 rows of 16
 constexpr int kDyBytes = 2 * kLineBytes, kValueBytes = 2 * kLineBytes, kCodeBytes = kGradRows * kGradHalf;
 constexpr int kGradStageBytes = kDyBytes + kValueBytes + kCodeBytes;
 constexpr int kGradStages = 5;
-// Two to a quarter of the lanes, 128 columns each.  8 and 4 warps: 8192 rows in 8 groups of 4096 x 7168 314 and 320 us, 2048
+// Two to a quarter of the lanes, 128 columns each.  8 and 4 warps, before the fence of the pair's arrivals (pair_arrive) added
+// 1 to 2 %: 8192 rows in 8 groups of 4096 x 7168 314 and 320 us, 2048
 // in 16 groups 171 and 226.
 constexpr int kWriteWarps = 8;
 constexpr int kFirstWriter = 2, kFirstConverter = kFirstWriter + kWriteWarps;
 // Warps that convert a stage.  Each stage has a team of its own: a barrier's parity tells one phase from the next alone, so
-// whoever waits for a stage's phase has to have seen the one before.  Teams of 2 and 4 warps: the same rows
+// whoever waits for a stage's phase has to have seen the one before.  Teams of 2 and 4 warps, measured as above: the same rows
 // 314 and 341 us, 171 and 182 (with 62 registers a thread instead of 93); of 1 against 2, when both were slower, 401 and 352.
 constexpr int kConvertTeam = 2;
 constexpr int kGradThreads = 32 * (kFirstConverter + kGradStages * kConvertTeam);   // load, multiply, write, convert

@@ -9,8 +9,8 @@ logical ranks' hidden rows and their routing and runs
                  -> weighted return -> combine
 
 with the residual kept beside it.  ``decode`` is the same layer for a few rows of one set: norm, then the whole of the
-experts in one call, or in the calls above where experts have several rows each.  Nothing in it waits for the GPU.  The command builds one layer with
-random weights, compares it with the same layer in FP32 and prints the median time of a pass.
+experts in one call, or in the calls above where experts have several rows each.  Nothing in it waits for the GPU.  The
+command builds one layer with random weights, compares it with the same layer in FP32 and prints the median time of a pass.
 """
 from __future__ import annotations
 
@@ -65,9 +65,9 @@ class ExpertLayer:
         q, scales, h, y = ep.rms_norm_fp8(x, self.norm_weight, residual=residual, want_y=True)
         experts, weights = route(y)
         (rows, k), held = experts.shape, self.up[0].shape[0]
-        # One call against the sorted calls, in us: 1, 4, 8, 16 and 32 rows with 8 of 32 experts of 7168 x 2048 63 and 69, 152
-        # and 155, 216 and 214, 251 and 222, 328 and 230; 8 and 32 rows with 2 of 8 65 and 66, 91 and 70; 1, 8 and 32 rows with
-        # 4 of 32 of 2048 x 1024 13 and 19, 35 and 38, 55 and 47.  So the one call up to two rows to an expert on average,
+        # One call against the sorted calls, in us: 1, 4, 8, 16 and 32 rows with 8 of 32 experts of 7168 x 2048 64 and 68, 154
+        # and 155, 220 and 213, 252 and 222, 331 and 229; 8 and 32 rows with 2 of 8 66 and 67, 92 and 70; 1, 8 and 32 rows with
+        # 4 of 32 of 2048 x 1024 14 and 19, 36 and 39, 56 and 48.  So the one call up to two rows to an expert on average,
         # where it takes as many rows and experts.
         if rows <= 128 and held <= 1024 and rows * k <= 2 * held:
             return ep.moe_few_rows(q, scales, experts, weights, *self.up, *self.down), h

@@ -218,7 +218,8 @@ def moe_few_rows(x: torch.Tensor, x_scales: Optional[torch.Tensor], indices: tor
     float8_e4m3fn with scales as ``matmul_fp8`` takes them; hidden and inner multiples of 16.  Negative ids and those
     outside first_expert .. first_expert + experts - 1 are left out; one that a row names several times counts once, with the
     sum of its weights.
-    rows * k up to 4096, rows * k * inner below 2^31.  The time is that of reading the named experts' weights; from some two
+    rows * k up to 4096, rows * k * inner below 2^31.  BF16 rows are brought to FP16 by blocks of 128 columns, exactly but for
+    what is 2^-28 of a block's largest value or less.  The time is that of reading the named experts' weights; from some two
     rows to an expert on, sorted rows with ``matmul_fp8_swiglu`` and ``matmul_fp8`` are faster."""
     code = _OUT_CODES.get(out_dtype)
     if code is None:
@@ -270,8 +271,9 @@ def rms_norm_join_backward(joined: Joined, y: torch.Tensor, dh: Optional[torch.T
                            gate: Optional[torch.Tensor] = None, pre_weight: Optional[torch.Tensor] = None,
                            residual_scale: float = 1.0, stream=None) -> JoinGradients:
     """Gradients of rms_norm_join from those for h and n ([rows][hidden] of y's type; dh None for zeros, dn given if
-    pre_weight is), for the 16-bit h that it returned.  Other arguments as there, hidden up to 8192.  Sums over rows are
-    in FP32, in an order that the shape fixes."""
+    pre_weight is), for the 16-bit h that it returned.  Other arguments as there, hidden up to 8192 (a row's
+    CTA holds the sums over rows in registers, 16 columns a thread).  Sums over rows are in FP32, in an order that the shape
+    fixes."""
     return JoinGradients(*_on(stream, _native().rms_norm_join_backward, y, joined.h, joined.post_rstd, joined.pre_rstd, dh,
                               dn, post_weight, gate, pre_weight, residual_scale))
 

@@ -467,7 +467,8 @@ typedef struct ep_join {
     int64_t gate_stride;
     const void* pre_weight;    /* [hidden] of dtype, or FP32 if pre_fp32 is not 0; 16-byte aligned; may be NULL */
     int64_t rows;
-    int hidden;                /* a multiple of 16 in 16..32768 (8192 for the gradient) */
+    int hidden;                /* a multiple of 16 in 16..32768 (8192 for the gradient, whose CTAs hold the sums over rows
+                                  in registers, 16 columns a thread) */
     int dtype;                 /* EP_BF16 or EP_FP16 */
     int post_fp32, pre_fp32, gate_kind, gate_fp32;
     float residual_scale, eps; /* eps >= 0 */
@@ -561,7 +562,7 @@ int ep_matmul_fp8_weight_gradient(const void* dy, int dtype, const void* a, cons
  * block's largest value or less.  Limits: rows up to 128, rows*topk up to 4096, rows*topk*inner below 2^31, experts up to
  * 1024, hidden up to 2^20 and inner up to 2^19, both multiples of 16.  The workspace holds ep_moe_few_workspace_bytes() at least, 16-byte aligned
  * (0 for no rows and for invalid shapes).  From some two rows to an expert on, rows sorted by expert and ep_matmul_fp8 are
- * faster: 64 rows that name 8 of 32 experts of 7168 x 2048 take 462 us here and 240 us there, 4 rows 152 and 155.
+ * faster: 64 rows that name 8 of 32 experts of 7168 x 2048 take 469 us here and 240 us there, 4 rows 154 and 155.
  */
 size_t ep_moe_few_workspace_bytes(int64_t rows, int topk, int inner);
 int ep_moe_few_rows(const void* x, const float* x_scales, int x_dtype, const int32_t* indices, const float* weights,
