@@ -2,8 +2,8 @@
 // bounded waits, tiled TMA loads, and the fifth-generation tensor cores with their tensor memory.
 //
 // Bounded waits.  Every wait gives up after kWaitCycles clock cycles, or the longer limit that a wait for a whole tile is
-// given (or as soon as another thread of the CTA gave up), records EP_ERR_DEVICE_TIMEOUT and returns false.  The warps that load and those that
-// make factors then leave; the multiplying and the scaling warps go through all their blocks, on whatever
+// given (or as soon as another thread of the CTA gave up), records EP_ERR_DEVICE_TIMEOUT and returns false.  The warps that
+// load and those that make factors then leave; the multiplying and the scaling warps go through all their blocks, on whatever
 // is there, because named barriers, whose waits have no limit, need every warp's arrivals in step.  What
 // is in flight is waited for (bounded again), tensor memory is freed, and the kernel returns.
 #pragma once

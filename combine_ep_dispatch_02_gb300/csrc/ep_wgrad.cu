@@ -34,13 +34,12 @@ constexpr int kLineBytes = 8192;                   // 64 columns x 64 rows of 16
 constexpr int kDyBytes = 2 * kLineBytes, kValueBytes = 2 * kLineBytes, kCodeBytes = kGradRows * kGradHalf;
 constexpr int kGradStageBytes = kDyBytes + kValueBytes + kCodeBytes;
 constexpr int kGradStages = 5;
-// Two to a quarter of the lanes, 128 columns each.  8 and 4 warps, before the fence of the pair's arrivals (pair_arrive) added
-// 1 to 2 %: 8192 rows in 8 groups of 4096 x 7168 314 and 320 us, 2048
-// in 16 groups 171 and 226.
+// Two to a quarter of the lanes, 128 columns each.  8 and 4 warps: 8192 rows in 8 groups of 4096 x 7168 314 and 320 us, 2048
+// in 16 groups 171 and 226 (before pair_arrive's fence, which adds 1 to 2 %, as below).
 constexpr int kWriteWarps = 8;
 constexpr int kFirstWriter = 2, kFirstConverter = kFirstWriter + kWriteWarps;
 // Warps that convert a stage.  Each stage has a team of its own: a barrier's parity tells one phase from the next alone, so
-// whoever waits for a stage's phase has to have seen the one before.  Teams of 2 and 4 warps, measured as above: the same rows
+// whoever waits for a stage's phase has to have seen the one before.  Teams of 2 and 4 warps: the same rows
 // 314 and 341 us, 171 and 182 (with 62 registers a thread instead of 93); of 1 against 2, when both were slower, 401 and 352.
 constexpr int kConvertTeam = 2;
 constexpr int kGradThreads = 32 * (kFirstConverter + kGradStages * kConvertTeam);   // load, multiply, write, convert
