@@ -432,8 +432,8 @@ int ep_return_rows_backward(const void* y, const float* weights, const void* dou
  *   inner        a multiple of 16 up to 2^20;  groups up to 4096;  columns up to 2^20;  rows up to 2^31-129
  * swiglu = 0: out [rows][columns], EP_BF16 or EP_FP16 by dtype, rounded once; out_scales is not used.
  * swiglu = 1 (dtype EP_FP8_E4M3, columns a multiple of 32): the first half of b's columns is the gate,
- * the second the up projection; z = gate * sigmoid(gate) * up in FP32 is quantised as by ep_rms_norm_fp8,
- * by the scale's reciprocal: out [rows][columns/2] codes, out_scales [rows][ceil(columns/256)].  A sigmoid below
+ * the second the up projection; z = gate * sigmoid(gate) * up in FP32 is quantised with the scales of
+ * ep_rms_norm_fp8, by their reciprocals: out [rows][columns/2] codes, out_scales [rows][ceil(columns/256)].  A sigmoid below
  * FP32's smallest normal number, 2^-126, counts as 0.
  * a, b and out are 16-byte aligned.  The result does not depend on timing: sums are added in a fixed order.
  * A bounded wait that runs out on the GPU is recorded as EP_ERR_DEVICE_TIMEOUT; out is then not valid.
@@ -515,7 +515,7 @@ int ep_rms_norm_join_backward(const ep_join* join, const void* h, const float* p
  *                offsets)
  *   q, scales    z = gate * sigmoid(gate) * up in FP32 as e4m3 codes [rows][inner], [rows][ceil(inner/128)]
  *   saved, saved_scales  gate_up as codes [rows][2*inner], [rows][ceil(2*inner/128)]
- * Both are quantised as by ep_rms_norm_join, by the scale's reciprocal.  A sigmoid below FP32's smallest normal number,
+ * Both are quantised as by ep_rms_norm_join.  A sigmoid below FP32's smallest normal number,
  * 2^-126, counts as 0.
  *
  * ep_swiglu_saved_backward takes the gradient at the saved values and lets it pass the quantiser of z unchanged:
